@@ -63,6 +63,7 @@ enum pa_device_error {
     PA_DEVERR_TIMEOUT = 8u,   /* a bounded wait inside a kernel ran out */
     PA_DEVERR_POSITION = 16u, /* a position past the block table's capacity */
     PA_DEVERR_LAYOUT = 32u,   /* a kernel found its shared memory misaligned; it did nothing */
+    PA_DEVERR_NO_PAGES = 64u, /* pa_batch_input_prep: a free list ran out */
 };
 
 /*
@@ -339,6 +340,186 @@ int pa_prefill_plan_pieces(int q_len, int q_start, int causal, int num_q_heads,
                            int *num_pieces, int *max_cost);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * Steps around the attention of a serving layer, and the 4-bit KV cache.  A step of a
+ * mixed batch is: pa_batch_input_prep once; per layer pa_qk_norm_rope_cache, then the
+ * attention calls.  The pages describe a single token's input preparation (see
+ * pa_decode_input_prep); these calls extend it to batches of any lengths, and none of the
+ * rest has a counterpart there.
+ * ---------------------------------------------------------------------------------------
+ *
+ * pa_batch_input_prep -- pages, block tables, positions and slots of one step of a mixed
+ * batch, from the requests' lengths, in one launch for every KV-cache group.  Sequence s has
+ * num_computed[s] tokens in the cache and brings num_new[s] more; num_new[s] <= 0 is an
+ * idle (padding) entry.  The step's tokens are numbered sequence by sequence.  Writes
+ *   seq_lens[s]        = num_computed[s] + num_new[s]          (0 for an idle entry)
+ *   query_start_loc[0] = 0, [s + 1] = [s] + num_new[s]         (+ 0 for an idle entry)
+ *   positions[t], seq_idx[t]   position and sequence of token t; -1, -1 behind the last one
+ *   and for each group g of block size bs:
+ *   block_tables[g]    entries ceil(num_computed / bs) .. ceil(seq_len / bs) - 1 of a
+ *                      sequence's row become new pages: free_pages[g][0], [1], ... in the
+ *                      order of the sequences.  Other entries are left as they are.
+ *   slot_mappings[g][t] = table[s, p / bs] * bs + p % bs       (-1 behind the last token)
+ *   pages_taken[g]     how many of free_pages[g] are now in use (may be NULL)
+ *   num_computed, num_new   int32 [num_seqs], device
+ *   num_tokens         length of positions, seq_idx and the slot mappings: at least the
+ *                      step's tokens.  Tokens past it are not written (nor do the pages that
+ *                      begin with them enter the tables) and set PA_DEVERR_POSITION.
+ *   block_tables, bt_strides, max_blocks, block_sizes, free_pages, num_free, slot_mappings:
+ *                      HOST arrays of num_groups entries (1 <= num_groups <= 8), holding
+ *                      device pointers and sizes; read during the call only
+ *   pages_taken        int32 [num_groups], device
+ * Errors on the device: a free list that runs out gives entries and slots of -1 and sets
+ * PA_DEVERR_NO_PAGES; a logical page >= max_blocks[g] takes no page, gives slot -1 and sets
+ * PA_DEVERR_POSITION, as does a negative entry of a page held before or of the free list;
+ * a negative num_computed, or lengths that pass 2^31 - 1, make the entry idle and set
+ * PA_DEVERR_SEQLEN.
+ */
+int pa_batch_input_prep(const int32_t *num_computed, const int32_t *num_new, int num_seqs,
+                        int num_groups, int32_t *const *block_tables, const int64_t *bt_strides,
+                        const int *max_blocks, const int *block_sizes,
+                        const int32_t *const *free_pages, const int *num_free, int num_tokens,
+                        int32_t *seq_lens, int32_t *query_start_loc, int32_t *positions,
+                        int32_t *seq_idx, int64_t *const *slot_mappings, int32_t *pages_taken,
+                        void *stream);
+
+/*
+ * pa_qk_norm_rope -- RMS norm of each query and key head and rotation by position.  Each
+ * row x of one head becomes
+ *     y = x / sqrt(mean(x^2) + eps) * (weight + weight_bias)
+ * in fp32, its first rotary_dim dims are rotated in pairs,
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * and it is rounded to BF16 once.
+ *   q, k        BF16 [num_tokens, heads, head_dim], tokens q_stride / k_stride elements
+ *               apart (multiples of 8): views of a packed projection are taken as they are
+ *   q_weight, k_weight   BF16 [head_dim]; weight_bias is 0, or 1 for weights kept around 0
+ *   cos_sin     fp32 [max_position, rotary_dim]: row p holds cos(p f_i), i < rotary_dim / 2,
+ *               then sin(p f_i)
+ *   interleaved 0: pair i is dims (i, i + rotary_dim / 2); otherwise dims (2i, 2i + 1)
+ *   positions   int32 [num_tokens]; a negative one is padding: the token's outputs are left
+ *               as they were.  One >= max_position does the same and sets
+ *               PA_DEVERR_POSITION.
+ *   q_out, k_out  rows like q and k, with strides of their own; may be q and k themselves
+ *               (with the same strides), otherwise they must not overlap any input
+ * head_dim 64, 128 or 256 (else PA_ERR_UNSUPPORTED); rotary_dim a multiple of 16, at most
+ * head_dim, 0 for no rotation.  num_tokens == 0 is a no-op.
+ */
+int pa_qk_norm_rope(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                    const pa_bf16 *q_weight, const pa_bf16 *k_weight, float weight_bias, float eps,
+                    const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                    const int32_t *positions, int num_tokens, int num_q_heads, int num_kv_heads,
+                    int head_dim, pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out,
+                    int64_t k_out_stride, void *stream);
+
+/*
+ * pa_qk_norm_rope_cache -- pa_qk_norm_rope with the KV write in the same launch: token i's
+ * normed and rotated key rows and its value rows v (unchanged) go to slot slot_mapping[i] of
+ * the caches, as pa_reshape_and_cache (cache_format PA_CACHE_BF16) or
+ * pa_reshape_and_cache_q4 (PA_CACHE_Q4; head_dim 256) would write them.  page_stride is in
+ * elements for a BF16 cache, in bytes for a 4-bit one.  Slots as in those calls; a token
+ * whose position is padding or out of range writes nothing.
+ */
+enum pa_cache_format { PA_CACHE_BF16 = 0, PA_CACHE_Q4 = 1 };
+
+int pa_qk_norm_rope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                          const pa_bf16 *v, int64_t v_stride, const pa_bf16 *q_weight,
+                          const pa_bf16 *k_weight, float weight_bias, float eps,
+                          const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                          const int32_t *positions, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, pa_bf16 *q_out, int64_t q_out_stride,
+                          int cache_format, void *k_cache, void *v_cache, int64_t page_stride,
+                          int64_t num_pages, const int64_t *slot_mapping, int block_size,
+                          void *stream);
+
+/*
+ * The 4-bit cache.  A row (one token of one KV head, 256 values) takes PA_Q4_ROW_BYTES
+ * instead of 512: it is cut into 4 groups of 64 dims, and group g keeps its minimum lo and
+ * a step s = bf16((max - lo) / 15), both BF16, and a code n = clamp(rint((x - lo) / s), 0,
+ * 15) per value (ties to even; 0 where s is 0).  It stands for lo + s * n.  A group that
+ * holds a NaN or an infinity (or spans more than fp32 does) reads back as NaN.
+ *
+ * K and V caches are separate arrays of pages, page_stride bytes apart (a multiple of 16,
+ * at least num_kv_heads * block_size * PA_Q4_ROW_BYTES); block_size is at most 2^20.  A page holds for each KV head
+ * first its tokens' codes, 128 bytes each, then their pairs (s, lo of group 0, s, lo of
+ * group 1, ...), 16 bytes each.  Dim 64g + 8u + j of the token at offset o of its page is
+ * in byte o * 128 + (u ^ (o % 8)) * 16 + 4g + j / 2 of the head's bytes, in the lower half
+ * for even j.  Block tables, slots and errors are those of the BF16 cache.
+ */
+#define PA_Q4_ROW_BYTES 144
+
+/*
+ * pa_reshape_and_cache_q4 -- KV write of new tokens into the 4-bit cache: pa_reshape_and_cache
+ * with quantisation.  key, value BF16 [num_tokens, num_kv_heads, 256], tokens key_stride /
+ * value_stride elements apart (multiples of 8).  Slots must differ from one another
+ * (negative ones, which are skipped, aside).
+ */
+int pa_reshape_and_cache_q4(const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value,
+                            int64_t value_stride, void *k_cache, void *v_cache,
+                            int64_t page_stride, int64_t num_pages, const int64_t *slot_mapping,
+                            int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                            void *stream);
+
+/*
+ * pa_gather_cache_q4 -- reads tokens back by slot: k_out, v_out BF16 [num_tokens,
+ * num_kv_heads, 256], contiguous, receive lo + s * n rounded to BF16.  Rows of negative
+ * slots are left as they were; a slot outside the pool does the same and sets
+ * PA_DEVERR_SLOT.
+ */
+int pa_gather_cache_q4(const void *k_cache, const void *v_cache, int64_t page_stride,
+                       int64_t num_pages, const int64_t *slot_mapping, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, pa_bf16 *k_out,
+                       pa_bf16 *v_out, void *stream);
+
+/*
+ * pa_decode_q4 -- pa_decode over the 4-bit cache: the attention of q over the values that
+ * the cache's codes stand for, accumulated in fp32.  The newest tokens must be in the cache
+ * (pa_qk_norm_rope_cache or pa_reshape_and_cache_q4 first).  Arguments and errors are those
+ * of pa_decode (without the fused write and with out on the device), but: page_stride is in
+ * bytes; seq_lens[s] may be 0, a padding entry, whose rows of out become zeros; the
+ * workspace is sized by pa_decode_q4_workspace_size.  A page outside the pool sets
+ * PA_DEVERR_PAGE and its tokens read as zeros.  Steps of V count as at most 2^80.
+ */
+size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_seq_len);
+
+int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int64_t page_stride,
+                 int64_t num_pages, const int32_t *block_table, int64_t bt_stride,
+                 const int32_t *seq_lens, int num_seqs, int max_seq_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * pa_prefill_chunk_q4, pa_prefill_varlen_q4 -- pa_prefill_chunk and pa_prefill_varlen over
+ * the 4-bit cache (the chunk's own tokens included, which must be in it).  The sequences are
+ * and the queries are first expanded into FP16 in the workspace (each query row and each KV
+ * head of a sequence scaled by a power of two: values are rounded to 2^-12, an eighth of
+ * BF16's step), which the prefill kernel then reads as pages.  The expansion is linear in the
+ * keys, the attention quadratic.  Arguments and errors are those of the BF16 calls, but: page_stride is in bytes, and the
+ * workspace is required.  With the bytes that the size functions give (1 KB per key and KV
+ * head, 0.5 KB per query row and head, and room for split items) items may be split; with
+ * less than the expansion needs the call is refused (PA_ERR_INVALID_ARG).
+ */
+size_t pa_prefill_q4_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size);
+
+int pa_prefill_chunk_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                        int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                        int q_len, int q_start, int causal, int num_q_heads, int num_kv_heads,
+                        int head_dim, int block_size, float scale, pa_bf16 *out, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
+                                           int num_seqs, int causal, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size);
+
+int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                         int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                         int64_t bt_stride, const int32_t *cu_seqlens_q,
+                         const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * pa_copy -- copies `bytes` bytes from src to dst with a kernel on `stream` (ordered like
  * the library's other launches, and capturable into a CUDA graph).  Each address may be
  * device memory or page-locked host memory (cudaHostAlloc / cudaMallocHost / registered
@@ -367,7 +548,7 @@ int pa_get_device_errors(unsigned int *bits, int clear, void *stream);
 
 /*
  * pa_set_kernel_events -- measurement hook.  The next pa_decode, pa_decode_append,
- * pa_prefill_chunk or pa_prefill_varlen call made by this host thread records `start` on
+ * pa_prefill_chunk or pa_prefill_varlen call (or 4-bit decode or prefill call) made by this host thread records `start` on
  * its stream immediately before it launches its main kernel (the split-context decode
  * kernel, or the prefill kernel) and `stop` immediately after that launch, then forgets
  * both.  Inside a stream capture the records carry cudaEventRecordExternal, so they

@@ -17,6 +17,15 @@ Functions (names follow the C ABI):
     prefill_varlen_workspace_size(...), prefill_varlen(q, k_cache, v_cache, block_table,
                                                cu_seqlens_q, seq_lens_k, causal, scale)
     prefill_plan(q_len, q_start, causal, num_q_heads, block_size, num_ctas)  (host only)
+    batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_pages, num_tokens)
+                                                                      -> mixed-step inputs
+    qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps)   -> q, k
+    qk_norm_rope_cache(q, k, v, ..., eps, k_cache, v_cache, slot_mapping)
+                                                                      -> q (K/V in place)
+    4-bit cache (uint8 tensors of q4_cache_shape(num_pages, block_size, num_kv_heads)):
+    reshape_and_cache_q4(...) (in place), gather_cache_q4(...) -> key, value
+    decode_q4(...), prefill_chunk_q4(...), prefill_varlen_q4(...) and their
+    *_workspace_size functions: as the calls without _q4
     device_errors(clear=True)
 """
 from __future__ import annotations
@@ -34,11 +43,16 @@ __all__ = ["load", "build", "slot_mapping", "decode_input_prep", "reshape_and_ca
            "decode", "decode_append", "prefill_chunk", "prefill_varlen", "prefill_plan",
            "prefill_workspace_size", "prefill_varlen_workspace_size", "prefill_plan_pieces", "device_errors", "set_kernel_events", "build_info", "PAError",
            "DEVERR_PAGE", "DEVERR_SEQLEN", "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_POSITION", "DEVERR_LAYOUT",
+           "DEVERR_NO_PAGES", "Q4_ROW_BYTES", "batch_input_prep", "qk_norm_rope",
+           "qk_norm_rope_cache", "q4_cache_shape", "reshape_and_cache_q4", "gather_cache_q4",
+           "decode_q4", "decode_q4_workspace_size", "prefill_chunk_q4",
+           "prefill_q4_workspace_size", "prefill_varlen_q4", "prefill_varlen_q4_workspace_size",
            "LIB_PATH"]
 
 LIB_PATH = _build.LIB
 DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_POSITION = 1, 2, 4, 8, 16
-DEVERR_LAYOUT = 32
+DEVERR_LAYOUT, DEVERR_NO_PAGES = 32, 64
+Q4_ROW_BYTES = 144  # PA_Q4_ROW_BYTES: a token of one KV head in the 4-bit cache
 ERR_TIMEOUT = 4  # PA_ERR_TIMEOUT
 
 _lib = None
@@ -87,6 +101,25 @@ def load():
                                         P], i32),
             "pa_prefill_varlen": ([P, P, P, i64, i64, P, i64, P, P, i32, i32, i32, i32, i32,
                                    i32, f32, P, P, sz, P], i32),
+            "pa_batch_input_prep": ([P, P, i32, i32, P, P, P, P, P, P, i32, P, P, P, P, P, P, P],
+                                    i32),
+            "pa_qk_norm_rope": ([P, i64, P, i64, P, P, f32, f32, P, i32, i32, i32, P, i32, i32,
+                                 i32, i32, P, i64, P, i64, P], i32),
+            "pa_qk_norm_rope_cache": ([P, i64, P, i64, P, i64, P, P, f32, f32, P, i32, i32, i32,
+                                       P, i32, i32, i32, i32, P, i64, i32, P, P, i64, i64, P, i32,
+                                       P], i32),
+            "pa_reshape_and_cache_q4": ([P, i64, P, i64, P, P, i64, i64, P, i32, i32, i32, i32,
+                                         P], i32),
+            "pa_gather_cache_q4": ([P, P, i64, i64, P, i32, i32, i32, i32, P, P, P], i32),
+            "pa_decode_q4_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
+            "pa_decode_q4": ([P, P, P, i64, i64, P, i64, P, i32, i32, i32, i32, i32, i32, f32, P,
+                              P, sz, P], i32),
+            "pa_prefill_q4_workspace_size": ([i32, i32, i32, i32, i32, i32, i32], sz),
+            "pa_prefill_chunk_q4": ([P, P, P, i64, i64, P, i32, i32, i32, i32, i32, i32, i32,
+                                     f32, P, P, sz, P], i32),
+            "pa_prefill_varlen_q4_workspace_size": ([P, P, i32, i32, i32, i32, i32, i32], sz),
+            "pa_prefill_varlen_q4": ([P, P, P, i64, i64, P, i64, P, P, i32, i32, i32, i32, i32,
+                                      i32, f32, P, P, sz, P], i32),
             "pa_copy": ([P, P, sz, P], i32),
             "pa_get_device_errors": ([ctypes.POINTER(ctypes.c_uint), i32, P], i32),
             "pa_set_kernel_events": ([P, P], i32),
@@ -429,6 +462,331 @@ def prefill_plan_pieces(q_len, q_start, causal, num_q_heads, num_kv_heads, block
            "pa_prefill_plan_pieces")
     pieces = [(arrs[0][p], arrs[1][p], arrs[2][p], arrs[3][p]) for p in range(npc.value)]
     return list(items)[:ni.value], pieces, mc.value
+
+
+def _same_device(first, *others):
+    """The stream that a call is queued on belongs to the current device: every tensor has
+    to lie there."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device() or any(t.device != dev for t in others
+                                                       if t is not None):
+        raise ValueError("all tensors must be on the current CUDA device")
+
+
+def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_pages, num_tokens,
+                     out=None):
+    """One mixed step's inputs from the requests' lengths (see pa_batch_input_prep).
+    num_computed, num_new: int32 [S]; per KV-cache group an int32 [S, n] block table, which
+    receives the new pages, a block size and an int32 list of free pages.  num_tokens: rows
+    of the per-token outputs, at least the step's tokens.  Returns a dict with seq_lens,
+    query_start_loc, positions, seq_idx, slot_mappings (one per group) and pages_taken (int32
+    [groups]); `out` may pass that dict back in to reuse its tensors."""
+    lib = load()
+    S, G, T = num_computed.shape[0], len(block_tables), int(num_tokens)
+    if len(block_sizes) != G or len(free_pages) != G or not 1 <= G <= 8:
+        raise ValueError("one block size and one free list per group, 1..8 groups")
+    for t, nm in ((num_computed, "num_computed"), (num_new, "num_new")):
+        _check(t, nm, torch.int32, 1)
+        if t.shape[0] != S or not t.is_contiguous():
+            raise ValueError("num_computed and num_new: contiguous, one entry per sequence")
+    for t, f in zip(block_tables, free_pages):
+        _check(t, "block_table", torch.int32, 2)
+        _check(f, "free_pages", torch.int32, 1)
+        if t.shape[0] < S or t.shape[1] < 1 or not f.is_contiguous() or \
+                (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError("block tables: one row per sequence, contiguous rows; free lists "
+                             "contiguous")
+    _same_device(num_computed, num_new, *block_tables, *free_pages)
+    if out is None:
+        dev, i32 = num_computed.device, torch.int32
+        out = {"seq_lens": torch.empty(S, dtype=i32, device=dev),
+               "query_start_loc": torch.empty(S + 1, dtype=i32, device=dev),
+               "positions": torch.empty(T, dtype=i32, device=dev),
+               "seq_idx": torch.empty(T, dtype=i32, device=dev),
+               "slot_mappings": [torch.empty(T, dtype=torch.int64, device=dev) for _ in range(G)],
+               "pages_taken": torch.empty(G, dtype=i32, device=dev)}
+    else:
+        sizes = (("seq_lens", S), ("query_start_loc", S + 1), ("positions", T), ("seq_idx", T),
+                 ("pages_taken", G))
+        if len(out["slot_mappings"]) != G:
+            raise ValueError("out: one slot mapping per group")
+        for t, n, dt in [(out[k], n, torch.int32) for k, n in sizes] + \
+                [(m, T, torch.int64) for m in out["slot_mappings"]]:
+            _check(t, "out", dt, 1)
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError("out: contiguous tensors of this call's sizes")
+            _same_device(num_computed, t)
+    arr = lambda ctype, vals: (ctype * G)(*vals)
+    ptrs = lambda ts: arr(ctypes.c_void_p, [t.data_ptr() for t in ts])
+    _raise(lib.pa_batch_input_prep(
+        _ptr(num_computed), _ptr(num_new), S, G, ptrs(block_tables),
+        arr(ctypes.c_int64, [_table_stride(t) for t in block_tables]),
+        arr(ctypes.c_int, [t.shape[1] for t in block_tables]),
+        arr(ctypes.c_int, [int(b) for b in block_sizes]), ptrs(free_pages),
+        arr(ctypes.c_int, [f.numel() for f in free_pages]), T, _ptr(out["seq_lens"]),
+        _ptr(out["query_start_loc"]), _ptr(out["positions"]), _ptr(out["seq_idx"]),
+        ptrs(out["slot_mappings"]), _ptr(out["pages_taken"]), _stream()), "pa_batch_input_prep")
+    return out
+
+
+def _table_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _token_rows(t, name, heads=None, dim=None):
+    """Checks BF16 [tokens, heads, dim] rows, each token's heads contiguous; returns the
+    distance between tokens."""
+    _check(t, name, torch.bfloat16, 3)
+    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: each token's rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _rope_args(q, k, q_weight, k_weight, cos_sin, positions):
+    T, hq, d = q.shape
+    qs, ks = _token_rows(q, "q"), _token_rows(k, "k", None, d)
+    if k.shape[0] != T:
+        raise ValueError("q and k must have the same number of tokens")
+    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _check(t, nm, torch.bfloat16, 1)
+        if t.shape[0] != d or not t.is_contiguous():
+            raise ValueError(f"{nm} must be a contiguous [head_dim] tensor")
+    _check(cos_sin, "cos_sin", torch.float32, 2)
+    _check(positions, "positions", torch.int32, 1)
+    if not cos_sin.is_contiguous() or not positions.is_contiguous() or positions.shape[0] != T:
+        raise ValueError("cos_sin and positions must be contiguous, one position per token")
+    return T, hq, k.shape[1], d, qs, ks
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved=False,
+                 weight_bias=0.0, q_out=None, k_out=None):
+    """RMS norm of each query and key head and rotation by position (see pa_qk_norm_rope).
+    q [T, Hq, D], k [T, Hkv, D] (views of a packed projection are taken as they are); cos_sin
+    fp32 [max_position, rotary_dim], cosines then sines.  q_out / k_out may be q / k.  Rows of
+    negative positions are left as they were.  Returns (q_out, k_out)."""
+    lib = load()
+    T, hq, hkv, d, qs, ks = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
+    q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty((T, hkv, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
+    qos, kos = _token_rows(q_out, "q_out", hq, d), _token_rows(k_out, "k_out", hkv, d)
+    if q_out.shape[0] != T or k_out.shape[0] != T:
+        raise ValueError("q_out and k_out must have q's number of tokens")
+    _same_device(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
+    _raise(lib.pa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
+                               float(weight_bias), float(eps), _ptr(cos_sin), cos_sin.shape[0],
+                               cos_sin.shape[1], int(bool(interleaved)), _ptr(positions), T, hq,
+                               hkv, d, _ptr(q_out), qos, _ptr(k_out), kos, _stream()),
+           "pa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos_sin, positions, eps, k_cache, v_cache,
+                       slot_mapping, interleaved=False, weight_bias=0.0, q_out=None):
+    """qk_norm_rope with the KV write in the same launch: the keys, and the values v as they
+    are, go to their slots of the caches (see pa_qk_norm_rope_cache), BF16 [num_pages,
+    block_size, Hkv, D] or 4-bit (uint8, q4_cache_shape).  Returns q_out."""
+    lib = load()
+    T, hq, hkv, d, qs, ks = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
+    vs = _token_rows(v, "v", hkv, d)
+    _check(slot_mapping, "slot_mapping", torch.int64, 1)
+    if v.shape[0] != T or slot_mapping.shape[0] != T or not slot_mapping.is_contiguous():
+        raise ValueError("v and slot_mapping must have one entry per token")
+    if isinstance(k_cache, torch.Tensor) and k_cache.dtype == torch.uint8:
+        fmt = 1
+        ps, bs, heads = _check_q4_cache(k_cache, v_cache)
+        dim = 256
+    else:
+        fmt = 0
+        ps = _check_cache(k_cache, v_cache)
+        _, bs, heads, dim = k_cache.shape
+    if (heads, dim) != (hkv, d):
+        raise ValueError("the caches' heads must be k's")
+    q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    qos = _token_rows(q_out, "q_out", hq, d)
+    if q_out.shape[0] != T:
+        raise ValueError("q_out must have q's number of tokens")
+    _same_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slot_mapping,
+                 q_out)
+    _raise(lib.pa_qk_norm_rope_cache(
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), float(weight_bias),
+        float(eps), _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+        _ptr(positions), T, hq, hkv, d, _ptr(q_out), qos, fmt, _ptr(k_cache), _ptr(v_cache), ps,
+        k_cache.shape[0], _ptr(slot_mapping), bs, _stream()), "pa_qk_norm_rope_cache")
+    return q_out
+
+
+def q4_cache_shape(num_pages, block_size, num_kv_heads):
+    """Shape of a 4-bit K or V cache (uint8; see pa.h for its bytes)."""
+    return (num_pages, num_kv_heads, block_size * Q4_ROW_BYTES)
+
+
+def _check_q4_cache(k_cache, v_cache):
+    """(page stride in bytes, block size, KV heads) of a pair of 4-bit caches."""
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(t, n, torch.uint8, 3)
+        if t.shape[2] % Q4_ROW_BYTES or t.shape[2] == 0 or t.stride(2) != 1 or \
+                (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError(f"{n}: each page must be a contiguous [Hkv, block_size * "
+                             f"{Q4_ROW_BYTES}] block of bytes")
+    page = k_cache.shape[1] * k_cache.shape[2]
+    ps = k_cache.stride(0) if k_cache.shape[0] > 1 else page
+    vps = v_cache.stride(0) if v_cache.shape[0] > 1 else page
+    if k_cache.shape != v_cache.shape or ps != vps:
+        raise ValueError("k_cache and v_cache must have the same shape and page stride")
+    return ps, k_cache.shape[2] // Q4_ROW_BYTES, k_cache.shape[1]
+
+
+def reshape_and_cache_q4(key, value, k_cache, v_cache, slot_mapping):
+    """Quantise key/value [T, Hkv, 256] into the 4-bit caches at slot_mapping (in place)."""
+    lib = load()
+    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
+    ks = _token_rows(key, "key", hkv, 256)
+    vs = _token_rows(value, "value", hkv, 256)
+    _check(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = key.shape[0]
+    if value.shape[0] != T or slot_mapping.shape[0] != T or not slot_mapping.is_contiguous():
+        raise ValueError("value and slot_mapping must have one entry per token")
+    _same_device(key, value, k_cache, v_cache, slot_mapping)
+    _raise(lib.pa_reshape_and_cache_q4(_ptr(key), ks, _ptr(value), vs, _ptr(k_cache),
+                                       _ptr(v_cache), ps, k_cache.shape[0], _ptr(slot_mapping), T,
+                                       hkv, 256, bs, _stream()), "pa_reshape_and_cache_q4")
+
+
+def gather_cache_q4(k_cache, v_cache, slot_mapping, k_out=None, v_out=None):
+    """The tokens at slot_mapping [T] as BF16 (k, v), each [T, Hkv, 256].  Rows of negative
+    slots are left as they were (zeros in tensors made here)."""
+    lib = load()
+    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
+    _check(slot_mapping, "slot_mapping", torch.int64, 1)
+    T = slot_mapping.shape[0]
+    outs = []
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.zeros((T, hkv, 256), dtype=torch.bfloat16, device=k_cache.device)
+        _check(t, nm, torch.bfloat16, 3)
+        if t.shape != (T, hkv, 256) or not t.is_contiguous():
+            raise ValueError(f"{nm} must be a contiguous [T, Hkv, 256] tensor")
+        outs.append(t)
+    if not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous")
+    _same_device(k_cache, v_cache, slot_mapping, *outs)
+    _raise(lib.pa_gather_cache_q4(_ptr(k_cache), _ptr(v_cache), ps, k_cache.shape[0],
+                                  _ptr(slot_mapping), T, hkv, 256, bs, _ptr(outs[0]),
+                                  _ptr(outs[1]), _stream()), "pa_gather_cache_q4")
+    return outs[0], outs[1]
+
+
+def decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                             max_seq_len) -> int:
+    return int(load().pa_decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                  block_size, max_seq_len))
+
+
+def _q4_out(out, q):
+    if out is None:
+        return torch.empty_like(q)
+    _check(out, "out", torch.bfloat16, 3)
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous BF16 tensor shaped like q")
+    return out
+
+
+def decode_q4(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, out=None,
+              workspace=None):
+    """q=1 decode over the 4-bit cache (see pa_decode_q4).  Returns out [S, Hq, 256] BF16;
+    rows of sequences of length 0 are zeros."""
+    lib = load()
+    _check(q, "q", torch.bfloat16, 3)
+    _check(block_table, "block_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
+    q = q.contiguous()
+    S, hq, d = q.shape
+    if block_table.shape[0] < S or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or \
+            seq_lens.shape[0] < S or not seq_lens.is_contiguous():
+        raise ValueError("block_table and seq_lens: one entry per sequence, contiguous rows")
+    if block_table.shape[1] * bs < max_seq_len:
+        raise ValueError("block_table rows are too short for max_seq_len")
+    out = _q4_out(out, q)
+    if workspace is None:
+        need = decode_q4_workspace_size(S, hq, hkv, d, bs, max_seq_len)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _same_device(q, k_cache, v_cache, block_table, seq_lens, out, workspace)
+    _raise(lib.pa_decode_q4(_ptr(q), _ptr(k_cache), _ptr(v_cache), ps, k_cache.shape[0],
+                            _ptr(block_table), _table_stride(block_table),
+                            _ptr(seq_lens), S, int(max_seq_len), hq, hkv, d, bs, float(scale),
+                            _ptr(out), _ptr(workspace),
+                            workspace.numel() * workspace.element_size(), _stream()),
+           "pa_decode_q4")
+    return out
+
+
+def prefill_q4_workspace_size(q_len, q_start, causal, num_q_heads, num_kv_heads, head_dim,
+                              block_size) -> int:
+    """Bytes of workspace for prefill_chunk_q4 (the expanded operands, and room for split items)."""
+    return int(load().pa_prefill_q4_workspace_size(int(q_len), int(q_start), int(bool(causal)),
+                                                   num_q_heads, num_kv_heads, head_dim,
+                                                   block_size))
+
+
+def prefill_chunk_q4(q, k_cache, v_cache, block_table, q_start, causal, scale, out=None,
+                     workspace=None):
+    """Causal (or full) chunk attention of one sequence over the 4-bit cache (see
+    pa_prefill_chunk_q4).  Without a workspace, one of prefill_q4_workspace_size bytes is
+    allocated for the call."""
+    bt = block_table.reshape(1, -1)
+    return prefill_varlen_q4(q, k_cache, v_cache, bt, [0, q.shape[0]],
+                             [int(q_start) + q.shape[0]], causal, scale, out, workspace)
+
+
+def _varlen_lens(cu_seqlens_q, seq_lens_k):
+    B = len(seq_lens_k)
+    if len(cu_seqlens_q) != B + 1:
+        raise ValueError("cu_seqlens_q: num_seqs + 1 offsets")
+    return ((ctypes.c_int32 * (B + 1))(*[int(x) for x in cu_seqlens_q]),
+            (ctypes.c_int32 * max(B, 1))(*[int(x) for x in seq_lens_k]), B)
+
+
+def prefill_varlen_q4_workspace_size(cu_seqlens_q, seq_lens_k, causal, num_q_heads, num_kv_heads,
+                                     head_dim, block_size) -> int:
+    """Bytes of workspace for prefill_varlen_q4 (the expanded operands, and room for split items)."""
+    cu, sk, B = _varlen_lens(cu_seqlens_q, seq_lens_k)
+    return int(load().pa_prefill_varlen_q4_workspace_size(cu, sk, B, int(bool(causal)),
+                                                          num_q_heads, num_kv_heads, head_dim,
+                                                          block_size))
+
+
+def prefill_varlen_q4(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k, causal, scale,
+                      out=None, workspace=None):
+    """Chunks of several sequences stacked row-wise in q, over the 4-bit cache (see
+    pa_prefill_varlen_q4).  cu_seqlens_q and seq_lens_k are host sequences of ints.  Without a
+    workspace, one of prefill_varlen_q4_workspace_size bytes is allocated for the call."""
+    lib = load()
+    _check(q, "q", torch.bfloat16, 3)
+    _check(block_table, "block_table", torch.int32, 2)
+    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
+    q = q.contiguous()
+    _, hq, d = q.shape
+    cu, sk, B = _varlen_lens(cu_seqlens_q, seq_lens_k)
+    if cu[B] != q.shape[0]:
+        raise ValueError("cu_seqlens_q must end at q's row count")
+    if block_table.shape[0] < B or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or \
+            (B and block_table.shape[1] * bs < max(sk)):
+        raise ValueError("block_table: one contiguous row per sequence, as long as its keys need")
+    out = _q4_out(out, q)
+    if workspace is None:
+        need = int(lib.pa_prefill_varlen_q4_workspace_size(cu, sk, B, int(bool(causal)), hq, hkv,
+                                                           d, bs))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _same_device(q, k_cache, v_cache, block_table, out, workspace)
+    _raise(lib.pa_prefill_varlen_q4(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), ps, k_cache.shape[0], _ptr(block_table),
+        _table_stride(block_table), cu, sk, B, int(bool(causal)), hq, hkv, d,
+        bs, float(scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream()), "pa_prefill_varlen_q4")
+    return out
 
 
 def set_kernel_events(start, stop):

@@ -492,7 +492,8 @@ static int prefill_launch(const pa_bf16 *q, int total_q, const pa_bf16 *k_cache,
                           int num_kv_heads, int head_dim, int block_size, float scale,
                           pa_bf16 *out, void *workspace, size_t workspace_bytes,
                           const DeviceInfo &dev, cudaEvent_t ev_start, cudaEvent_t ev_stop,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, const float *q_factor = nullptr,
+                          const float2 *kv_factor = nullptr) {
     constexpr int kM = 3 + pa::kPfMaxPackMaps;  // index of the first per-sequence map
     CUtensorMap maps[kM + 2 * pa::kPfMaxSeqs];
     const int group = num_q_heads / num_kv_heads;
@@ -544,6 +545,8 @@ static int prefill_launch(const pa_bf16 *q, int total_q, const pa_bf16 *k_cache,
     a.out = out;
     a.err = dev.err;
     a.num_sms = dev.num_sms;
+    a.q_factor = q_factor;
+    a.kv_factor = kv_factor;
     a.ev_start = ev_start;
     a.ev_stop = ev_stop;
     if (diag_enabled())
@@ -679,6 +682,429 @@ int pa_prefill_varlen(const pa_bf16 *q, const pa_bf16 *k_cache, const pa_bf16 *v
             return rc;
     }
     return PA_OK;
+}
+
+// ------------------------------------------------------------- mixed-step inputs
+int pa_batch_input_prep(const int32_t *num_computed, const int32_t *num_new, int num_seqs,
+                        int num_groups, int32_t *const *block_tables, const int64_t *bt_strides,
+                        const int *max_blocks, const int *block_sizes,
+                        const int32_t *const *free_pages, const int *num_free, int num_tokens,
+                        int32_t *seq_lens, int32_t *query_start_loc, int32_t *positions,
+                        int32_t *seq_idx, int64_t *const *slot_mappings, int32_t *pages_taken,
+                        void *stream) {
+    if (num_seqs < 0 || num_tokens < 0 || num_groups < 1 || num_groups > pa::kPrepMaxGroups)
+        return PA_ERR_INVALID_ARG;
+    if (!block_tables || !bt_strides || !max_blocks || !block_sizes || !free_pages || !num_free ||
+        !slot_mappings)
+        return PA_ERR_INVALID_ARG;
+    pa::BatchPrepArgs a = {};
+    for (int g = 0; g < num_groups; ++g) {
+        if ((num_seqs > 0 && !block_tables[g]) || (num_tokens > 0 && !slot_mappings[g]) ||
+            block_sizes[g] < 1 || max_blocks[g] < 1 || bt_strides[g] < max_blocks[g] ||
+            num_free[g] < 0 || (num_free[g] > 0 && !free_pages[g]) ||
+            (reinterpret_cast<uintptr_t>(slot_mappings[g]) & 7u))
+            return PA_ERR_INVALID_ARG;
+        a.g[g] = pa::BatchPrepGroup{block_tables[g], bt_strides[g], max_blocks[g], block_sizes[g],
+                                    free_pages[g],   num_free[g],   slot_mappings[g],
+                                    pages_taken ? pages_taken + g : nullptr};
+    }
+    if (!query_start_loc || (num_seqs > 0 && (!num_computed || !num_new || !seq_lens)) ||
+        (num_tokens > 0 && (!positions || !seq_idx)))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    a.num_computed = num_computed;
+    a.num_new = num_new;
+    a.num_seqs = num_seqs;
+    a.num_tokens = num_tokens;
+    a.num_groups = num_groups;
+    a.seq_lens = seq_lens;
+    a.query_start_loc = query_start_loc;
+    a.positions = positions;
+    a.seq_idx = seq_idx;
+    a.err = dev.err;
+    return pa::launch_batch_prep(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                      : PA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------- norm + rotation
+constexpr int kQ4MaxBlock = 1 << 20;  // a head's bytes of a page stay within 32 bits
+
+// A [num_tokens, heads, head_dim] operand whose tokens are `stride` elements apart.
+static bool rows_ok(const void *p, int64_t stride, int64_t row) {
+    return p && aligned16(p) && stride >= row && stride % 8 == 0;
+}
+
+static int rope_impl(pa::RopeArgs &a, void *stream) {
+    if (a.num_tokens < 0 || a.num_q_heads < 1 || a.num_kv_heads < 1 || a.head_dim < 1 ||
+        a.num_q_heads > 65535 || a.num_kv_heads > 65535 || a.max_position < 1 || a.rotary_dim < 0 ||
+        !(a.eps >= 0.f) || !isfinite(a.eps) || !isfinite(a.weight_bias))
+        return PA_ERR_INVALID_ARG;
+    if (a.rotary_dim % 16 || a.rotary_dim > a.head_dim) return PA_ERR_INVALID_ARG;
+    if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return PA_ERR_UNSUPPORTED;
+    if (a.cache == 2 && a.head_dim != pa::kHeadDim) return PA_ERR_UNSUPPORTED;
+    if (a.num_tokens == 0) return PA_OK;
+    const int64_t qrow = (int64_t)a.num_q_heads * a.head_dim;
+    const int64_t krow = (int64_t)a.num_kv_heads * a.head_dim;
+    if (!rows_ok(a.q, a.q_stride, qrow) || !rows_ok(a.k, a.k_stride, krow) ||
+        !rows_ok(a.q_out, a.q_out_stride, qrow) || !a.positions || !a.q_weight || !a.k_weight ||
+        !aligned16(a.q_weight) || !aligned16(a.k_weight) ||
+        (a.rotary_dim > 0 && (!a.cos_sin || !aligned16(a.cos_sin))))
+        return PA_ERR_INVALID_ARG;
+    if (a.cache) {
+        const int64_t page = a.cache == 1
+                                 ? (int64_t)a.block_size * krow
+                                 : (int64_t)a.block_size * a.num_kv_heads * PA_Q4_ROW_BYTES;
+        const int64_t unit = a.cache == 1 ? 8 : 16;
+        if (a.block_size < 1 || (a.cache == 2 && a.block_size > kQ4MaxBlock) ||
+            a.num_pages < 1 || a.page_stride < page || a.page_stride % unit ||
+            !rows_ok(a.v, a.v_stride, krow) || !a.k_cache || !a.v_cache || !aligned16(a.k_cache) ||
+            !aligned16(a.v_cache) || !a.slot_mapping ||
+            (reinterpret_cast<uintptr_t>(a.slot_mapping) & 7u))
+            return PA_ERR_INVALID_ARG;
+    } else if (!rows_ok(a.k_out, a.k_out_stride, krow)) {
+        return PA_ERR_INVALID_ARG;
+    }
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    a.err = dev.err;
+    return pa::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_qk_norm_rope(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                    const pa_bf16 *q_weight, const pa_bf16 *k_weight, float weight_bias, float eps,
+                    const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                    const int32_t *positions, int num_tokens, int num_q_heads, int num_kv_heads,
+                    int head_dim, pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out,
+                    int64_t k_out_stride, void *stream) {
+    pa::RopeArgs a = {};
+    a.q = q; a.q_stride = q_stride; a.k = k; a.k_stride = k_stride;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.weight_bias = weight_bias; a.eps = eps;
+    a.cos_sin = cos_sin; a.max_position = max_position; a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved; a.positions = positions; a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads; a.num_kv_heads = num_kv_heads; a.head_dim = head_dim;
+    a.q_out = q_out; a.q_out_stride = q_out_stride; a.k_out = k_out; a.k_out_stride = k_out_stride;
+    return rope_impl(a, stream);
+}
+
+int pa_qk_norm_rope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                          const pa_bf16 *v, int64_t v_stride, const pa_bf16 *q_weight,
+                          const pa_bf16 *k_weight, float weight_bias, float eps,
+                          const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                          const int32_t *positions, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, pa_bf16 *q_out, int64_t q_out_stride,
+                          int cache_format, void *k_cache, void *v_cache, int64_t page_stride,
+                          int64_t num_pages, const int64_t *slot_mapping, int block_size,
+                          void *stream) {
+    if (cache_format != PA_CACHE_BF16 && cache_format != PA_CACHE_Q4) return PA_ERR_INVALID_ARG;
+    pa::RopeArgs a = {};
+    a.q = q; a.q_stride = q_stride; a.k = k; a.k_stride = k_stride; a.v = v; a.v_stride = v_stride;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.weight_bias = weight_bias; a.eps = eps;
+    a.cos_sin = cos_sin; a.max_position = max_position; a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved; a.positions = positions; a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads; a.num_kv_heads = num_kv_heads; a.head_dim = head_dim;
+    a.q_out = q_out; a.q_out_stride = q_out_stride;
+    a.cache = cache_format == PA_CACHE_BF16 ? 1 : 2;
+    a.k_cache = static_cast<uint8_t *>(k_cache); a.v_cache = static_cast<uint8_t *>(v_cache);
+    a.page_stride = page_stride; a.num_pages = num_pages; a.slot_mapping = slot_mapping;
+    a.block_size = block_size;
+    return rope_impl(a, stream);
+}
+
+// ------------------------------------------------------------- 4-bit cache
+// The cache arguments shared by the 4-bit calls.
+static int check_q4_cache(const void *k_cache, const void *v_cache, int64_t page_stride,
+                          int64_t num_pages, int num_kv_heads, int head_dim, int block_size) {
+    if (num_kv_heads < 1 || num_kv_heads > 65535 || head_dim < 1 || block_size < 1 ||
+        block_size > kQ4MaxBlock || num_pages < 1 || num_pages > 0x7fffffffLL)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != pa::kHeadDim) return PA_ERR_UNSUPPORTED;
+    if (page_stride < (int64_t)block_size * num_kv_heads * PA_Q4_ROW_BYTES || page_stride % 16)
+        return PA_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+int pa_reshape_and_cache_q4(const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value,
+                            int64_t value_stride, void *k_cache, void *v_cache,
+                            int64_t page_stride, int64_t num_pages, const int64_t *slot_mapping,
+                            int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                            void *stream) {
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (int rc = check_q4_cache(k_cache, v_cache, page_stride, num_pages, num_kv_heads, head_dim,
+                                block_size))
+        return rc;
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    if (!rows_ok(key, key_stride, row) || !rows_ok(value, value_stride, row) || !slot_mapping ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    const pa::Q4WriteArgs a{key, value, key_stride, value_stride, static_cast<uint8_t *>(k_cache),
+                            static_cast<uint8_t *>(v_cache), page_stride, num_pages, slot_mapping,
+                            num_tokens, num_kv_heads, block_size, dev.err};
+    return pa::launch_write_q4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                    : PA_ERR_CUDA;
+}
+
+int pa_gather_cache_q4(const void *k_cache, const void *v_cache, int64_t page_stride,
+                       int64_t num_pages, const int64_t *slot_mapping, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, pa_bf16 *k_out,
+                       pa_bf16 *v_out, void *stream) {
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (int rc = check_q4_cache(k_cache, v_cache, page_stride, num_pages, num_kv_heads, head_dim,
+                                block_size))
+        return rc;
+    if (!slot_mapping || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || !k_out || !v_out ||
+        !aligned16(k_out) || !aligned16(v_out))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    const pa::Q4GatherArgs a{static_cast<const uint8_t *>(k_cache),
+                             static_cast<const uint8_t *>(v_cache), page_stride, num_pages,
+                             slot_mapping, num_tokens, num_kv_heads, block_size, k_out, v_out,
+                             dev.err};
+    return pa::launch_gather_q4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                     : PA_ERR_CUDA;
+}
+
+size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_seq_len) {
+    if (num_seqs < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_dim != pa::kHeadDim ||
+        block_size < 1 || max_seq_len < 1 || num_q_heads % num_kv_heads)
+        return 0;
+    DeviceInfo dev;
+    if (device_info(&dev)) return 0;
+    return pa::decode_workspace_bytes(
+        num_seqs, num_q_heads,
+        pa::plan_decode_q4(num_seqs, num_kv_heads, block_size, max_seq_len, dev.num_sms));
+}
+
+int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int64_t page_stride,
+                 int64_t num_pages, const int32_t *block_table, int64_t bt_stride,
+                 const int32_t *seq_lens, int num_seqs, int max_seq_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !block_table || !seq_lens || !out || !workspace) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 1 || num_seqs > 65535 || max_seq_len < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
+        num_q_heads > 65535 || num_q_heads % num_kv_heads)
+        return PA_ERR_INVALID_ARG;
+    if (int rc = check_q4_cache(k_cache, v_cache, page_stride, num_pages, num_kv_heads, head_dim,
+                                block_size))
+        return rc;
+    if (num_q_heads / num_kv_heads > pa::kDecMaxGroup) return PA_ERR_UNSUPPORTED;
+    if (bt_stride < ((int64_t)max_seq_len + block_size - 1) / block_size) return PA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    const pa::DecodePlan plan =
+        pa::plan_decode_q4(num_seqs, num_kv_heads, block_size, max_seq_len, dev.num_sms);
+    if (workspace_bytes < pa::decode_workspace_bytes(num_seqs, num_q_heads, plan))
+        return PA_ERR_INVALID_ARG;
+    pa::DecodeQ4Args a = {};
+    a.q = q;
+    a.k_cache = static_cast<const uint8_t *>(k_cache);
+    a.v_cache = static_cast<const uint8_t *>(v_cache);
+    a.page_stride = page_stride;
+    a.num_pages = num_pages;
+    a.block_table = block_table;
+    a.bt_stride = bt_stride;
+    a.seq_lens = seq_lens;
+    a.num_seqs = num_seqs;
+    a.max_seq_len = max_seq_len;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.scale = scale;
+    a.out = out;
+    a.workspace = workspace;
+    a.err = dev.err;
+    take_kernel_events(&a.ev_start, &a.ev_stop);
+    if (diag_enabled())
+        fprintf(stderr, "[pa] decode_q4: seqs=%d max_seq_len=%d bs=%d splits=%d tiles/split=%d\n",
+                num_seqs, max_seq_len, block_size, plan.num_splits, plan.tiles_per_split);
+    return pa::launch_decode_q4(a, plan, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+// Workspace of the 4-bit prefill: the batch's K, then its V, as FP16 pages, the queries as
+// FP16, the factors that undo their scaling, the heads' ranges, the pages' block tables, and
+// the room for split items; each part 256-byte aligned.  Batches are of kPfMaxSeqs chunks,
+// one after another in the same workspace (the queries of all of them are converted with the
+// first).
+struct PrefillQ4Layout {
+    int64_t pages = 0;      // output pages of the batch
+    int table_stride = 0;   // pages of its longest sequence
+    int ranges = 0;         // entries of the ranges, per KV head
+    size_t q = 0, kv = 0, q_factor = 0, kv_factor = 0, range = 0, table = 0;  // bytes
+    size_t pieces = 0;
+    size_t fixed() const { return q + q_factor + 2 * kv + kv_factor + range + table; }
+};
+static size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+static PrefillQ4Layout prefill_q4_layout(const pa::PrefillSeq *seqs, int cnt, int total_q,
+                                         int causal, int num_q_heads, int num_kv_heads,
+                                         int num_sms) {
+    static thread_local pa::PrefillSchedule sched;
+    PrefillQ4Layout l;
+    for (int b = 0; b < cnt; ++b) {
+        const int keys = seqs[b].q_start + seqs[b].q_len;
+        const int pages = (keys - 1) / pa::kQ4PrefillPage + 1;
+        l.pages += pages;
+        l.table_stride = std::max(l.table_stride, pages);
+        l.ranges += (keys - 1) / pa::kQ4RangeKeys + 1;
+    }
+    l.q = (size_t)total_q * num_q_heads * pa::kHeadDim * 2;
+    l.q_factor = up256((size_t)total_q * num_q_heads * 4);
+    l.kv = (size_t)l.pages * pa::kQ4PrefillPage * num_kv_heads * pa::kHeadDim * 2;
+    l.kv_factor = up256((size_t)cnt * num_kv_heads * sizeof(float2));
+    l.range = up256((size_t)l.ranges * num_kv_heads * sizeof(float2));
+    l.table = up256((size_t)cnt * l.table_stride * 4);
+    if (prefill_schedule(seqs, cnt, causal, num_q_heads, num_q_heads / num_kv_heads,
+                         pa::kQ4PrefillPage, num_sms, (size_t)pa::kPfMaxPieces * pa::kPfSlotBytes,
+                         &sched))
+        l.pieces = (size_t)sched.num_pieces * pa::kPfSlotBytes;
+    return l;
+}
+
+size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
+                                           int num_seqs, int causal, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size) try {
+    std::vector<pa::PrefillSeq> seqs;
+    if (!varlen_chunks(cu_seqlens_q, seq_lens_k, num_seqs, &seqs) || num_q_heads < 1 ||
+        num_kv_heads < 1 || num_q_heads % num_kv_heads || head_dim != pa::kHeadDim ||
+        block_size < 1)
+        return 0;
+    DeviceInfo dev;
+    if (device_info(&dev)) return 0;
+    size_t need = 0;
+    for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
+        const int cnt = (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0);
+        const PrefillQ4Layout l =
+            prefill_q4_layout(&seqs[s0], cnt, cu_seqlens_q[num_seqs], causal ? 1 : 0, num_q_heads,
+                              num_kv_heads, dev.num_sms);
+        need = std::max(need, l.fixed() + l.pieces);
+    }
+    return need;
+} catch (...) {  // out of host memory
+    return 0;
+}
+
+int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                         int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                         int64_t bt_stride, const int32_t *cu_seqlens_q,
+                         const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                         void *workspace, size_t workspace_bytes, void *stream) try {
+    std::vector<pa::PrefillSeq> seqs;
+    if (!varlen_chunks(cu_seqlens_q, seq_lens_k, num_seqs, &seqs)) return PA_ERR_INVALID_ARG;
+    if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads > 65535 || num_q_heads % num_kv_heads)
+        return PA_ERR_INVALID_ARG;
+    if (int rc = check_q4_cache(k_cache, v_cache, page_stride, num_pages, num_kv_heads, head_dim,
+                                block_size))
+        return rc;
+    if (num_q_heads / num_kv_heads > pa::kDecMaxGroup) return PA_ERR_UNSUPPORTED;
+    if (seqs.empty()) return PA_OK;
+    if (!q || !block_table || !out || !workspace || !isfinite(scale) || !aligned16(q) ||
+        !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_INVALID_ARG;
+    for (const pa::PrefillSeq &s : seqs)
+        if (bt_stride < (s.q_start + s.q_len - 1) / block_size + 1) return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    causal = causal ? 1 : 0;
+    std::vector<PrefillQ4Layout> layouts;
+    for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
+        layouts.push_back(prefill_q4_layout(&seqs[s0],
+                                            (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0),
+                                            cu_seqlens_q[num_seqs], causal, num_q_heads,
+                                            num_kv_heads, dev.num_sms));
+        // Split items are an option (as in pa_prefill_varlen); the pages are not.
+        if (workspace_bytes < layouts.back().fixed()) return PA_ERR_INVALID_ARG;
+    }
+    cudaEvent_t e0, e1;
+    take_kernel_events(&e0, &e1);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int total_q = cu_seqlens_q[num_seqs];
+    for (size_t i = 0, s0 = 0; s0 < seqs.size(); ++i, s0 += pa::kPfMaxSeqs) {
+        const int cnt = (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0);
+        const PrefillQ4Layout &l = layouts[i];
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        pa::Q4ExpandArgs x = {};
+        x.q = q;
+        x.q_rows = s0 == 0 ? (int64_t)total_q * num_q_heads : 0;
+        x.k_cache = static_cast<const uint8_t *>(k_cache);
+        x.v_cache = static_cast<const uint8_t *>(v_cache);
+        x.page_stride = page_stride;
+        x.num_pages = num_pages;
+        x.block_table = block_table;
+        x.bt_stride = bt_stride;
+        x.num_kv_heads = num_kv_heads;
+        x.block_size = block_size;
+        x.num_seqs = cnt;
+        x.num_ranges = l.ranges;
+        x.q_out = reinterpret_cast<uint16_t *>(ws);
+        x.q_factor = reinterpret_cast<float *>(ws += l.q);
+        x.k_out = reinterpret_cast<uint16_t *>(ws += l.q_factor);
+        x.v_out = reinterpret_cast<uint16_t *>(ws += l.kv);
+        x.kv_factor = reinterpret_cast<float2 *>(ws += l.kv);
+        x.ranges = reinterpret_cast<float2 *>(ws += l.kv_factor);
+        x.table_out = reinterpret_cast<int32_t *>(ws += l.range);
+        ws += l.table;
+        x.table_stride = l.table_stride;
+        x.err = dev.err;
+        pa::PrefillSeq chunk[pa::kPfMaxSeqs];
+        int page = 0, range = 0;
+        for (int b = 0; b < cnt; ++b) {
+            const pa::PrefillSeq &s = seqs[s0 + b];
+            x.seq[b] = pa::Q4ExpandSeq{page, range, s.q_start + s.q_len, s.bt_row};
+            range += (s.q_start + s.q_len - 1) / pa::kQ4RangeKeys + 1;
+            chunk[b] = s;
+            chunk[b].bt_row = b;
+            page += (s.q_start + s.q_len - 1) / pa::kQ4PrefillPage + 1;
+        }
+        if (pa::launch_expand_q4(x, l.pages, st) != cudaSuccess) return PA_ERR_CUDA;
+        if (int rc = prefill_launch(
+                x.q_out, total_q, x.k_out, x.v_out, (int64_t)pa::kQ4PrefillPage * num_kv_heads * head_dim,
+                l.pages, x.table_out, l.table_stride, chunk, cnt, causal, num_q_heads, num_kv_heads,
+                head_dim, pa::kQ4PrefillPage, scale, out,
+                workspace_bytes > l.fixed() ? ws : nullptr, workspace_bytes - l.fixed(), dev,
+                s0 == 0 ? e0 : nullptr, s0 + cnt == seqs.size() ? e1 : nullptr, st, x.q_factor,
+                x.kv_factor))
+            return rc;
+    }
+    return PA_OK;
+} catch (...) {  // out of host memory
+    return PA_ERR_INVALID_ARG;
+}
+
+size_t pa_prefill_q4_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size) {
+    if (q_len < 1 || q_start < 0 || (int64_t)q_start + q_len > 0x7fffffffLL) return 0;
+    const int32_t cu[2] = {0, q_len}, len = q_start + q_len;
+    return pa_prefill_varlen_q4_workspace_size(cu, &len, 1, causal, num_q_heads, num_kv_heads,
+                                               head_dim, block_size);
+}
+
+int pa_prefill_chunk_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                        int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                        int q_len, int q_start, int causal, int num_q_heads, int num_kv_heads,
+                        int head_dim, int block_size, float scale, pa_bf16 *out, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    if (q_len < 1 || q_start < 0 || (int64_t)q_start + q_len > 0x7fffffffLL || block_size < 1)
+        return PA_ERR_INVALID_ARG;
+    const int32_t cu[2] = {0, q_len}, len = q_start + q_len;
+    return pa_prefill_varlen_q4(q, k_cache, v_cache, page_stride, num_pages, block_table,
+                                (len - 1) / block_size + 1, cu, &len, 1, causal, num_q_heads,
+                                num_kv_heads, head_dim, block_size, scale, out, workspace,
+                                workspace_bytes, stream);
 }
 
 int pa_set_kernel_events(void *start, void *stop) {

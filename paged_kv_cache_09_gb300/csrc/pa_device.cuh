@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,7 +17,7 @@ constexpr int kChunks = kHeadDim / kChunkElems;
 
 // Bits of the device error word (same values as PA_DEVERR_* in pa.h).
 constexpr unsigned kErrPage = 1u, kErrSeqLen = 2u, kErrSlot = 4u, kErrTimeout = 8u,
-                   kErrPosition = 16u, kErrLayout = 32u;
+                   kErrPosition = 16u, kErrLayout = 32u, kErrNoPages = 64u;
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer: 2 s in the
 // library.  The test build (PA_TEST_HOOKS) sets a short limit so that its failure-path
@@ -265,11 +266,11 @@ __device__ __forceinline__ uint64_t umma_sdesc_sw128(uint32_t smem_addr,
     return d;
 }
 
-// Instruction descriptor of tcgen05.mma kind::f16 with BF16 inputs and an fp32
-// accumulator: D format [4,6) = 1 (F32), A format [7,10) = 1 (BF16), B format
-// [10,13) = 1 (BF16), A / B MN-major bits 15 / 16, N>>3 at [17,23), M>>4 at [24,29).
-__host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) |
+// Instruction descriptor of tcgen05.mma kind::f16 with BF16 (or both FP16) inputs and an
+// fp32 accumulator: D format [4,6) = 1 (F32), A format [7,10) = 1 (BF16; 0 FP16), B format
+// [10,13) = 1 (BF16; 0 FP16), A / B MN-major bits 15 / 16, N>>3 at [17,23), M>>4 at [24,29).
+__host__ __device__ constexpr uint32_t umma_idesc(bool half, int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)a_mn << 15) |
            ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
@@ -405,6 +406,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// Two floats -> one register of two FP16 (round to nearest even), low half = lo.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

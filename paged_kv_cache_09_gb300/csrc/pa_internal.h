@@ -16,8 +16,9 @@ uintptr_t current_context();
 
 // Raises a kernel's dynamic shared-memory limit once per (kernel slot, device context),
 // so that later launches (possibly under stream capture) make no attribute call.  Slots:
-// 0 and 3 the two decode kernel shapes, 1, 2, 4, 5 the four prefill kernel variants.
-constexpr int kSmemSlots = 8;
+// 0 and 3 the two decode kernel shapes, 1, 2, 4, 5 the four prefill kernel variants with
+// BF16 operands, 7, 8, 10, 11 those with FP16 operands, 6 the 4-bit decode.
+constexpr int kSmemSlots = 12;
 cudaError_t set_smem_once(const void *kernel, int bytes, int slot);
 
 // Launches a kernel with programmatic dependent launch allowed: it may start while the
@@ -149,6 +150,128 @@ struct DecodeArgs {
 // dims (the two tiles of a ring stage are two boxes, from one page or from two).
 cudaError_t launch_decode(const CUtensorMap *tmaps, const DecodeArgs &a, const DecodePlan &plan,
                           cudaStream_t stream);
+
+// Where a plan's partial sums and (max, sum) pairs lie in the decode workspace, and the
+// launch that merges them into BF16 rows.
+void decode_ws_parts(void *workspace, int num_seqs, int num_q_heads, const DecodePlan &plan,
+                     float **part_o, float2 **part_ml);
+cudaError_t launch_decode_combine(float *part_o, float2 *part_ml, int num_seqs, int num_q_heads,
+                                  int num_splits, uint16_t *out, cudaStream_t stream);
+
+// ----------------------------------------------------------------- 4-bit cache
+// Strides are in BF16 elements for rows, in bytes for cache pages.
+struct Q4WriteArgs {
+    const uint16_t *key, *value;
+    int64_t key_stride, value_stride;  // between tokens
+    uint8_t *k_cache, *v_cache;
+    int64_t page_stride, num_pages;
+    const int64_t *slot_mapping;
+    int num_tokens, num_kv_heads, block_size;
+    unsigned *err;
+};
+cudaError_t launch_write_q4(const Q4WriteArgs &a, cudaStream_t stream);
+
+struct Q4GatherArgs {
+    const uint8_t *k_cache, *v_cache;
+    int64_t page_stride, num_pages;
+    const int64_t *slot_mapping;
+    int num_tokens, num_kv_heads, block_size;
+    uint16_t *k_out, *v_out;
+    unsigned *err;
+};
+cudaError_t launch_gather_q4(const Q4GatherArgs &a, cudaStream_t stream);
+
+// Sequences of the 4-bit cache as FP16 pages of kQ4PrefillPage tokens (a multiple of the
+// prefill kernel's 64-key blocks) beside FP16 queries, for the prefill kernel.
+constexpr int kQ4PrefillPage = 256;
+constexpr int kQ4ExpandKeys = 64;  // keys of one head per CTA of the expansion
+constexpr int kQ4RangeKeys = 1024; // keys of one head per CTA of the range pass
+struct Q4ExpandSeq {
+    int page0;     // its first output page; its keys fill ceil(num_keys / kQ4PrefillPage)
+    int range0;    // its first entry of `ranges` (per KV head, ceil(num_keys / kQ4RangeKeys))
+    int num_keys;
+    int bt_row;    // its row of the block table
+};
+struct Q4ExpandArgs {
+    const uint16_t *q;       // BF16 [q_rows], q_rows = tokens * num_q_heads rows of 256
+    int64_t q_rows;
+    const uint8_t *k_cache, *v_cache;
+    int64_t page_stride, num_pages;
+    const int32_t *block_table;
+    int64_t bt_stride;
+    int num_kv_heads, block_size, num_seqs, num_ranges;
+    Q4ExpandSeq seq[32];
+    uint16_t *q_out;         // FP16 rows, each scaled by a power of two, and what undoes it
+    float *q_factor;
+    float2 *ranges;          // [num_kv_heads, num_ranges]: bounds of |K| and |V|
+    float2 *kv_factor;       // [num_seqs, num_kv_heads]
+    uint16_t *k_out, *v_out;
+    int32_t *table_out;      // [num_seqs, table_stride]: the output pages of each sequence
+    int64_t table_stride;
+    unsigned *err;
+};
+// Two launches: ranges and queries, then keys and values.
+cudaError_t launch_expand_q4(const Q4ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
+
+struct DecodeQ4Args {
+    const uint16_t *q;
+    const uint8_t *k_cache, *v_cache;
+    int64_t page_stride, num_pages;
+    const int32_t *block_table;
+    int64_t bt_stride;
+    const int32_t *seq_lens;
+    int num_seqs, max_seq_len, num_q_heads, num_kv_heads, block_size;
+    float scale;
+    uint16_t *out;
+    void *workspace;
+    unsigned *err;
+    cudaEvent_t ev_start, ev_stop;
+};
+DecodePlan plan_decode_q4(int num_seqs, int num_kv_heads, int block_size, int max_seq_len,
+                          int num_sms);
+cudaError_t launch_decode_q4(const DecodeQ4Args &a, const DecodePlan &plan, cudaStream_t stream);
+
+// ----------------------------------------------------------------- norm + rotation
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // between tokens
+    const uint16_t *q_weight, *k_weight;
+    float weight_bias, eps;
+    const float *cos_sin;                  // [max_position, rotary_dim]
+    const int32_t *positions;
+    int max_position, rotary_dim, interleaved;
+    int num_tokens, num_q_heads, num_kv_heads, head_dim;
+    uint16_t *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    // KV write (cache 0: none, 1: BF16, 2: 4-bit).  page_stride in elements (BF16) or bytes.
+    int cache;
+    uint8_t *k_cache, *v_cache;
+    int64_t page_stride, num_pages;
+    const int64_t *slot_mapping;
+    int block_size;
+    unsigned *err;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs &a, cudaStream_t stream);
+
+// ----------------------------------------------------------------- mixed-step inputs
+constexpr int kPrepTokens = 1024;  // rows per CTA
+struct BatchPrepGroup {
+    int32_t *block_table;
+    int64_t bt_stride;
+    int max_blocks, block_size;
+    const int32_t *free_pages;
+    int num_free;
+    int64_t *slot_mapping;
+    int32_t *pages_taken;
+};
+struct BatchPrepArgs {
+    const int32_t *num_computed, *num_new;
+    int num_seqs, num_tokens, num_groups;
+    int32_t *seq_lens, *query_start_loc, *positions, *seq_idx;
+    BatchPrepGroup g[kPrepMaxGroups];
+    unsigned *err;
+};
+cudaError_t launch_batch_prep(const BatchPrepArgs &a, cudaStream_t stream);
 
 // ----------------------------------------------------------------- prefill
 constexpr int kPfQRows = 128;      // query rows per work item (one TMEM lane each)
@@ -282,6 +405,11 @@ struct PrefillArgs {
     float scale;
     uint16_t *out;
     unsigned *err;
+    // FP16 operands (the tensor maps' Q, K and V hold FP16): the powers of two that undo the
+    // scaling of each query row and head, and of each sequence's K and V by KV head.  NULL:
+    // BF16 operands.
+    const float *q_factor;   // [rows, num_q_heads]
+    const float2 *kv_factor; // [num_seqs, num_kv_heads]
     cudaEvent_t ev_start, ev_stop;  // optional: recorded around the prefill kernel
     int num_sms;                    // persistent grid size bound
 };

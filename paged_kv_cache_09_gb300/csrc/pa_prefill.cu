@@ -49,6 +49,7 @@
 //             item's last PV is done, they load O into registers (BF16, normalised),
 //             release O to the next item's PVs, then store the rows to out (a piece of a
 //             split item: fp32 partials to the workspace).
+// (FP16 operands: P in one part, see kHalf below.)
 // TMEM columns: O [0, 256), S [256, 512); P of quarter q: hi at 256+64q, lo at +32.
 //
 // Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT, flags the CTA to
@@ -128,7 +129,16 @@ struct DevPieces {
 template <>
 struct DevPieces<false> {};
 
-template <int kSeqs, bool kExt>
+template <bool kHalf>
+struct DevFactors {};
+template <>
+struct DevFactors<true> {
+    const float *q;    // [rows, Hq]: powers of two that undo the rows' scaling
+    const float2 *kv;  // [sequence of the launch, Hkv]: those of K and of V
+    int num_kv_heads;
+};
+
+template <int kSeqs, bool kExt, bool kHalf>
 struct TcParams {
     const int32_t *block_table;  // row b of sequence b, bt_stride entries apart
     int64_t bt_stride;
@@ -148,6 +158,7 @@ struct TcParams {
     SeqInfo seq[kSeqs];
     DevSchedule sched;       // static item -> CTA assignment
     DevPieces<kExt> pc;   // pieces of split items (extended build only)
+    DevFactors<kHalf> f;  // FP16 operands only
 };
 
 template <int kSeqs>
@@ -158,7 +169,7 @@ struct TcMaps {
     CUtensorMap k_last[kSeqs], v_last[kSeqs];  // cut at each sequence's last token
 };
 
-static_assert(sizeof(TcMaps<kPfMaxSeqs>) + sizeof(TcParams<kPfMaxSeqs, true>) <= 32764,
+static_assert(sizeof(TcMaps<kPfMaxSeqs>) + sizeof(TcParams<kPfMaxSeqs, true, true>) <= 32764,
               "the kernel's parameters fit the 32 KB parameter space");
 
 struct Item {
@@ -178,8 +189,8 @@ struct Item {
 // neither use the kernel built without them, so plain plans run the plain code (piece
 // support measured 1.6% slower on the q=4096 chunk when always compiled in, packed
 // tiles another 1.5%).
-template <int kSeqs, bool kExt>
-__device__ __forceinline__ bool item_of(const TcParams<kSeqs, kExt> &p, int k, Item &it) {
+template <int kSeqs, bool kExt, bool kHalf>
+__device__ __forceinline__ bool item_of(const TcParams<kSeqs, kExt, kHalf> &p, int k, Item &it) {
     const int G = gridDim.x, b = blockIdx.x;
     int idx, piece = -1;
     if (p.sched.num_ctas) {
@@ -244,10 +255,17 @@ __device__ __forceinline__ bool item_of(const TcParams<kSeqs, kExt> &p, int k, I
 __device__ int g_test_skip_unit = -1;
 #endif
 
-template <int kSeqs, bool kExt>
+// kHalf: Q, K and V are FP16, each row of Q and each KV head of a sequence scaled by a power
+// of two (the 4-bit cache's prefill makes them so).  With 11 significant bits P needs one
+// part instead of two, so a tile takes 32 MMAs instead of 48, and K and V lose an eighth of
+// what they would in BF16.  P is kept 2^7 times as large (at most 2^15): full precision down
+// to 2^-21 of a row's largest weight.
+constexpr float kHalfHeadroom = 7.f;
+
+template <int kSeqs, bool kExt, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ TcMaps<kSeqs> maps,
-                      const __grid_constant__ TcParams<kSeqs, kExt> p) {
+                      const __grid_constant__ TcParams<kSeqs, kExt, kHalf> p) {
     extern __shared__ __align__(16) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {  // CTA-uniform; nothing has been set up yet
         if (threadIdx.x == 0) atomicOr(p.err, kErrLayout);
@@ -316,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int q_loads = 0;
             Item it;
             bool stop = false;
-            for (int k = 0; !stop && (item_of<kSeqs, kExt>(p, k, it)); ++k) {
+            for (int k = 0; !stop && (item_of<kSeqs, kExt, kHalf>(p, k, it)); ++k) {
                 if (k > 0 && !mbar_wait_abort(&bars[kQEmpty], (k - 1) & 1, p.err, abort)) break;
                 ++q_loads;
                 const bool pk = kExt && it.hp > 1;
@@ -398,14 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
-            constexpr uint32_t kIdQK = umma_idesc_bf16(kBM, kBN, 0, 0);
-            constexpr uint32_t kIdPV = umma_idesc_bf16(kBM, kHeadDim, 0, 1);
+            constexpr uint32_t kIdQK = umma_idesc(kHalf, kBM, kBN, 0, 0);
+            constexpr uint32_t kIdPV = umma_idesc(kHalf, kBM, kHeadDim, 0, 1);
             const uint32_t q_addr = smem_u32(qs), ring_addr = smem_u32(ring);
             const uint32_t sbuf = tmem + kColS, obuf = tmem + kColO;
             uint32_t u = 0, jt = 0;
             Item it;
             bool stop = false;
-            for (int k = 0; !stop && (item_of<kSeqs, kExt>(p, k, it)); ++k) {
+            for (int k = 0; !stop && (item_of<kSeqs, kExt, kHalf>(p, k, it)); ++k) {
                 if (!mbar_wait_abort(&bars[kQFull], k & 1, p.err, abort)) break;
                 tc_fence_after();
                 for (int j = it.jb; j < it.je && !stop; ++j) {
@@ -457,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int ks = 0; ks < kBlk / 16; ++ks) {
                             umma_ts(obuf, phi + 8 * ks, vd[ks], kIdPV, (jr | qq | ks) != 0);
-                            umma_ts(obuf, phi + 32 + 8 * ks, vd[ks], kIdPV, 1);
+                            if (!kHalf) umma_ts(obuf, phi + 32 + 8 * ks, vd[ks], kIdPV, 1);
                         }
                         umma_commit(&bars[kRingEmpty + s]);
                         umma_commit(&bars[kPvDone + qq]);
@@ -486,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Loop-invariant parameters, read once into registers.
         const int block_size = p.block_size, blocks_per_page = p.blocks_per_page;
         const bool causal = p.causal != 0, neg = p.neg != 0;
-        const float sc = p.sc;
+        float sc = p.sc;
         uint64_t *pair = &bars[kPair + lq];
         uint32_t pc = 0;  // exchanges done by this pair (both warps count alike)
         // Publishes v, meets the partner warp, returns the partner's value.  The meeting
@@ -506,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t jt = 0;
         Item it;
         bool stop = false;
-        for (int k = 0; !stop && (item_of<kSeqs, kExt>(p, k, it)); ++k) {
+        for (int k = 0; !stop && (item_of<kSeqs, kExt, kHalf>(p, k, it)); ++k) {
             // This lane's query row is tile row rpos (of head it.h + row % hp in a packed
             // item; lanes past hp * rows, and rows past the chunk's end, are computed but
             // not stored).
@@ -515,6 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it.hp > 1) rpos = row / it.hp;
             }
             const int qpos = it.q_start + it.r0 + rpos;
+            if constexpr (kHalf) {
+                const int rh = it.h + (it.hp > 1 ? row - rpos * it.hp : 0);
+                const float fq =
+                    rpos < it.rows
+                        ? p.f.q[(int64_t)(it.q_off + it.r0 + rpos) * p.num_q_heads + rh]
+                        : 1.f;
+                // (never 0, as p.sc: a masked score is -inf and stays that)
+                sc = fmaxf(p.sc * fq * p.f.kv[it.b * p.f.num_kv_heads + it.g].x, FLT_MIN);
+            }
             float m_used = -CUDART_INF_F, l = 0.f;
             // First token of block kb = 4j + qq and its in-page index, advanced quarter by
             // quarter (no division: it would wait behind the partner warp's exps on the MUFU).
@@ -589,7 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l *= alpha;
                         m_used = m_new;
                     }
-                    const float nmu = m_used == -CUDART_INF_F ? 0.f : -m_used;
+                    const float nmu = m_used == -CUDART_INF_F
+                                          ? 0.f
+                                          : (kHalf ? kHalfHeadroom - m_used : -m_used);
                     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
                     uint32_t hi[16], lo[16];
 #pragma unroll
@@ -598,13 +627,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fma2_bc(e0, e1, x[2 * i], x[2 * i + 1], sc, nmu);
                         const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
                         add2(sa[i & 3], sb[i & 3], sa[i & 3], sb[i & 3], p0, p1);
-                        hi[i] = pack_bf16x2(p0, p1);
-                        float r0, r1;
-                        sub2(r0, r1, p0, p1, bf16_lo(hi[i]), bf16_hi(hi[i]));
-                        lo[i] = pack_bf16x2(r0, r1);
+                        if constexpr (kHalf) {
+                            hi[i] = pack_f16x2(p0, p1);
+                        } else {
+                            hi[i] = pack_bf16x2(p0, p1);
+                            float r0, r1;
+                            sub2(r0, r1, p0, p1, bf16_lo(hi[i]), bf16_hi(hi[i]));
+                            lo[i] = pack_bf16x2(r0, r1);
+                        }
                     }
                     tmem_st16(sbase + 64 * qq + 16 * hf, hi);
-                    tmem_st16(sbase + 64 * qq + 32 + 16 * hf, lo);
+                    if constexpr (!kHalf) tmem_st16(sbase + 64 * qq + 32 + 16 * hf, lo);
                     l += ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
                     // Moving the running max rescales this row of O (this warp's half of the
                     // columns), which the PVs of the tile's earlier quarters may still be
@@ -673,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t obase = tmem + ((uint32_t)(lq * 32) << 16) + kColO + 128 * eh;
         uint32_t jt = 0;
         Item it;
-        for (int k = 0; item_of<kSeqs, kExt>(p, k, it); ++k) {
+        for (int k = 0; item_of<kSeqs, kExt, kHalf>(p, k, it); ++k) {
             if (!__all_sync(0xffffffffu,
                             mbar_wait_abort(&bars[kEpiReady], k & 1, p.err, abort) &&
                                 mbar_wait_abort(&bars[kPvDone + 3],
@@ -689,6 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const bool present = rpos < it.rows;
+            float fv = 1.f;  // undoes V's scaling
+            if constexpr (kHalf) fv = p.f.kv[it.b * p.f.num_kv_heads + it.g].y;
             if (kExt && it.slot >= 0) {
                 float *po = p.ws_o + ((int64_t)it.slot * kBM + row) * kHeadDim + 128 * eh;
 #pragma unroll 1
@@ -701,6 +736,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars[kOEmpty]);
                     }
+                    if constexpr (kHalf) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            r[i] = __float_as_uint(__uint_as_float(r[i]) * fv);
+                    }
                     if (present) {
                         float4 *d4 = reinterpret_cast<float4 *>(po + 32 * c);
 #pragma unroll
@@ -712,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                const float inv = lt > 0.f ? 1.f / lt : 0.f;
+                const float inv = lt > 0.f ? fv / lt : 0.f;
                 uint32_t b[64];  // this warp's 128 columns of the row as BF16 pairs
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -862,11 +902,11 @@ cudaError_t set_prefill_test_hook(int skip_unit) {
 
 namespace {
 
-template <int kSeqs, bool kExt>
+template <int kSeqs, bool kExt, bool kHalf>
 cudaError_t launch_prefill_n(const CUtensorMap *tmaps, const PrefillArgs &a, int slot,
                              cudaStream_t stream) {
     cudaError_t e = set_smem_once(
-        reinterpret_cast<const void *>(prefill_tc_kernel<kSeqs, kExt>), kSmemBytes, slot);
+        reinterpret_cast<const void *>(prefill_tc_kernel<kSeqs, kExt, kHalf>), kSmemBytes, slot);
     if (e != cudaSuccess) return e;
     TcMaps<kSeqs> maps;
     constexpr int kM = 3 + kPfMaxPackMaps;  // the first per-sequence map
@@ -874,7 +914,12 @@ cudaError_t launch_prefill_n(const CUtensorMap *tmaps, const PrefillArgs &a, int
     for (int i = 0; i < kPfMaxPackMaps; ++i) maps.qp[i] = tmaps[1 + i];
     maps.k = tmaps[kM - 2];
     maps.v = tmaps[kM - 1];
-    TcParams<kSeqs, kExt> p;
+    TcParams<kSeqs, kExt, kHalf> p;
+    if constexpr (kHalf) {
+        p.f.q = a.q_factor;
+        p.f.kv = a.kv_factor;
+        p.f.num_kv_heads = a.num_kv_heads;
+    }
     p.block_table = a.block_table;
     p.bt_stride = a.bt_stride;
     p.causal = a.causal;
@@ -936,7 +981,7 @@ cudaError_t launch_prefill_n(const CUtensorMap *tmaps, const PrefillArgs &a, int
         p.sched.num_ctas = 0;
     }
     if (a.ev_start && (e = record_event(a.ev_start, stream)) != cudaSuccess) return e;
-    e = launch_pdl(prefill_tc_kernel<kSeqs, kExt>, dim3(grid), dim3(kThreads), kSmemBytes, stream,
+    e = launch_pdl(prefill_tc_kernel<kSeqs, kExt, kHalf>, dim3(grid), dim3(kThreads), kSmemBytes, stream,
                    maps, p);
     if (e != cudaSuccess) return e;
     if (num_split > 0) {
@@ -972,18 +1017,25 @@ cudaError_t launch_prefill_n(const CUtensorMap *tmaps, const PrefillArgs &a, int
 
 }  // namespace
 
-cudaError_t launch_prefill(const CUtensorMap *tmaps, const PrefillArgs &a, cudaStream_t stream) {
-    if (a.num_seqs < 1 || a.num_seqs > kPfMaxSeqs) return cudaErrorInvalidValue;
+template <bool kHalf>
+static cudaError_t launch_prefill_as(const CUtensorMap *tmaps, const PrefillArgs &a, int slot,
+                                     cudaStream_t stream) {
     // The extended kernel when the plan has pieces of split items or a chunk ends in a
     // packed query tile.
     bool ext = a.sched && a.sched->num_ctas > 0 && a.sched->num_pieces > 0;
     for (int b = 0; b < a.num_seqs; ++b)
         ext = ext || prefill_tile_heads(a.seqs[b].q_len, a.group) > 1;
     if (a.num_seqs == 1)
-        return ext ? launch_prefill_n<1, true>(tmaps, a, 4, stream)
-                   : launch_prefill_n<1, false>(tmaps, a, 1, stream);
-    return ext ? launch_prefill_n<kPfMaxSeqs, true>(tmaps, a, 5, stream)
-               : launch_prefill_n<kPfMaxSeqs, false>(tmaps, a, 2, stream);
+        return ext ? launch_prefill_n<1, true, kHalf>(tmaps, a, slot + 3, stream)
+                   : launch_prefill_n<1, false, kHalf>(tmaps, a, slot, stream);
+    return ext ? launch_prefill_n<kPfMaxSeqs, true, kHalf>(tmaps, a, slot + 4, stream)
+               : launch_prefill_n<kPfMaxSeqs, false, kHalf>(tmaps, a, slot + 1, stream);
+}
+
+cudaError_t launch_prefill(const CUtensorMap *tmaps, const PrefillArgs &a, cudaStream_t stream) {
+    if (a.num_seqs < 1 || a.num_seqs > kPfMaxSeqs) return cudaErrorInvalidValue;
+    return a.q_factor ? launch_prefill_as<true>(tmaps, a, 7, stream)
+                      : launch_prefill_as<false>(tmaps, a, 1, stream);
 }
 
 }  // namespace pa

@@ -1,0 +1,195 @@
+// pa_prep.cu -- a mixed step's inputs from the requests' lengths: new pages, block tables,
+// token positions, owners and slots.
+//
+// For sequence s with c = num_computed[s] tokens in the cache and n = num_new[s] more:
+// its step's tokens are rows start_s .. start_s + n - 1 (start = running sum of n), at
+// positions c .. c + n - 1; of cache group g it needs ceil((c + n) / bs) - ceil(c / bs)
+// new pages, which it takes from the free list after those of the sequences before it.
+//
+// Integer work on a few hundred KB: bound by launch and by dependent reads, so it is one
+// launch without any exchange between CTAs.  Each CTA owns kPrepTokens consecutive rows
+// and computes the running sums of all sequences itself (a few rounds of a block scan; a
+// launch or a grid barrier more would cost more than that).  Sequences that start in its
+// rows leave a mark there, a max-scan over the rows finds each row's sequence, and each
+// row's thread writes its outputs.  A new page begins at a row whose position is a
+// multiple of bs, so that row's thread writes the page's table entry; entries of the
+// pages held before are only read.  No entry is both read and written.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = kPrepTokens / kThreads;  // rows per thread
+constexpr int kWarps = kThreads / 32;
+
+struct Mark {
+    int seq;        // the sequence that starts (or continues) at this row
+    int pos;        // the position of this row
+    int len;        // c + n
+    int page_first; // index, in the free list, of the sequence's first new page
+    int have;       // pages held before
+};
+
+// Exclusive running sums over the block of (rows, pages), and the block's totals.
+__device__ __forceinline__ void block_sums(int64_t &rows, int64_t &pages, int64_t &rows_all,
+                                           int64_t &pages_all, int64_t (&sh)[2][kWarps]) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t r = rows, p = pages;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, r, d), b = __shfl_up_sync(0xffffffffu, p, d);
+        if (lane >= d) {
+            r += a;
+            p += b;
+        }
+    }
+    __syncthreads();  // sh is free
+    if (lane == 31) {
+        sh[0][w] = r;
+        sh[1][w] = p;
+    }
+    __syncthreads();
+    rows_all = pages_all = 0;
+    int64_t br = 0, bp = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == w) {
+            br = rows_all;
+            bp = pages_all;
+        }
+        rows_all += sh[0][i];
+        pages_all += sh[1][i];
+    }
+    rows = br + r - rows;
+    pages = bp + p - pages;
+}
+
+__global__ void __launch_bounds__(kThreads) batch_prep_kernel(const __grid_constant__ BatchPrepArgs a) {
+    __shared__ Mark marks[kPrepTokens];
+    __shared__ short head[kPrepTokens];  // the row of a mark, or -1
+    __shared__ int64_t sums[2][kWarps];
+    __shared__ int warp_max[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int64_t t0 = (int64_t)blockIdx.x * kPrepTokens;
+    const BatchPrepGroup g = a.g[blockIdx.y];
+    const bool meta = blockIdx.x == 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) head[tid + i * kThreads] = -1;
+    pdl_wait();
+    pdl_trigger();
+
+    if (meta && blockIdx.y == 0 && tid == 0) a.query_start_loc[0] = 0;
+    int64_t rows0 = 0, pages0 = 0;  // of the sequences before this round
+    for (int base = 0; base < a.num_seqs; base += kThreads) {
+        const int s = base + tid;
+        int c = 0, n = 0;
+        if (s < a.num_seqs) {
+            c = a.num_computed[s];
+            n = a.num_new[s];
+        }
+        if (n <= 0) {
+            n = 0;  // an idle entry
+        } else if (c < 0 || n > 0x7fffffff - c) {
+            n = 0;
+            if (meta && blockIdx.y == 0) atomicOr(a.err, kErrSeqLen);
+        }
+        const int have = n ? c / g.block_size + (c % g.block_size != 0) : 0;
+        const int len = n ? c + n : 0;
+        const int want = len / g.block_size + (len % g.block_size != 0);
+        int64_t start = n, first = n ? max(min(want, g.max_blocks) - min(have, g.max_blocks), 0) : 0;
+        int64_t rows_all, pages_all;
+        block_sums(start, first, rows_all, pages_all, sums);
+        start += rows0;
+        first += pages0;
+        rows0 += rows_all;
+        pages0 += pages_all;
+        if (s < a.num_seqs && n && start < t0 + kPrepTokens && start + n > t0) {
+            const int at = start > t0 ? (int)(start - t0) : 0;
+            head[at] = (short)at;
+            marks[at] = Mark{s, (int)(c + (t0 + at - start)), len, (int)min(first, (int64_t)0x7fffffff),
+                             have};
+        }
+        if (meta && blockIdx.y == 0 && s < a.num_seqs) {
+            a.seq_lens[s] = len;
+            a.query_start_loc[s + 1] = (int)min(start + n, (int64_t)0x7fffffff);
+        }
+        if (!meta && rows0 >= t0 + kPrepTokens) break;  // the rest lies behind this CTA's rows
+    }
+    if (meta && tid == 0) {
+        if (g.pages_taken) *g.pages_taken = (int)min(pages0, (int64_t)g.num_free);
+        if (pages0 > g.num_free) atomicOr(a.err, kErrNoPages);
+        if (blockIdx.y == 0 && rows0 > a.num_tokens) atomicOr(a.err, kErrPosition);
+    }
+    __syncthreads();
+
+    // Each row's mark: the last one at or before it (thread t owns rows t kRows ..).
+    int own[kRows], run = -1;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        run = max(run, (int)head[tid * kRows + i]);
+        own[i] = run;
+    }
+    int up = run;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int b = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane >= d) up = max(up, b);
+    }
+    if (lane == 31) warp_max[w] = up;
+    int before = __shfl_up_sync(0xffffffffu, up, 1);
+    if (lane == 0) before = -1;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+        if (i < w) before = max(before, warp_max[i]);
+
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int row = tid * kRows + i;
+        const int64_t t = t0 + row;
+        if (t >= a.num_tokens) return;
+        const int m = max(own[i], before);
+        int seq = -1, pos = -1;
+        int64_t slot = -1;
+        if (m >= 0 && t < rows0) {
+            const Mark mk = marks[m];
+            pos = mk.pos + (row - m);
+            seq = mk.seq;
+            const int blk = pos / g.block_size, off = pos - blk * g.block_size;
+            if (blk < g.max_blocks) {
+                int32_t *entry = g.block_table + (int64_t)seq * g.bt_stride + blk;
+                int page;
+                if (blk < mk.have) {
+                    page = *entry;
+                } else {
+                    const int64_t at = (int64_t)mk.page_first + (blk - mk.have);
+                    page = at < g.num_free ? g.free_pages[at] : -1;
+                    if (off == 0) *entry = page;
+                }
+                if (page >= 0)
+                    slot = (int64_t)page * g.block_size + off;
+                else if (blk < mk.have || mk.page_first + (blk - mk.have) < g.num_free)
+                    atomicOr(a.err, kErrPosition);
+            } else {
+                atomicOr(a.err, kErrPosition);
+            }
+        }
+        if (blockIdx.y == 0) {
+            a.positions[t] = pos;
+            a.seq_idx[t] = seq;
+        }
+        g.slot_mapping[t] = slot;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_batch_prep(const BatchPrepArgs &a, cudaStream_t stream) {
+    const int blocks = a.num_tokens > 0 ? (a.num_tokens - 1) / kPrepTokens + 1 : 1;
+    return launch_pdl(batch_prep_kernel, dim3(blocks, a.num_groups), dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace pa
