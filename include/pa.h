@@ -461,9 +461,8 @@ int pa_reshape_and_cache_q4(const pa_bf16 *key, int64_t key_stride, const pa_bf1
 
 /*
  * pa_gather_cache_q4 -- reads tokens back by slot: k_out, v_out BF16 [num_tokens,
- * num_kv_heads, 256], contiguous, receive lo + s * n rounded to BF16.  Rows of negative
- * slots are left as they were; a slot outside the pool does the same and sets
- * PA_DEVERR_SLOT.
+ * num_kv_heads, 256], contiguous, receive lo + s * n rounded to BF16; zeros for a negative
+ * slot, and for one outside the pool, which sets PA_DEVERR_SLOT.
  */
 int pa_gather_cache_q4(const void *k_cache, const void *v_cache, int64_t page_stride,
                        int64_t num_pages, const int64_t *slot_mapping, int num_tokens,

@@ -74,6 +74,8 @@ def build(force: bool = False) -> str:
 def load():
     """Load libpa.so and declare the C signatures.  Raises if it is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -135,11 +137,12 @@ def load():
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # torch.cuda.current_stream() builds a Stream object: 2.8 us of a call's host time
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check(t, name, dtype, ndim=None):
@@ -464,13 +467,55 @@ def prefill_plan_pieces(q_len, q_start, causal, num_q_heads, num_kv_heads, block
     return list(items)[:ni.value], pieces, mc.value
 
 
-def _same_device(first, *others):
-    """The stream that a call is queued on belongs to the current device: every tensor has
-    to lie there."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device() or any(t.device != dev for t in others
-                                                       if t is not None):
-        raise ValueError("all tensors must be on the current CUDA device")
+_BF16, _I32, _I64, _U8, _F32 = (torch.bfloat16, torch.int32, torch.int64, torch.uint8,
+                                torch.float32)
+
+
+def _device():
+    """The current device, on whose stream a call is queued (none: no tensor is on it)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
+
+
+def _need(t, name, dtype, ndim, dev):
+    """t's shape, if it is a `dtype` tensor of ndim dims on device dev, the current one."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and \
+            t.dim() == ndim:
+        return t.shape
+    _check(t, name, dtype, ndim)
+    raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _vector(t, name, dtype, n, dev):
+    """Checks a contiguous vector of n entries (any number for None); returns its address."""
+    shape = _need(t, name, dtype, 1, dev)
+    if (n is not None and shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and have {n} entries")
+    return t.data_ptr()
+
+
+def _table(t, name, rows, dev):
+    """Checks an int32 block table of at least `rows` rows, each contiguous; returns (width,
+    distance between rows)."""
+    have, width = _need(t, name, _I32, 2, dev)
+    row, col = t.stride()
+    if have < rows or (have and width > 1 and col != 1):
+        raise ValueError(f"{name}: one row per sequence, contiguous rows")
+    return width, row if have > 1 else width
+
+
+def _token_rows(t, name, tokens, heads, dim, dev):
+    """Checks BF16 [tokens, heads, dim] rows, each token's heads contiguous; returns the
+    distance between tokens."""
+    shape = _need(t, name, _BF16, 3, dev)
+    if shape != (tokens, heads, dim):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {tuple(shape)}")
+    a, b, c = t.stride()
+    if (c != 1 and dim > 1) or (b != dim and heads > 1):
+        raise ValueError(f"{name}: each token's rows must be contiguous")
+    return a if tokens > 1 else heads * dim
 
 
 def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_pages, num_tokens,
@@ -481,83 +526,53 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     of the per-token outputs, at least the step's tokens.  Returns a dict with seq_lens,
     query_start_loc, positions, seq_idx, slot_mappings (one per group) and pages_taken (int32
     [groups]); `out` may pass that dict back in to reuse its tensors."""
-    lib = load()
-    S, G, T = num_computed.shape[0], len(block_tables), int(num_tokens)
+    lib, dev = _lib or load(), _device()
+    G, T = len(block_tables), int(num_tokens)
     if len(block_sizes) != G or len(free_pages) != G or not 1 <= G <= 8:
         raise ValueError("one block size and one free list per group, 1..8 groups")
-    for t, nm in ((num_computed, "num_computed"), (num_new, "num_new")):
-        _check(t, nm, torch.int32, 1)
-        if t.shape[0] != S or not t.is_contiguous():
-            raise ValueError("num_computed and num_new: contiguous, one entry per sequence")
-    for t, f in zip(block_tables, free_pages):
-        _check(t, "block_table", torch.int32, 2)
-        _check(f, "free_pages", torch.int32, 1)
-        if t.shape[0] < S or t.shape[1] < 1 or not f.is_contiguous() or \
-                (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError("block tables: one row per sequence, contiguous rows; free lists "
-                             "contiguous")
-    _same_device(num_computed, num_new, *block_tables, *free_pages)
+    S = _need(num_computed, "num_computed", _I32, 1, dev)[0]
+    computed = _vector(num_computed, "num_computed", _I32, S, dev)
+    new = _vector(num_new, "num_new", _I32, S, dev)
+    widths, strides = zip(*[_table(t, "block_table", S, dev) for t in block_tables])
+    free = [_vector(f, "free_pages", _I32, None, dev) for f in free_pages]
     if out is None:
-        dev, i32 = num_computed.device, torch.int32
-        out = {"seq_lens": torch.empty(S, dtype=i32, device=dev),
-               "query_start_loc": torch.empty(S + 1, dtype=i32, device=dev),
-               "positions": torch.empty(T, dtype=i32, device=dev),
-               "seq_idx": torch.empty(T, dtype=i32, device=dev),
-               "slot_mappings": [torch.empty(T, dtype=torch.int64, device=dev) for _ in range(G)],
-               "pages_taken": torch.empty(G, dtype=i32, device=dev)}
-    else:
-        sizes = (("seq_lens", S), ("query_start_loc", S + 1), ("positions", T), ("seq_idx", T),
-                 ("pages_taken", G))
-        if len(out["slot_mappings"]) != G:
-            raise ValueError("out: one slot mapping per group")
-        for t, n, dt in [(out[k], n, torch.int32) for k, n in sizes] + \
-                [(m, T, torch.int64) for m in out["slot_mappings"]]:
-            _check(t, "out", dt, 1)
-            if t.numel() != n or not t.is_contiguous():
-                raise ValueError("out: contiguous tensors of this call's sizes")
-            _same_device(num_computed, t)
-    arr = lambda ctype, vals: (ctype * G)(*vals)
-    ptrs = lambda ts: arr(ctypes.c_void_p, [t.data_ptr() for t in ts])
+        at = num_computed.device
+        out = {"seq_lens": torch.empty(S, dtype=_I32, device=at),
+               "query_start_loc": torch.empty(S + 1, dtype=_I32, device=at),
+               "positions": torch.empty(T, dtype=_I32, device=at),
+               "seq_idx": torch.empty(T, dtype=_I32, device=at),
+               "slot_mappings": [torch.empty(T, dtype=_I64, device=at) for _ in range(G)],
+               "pages_taken": torch.empty(G, dtype=_I32, device=at)}
+    slots = out["slot_mappings"]
+    if len(slots) != G:
+        raise ValueError("out: one slot mapping per group")
+    pointers, ints = ctypes.c_void_p * G, ctypes.c_int * G
     _raise(lib.pa_batch_input_prep(
-        _ptr(num_computed), _ptr(num_new), S, G, ptrs(block_tables),
-        arr(ctypes.c_int64, [_table_stride(t) for t in block_tables]),
-        arr(ctypes.c_int, [t.shape[1] for t in block_tables]),
-        arr(ctypes.c_int, [int(b) for b in block_sizes]), ptrs(free_pages),
-        arr(ctypes.c_int, [f.numel() for f in free_pages]), T, _ptr(out["seq_lens"]),
-        _ptr(out["query_start_loc"]), _ptr(out["positions"]), _ptr(out["seq_idx"]),
-        ptrs(out["slot_mappings"]), _ptr(out["pages_taken"]), _stream()), "pa_batch_input_prep")
+        computed, new, S, G, pointers(*[t.data_ptr() for t in block_tables]),
+        (ctypes.c_int64 * G)(*strides), ints(*widths), ints(*map(int, block_sizes)),
+        pointers(*free), ints(*[f.shape[0] for f in free_pages]), T,
+        _vector(out["seq_lens"], "seq_lens", _I32, S, dev),
+        _vector(out["query_start_loc"], "query_start_loc", _I32, S + 1, dev),
+        _vector(out["positions"], "positions", _I32, T, dev),
+        _vector(out["seq_idx"], "seq_idx", _I32, T, dev),
+        pointers(*[_vector(m, "slot_mapping", _I64, T, dev) for m in slots]),
+        _vector(out["pages_taken"], "pages_taken", _I32, G, dev), _stream()),
+        "pa_batch_input_prep")
     return out
 
 
-def _table_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _token_rows(t, name, heads=None, dim=None):
-    """Checks BF16 [tokens, heads, dim] rows, each token's heads contiguous; returns the
-    distance between tokens."""
-    _check(t, name, torch.bfloat16, 3)
-    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name}: each token's rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _rope_args(q, k, q_weight, k_weight, cos_sin, positions):
-    T, hq, d = q.shape
-    qs, ks = _token_rows(q, "q"), _token_rows(k, "k", None, d)
-    if k.shape[0] != T:
-        raise ValueError("q and k must have the same number of tokens")
-    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _check(t, nm, torch.bfloat16, 1)
-        if t.shape[0] != d or not t.is_contiguous():
-            raise ValueError(f"{nm} must be a contiguous [head_dim] tensor")
-    _check(cos_sin, "cos_sin", torch.float32, 2)
-    _check(positions, "positions", torch.int32, 1)
-    if not cos_sin.is_contiguous() or not positions.is_contiguous() or positions.shape[0] != T:
-        raise ValueError("cos_sin and positions must be contiguous, one position per token")
-    return T, hq, k.shape[1], d, qs, ks
+def _rope_args(q, k, q_weight, k_weight, cos_sin, positions, dev):
+    """(tokens, query heads, KV heads, head_dim, token strides of q and k, the addresses of the
+    weights, the table's sizes, the address of the positions)"""
+    T, hq, d = _need(q, "q", _BF16, 3, dev)
+    hkv = _need(k, "k", _BF16, 3, dev)[1]
+    qs, ks = _token_rows(q, "q", T, hq, d, dev), _token_rows(k, "k", T, hkv, d, dev)
+    rows, rot = _need(cos_sin, "cos_sin", _F32, 2, dev)
+    if not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous")
+    return (T, hq, hkv, d, qs, ks, _vector(q_weight, "q_weight", _BF16, d, dev),
+            _vector(k_weight, "k_weight", _BF16, d, dev), rows, rot,
+            _vector(positions, "positions", _I32, T, dev))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved=False,
@@ -566,19 +581,18 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved=
     q [T, Hq, D], k [T, Hkv, D] (views of a packed projection are taken as they are); cos_sin
     fp32 [max_position, rotary_dim], cosines then sines.  q_out / k_out may be q / k.  Rows of
     negative positions are left as they were.  Returns (q_out, k_out)."""
-    lib = load()
-    T, hq, hkv, d, qs, ks = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((T, hkv, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
-    qos, kos = _token_rows(q_out, "q_out", hq, d), _token_rows(k_out, "k_out", hkv, d)
-    if q_out.shape[0] != T or k_out.shape[0] != T:
-        raise ValueError("q_out and k_out must have q's number of tokens")
-    _same_device(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
-    _raise(lib.pa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight),
-                               float(weight_bias), float(eps), _ptr(cos_sin), cos_sin.shape[0],
-                               cos_sin.shape[1], int(bool(interleaved)), _ptr(positions), T, hq,
-                               hkv, d, _ptr(q_out), qos, _ptr(k_out), kos, _stream()),
-           "pa_qk_norm_rope")
+    lib, dev = _lib or load(), _device()
+    T, hq, hkv, d, qs, ks, qw, kw, rows, rot, pos = _rope_args(q, k, q_weight, k_weight, cos_sin,
+                                                               positions, dev)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, hkv, d), dtype=_BF16, device=k.device)
+    _raise(lib.pa_qk_norm_rope(
+        q.data_ptr(), qs, k.data_ptr(), ks, qw, kw, float(weight_bias), float(eps),
+        cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, pos, T, hq, hkv, d,
+        q_out.data_ptr(), _token_rows(q_out, "q_out", T, hq, d, dev), k_out.data_ptr(),
+        _token_rows(k_out, "k_out", T, hkv, d, dev), _stream()), "pa_qk_norm_rope")
     return q_out, k_out
 
 
@@ -587,33 +601,32 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos_sin, positions, eps, k_c
     """qk_norm_rope with the KV write in the same launch: the keys, and the values v as they
     are, go to their slots of the caches (see pa_qk_norm_rope_cache), BF16 [num_pages,
     block_size, Hkv, D] or 4-bit (uint8, q4_cache_shape).  Returns q_out."""
-    lib = load()
-    T, hq, hkv, d, qs, ks = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    vs = _token_rows(v, "v", hkv, d)
-    _check(slot_mapping, "slot_mapping", torch.int64, 1)
-    if v.shape[0] != T or slot_mapping.shape[0] != T or not slot_mapping.is_contiguous():
-        raise ValueError("v and slot_mapping must have one entry per token")
-    if isinstance(k_cache, torch.Tensor) and k_cache.dtype == torch.uint8:
-        fmt = 1
-        ps, bs, heads = _check_q4_cache(k_cache, v_cache)
+    lib, dev = _lib or load(), _device()
+    T, hq, hkv, d, qs, ks, qw, kw, rows, rot, pos = _rope_args(q, k, q_weight, k_weight, cos_sin,
+                                                               positions, dev)
+    vs = _token_rows(v, "v", T, hkv, d, dev)
+    slots = _vector(slot_mapping, "slot_mapping", _I64, T, dev)
+    fmt = 1 if isinstance(k_cache, torch.Tensor) and k_cache.dtype is _U8 else 0
+    if fmt:
+        pages, ps, bs, heads = _q4_cache(k_cache, v_cache, dev)
         dim = 256
     else:
-        fmt = 0
         ps = _check_cache(k_cache, v_cache)
-        _, bs, heads, dim = k_cache.shape
-    if (heads, dim) != (hkv, d):
+        pages, bs, heads, dim = k_cache.shape
+        if k_cache.get_device() != dev or v_cache.get_device() != dev:
+            raise ValueError("the caches must be on the current CUDA device")
+    if heads != hkv or dim != d:
         raise ValueError("the caches' heads must be k's")
-    q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    qos = _token_rows(q_out, "q_out", hq, d)
-    if q_out.shape[0] != T:
-        raise ValueError("q_out must have q's number of tokens")
-    _same_device(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, slot_mapping,
-                 q_out)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
+        qos = hq * d
+    else:
+        qos = _token_rows(q_out, "q_out", T, hq, d, dev)
     _raise(lib.pa_qk_norm_rope_cache(
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), float(weight_bias),
-        float(eps), _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-        _ptr(positions), T, hq, hkv, d, _ptr(q_out), qos, fmt, _ptr(k_cache), _ptr(v_cache), ps,
-        k_cache.shape[0], _ptr(slot_mapping), bs, _stream()), "pa_qk_norm_rope_cache")
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, float(weight_bias),
+        float(eps), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, pos, T, hq, hkv, d,
+        q_out.data_ptr(), qos, fmt, k_cache.data_ptr(), v_cache.data_ptr(), ps, pages, slots, bs,
+        _stream()), "pa_qk_norm_rope_cache")
     return q_out
 
 
@@ -622,60 +635,51 @@ def q4_cache_shape(num_pages, block_size, num_kv_heads):
     return (num_pages, num_kv_heads, block_size * Q4_ROW_BYTES)
 
 
-def _check_q4_cache(k_cache, v_cache):
-    """(page stride in bytes, block size, KV heads) of a pair of 4-bit caches."""
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(t, n, torch.uint8, 3)
-        if t.shape[2] % Q4_ROW_BYTES or t.shape[2] == 0 or t.stride(2) != 1 or \
-                (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError(f"{n}: each page must be a contiguous [Hkv, block_size * "
-                             f"{Q4_ROW_BYTES}] block of bytes")
-    page = k_cache.shape[1] * k_cache.shape[2]
-    ps = k_cache.stride(0) if k_cache.shape[0] > 1 else page
-    vps = v_cache.stride(0) if v_cache.shape[0] > 1 else page
-    if k_cache.shape != v_cache.shape or ps != vps:
+def _q4_cache(k_cache, v_cache, dev):
+    """(pages, page stride in bytes, block size, KV heads) of a pair of 4-bit caches."""
+    shape = _need(k_cache, "k_cache", _U8, 3, dev)
+    pages, heads, run = shape
+    stride = k_cache.stride()
+    if _need(v_cache, "v_cache", _U8, 3, dev) != shape or \
+            (v_cache.stride() != stride and not (k_cache.is_contiguous() and
+                                                 v_cache.is_contiguous())):
         raise ValueError("k_cache and v_cache must have the same shape and page stride")
-    return ps, k_cache.shape[2] // Q4_ROW_BYTES, k_cache.shape[1]
+    if run % Q4_ROW_BYTES or run == 0 or stride[2] != 1 or (heads > 1 and stride[1] != run):
+        raise ValueError("each page of a 4-bit cache must be a contiguous [Hkv, block_size * "
+                         f"{Q4_ROW_BYTES}] block of bytes")
+    return pages, stride[0] if pages > 1 else heads * run, run // Q4_ROW_BYTES, heads
 
 
 def reshape_and_cache_q4(key, value, k_cache, v_cache, slot_mapping):
     """Quantise key/value [T, Hkv, 256] into the 4-bit caches at slot_mapping (in place)."""
-    lib = load()
-    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
-    ks = _token_rows(key, "key", hkv, 256)
-    vs = _token_rows(value, "value", hkv, 256)
-    _check(slot_mapping, "slot_mapping", torch.int64, 1)
-    T = key.shape[0]
-    if value.shape[0] != T or slot_mapping.shape[0] != T or not slot_mapping.is_contiguous():
-        raise ValueError("value and slot_mapping must have one entry per token")
-    _same_device(key, value, k_cache, v_cache, slot_mapping)
-    _raise(lib.pa_reshape_and_cache_q4(_ptr(key), ks, _ptr(value), vs, _ptr(k_cache),
-                                       _ptr(v_cache), ps, k_cache.shape[0], _ptr(slot_mapping), T,
-                                       hkv, 256, bs, _stream()), "pa_reshape_and_cache_q4")
+    lib, dev = _lib or load(), _device()
+    pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
+    T = _need(key, "key", _BF16, 3, dev)[0]
+    _raise(lib.pa_reshape_and_cache_q4(
+        key.data_ptr(), _token_rows(key, "key", T, hkv, 256, dev), value.data_ptr(),
+        _token_rows(value, "value", T, hkv, 256, dev), k_cache.data_ptr(), v_cache.data_ptr(), ps,
+        pages, _vector(slot_mapping, "slot_mapping", _I64, T, dev), T, hkv, 256, bs, _stream()),
+        "pa_reshape_and_cache_q4")
 
 
 def gather_cache_q4(k_cache, v_cache, slot_mapping, k_out=None, v_out=None):
-    """The tokens at slot_mapping [T] as BF16 (k, v), each [T, Hkv, 256].  Rows of negative
-    slots are left as they were (zeros in tensors made here)."""
-    lib = load()
-    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
-    _check(slot_mapping, "slot_mapping", torch.int64, 1)
+    """The tokens at slot_mapping [T] as BF16 (k, v), each [T, Hkv, 256]; zeros for negative
+    slots."""
+    lib, dev = _lib or load(), _device()
+    pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
+    slots = _vector(slot_mapping, "slot_mapping", _I64, None, dev)
     T = slot_mapping.shape[0]
-    outs = []
+    if k_out is None:
+        k_out = torch.empty((T, hkv, 256), dtype=_BF16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty((T, hkv, 256), dtype=_BF16, device=k_cache.device)
     for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.zeros((T, hkv, 256), dtype=torch.bfloat16, device=k_cache.device)
-        _check(t, nm, torch.bfloat16, 3)
-        if t.shape != (T, hkv, 256) or not t.is_contiguous():
+        if _need(t, nm, _BF16, 3, dev) != (T, hkv, 256) or not t.is_contiguous():
             raise ValueError(f"{nm} must be a contiguous [T, Hkv, 256] tensor")
-        outs.append(t)
-    if not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be contiguous")
-    _same_device(k_cache, v_cache, slot_mapping, *outs)
-    _raise(lib.pa_gather_cache_q4(_ptr(k_cache), _ptr(v_cache), ps, k_cache.shape[0],
-                                  _ptr(slot_mapping), T, hkv, 256, bs, _ptr(outs[0]),
-                                  _ptr(outs[1]), _stream()), "pa_gather_cache_q4")
-    return outs[0], outs[1]
+    _raise(lib.pa_gather_cache_q4(k_cache.data_ptr(), v_cache.data_ptr(), ps, pages, slots, T, hkv,
+                                  256, bs, k_out.data_ptr(), v_out.data_ptr(), _stream()),
+           "pa_gather_cache_q4")
+    return k_out, v_out
 
 
 def decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -684,41 +688,43 @@ def decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, bloc
                                                   block_size, max_seq_len))
 
 
-def _q4_out(out, q):
+def _q4_out(out, q, dev):
     if out is None:
         return torch.empty_like(q)
-    _check(out, "out", torch.bfloat16, 3)
-    if out.shape != q.shape or not out.is_contiguous():
+    if _need(out, "out", _BF16, 3, dev) != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous BF16 tensor shaped like q")
     return out
+
+
+def _q4_workspace(workspace, need, dev, device):
+    """(tensor, address, bytes) of a caller's workspace, or of a fresh one of need() bytes."""
+    if workspace is None:
+        workspace = torch.empty(max(need(), 256), dtype=_U8, device=device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or \
+            not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on the current CUDA device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def decode_q4(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, out=None,
               workspace=None):
     """q=1 decode over the 4-bit cache (see pa_decode_q4).  Returns out [S, Hq, 256] BF16;
     rows of sequences of length 0 are zeros."""
-    lib = load()
-    _check(q, "q", torch.bfloat16, 3)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
+    lib, dev = _lib or load(), _device()
+    S, hq, d = _need(q, "q", _BF16, 3, dev)
     q = q.contiguous()
-    S, hq, d = q.shape
-    if block_table.shape[0] < S or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or \
-            seq_lens.shape[0] < S or not seq_lens.is_contiguous():
-        raise ValueError("block_table and seq_lens: one entry per sequence, contiguous rows")
-    if block_table.shape[1] * bs < max_seq_len:
+    pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
+    width, row = _table(block_table, "block_table", S, dev)
+    if _need(seq_lens, "seq_lens", _I32, 1, dev)[0] < S or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous, one entry per sequence")
+    if width * bs < max_seq_len:
         raise ValueError("block_table rows are too short for max_seq_len")
-    out = _q4_out(out, q)
-    if workspace is None:
-        need = decode_q4_workspace_size(S, hq, hkv, d, bs, max_seq_len)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _same_device(q, k_cache, v_cache, block_table, seq_lens, out, workspace)
-    _raise(lib.pa_decode_q4(_ptr(q), _ptr(k_cache), _ptr(v_cache), ps, k_cache.shape[0],
-                            _ptr(block_table), _table_stride(block_table),
-                            _ptr(seq_lens), S, int(max_seq_len), hq, hkv, d, bs, float(scale),
-                            _ptr(out), _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream()),
+    out = _q4_out(out, q, dev)
+    _keep, ws, ws_bytes = _q4_workspace(
+        workspace, lambda: decode_q4_workspace_size(S, hq, hkv, d, bs, max_seq_len), dev, q.device)
+    _raise(lib.pa_decode_q4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ps, pages,
+                            block_table.data_ptr(), row, seq_lens.data_ptr(), S, int(max_seq_len),
+                            hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes, _stream()),
            "pa_decode_q4")
     return out
 
@@ -763,28 +769,24 @@ def prefill_varlen_q4(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k
     """Chunks of several sequences stacked row-wise in q, over the 4-bit cache (see
     pa_prefill_varlen_q4).  cu_seqlens_q and seq_lens_k are host sequences of ints.  Without a
     workspace, one of prefill_varlen_q4_workspace_size bytes is allocated for the call."""
-    lib = load()
-    _check(q, "q", torch.bfloat16, 3)
-    _check(block_table, "block_table", torch.int32, 2)
-    ps, bs, hkv = _check_q4_cache(k_cache, v_cache)
+    lib, dev = _lib or load(), _device()
+    rows, hq, d = _need(q, "q", _BF16, 3, dev)
     q = q.contiguous()
-    _, hq, d = q.shape
+    pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
     cu, sk, B = _varlen_lens(cu_seqlens_q, seq_lens_k)
-    if cu[B] != q.shape[0]:
+    if cu[B] != rows:
         raise ValueError("cu_seqlens_q must end at q's row count")
-    if block_table.shape[0] < B or (block_table.shape[1] > 1 and block_table.stride(1) != 1) or \
-            (B and block_table.shape[1] * bs < max(sk)):
-        raise ValueError("block_table: one contiguous row per sequence, as long as its keys need")
-    out = _q4_out(out, q)
-    if workspace is None:
-        need = int(lib.pa_prefill_varlen_q4_workspace_size(cu, sk, B, int(bool(causal)), hq, hkv,
-                                                           d, bs))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _same_device(q, k_cache, v_cache, block_table, out, workspace)
+    width, stride = _table(block_table, "block_table", B, dev)
+    if B and width * bs < max(sk):
+        raise ValueError("block_table rows are too short for the sequences' keys")
+    out = _q4_out(out, q, dev)
+    causal = 1 if causal else 0
+    _keep, ws, ws_bytes = _q4_workspace(
+        workspace, lambda: int(lib.pa_prefill_varlen_q4_workspace_size(cu, sk, B, causal, hq, hkv,
+                                                                       d, bs)), dev, q.device)
     _raise(lib.pa_prefill_varlen_q4(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), ps, k_cache.shape[0], _ptr(block_table),
-        _table_stride(block_table), cu, sk, B, int(bool(causal)), hq, hkv, d,
-        bs, float(scale), _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ps, pages, block_table.data_ptr(),
+        stride, cu, sk, B, causal, hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes,
         _stream()), "pa_prefill_varlen_q4")
     return out
 

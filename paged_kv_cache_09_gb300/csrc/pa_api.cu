@@ -879,9 +879,7 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
         return 0;
     DeviceInfo dev;
     if (device_info(&dev)) return 0;
-    return pa::decode_workspace_bytes(
-        num_seqs, num_q_heads,
-        pa::plan_decode_q4(num_seqs, num_kv_heads, block_size, max_seq_len, dev.num_sms));
+    return pa::decode_q4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, dev.num_sms);
 }
 
 int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int64_t page_stride,
@@ -903,11 +901,11 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
         return PA_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (int rc = device_info(&dev)) return rc;
-    const pa::DecodePlan plan =
-        pa::plan_decode_q4(num_seqs, num_kv_heads, block_size, max_seq_len, dev.num_sms);
-    if (workspace_bytes < pa::decode_workspace_bytes(num_seqs, num_q_heads, plan))
+    if (workspace_bytes <
+        pa::decode_q4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, dev.num_sms))
         return PA_ERR_INVALID_ARG;
     pa::DecodeQ4Args a = {};
+    a.num_sms = dev.num_sms;
     a.q = q;
     a.k_cache = static_cast<const uint8_t *>(k_cache);
     a.v_cache = static_cast<const uint8_t *>(v_cache);
@@ -927,11 +925,10 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
     a.err = dev.err;
     take_kernel_events(&a.ev_start, &a.ev_stop);
     if (diag_enabled())
-        fprintf(stderr, "[pa] decode_q4: seqs=%d max_seq_len=%d bs=%d splits=%d tiles/split=%d\n",
-                num_seqs, max_seq_len, block_size, plan.num_splits, plan.tiles_per_split);
-    return pa::launch_decode_q4(a, plan, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+        fprintf(stderr, "[pa] decode_q4: seqs=%d max_seq_len=%d bs=%d\n", num_seqs, max_seq_len,
+                block_size);
+    return pa::launch_decode_q4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                     : PA_ERR_CUDA;
 }
 
 // Workspace of the 4-bit prefill: the batch's K, then its V, as FP16 pages, the queries as

@@ -59,18 +59,18 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q4_kernel(const Q4GatherAr
     const int h = (int)(row - t * a.num_kv_heads);
     if (t >= a.num_tokens) return;
     const int64_t slot = a.slot_mapping[t];
-    if (slot < 0) return;
     const int64_t page = slot / a.block_size;
-    if (page >= a.num_pages) {
-        if (lane == 0) atomicOr(a.err, kErrSlot);
-        return;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;  // padding, and a slot outside the pool
+    if (slot >= 0 && page < a.num_pages) {
+        const int o = (int)(slot - page * a.block_size);
+        const int64_t run = page * a.page_stride + (int64_t)h * a.block_size * kQ4RowBytes;
+        k = q4_load_row(a.k_cache + run, a.block_size, o, lane);
+        v = q4_load_row(a.v_cache + run, a.block_size, o, lane);
+    } else if (slot >= 0 && lane == 0) {
+        atomicOr(a.err, kErrSlot);
     }
-    const int o = (int)(slot - page * a.block_size);
-    const int64_t run = page * a.page_stride + (int64_t)h * a.block_size * kQ4RowBytes;
-    reinterpret_cast<uint4 *>(a.k_out + row * kHeadDim)[lane] =
-        q4_load_row(a.k_cache + run, a.block_size, o, lane);
-    reinterpret_cast<uint4 *>(a.v_out + row * kHeadDim)[lane] =
-        q4_load_row(a.v_cache + run, a.block_size, o, lane);
+    reinterpret_cast<uint4 *>(a.k_out + row * kHeadDim)[lane] = k;
+    reinterpret_cast<uint4 *>(a.v_out + row * kHeadDim)[lane] = v;
 }
 
 // ---- prefill: FP16 operands from the 4-bit cache and BF16 queries

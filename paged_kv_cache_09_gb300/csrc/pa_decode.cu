@@ -764,25 +764,6 @@ DecodeWsLayout decode_ws_layout(int num_seqs, int num_q_heads, const DecodePlan 
 }
 }  // namespace
 
-void decode_ws_parts(void *workspace, int num_seqs, int num_q_heads, const DecodePlan &plan,
-                     float **part_o, float2 **part_ml) {
-    *part_o = static_cast<float *>(workspace);
-    *part_ml = reinterpret_cast<float2 *>(
-        static_cast<uint8_t *>(workspace) + decode_ws_layout(num_seqs, num_q_heads, plan).o_bytes);
-}
-
-cudaError_t launch_decode_combine(float *part_o, float2 *part_ml, int num_seqs, int num_q_heads,
-                                  int num_splits, uint16_t *out, cudaStream_t stream) {
-    DecodeKParams p = {};
-    p.part_o = part_o;
-    p.part_ml = part_ml;
-    p.num_q_heads = num_q_heads;
-    p.num_splits = num_splits;
-    p.out = out;
-    return launch_pdl(decode_combine_kernel, dim3(num_q_heads * kCombineParts, num_seqs),
-                      dim3(kCombineThreads), 0, stream, p);
-}
-
 size_t decode_workspace_bytes(int num_seqs, int num_q_heads, const DecodePlan &plan) {
     const DecodeWsLayout l = decode_ws_layout(num_seqs, num_q_heads, plan);
     return l.o_bytes + l.ml_bytes;
@@ -815,7 +796,9 @@ cudaError_t launch_decode(const CUtensorMap *tmaps, const DecodeArgs &a, const D
     p.num_splits = plan.num_splits;
     p.num_pages = a.num_pages;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    decode_ws_parts(a.workspace, a.num_seqs, a.num_q_heads, plan, &p.part_o, &p.part_ml);
+    const DecodeWsLayout ws = decode_ws_layout(a.num_seqs, a.num_q_heads, plan);
+    p.part_o = static_cast<float *>(a.workspace);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.workspace) + ws.o_bytes);
     p.out = a.out;
     p.err = a.err;
     p.k_cache_w = a.k_cache_w;

@@ -1,5 +1,5 @@
-// pa_decode_q4.cu -- q=1 decode over the 4-bit cache (format: pa_q4.cuh): split-context
-// kernel; the splits are merged by the BF16 decode's combine kernel.
+// pa_decode_q4.cu -- q=1 decode over the 4-bit cache (format: pa_q4.cuh): a kernel that
+// streams the cache, and one that merges the parts of sequences that it cut.
 //
 // For query head h of KV head g, over the sequence's tokens t < seq_len,
 //     out = softmax_t(scale q . khat_t) . vhat_t,   khat, vhat = lo + s n per group of 64.
@@ -10,34 +10,39 @@
 // so a step costs a multiplication per (token, group, head), not per value.
 //
 // Bytes: 288 per token and KV head (1024 in BF16).  At the copy bandwidth an SM has to
-// take a 16-token tile (4.6 KB) about every 100 ns, so besides HBM the instruction count per
-// value matters; it goes to widening codes:
-//   * a code becomes FP16 by one three-input logic operation: (w & 0x000f000f) | 0x6400..
-//     is the pair (1024 + n, 1024 + n'), (w & 0x00f000f0) | 0x5400.. the pair 64 + n; one
-//     shift by 8 serves the other two pairs of a word: 5 operations for 8 codes;
-//   * K: pairs of the 1024 kind lose 1032 by a half2 addition (n - 8, exact); those of the
-//     64 kind keep their offset, and the accumulators start from the constant
-//     8 sum(q) - 72 sum(q of those dims), so that they end as sum q n.  At 64 the offset
-//     costs 1e-6 of the score's scale; at 1024 it would cost 2e-5;
-//   * V: pairs run along tokens, so two tokens' words are first interleaved by halves (two
-//     byte permutations for 16 codes); every pair is brought to n - 8 exactly by a half2
-//     addition, since an offset would be summed over all tokens and cancel at the end
-//     against a sum thousands of times smaller than it.
+// take a 16-token tile (4.6 KB) about every 100 ns (200 cycles), so besides HBM the
+// instructions count; most of them widen codes.
+//   * Four bits in the low bits of an FP16 are the subnormal n 2^-24, and in bits 4 to 7 the
+//     subnormal n 2^-20: a mask alone makes a pair of codes an exact operand of the tensor
+//     cores; 5 operations widen 8 codes.  The 2^4 between the two kinds is put into q (K) and
+//     taken out of the sums at the end (V).  (As FP8 operands codes would need 3 operations for
+//     8, but FP8 operands of this MMA are converted to FP16 first: measured slower.)
+//   * V's pairs run along tokens: two tokens' words are interleaved by halves first (two byte
+//     permutations for 16 codes).
+//   * The lo terms of the scores are one more BF16 product over (group, part of sum(q)) with
+//     sum(q) in three BF16 parts: one MMA instead of 16 multiply-adds.
 // q becomes FP16 after scaling each head by a power of two (largest value in [2^13, 2^14)):
-// exact for values down to 2^-30 of the head's largest, and below that off by less than
-// 2^-38 of it.  The weights p s become FP16 (2^-12 relative): an eighth of the output's own
-// rounding to BF16.
-// So that they neither overflow nor vanish, the running reference M is the largest
-// score + log2(largest step of the token), not the largest score: p_t = 2^(score_t - M + 15)
-// is kept in fp32 and p_t s_tg <= 2^15, which leaves 29 binades of full precision below the
-// largest weight (a group whose steps are that much smaller than another's still gets its
-// own).  The step is taken within [2^-80, 2^80] for this.
+// exact for values down to 2^-24 of the head's largest, and below that off by less than
+// 2^-34 of it.
+// The weights p s become FP16 (2^-12 relative): an eighth of the output's own rounding to BF16.
+// So that they neither overflow nor vanish, p is taken relative to 2^M, M = running largest
+// score + log2 of the running largest step of V - 7, both at most 2^8 behind the true ones:
+// p s <= 2^15, and weights down to 2^-21 of the largest keep 11 bits.  The reference moves
+// (and the sums are rescaled) only when a score passes it by more than 8, which needs one
+// vote a step instead of a reduction over the tokens.  Steps are taken as at most 2^80.
 //
-// Work split: grid (splits, KV heads, sequences), four consumer warps and a producer warp a
-// CTA, two CTAs an SM (one's prologue and merge behind the other's stream).  A ring stage
-// is four 16-token tiles, one a consumer warp.  The producer's 16 lanes bring one run
-// each (codes and pairs of K and of V of one tile) by bulk copies: contiguous, needing no
-// tensor map, and never longer than the page's and the sequence's valid rows.
+// Work split: the tiles of all (sequence, KV head) pairs in a row, cut evenly over two CTAs an
+// SM, so that uneven lengths leave no SM idle; each CTA finds its share from the lengths.  A pair
+// that one CTA holds whole is finished there; the others leave a part per CTA (sums relative to
+// their reference), which a second kernel merges.
+// Within a CTA each warp streams pairs of 16-token tiles of its own (every kW-th pair) through a
+// ring of its own: eight of its lanes bring one run each (codes and pairs of K and of V, of each
+// tile) by bulk copies, which are contiguous, need no tensor map and are never longer than the
+// page's and the sequence's valid rows.  Nothing is exchanged between warps before the merge.
+// A warp keeps all 256 dims' sums (64 registers) and works on two tiles at once, whose MMA chains
+// are interleaved: 8 such warps an SM ran faster than 12 with 168 registers each, or 16 in pairs
+// that shared the dims (16 sequences of 4K..32K keys: 82, 96 and 104 us), because the extra warps
+// cost instructions (spills, exchanges, loads) and instructions are what bounds.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -50,18 +55,37 @@ namespace pa {
 namespace {
 
 constexpr int kTile = kDecTile;                       // 16 tokens
-constexpr int kC = 4;                                 // consumer warps = tiles per stage
-constexpr int kStages = 5;
+constexpr int kW = 4, kThreads = kW * 32;             // warps of a CTA
+constexpr int kDepth = 2;                             // pairs of tiles in a warp's ring
 constexpr int kTileCodes = kTile * kQ4CodeBytes;      // 2 KB
 constexpr int kTilePairs = kTile * kQ4PairBytes;      // 256 B
-constexpr int kTileBytes = 2 * (kTileCodes + kTilePairs);  // K codes, V codes, K pairs, V pairs
-constexpr int kStageBytes = kC * kTileBytes;          // 18 KB
-constexpr int kRingBytes = kStages * kStageBytes;
-constexpr int kThreads = (kC + 1) * 32;
+// A slot: K codes of both tiles, V codes, K pairs, V pairs.
+constexpr int kSlotBytes = 4 * (kTileCodes + kTilePairs);
+constexpr int kOffV = 2 * kTileCodes, kOffPairs = 4 * kTileCodes, kOffVPairs = kOffPairs + 2 * kTilePairs;
+constexpr int kRingBytes = kW * kDepth * kSlotBytes;
 constexpr int kMergeRow = kHeadDim + 4;
-constexpr int kSmem = kRingBytes + 2 * kStages * 8 + 16;
-constexpr float kHeadroom = 15.f;                     // log2 of the largest weight
-static_assert(kC * kDecMaxGroup * (kMergeRow + 2) * 4 <= kRingBytes, "merge buffers reuse the ring");
+// Shared memory: rings; the merge's rows and (reference, sum) pairs; q's fragments (8 x 512
+// bytes, and sums and scales); barriers and valid rows.
+constexpr int kOffMerge = kRingBytes, kOffMl = kOffMerge + kW * kDecMaxGroup * kMergeRow * 4;
+constexpr int kOffQ = kOffMl + kW * kDecMaxGroup * 8, kOffBars = kOffQ + 9 * 512;
+constexpr int kSmem = kOffBars + kW * kDepth * 16 + 16;
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+constexpr int kMinShare = 2 * kW;                     // tiles of the smallest share
+constexpr float kHeadroom = 7.f, kLag = 8.f;          // log2 units: p s <= 2^(kHeadroom + kLag)
+
+// Division of n < 2^31 by a constant of the launch.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        return (__umulhi(n, mul) + n) >> shift;
+    }
+};
+FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+    return f;
+}
 
 struct Params {
     const uint16_t *q;
@@ -70,10 +94,16 @@ struct Params {
     const int32_t *block_table;
     int64_t bt_stride;
     const int32_t *seq_lens;
-    int max_seq_len, num_q_heads, group, block_size, tiles_per_page, tiles_per_split, num_splits;
+    int num_seqs, max_seq_len, num_q_heads, num_kv_heads, group, block_size, tiles_per_page;
+    FastDiv by_block, by_tpp;
     float scale_log2;
+    // Part i: fp32 sums [group, 256] and (reference, sum of weights) [group].  CTA b's part of
+    // pair x is part b + x (one of the two grows from part to part, so no two are the same).
     float *part_o;
     float2 *part_ml;
+    int2 *info;  // [pairs]: a pair's first part and how many (0: finished by one CTA)
+    int64_t parts;
+    uint16_t *out;
     unsigned *err;
 };
 
@@ -95,34 +125,25 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+// The same from D = 0.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// (a & b) | c in one operation.
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-constexpr uint32_t kMinus1032 = 0xe408e408u;  // (-1032, -1032)
-constexpr uint32_t kMinus72 = 0xd480d480u;    // (-72, -72)
 
-// The four pairs (n_k, n_{k+4}) of a word's codes as FP16: k even as n - 8, k odd as
-// 64 + n (keep64) or n - 8.
-template <bool keep64>
+// The four pairs (codes k, k + 4) of a word as FP16 subnormals: k
+// even as n 2^-24, k odd as n 2^-20.  The last comes from a subtraction (of (n2 + 16 n3) 2^-24 and
+// n2 2^-24, exact): it runs beside the logic unit, which bounds this kernel.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&x)[4]) {
-    const uint32_t w8 = w >> 8;
-    x[0] = h2_add(and_or(w, 0x000f000fu, 0x64006400u), kMinus1032);
-    x[1] = and_or(w, 0x00f000f0u, 0x54005400u);
-    x[2] = h2_add(and_or(w8, 0x000f000fu, 0x64006400u), kMinus1032);
-    x[3] = and_or(w8, 0x00f000f0u, 0x54005400u);
-    if (!keep64) {
-        x[1] = h2_add(x[1], kMinus72);
-        x[3] = h2_add(x[3], kMinus72);
-    }
+    const uint32_t high = __byte_perm(w, 0, 0x4341);  // the halves' upper bytes
+    x[0] = w & 0x000f000fu;
+    x[1] = w & 0x00f000f0u;
+    x[2] = high & 0x000f000fu;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x[3]) : "r"(high), "r"(x[2]));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -136,398 +157,654 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int g) {
     return g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w;
 }
 
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
 }
 
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+__device__ __forceinline__ int tiles_of(const Params &p, int len) {
+    const int full = (int)p.by_block(len);
+    return full * p.tiles_per_page + ((len - full * p.block_size + kTile - 1) >> 4);
 }
 
-__device__ __forceinline__ int tiles_of(int len, int block_size, int tpp) {
-    const int full = len / block_size;
-    return full * tpp + (len - full * block_size + kTile - 1) / kTile;
+// Tiles of sequence s (none past the last); lengths out of range are cut to it.
+__device__ __forceinline__ int seq_tiles(const Params &p, int s, int *len, bool report) {
+    int L = s < p.num_seqs ? p.seq_lens[s] : 0;
+    if (L < 0 || L > p.max_seq_len) {
+        if (report) atomicOr(p.err, kErrSeqLen);
+        L = L < 0 ? 0 : p.max_seq_len;
+    }
+    *len = L;
+    return tiles_of(p, L);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) decode_q4_split_kernel(const Params p) {
+// CTA b's first tile when `total` tiles are cut over `ctas`: the first r shares have one more.
+struct Shares {
+    uint32_t q, r;
+    __device__ __forceinline__ uint32_t begin(uint32_t b) const { return b * q + min(b, r); }
+    __device__ __forceinline__ uint32_t owner(uint32_t tile) const {
+        const uint32_t big = r * (q + 1);
+        return tile < big ? tile / (q + 1) : r + (tile - big) / q;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);
-    uint64_t *empty = full + kStages;
-    volatile int *abort = reinterpret_cast<volatile int *>(empty + kStages);
-    const int split = blockIdx.x, g = blockIdx.y, seq = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars) + warp * kDepth;  // this warp's ring,
+    int2 *rows_in = reinterpret_cast<int2 *>(smem + kOffBars + kW * kDepth * 8) + warp * kDepth;  // its valid rows
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffBars + kW * kDepth * 16);
+    uint8_t *ring = smem + warp * kDepth * kSlotBytes;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kC);
-        }
-        *abort = 0;
+    if (lane == 0) {
+        for (int s = 0; s < kDepth; ++s) mbar_init(&full[s], 1);
+        if (warp == 0) *abort = 0;
         fence_mbar_init();
     }
     __syncthreads();
     pdl_wait();
     pdl_trigger();
 
+    // ---- this CTA's share of all tiles, and the segment that it begins with: tile t0 of KV head
+    // g of sequence seq (every warp finds the same)
     const int tpp = p.tiles_per_page;
-    const int t0 = split * p.tiles_per_split;
-    const int32_t *bt = p.block_table + (int64_t)seq * p.bt_stride;
-    // The producer's first table entry is read beside the length: tile t0 + lane / 4 lies
-    // in the row when it is a tile of the longest allowed sequence.
-    const int max_tiles = tiles_of(p.max_seq_len, p.block_size, tpp);
-    int page = 0;
-    if (warp == kC && lane < 4 * kC && t0 + (lane >> 2) < max_tiles) page = bt[(t0 + (lane >> 2)) / tpp];
-    int seq_len = p.seq_lens[seq];
-    if (seq_len < 0 || seq_len > p.max_seq_len) {
-        if (threadIdx.x == 0 && split == 0 && g == 0) atomicOr(p.err, kErrSeqLen);
-        seq_len = seq_len < 0 ? 0 : p.max_seq_len;
-    }
-    const int t1 = min(tiles_of(seq_len, p.block_size, tpp), t0 + p.tiles_per_split);
-    const int64_t part0 = ((int64_t)seq * p.num_q_heads + g * p.group) * p.num_splits + split;
-    if (t0 >= t1) {  // no tiles of this sequence: an empty partial, which the merge skips
-        if (threadIdx.x < p.group)
-            p.part_ml[part0 + (int64_t)threadIdx.x * p.num_splits] = make_float2(-CUDART_INF_F, 0.f);
-        return;
-    }
-    const int n = t1 - t0, nst = (n + kC - 1) / kC;
-
-    if (warp == kC) {
-        // ------------------------------------------------------------ producer
-        const uint64_t pol = l2_evict_first_policy();
-        const int ti = lane >> 2, kind = lane & 3;  // the lane's tile of a stage, and its run
-        const int64_t head = (int64_t)g * p.block_size * kQ4RowBytes;
-        const uint8_t *base = ((kind & 1) ? p.v_cache : p.k_cache) + head +
-                              (kind >= 2 ? (int64_t)p.block_size * kQ4CodeBytes : 0);
-        const int row_bytes = kind >= 2 ? kQ4PairBytes : kQ4CodeBytes;
-        const int dst_off = ti * kTileBytes + (kind >= 2 ? 2 * kTileCodes + (kind - 2) * kTilePairs
-                                                         : kind * kTileCodes);
-        int issued = 0;  // stages loaded
-        for (int m = 0; m < nst; ++m) {
-            const int s = m % kStages;
-            const int j = t0 + m * kC + ti;
-            const bool mine = lane < 4 * kC && j < t1;
-            // The next stage's table entry is read before this stage's wait.
-            const int jn = j + kC;
-            const int page_next = lane < 4 * kC && jn < t1 ? bt[jn / tpp] : 0;
-            if (m >= kStages &&
-                !__all_sync(0xffffffffu,
-                            mbar_wait_abort(&empty[s], ((m / kStages) - 1) & 1, p.err, abort)))
-                break;
-            int bytes = 0;
-            const uint8_t *src = nullptr;
-            uint8_t *dst = smem + s * kStageBytes + dst_off;
-            if (mine) {
-                const int lp = j / tpp, off = (j - lp * tpp) * kTile;
-                const int rows = min(kTile, min(p.block_size - off, seq_len - (lp * p.block_size + off)));
-                bytes = rows * row_bytes;
-                if (page >= 0 && page < p.num_pages) {
-                    src = base + page * p.page_stride + (int64_t)off * row_bytes;
-                } else {
-                    // Outside the pool: reported, and read as zeros (steps and minima of 0).
-                    if (kind == 0) atomicOr(p.err, kErrPage);
-                    if (kind >= 2)
-                        for (int i = 0; i < bytes / 16; ++i)
-                            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    bytes = 0;
-                }
-            }
-            const int total = __reduce_add_sync(0xffffffffu, bytes);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], total);
-            __syncwarp();
-            if (bytes) bulk_load(dst, src, bytes, &full[s], pol);
-            issued = m + 1;
-            page = page_next;
+    Shares shares;
+    uint32_t at, end;  // the next tile of all, and the share's end
+    int seq, g, t0, seq_len, tiles;
+    // Finds them, with the tiles and lengths of the first 32 sequences given; false: no share.
+    auto place = [&](int first_tiles, int first_len) {
+        uint64_t all = 0;
+        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+            int len;
+            uint64_t t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, blockIdx.x == 0 && warp == 0);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+            all += t;
         }
-        // Every load lands before the ring is reused by the merge or left.
-        for (int m = max(0, issued - kStages); m < issued; ++m)
-            mbar_wait(&full[m % kStages], (m / kStages) & 1, p.err);
-        __syncwarp();
-        bar_sync(1, kThreads);
-        return;
-    }
+        all *= p.num_kv_heads;
+        if (all > 0x7fffffffu) {  // (as many tiles as 600 GB of cache hold, counting shared pages again)
+            if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
+            return false;
+        }
+        const uint32_t total = (uint32_t)all;
+        const uint32_t ctas = min(gridDim.x, (total + kMinShare - 1) / kMinShare);
+        if (blockIdx.x >= ctas) return false;
+        shares.q = total / ctas;
+        shares.r = total - shares.q * ctas;
+        at = shares.begin(blockIdx.x);
+        end = shares.begin(blockIdx.x + 1);
+        uint32_t before = 0;
+        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+            int len = first_len;
+            const int t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, false);
+            uint32_t sum = t;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, (before + sum) * p.num_kv_heads > at);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                seq = s0 + l;
+                seq_len = __shfl_sync(0xffffffffu, len, l);
+                tiles = __shfl_sync(0xffffffffu, t, l);
+                const uint32_t rem = at - (before + __shfl_sync(0xffffffffu, sum - t, l)) * p.num_kv_heads;
+                g = (int)(rem / (uint32_t)tiles);
+                t0 = (int)(rem - (uint32_t)g * tiles);
+                return true;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        return false;  // (not reached: at < total)
+    };
 
-    // ---------------------------------------------------------------- consumers
     const int r = lane >> 2, c = lane & 3;
-    // q as FP16 B fragments: lane (head r, column c) holds dims 64g + 8(2c + h) + j; MMA i
-    // of word h takes the pairs (2i, 2i + 4) and (2i + 1, 2i + 5).
-    uint32_t qf[4][2][4];
-    float init0[4], init1[4], qs0[4], qs1[4], sc0, sc1;  // of heads 2c and 2c + 1
-    {
-        const bool hv = r < p.group;
+    const uint32_t q_frag = smem_u32(smem + kOffQ) + lane * 16;
+    // Lanes 0 .. 7 load: lane = 4 x (tile of the pair) + run (K codes, V codes, K pairs, V pairs).
+    const int l_tile = (lane >> 2) & 1, kind = lane & 3;
+    const int l_bytes = kind >= 2 ? kQ4PairBytes : kQ4CodeBytes;
+    uint8_t *l_dst = ring + (kind >= 2 ? kOffPairs + (2 * (kind - 2) + l_tile) * kTilePairs
+                                       : (2 * kind + l_tile) * kTileCodes);
+    const uint8_t *l_src;            // of the KV head's codes or pairs
+    const int32_t *bt;
+    int j_in, lp_in, tip_in, page_in, t1, n;
+    uint32_t it = 0;  // the warp's steps: slots and phases go on from segment to segment
+    bool gave_up;  // a wait ran out: this and the CTA's remaining segments contribute nothing
+
+    // Starts a segment: tiles [t0, t1) of KV head g of sequence seq.
+    auto begin_segment = [&]() {
+        t1 = (int)min((uint32_t)tiles, t0 + (end - at));
+        n = !*abort && t0 + 2 * warp < t1 ? (t1 - t0 - 2 * warp + 2 * kW - 1) / (2 * kW) : 0;
+        bt = p.block_table + (int64_t)seq * p.bt_stride;
+        j_in = t0 + 2 * warp + l_tile;  // this lane's next tile
+        lp_in = (int)p.by_tpp(j_in);
+        tip_in = j_in - lp_in * tpp;
+        page_in = j_in < t1 ? bt[lp_in] : 0;
+        l_src = ((kind & 1) ? p.v_cache : p.k_cache) + (int64_t)g * p.block_size * kQ4RowBytes +
+                (kind >= 2 ? (int64_t)p.block_size * kQ4CodeBytes : 0);
+    };
+    // Loads the warp's pair i, its next, into slot i % kDepth.
+    auto load = [&](uint32_t i) {
+        const uint32_t s = i % kDepth;
+        const int page = page_in, off = tip_in * kTile;
+        const int rows = j_in < t1 ? min(kTile, min(p.block_size - off,
+                                                    seq_len - lp_in * p.block_size - off))
+                                   : 0;
+        const bool inside = page >= 0 && page < p.num_pages;
+        uint8_t *dst = l_dst + s * kSlotBytes;
+        const uint8_t *src = l_src + page * p.page_stride + (int64_t)off * l_bytes;
+        if (lane == 0 || lane == 4) (&rows_in[s].x)[l_tile] = rows;
+        // The next pair's table entry, read ahead of its use.
+        j_in += 2 * kW;
+        for (tip_in += 2 * kW; tip_in >= tpp; tip_in -= tpp) ++lp_in;
+        if (j_in < t1) page_in = bt[lp_in];
+        if (rows > 0 && !inside && lane < 8) {
+            // Outside the pool: reported, and read as zeros (steps and minima of 0).
+            if (kind == 0) atomicOr(p.err, kErrPage);
+            if (kind >= 2)
+                for (int k = 0; k < rows; ++k) reinterpret_cast<uint4 *>(dst)[k] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+        }
+        // Two tiles that follow one another in a page come as one run (a copy's cost hardly
+        // grows with its size): lanes 0 .. 3 then take both tiles' rows.
+        int mine = inside ? rows : 0;
+        const int other = __shfl_xor_sync(0xffffffffu, mine, 4);
+        const int next = __shfl_xor_sync(0xffffffffu, off, 4);  // lanes 0 .. 3: tile 1's place
+        const int total = mine + other;
+        const bool joined = __shfl_sync(0xffffffffu, (int)(mine == kTile && other > 0 && next == off + kTile), 0);
+        if (joined) mine = l_tile ? 0 : total;
+        __syncwarp();  // zeros go before the arrival
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], total * 2 * kQ4RowBytes);
+        __syncwarp();
+        if (lane < 8 && mine) bulk_load(dst, src, mine * l_bytes, &full[s], l2_evict_first_policy());
+    };
+    int loaded = 0;
+    auto first_loads = [&]() {
+        for (loaded = 0; loaded < min(n, kDepth - 1); ++loaded) load(it + loaded);
+    };
+    // q as FP16 B fragments in shared memory: lane (head r, column c) holds dims 64g + 8(2c + h)
+    // + j; MMA i of word h takes the pairs (2i, 2i + 4) and (2i + 1, 2i + 5), the latter 2^-4 as
+    // large.  Each warp loads all of q (for the heads' largest values) and makes one group's.
+    uint4 raw[8];
+    auto load_q = [&]() {
         const uint4 *qrow = reinterpret_cast<const uint4 *>(
-            p.q + ((int64_t)seq * p.num_q_heads + g * p.group + (hv ? r : 0)) * kHeadDim);
-        uint4 raw[4][2];
+            p.q + ((int64_t)seq * p.num_q_heads + g * p.group + (r < p.group ? r : 0)) * kHeadDim);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            raw[k] = r < p.group ? qrow[(k >> 1) * 8 + 2 * c + (k & 1)] : make_uint4(0, 0, 0, 0);
+    };
+    auto make_q = [&]() {
+        uint4 *own = reinterpret_cast<uint4 *>(smem + kOffQ) + lane;
         uint32_t amax = 0;
 #pragma unroll
-        for (int gg = 0; gg < 4; ++gg)
+        for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                raw[gg][h] = hv ? qrow[gg * 8 + 2 * c + h] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = word(raw[gg][h], i);
-                    amax = max(amax, max((w << 16) & 0x7fff0000u, w & 0x7fff0000u));
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                amax = max(amax, max((word(raw[k], i) << 16) & 0x7fff0000u, word(raw[k], i) & 0x7fff0000u));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // A power of two f that brings the head's largest value to [2^13, 2^14).
         const int e = (int)(amax >> 23);
         const float f = e == 255 ? 1.f : __uint_as_float((uint32_t)min(254, max(1, 267 - e)) << 23);
-        const float sc = p.scale_log2 / f;
+        static_assert(kW == 4, "a warp a group");
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 mine = raw[h];
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                if (warp == k) mine = raw[2 * k + h];
+            float v[8];
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_lo(word(mine, i)) * f;
+                v[2 * i + 1] = bf16_hi(word(mine, i)) * f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum += v[i] + v[i + 4];
+                x[i] = i & 1 ? pack_f16x2(v[i] * 0x1p-4f, v[i + 4] * 0x1p-4f) : pack_f16x2(v[i], v[i + 4]);
+            }
+            own[(2 * warp + h) * 32] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        // sum(q) 2^-24 of head r and group c in three BF16 parts, and the scales of the columns'
+        // heads
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= 0x1p-24f;
+        const float p1 = __bfloat162float(__float2bfloat16_rn(sum));
+        const float p2 = __bfloat162float(__float2bfloat16_rn(sum - p1));
+        const float sc = p.scale_log2 * 0x1p24f / f;
+        const float sc0 = __shfl_sync(0xffffffffu, sc, 8 * c), sc1 = __shfl_sync(0xffffffffu, sc, 8 * c + 4);
+        if (c == warp)
+            own[8 * 32] = make_uint4(pack_bf16x2(p1, p2), pack_bf16x2(sum - p1 - p2, 0.f),
+                                     __float_as_uint(sc0), __float_as_uint(sc1));
+    };
+
+    // With one sequence, its length is nearly always the longest allowed: the table entry and q are
+    // then read beside the length instead of after it.
+    int len;
+    const int actual = seq_tiles(p, lane, &len, blockIdx.x == 0 && warp == 0);
+    bool guess = p.num_seqs == 1, placed;
+    for (;;) {
+        placed = guess ? place(lane == 0 ? tiles_of(p, p.max_seq_len) : 0, p.max_seq_len)
+                       : place(actual, len);
+        if (placed) {
+            begin_segment();
+            load_q();
+        }
+        if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
+        guess = false;
+    }
+    if (!placed) return;
+    first_loads();
+    make_q();
+    __syncthreads();  // q is ready
+    for (;;) {
+        // [group][dim pair][(dim, head) of the pairs], of even dims 2^24 and of odd dims 2^20
+        // times too small
+        float o[4][4][4];
+        float low0[4], low1[4];  // this lane's share of sum p lo
 #pragma unroll
         for (int gg = 0; gg < 4; ++gg) {
-            float sum = 0.f, odd = 0.f;
+            low0[gg] = low1[gg] = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v[8];
+            for (int k = 0; k < 4; ++k) o[gg][k][0] = o[gg][k][1] = o[gg][k][2] = o[gg][k][3] = 0.f;
+        }
+        // Running references: largest scores (of heads 2c, 2c + 1) and largest step, the latter a
+        // power of two 2^eb.
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, eb = 0.f, big = 0.f, l0 = 0.f, l1 = 0.f;
+
+        for (int i = 0; i < n; ++i) {
+            if (loaded < n) load(it + loaded++);  // into the slot that the previous pair has left
+            const uint32_t s = (it + i) % kDepth;
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait_abort(&full[s], ((it + i) / kDepth) & 1, p.err, abort)))
+                break;
+            const int2 nv = rows_in[s];
+            const uint32_t base = smem_u32(ring) + s * kSlotBytes;
+
+            // ---- scores of tokens r and r + 8 of each tile, heads 2c and 2c + 1: 8 accumulators
+            // (tile, group) in turn
+            float x[2][4];
+            uint32_t steps = 0;  // the largest step of V, a BF16 in the lower half
+            {
+                const uint4 qa = lds128(q_frag + 8 * 512);  // sums of (head r, group c); scales
+                const uint32_t ka = base + r * 128 + (((2 * c) ^ r) << 4);
+                const uint32_t pa = base + kOffPairs + r * 16;
+                float a[2][4][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = bf16_lo(word(raw[gg][h], i)) * f;
-                    v[2 * i + 1] = bf16_hi(word(raw[gg][h], i)) * f;
+                for (int h = 0; h < 2; ++h) {
+                    uint4 k0[2], k1[2];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        k0[t] = lds128((h ? ka ^ 16 : ka) + t * kTileCodes);
+                        k1[t] = lds128((h ? ka ^ 16 : ka) + t * kTileCodes + 1024);
+                    }
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) {
+                        const uint4 q = lds128(q_frag + (2 * gg + h) * 512);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            uint32_t u[4], v[4];
+                            widen(word(k0[t], gg), u);
+                            widen(word(k1[t], gg), v);
+                            if (h == 0)
+                                mma_f16_zero(a[t][gg], u[0], v[0], u[1], v[1], q.x, q.y);
+                            else
+                                mma_f16(a[t][gg], u[0], v[0], u[1], v[1], q.x, q.y);
+                            mma_f16(a[t][gg], u[2], v[2], u[3], v[3], q.z, q.w);
+                        }
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    qf[gg][h][i] = pack_f16x2(v[i], v[i + 4]);
-                    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&qf[gg][h][i]));
-                    sum += back.x + back.y;
-                    if (i & 1) odd += back.x + back.y;
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t kp = pa + t * kTilePairs;
+                    const uint32_t lo0 = __byte_perm(lds32(kp + c * 4), 0, 0x3232);
+                    const uint32_t lo1 = __byte_perm(lds32(kp + c * 4 + 128), 0, 0x3232);
+                    const uint4 pr0 = lds128(kp), pr1 = lds128(kp + 128);
+                    const uint4 vp0 = lds128(kp + 2 * kTilePairs), vp1 = lds128(kp + 2 * kTilePairs + 128);
+                    uint32_t b0 = max_bf16x2(max_bf16x2(vp0.x, vp0.y), max_bf16x2(vp0.z, vp0.w));
+                    uint32_t b1 = max_bf16x2(max_bf16x2(vp1.x, vp1.y), max_bf16x2(vp1.z, vp1.w));
+                    x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+                    mma_bf16_16816(x[t], lo0, lo1, lo0, lo1, qa.x, qa.y);
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) {
+                        const float s0 = q4_step(word(pr0, gg)), s1 = q4_step(word(pr1, gg));
+                        x[t][0] = fmaf(s0, a[t][gg][0], x[t][0]);
+                        x[t][1] = fmaf(s0, a[t][gg][1], x[t][1]);
+                        x[t][2] = fmaf(s1, a[t][gg][2], x[t][2]);
+                        x[t][3] = fmaf(s1, a[t][gg][3], x[t][3]);
+                    }
+                    x[t][0] *= __uint_as_float(qa.z);
+                    x[t][1] *= __uint_as_float(qa.w);
+                    x[t][2] *= __uint_as_float(qa.z);
+                    x[t][3] *= __uint_as_float(qa.w);
+                    const int nvalid = t ? nv.y : nv.x;
+                    if (nvalid < kTile) {  // what lies behind the valid rows may be anything
+                        if (r >= nvalid) {
+                            x[t][0] = x[t][1] = -CUDART_INF_F;
+                            b0 = 0;
+                        }
+                        if (r + 8 >= nvalid) {
+                            x[t][2] = x[t][3] = -CUDART_INF_F;
+                            b1 = 0;
+                        }
+                    }
+                    steps = max_bf16x2(steps, max_bf16x2(b0, b1));
                 }
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            odd += __shfl_xor_sync(0xffffffffu, odd, 1);
-            odd += __shfl_xor_sync(0xffffffffu, odd, 2);
-            const float in = 8.f * (sum - odd) - 64.f * odd;  // codes come as n - 8 and 64 + n
-            init0[gg] = __shfl_sync(0xffffffffu, in, 8 * c);
-            init1[gg] = __shfl_sync(0xffffffffu, in, 8 * c + 4);
-            qs0[gg] = __shfl_sync(0xffffffffu, sum, 8 * c);
-            qs1[gg] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-        }
-        sc0 = __shfl_sync(0xffffffffu, sc, 8 * c);
-        sc1 = __shfl_sync(0xffffffffu, sc, 8 * c + 4);
-    }
 
-    float o[4][4][4];  // [group][dim pair][(dim, head) of the pairs]
-    float low0[4], low1[4];  // this lane's share of sum p lo'
+            // ---- references: moved when a score passes by more than kLag, or a step at all
+            float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+            float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+            float step = bf16_lo(steps);
+            if (__any_sync(0xffffffffu, mx0 > m0 + kLag || mx1 > m1 + kLag || step > big)) {
 #pragma unroll
-    for (int gg = 0; gg < 4; ++gg) {
-        low0[gg] = low1[gg] = 0.f;
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+                    step = fmaxf(step, __shfl_xor_sync(0xffffffffu, step, sh));
+                }
+                const float old0 = m0 + eb, old1 = m1 + eb;
+                m0 = fmaxf(m0, mx0);
+                m1 = fmaxf(m1, mx1);
+                if (step > big) {  // the next power of two (within [2^-80, 2^80])
+                    const int e = min(80, max(-80, (int)(__float_as_uint(step) >> 23) - 126));
+                    eb = (float)e;
+                    big = e == 80 ? CUDART_INF_F : __uint_as_float((uint32_t)(e + 127) << 23);
+                }
+                const float al0 = old0 == -CUDART_INF_F ? 0.f : ex2_approx(old0 - (m0 + eb));
+                const float al1 = old1 == -CUDART_INF_F ? 0.f : ex2_approx(old1 - (m1 + eb));
+                l0 *= al0;
+                l1 *= al1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[gg][i][0] = o[gg][i][1] = o[gg][i][2] = o[gg][i][3] = 0.f;
-    }
-    float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
-
-    for (int m = 0; m < nst; ++m) {
-        const int i = m * kC + warp;
-        if (i >= n) break;
-        const int s = m % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait_abort(&full[s], (m / kStages) & 1, p.err, abort)))
-            break;
-        const int j = t0 + i, lp = j / tpp, off = (j - lp * tpp) * kTile;
-        const int nvalid = min(kTile, min(p.block_size - off, seq_len - (lp * p.block_size + off)));
-        const uint32_t kb = smem_u32(smem + s * kStageBytes + warp * kTileBytes);
-        const uint32_t vb = kb + kTileCodes, kp = vb + kTileCodes, vp = kp + kTilePairs;
-        const bool in0 = r < nvalid, in1 = r + 8 < nvalid;
-
-        // ---- scores: tokens r and r + 8, heads 2c and 2c + 1
-        float x00 = 0.f, x01 = 0.f, x10 = 0.f, x11 = 0.f;
-        {
-            const uint32_t a0 = kb + r * 128 + (((2 * c) ^ r) << 4);
-            const uint4 k00 = lds128(a0), k01 = lds128(a0 ^ 16);
-            const uint4 k10 = lds128(a0 + 1024), k11 = lds128((a0 ^ 16) + 1024);
-            const uint4 pr0 = lds128(kp + r * 16), pr1 = lds128(kp + r * 16 + 128);
+                for (int gg = 0; gg < 4; ++gg) {
+                    low0[gg] *= al0;
+                    low1[gg] *= al1;
 #pragma unroll
-            for (int gg = 0; gg < 4; ++gg) {
-                float a[4] = {init0[gg], init1[gg], init0[gg], init1[gg]};
-                uint32_t x[4], y[4];
-                widen<true>(word(k00, gg), x);
-                widen<true>(word(k10, gg), y);
-                mma_f16(a, x[0], y[0], x[1], y[1], qf[gg][0][0], qf[gg][0][1]);
-                mma_f16(a, x[2], y[2], x[3], y[3], qf[gg][0][2], qf[gg][0][3]);
-                widen<true>(word(k01, gg), x);
-                widen<true>(word(k11, gg), y);
-                mma_f16(a, x[0], y[0], x[1], y[1], qf[gg][1][0], qf[gg][1][1]);
-                mma_f16(a, x[2], y[2], x[3], y[3], qf[gg][1][2], qf[gg][1][3]);
-                const float s0 = q4_step(word(pr0, gg)), lo0 = q4_low(word(pr0, gg));
-                const float s1 = q4_step(word(pr1, gg)), lo1 = q4_low(word(pr1, gg));
-                x00 = fmaf(s0, a[0], fmaf(lo0, qs0[gg], x00));
-                x01 = fmaf(s0, a[1], fmaf(lo0, qs1[gg], x01));
-                x10 = fmaf(s1, a[2], fmaf(lo1, qs0[gg], x10));
-                x11 = fmaf(s1, a[3], fmaf(lo1, qs1[gg], x11));
+                    for (int k = 0; k < 4; ++k) {
+                        o[gg][k][0] *= al0;
+                        o[gg][k][1] *= al1;
+                        o[gg][k][2] *= al0;
+                        o[gg][k][3] *= al1;
+                    }
+                }
             }
-        }
-        x00 = in0 ? x00 * sc0 : -CUDART_INF_F;
-        x01 = in0 ? x01 * sc1 : -CUDART_INF_F;
-        x10 = in1 ? x10 * sc0 : -CUDART_INF_F;
-        x11 = in1 ? x11 * sc1 : -CUDART_INF_F;
+            const float mu0 = m0 == -CUDART_INF_F ? 0.f : m0 + eb - kHeadroom;
+            const float mu1 = m1 == -CUDART_INF_F ? 0.f : m1 + eb - kHeadroom;
 
-        // ---- online softmax against M = max(score + log2(largest step))
-        uint4 pr0 = lds128(vp + r * 16), pr1 = lds128(vp + r * 16 + 128);
-        if (!in0) pr0 = make_uint4(0, 0, 0, 0);  // what is masked may hold anything
-        if (!in1) pr1 = make_uint4(0, 0, 0, 0);
-        float big0 = 0x1p-80f, big1 = 0x1p-80f;
+            // ---- O^T += V^T (p s)^T, two tokens' codes a register
 #pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-            big0 = fmaxf(big0, q4_step(word(pr0, gg)));
-            big1 = fmaxf(big1, q4_step(word(pr1, gg)));
+            for (int t = 0; t < 2; ++t) {
+                const float p00 = ex2_approx(x[t][0] - mu0), p01 = ex2_approx(x[t][1] - mu1);
+                const float p10 = ex2_approx(x[t][2] - mu0), p11 = ex2_approx(x[t][3] - mu1);
+                l0 += p00 + p10;
+                l1 += p01 + p11;
+                const uint32_t vt = base + kOffV + t * kTileCodes;
+                const uint32_t v0 = vt + 2 * c * 128 + ((r ^ (2 * c)) << 4), v1 = (v0 ^ 16) + 128;
+                const uint4 va = lds128(v0), vb = lds128(v1);                // tokens 2c, 2c + 1
+                const uint4 vc = lds128(v0 + 1024), vd = lds128(v1 + 1024);  // tokens 2c + 8, 2c + 9
+                const uint32_t vp = base + kOffVPairs + t * kTilePairs + r * 16;
+                uint4 vp0 = lds128(vp), vp1 = lds128(vp + 128);
+                const int nvalid = t ? nv.y : nv.x;
+                if (nvalid < kTile) {
+                    if (r >= nvalid) vp0 = make_uint4(0, 0, 0, 0);
+                    if (r + 8 >= nvalid) vp1 = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int gg = 0; gg < 4; ++gg) {
+                    const float s0 = q4_step(word(vp0, gg)), s1 = q4_step(word(vp1, gg));
+                    const float lo0 = q4_low(word(vp0, gg)), lo1 = q4_low(word(vp1, gg));
+                    low0[gg] = fmaf(p00, lo0, fmaf(p10, lo1, low0[gg]));
+                    low1[gg] = fmaf(p01, lo0, fmaf(p11, lo1, low1[gg]));
+                    const uint32_t b0 = movmatrix_t(pack_f16x2(p00 * s0, p01 * s0));
+                    const uint32_t b1 = movmatrix_t(pack_f16x2(p10 * s1, p11 * s1));
+                    uint32_t u[4], v[4];
+                    widen(__byte_perm(word(va, gg), word(vb, gg), 0x5410), u);
+                    widen(__byte_perm(word(vc, gg), word(vd, gg), 0x5410), v);
+                    mma_f16(o[gg][0], u[0], u[1], v[0], v[1], b0, b1);
+                    mma_f16(o[gg][1], u[2], u[3], v[2], v[3], b0, b1);
+                    widen(__byte_perm(word(va, gg), word(vb, gg), 0x7632), u);
+                    widen(__byte_perm(word(vc, gg), word(vd, gg), 0x7632), v);
+                    mma_f16(o[gg][2], u[0], u[1], v[0], v[1], b0, b1);
+                    mma_f16(o[gg][3], u[2], u[3], v[2], v[3], b0, b1);
+                }
+            }
+            __syncwarp();  // the slot is free
         }
-        big0 = lg2_approx(fminf(big0, 0x1p80f));
-        big1 = lg2_approx(fminf(big1, 0x1p80f));
-        float mx0 = fmaxf(x00 + big0, x10 + big1), mx1 = fmaxf(x01 + big0, x11 + big1);
+        // Every load lands before its slot is loaded again or left (when a wait gave up).
+        for (uint32_t i = it + max(0, loaded - kDepth); i < it + loaded; ++i)
+            mbar_wait(&full[i % kDepth], (i / kDepth) & 1, p.err);
+        it += n;
+        m0 += eb;
+        m1 += eb;
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
-        }
-        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-        const float mu0 = mn0 == -CUDART_INF_F ? 0.f : mn0 - kHeadroom;
-        const float mu1 = mn1 == -CUDART_INF_F ? 0.f : mn1 - kHeadroom;
-        const float p00 = ex2_approx(x00 - mu0), p01 = ex2_approx(x01 - mu1);
-        const float p10 = ex2_approx(x10 - mu0), p11 = ex2_approx(x11 - mu1);
-        if (__any_sync(0xffffffffu, mn0 != m0 || mn1 != m1)) {
-            const float al0 = m0 == -CUDART_INF_F ? 0.f : ex2_approx(m0 - mn0);
-            const float al1 = m1 == -CUDART_INF_F ? 0.f : ex2_approx(m1 - mn1);
-            l0 *= al0;
-            l1 *= al1;
+            l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
 #pragma unroll
             for (int gg = 0; gg < 4; ++gg) {
-                low0[gg] *= al0;
-                low1[gg] *= al1;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[gg][k][0] *= al0;
-                    o[gg][k][1] *= al1;
-                    o[gg][k][2] *= al0;
-                    o[gg][k][3] *= al1;
-                }
+                low0[gg] += __shfl_xor_sync(0xffffffffu, low0[gg], sh);
+                low1[gg] += __shfl_xor_sync(0xffffffffu, low1[gg], sh);
             }
-            m0 = mn0;
-            m1 = mn1;
         }
-        l0 += p00 + p10;
-        l1 += p01 + p11;
 
-        // ---- O^T += V^T (p s)^T, two tokens' codes a register
-        const uint32_t v0 = vb + 2 * c * 128 + ((r ^ (2 * c)) << 4);  // token 2c, unit r
-        const uint4 va = lds128(v0), vc = lds128(v0 + 1024);           // tokens 2c, 2c + 8
-        const uint32_t v1 = (v0 ^ 16) + 128;
-        const uint4 vb1 = lds128(v1), vd = lds128(v1 + 1024);          // tokens 2c + 1, 2c + 9
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-            const float s0 = q4_step(word(pr0, gg)), s1 = q4_step(word(pr1, gg));
-            // codes come as n - 8: their constant part joins the minimum
-            const float lo0 = fmaf(8.f, s0, q4_low(word(pr0, gg)));
-            const float lo1 = fmaf(8.f, s1, q4_low(word(pr1, gg)));
-            low0[gg] = fmaf(p00, lo0, fmaf(p10, lo1, low0[gg]));
-            low1[gg] = fmaf(p01, lo0, fmaf(p11, lo1, low1[gg]));
-            const uint32_t b0 = movmatrix_t(pack_f16x2(p00 * s0, p01 * s0));
-            const uint32_t b1 = movmatrix_t(pack_f16x2(p10 * s1, p11 * s1));
-            uint32_t x[4], y[4];
-            widen<false>(__byte_perm(word(va, gg), word(vb1, gg), 0x5410), x);
-            widen<false>(__byte_perm(word(vc, gg), word(vd, gg), 0x5410), y);
-            mma_f16(o[gg][0], x[0], x[1], y[0], y[1], b0, b1);
-            mma_f16(o[gg][1], x[2], x[3], y[2], y[3], b0, b1);
-            widen<false>(__byte_perm(word(va, gg), word(vb1, gg), 0x7632), x);
-            widen<false>(__byte_perm(word(vc, gg), word(vd, gg), 0x7632), y);
-            mma_f16(o[gg][2], x[0], x[1], y[0], y[1], b0, b1);
-            mma_f16(o[gg][3], x[2], x[3], y[2], y[3], b0, b1);
+        // ---- the next segment's first loads and its q, before this one's merge
+        const int64_t pair = (int64_t)seq * p.num_kv_heads + g, part = blockIdx.x + pair;
+        const bool whole = t0 == 0 && t1 == tiles;
+        if (threadIdx.x == 0 && t0 == 0)
+            p.info[pair] = make_int2((int)part, whole ? 0 : (int)(shares.owner(at + tiles - 1) - blockIdx.x) + 1);
+        uint16_t *out_rows = p.out + ((int64_t)seq * p.num_q_heads + g * p.group) * kHeadDim;
+        at += t1 - t0;
+        const bool more = at < end;
+        if (more) {
+            t0 = 0;
+            if (++g == p.num_kv_heads) {
+                g = 0;
+                do tiles = seq_tiles(p, ++seq, &seq_len, false);
+                while (tiles == 0 && seq < p.num_seqs);
+            }
+            begin_segment();
+            load_q();
+            first_loads();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+
+        // ------------------------------------------------------------ merge of the warps
+        float *red_o = reinterpret_cast<float *>(smem + kOffMerge);      // [warp][head][row]
+        float2 *red_ml = reinterpret_cast<float2 *>(smem + kOffMl);      // [warp][head]
+        if (lane < 4) {
+            red_ml[warp * kDecMaxGroup + 2 * c] = make_float2(m0, l0);
+            red_ml[warp * kDecMaxGroup + 2 * c + 1] = make_float2(m1, l1);
+        }
+        {
+            float *row0 = red_o + (warp * kDecMaxGroup + 2 * c) * kMergeRow + 8 * r;
+#pragma unroll
+            for (int gg = 0; gg < 4; ++gg)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    auto row = [&](int h, float low) {
+                        return make_float4(
+                            fmaf(o[gg][2 * k][h], 0x1p24f, low), fmaf(o[gg][2 * k][2 + h], 0x1p20f, low),
+                            fmaf(o[gg][2 * k + 1][h], 0x1p24f, low),
+                            fmaf(o[gg][2 * k + 1][2 + h], 0x1p20f, low));
+                    };
+                    *reinterpret_cast<float4 *>(row0 + gg * 64 + k * 4) = row(0, low0[gg]);
+                    *reinterpret_cast<float4 *>(row0 + kMergeRow + gg * 64 + k * 4) = row(1, low1[gg]);
+                }
+        }
+        __syncthreads();  // every warp's rows are there, and q is no longer read
+        gave_up = *abort != 0;
+        if (more) make_q();
+        for (int qd = threadIdx.x; qd < p.group * (kHeadDim / 4); qd += kThreads) {
+            const int h = qd / (kHeadDim / 4), d = (qd - h * (kHeadDim / 4)) * 4;
+            float M = -CUDART_INF_F;
+            float2 ml[kW];
+#pragma unroll
+            for (int v = 0; v < kW; ++v) {
+                ml[v] = red_ml[v * kDecMaxGroup + h];
+                M = fmaxf(M, ml[v].x);
+            }
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < kW; ++v) {
+                const float e = M == -CUDART_INF_F ? 0.f : ex2_approx(ml[v].x - M);
+                const float4 f = *reinterpret_cast<const float4 *>(red_o + (v * kDecMaxGroup + h) * kMergeRow + d);
+                L += e * ml[v].y;
+                O.x += e * f.x;
+                O.y += e * f.y;
+                O.z += e * f.z;
+                O.w += e * f.w;
+            }
+            if (gave_up) {  // an empty part, or zeros
+                O = make_float4(0.f, 0.f, 0.f, 0.f);
+                M = -CUDART_INF_F;
+                L = 0.f;
+            }
+            if (whole) {
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                *reinterpret_cast<uint2 *>(out_rows + h * kHeadDim + d) =
+                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + (part * p.group + h) * kHeadDim + d) = O;
+                if (d == 0) p.part_ml[part * p.group + h] = make_float2(M, L);
+            }
+        }
+
+        if (!more) return;
+        __syncthreads();  // q is ready, and the merge's rows are free
     }
+}
 
+// Merges a row's parts: sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j, M = max m_j; an empty
+// part has m = -inf.  All loads of a round are in
+// flight together.
+//   few rows:  8 warps and 4 CTAs a row (64 dims each), for the latency of many parts
+//   many rows: two warps a row (128 dims each), 4 rows a CTA
+template <bool kFew>
+__global__ void __launch_bounds__(256) decode_q4_merge_kernel(const __grid_constant__ Params p) {
+    constexpr int kWarps = kFew ? 8 : 1, kRound = 4;
+    constexpr int kVec = kFew ? 1 : 2;  // float2 a lane
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = kFew ? blockIdx.x >> 2 : (int64_t)blockIdx.x * 4 + (warp >> 1);
+    const int d0 = kFew ? (blockIdx.x & 3) * 64 : (warp & 1) * 128;
+    pdl_wait();
+    pdl_trigger();
+    if (row >= (int64_t)p.num_seqs * p.num_q_heads) return;  // (warp-uniform; kFew: never)
+    const int seq = (int)(row / p.num_q_heads), h = (int)(row - (int64_t)seq * p.num_q_heads);
+    const int len = p.seq_lens[seq];
+    const int2 info = p.info[(int64_t)seq * p.num_kv_heads + h / p.group];
+    uint16_t *out = p.out + row * kHeadDim + d0;
+    if (len <= 0) {
+        if (kFew ? warp == 0 : true)
 #pragma unroll
-    for (int sh = 4; sh < 32; sh <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-            low0[gg] += __shfl_xor_sync(0xffffffffu, low0[gg], sh);
-            low1[gg] += __shfl_xor_sync(0xffffffffu, low1[gg], sh);
-        }
-    }
-
-    // ---------------------------------------------------------------- CTA merge
-    bar_sync(1, kThreads);  // every tile consumed, no load in flight
-    if (*abort) {
-        if (threadIdx.x < p.group)
-            p.part_ml[part0 + (int64_t)threadIdx.x * p.num_splits] = make_float2(-CUDART_INF_F, 0.f);
+            for (int v = 0; v < kVec; ++v) reinterpret_cast<uint32_t *>(out)[v * 32 + lane] = 0;
         return;
     }
-    float *red_o = reinterpret_cast<float *>(smem);  // [warp][head][row]
-    float *red_m = red_o + kC * kDecMaxGroup * kMergeRow;
-    float *red_l = red_m + kC * kDecMaxGroup;
-    if (lane < 4) {
-        red_m[warp * kDecMaxGroup + 2 * c] = m0;
-        red_m[warp * kDecMaxGroup + 2 * c + 1] = m1;
-        red_l[warp * kDecMaxGroup + 2 * c] = l0;
-        red_l[warp * kDecMaxGroup + 2 * c + 1] = l1;
-    }
-    {
-        float *w0 = red_o + (warp * kDecMaxGroup + 2 * c) * kMergeRow + 8 * r;
+    const int count = info.y;
+    if (count <= 0 || info.x < 0 || info.x + (int64_t)count > p.parts) return;
+    const int64_t first = (int64_t)info.x * p.group + h % p.group;  // parts are p.group rows apart
+    float M = -CUDART_INF_F, L = 0.f;
+    float2 acc[kVec];
 #pragma unroll
-        for (int gg = 0; gg < 4; ++gg)
+    for (int v = 0; v < kVec; ++v) acc[v] = make_float2(0.f, 0.f);
+    for (int j0 = kFew ? warp : 0; j0 < count; j0 += kWarps * kRound) {
+        float2 o[kRound][kVec], ml[kRound];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                *reinterpret_cast<float4 *>(w0 + gg * 64 + k * 4) =
-                    make_float4(o[gg][2 * k][0] + low0[gg], o[gg][2 * k][2] + low0[gg],
-                                o[gg][2 * k + 1][0] + low0[gg], o[gg][2 * k + 1][2] + low0[gg]);
-                *reinterpret_cast<float4 *>(w0 + kMergeRow + gg * 64 + k * 4) =
-                    make_float4(o[gg][2 * k][1] + low1[gg], o[gg][2 * k][3] + low1[gg],
-                                o[gg][2 * k + 1][1] + low1[gg], o[gg][2 * k + 1][3] + low1[gg]);
-            }
-    }
-    bar_sync(2, kC * 32);
-    for (int qd = threadIdx.x; qd < p.group * (kHeadDim / 4); qd += kC * 32) {
-        const int h = qd / (kHeadDim / 4), d = (qd - h * (kHeadDim / 4)) * 4;
-        float M = -CUDART_INF_F;
+        for (int k = 0; k < kRound; ++k) {
+            const int j = j0 + k * kWarps;
+            const int64_t at = first + (int64_t)j * p.group;
+            ml[k] = j < count ? ld_f2_ordered(p.part_ml + at) : make_float2(-CUDART_INF_F, 0.f);
 #pragma unroll
-        for (int w = 0; w < kC; ++w) M = fmaxf(M, red_m[w * kDecMaxGroup + h]);
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kC; ++w) {
-            const float e = M == -CUDART_INF_F ? 0.f : ex2_approx(red_m[w * kDecMaxGroup + h] - M);
-            const float4 v =
-                *reinterpret_cast<const float4 *>(red_o + (w * kDecMaxGroup + h) * kMergeRow + d);
-            L += e * red_l[w * kDecMaxGroup + h];
-            O.x += e * v.x;
-            O.y += e * v.y;
-            O.z += e * v.z;
-            O.w += e * v.w;
+            for (int v = 0; v < kVec; ++v)
+                o[k][v] = j < count ? ld_f2_ordered(reinterpret_cast<const float2 *>(
+                                          p.part_o + at * kHeadDim + d0) + v * 32 + lane)
+                                    : make_float2(0.f, 0.f);
         }
-        const int64_t pi = part0 + (int64_t)h * p.num_splits;
-        *reinterpret_cast<float4 *>(p.part_o + pi * kHeadDim + d) = O;
-        if (d == 0) p.part_ml[pi] = make_float2(M, L);
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) mn = fmaxf(mn, ml[k].x);
+        const float f = M == -CUDART_INF_F ? 0.f : ex2_approx(M - mn);
+        M = mn;
+        L *= f;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            acc[v].x *= f;
+            acc[v].y *= f;
+        }
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) {
+            const float e = ml[k].x == -CUDART_INF_F ? 0.f : ex2_approx(ml[k].x - M);
+            if (e == 0.f) continue;  // an empty part's sums are not used
+            L = fmaf(e, ml[k].y, L);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                acc[v].x = fmaf(e, o[k][v].x, acc[v].x);
+                acc[v].y = fmaf(e, o[k][v].y, acc[v].y);
+            }
+        }
     }
+    if (kFew) {
+        __shared__ float2 so[kWarps][32], sml[kWarps];
+        so[warp][lane] = acc[0];
+        if (lane == 0) sml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (warp) return;
+        M = -CUDART_INF_F;
+        L = 0.f;
+        acc[0] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float e = sml[w].x == -CUDART_INF_F ? 0.f : ex2_approx(sml[w].x - M);
+            L = fmaf(e, sml[w].y, L);
+            acc[0].x = fmaf(e, so[w][lane].x, acc[0].x);
+            acc[0].y = fmaf(e, so[w][lane].y, acc[0].y);
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int v = 0; v < kVec; ++v)
+        reinterpret_cast<uint32_t *>(out)[v * 32 + lane] = pack_bf16x2(acc[v].x * inv, acc[v].y * inv);
 }
 
 }  // namespace
 
-// Tiles per split: all CTAs resident at once (two an SM) when the longest allowed length
-// gives each at least a stage, and never more than kDecMaxSplits splits.
-DecodePlan plan_decode_q4(int num_seqs, int num_kv_heads, int block_size, int max_seq_len,
-                          int num_sms) {
-    DecodePlan pl;
-    pl.tiles_per_page = (block_size + kTile - 1) / kTile;
-    const int full = max_seq_len / block_size;
-    pl.max_tiles = full * pl.tiles_per_page + (max_seq_len - full * block_size + kTile - 1) / kTile;
-    const long long pairs = (long long)num_seqs * num_kv_heads;
-    const long long want = std::max(1ll, (2ll * num_sms + pairs - 1) / pairs);
-    int tps = (int)((pl.max_tiles + want - 1) / want);
-    tps = std::max(tps, (pl.max_tiles + kDecMaxSplits - 1) / kDecMaxSplits);
-    pl.tiles_per_split = (std::max(tps, 1) + kC - 1) / kC * kC;
-    pl.num_splits = (pl.max_tiles + pl.tiles_per_split - 1) / pl.tiles_per_split;
-    return pl;
+// Workspace: the parts' sums, their (reference, sum) pairs, and the pairs' info, each
+// 256-byte aligned.  A part is numbered CTA + pair, so there are at most CTAs + pairs.
+namespace {
+struct WsLayout {
+    int64_t parts;
+    size_t o, ml, info;
+};
+WsLayout ws_layout(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms) {
+    WsLayout l;
+    const int64_t pairs = (int64_t)num_seqs * num_kv_heads, group = num_q_heads / num_kv_heads;
+    l.parts = pairs + 2 * num_sms;
+    l.o = (size_t)l.parts * group * kHeadDim * 4;
+    l.ml = ((size_t)l.parts * group * sizeof(float2) + 255) & ~size_t(255);
+    l.info = ((size_t)pairs * sizeof(int2) + 255) & ~size_t(255);
+    return l;
+}
+}  // namespace
+
+size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms) {
+    const WsLayout l = ws_layout(num_seqs, num_q_heads, num_kv_heads, num_sms);
+    return l.o + l.ml + l.info;
 }
 
-cudaError_t launch_decode_q4(const DecodeQ4Args &a, const DecodePlan &plan, cudaStream_t stream) {
-    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_q4_split_kernel), kSmem, 6);
+cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream) {
+    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_q4_stream_kernel), kSmem, 6);
     if (e != cudaSuccess) return e;
     Params p;
     p.q = a.q;
@@ -538,23 +815,37 @@ cudaError_t launch_decode_q4(const DecodeQ4Args &a, const DecodePlan &plan, cuda
     p.block_table = a.block_table;
     p.bt_stride = a.bt_stride;
     p.seq_lens = a.seq_lens;
+    p.num_seqs = a.num_seqs;
     p.max_seq_len = a.max_seq_len;
     p.num_q_heads = a.num_q_heads;
+    p.num_kv_heads = a.num_kv_heads;
     p.group = a.num_q_heads / a.num_kv_heads;
     p.block_size = a.block_size;
-    p.tiles_per_page = plan.tiles_per_page;
-    p.tiles_per_split = plan.tiles_per_split;
-    p.num_splits = plan.num_splits;
+    p.tiles_per_page = (a.block_size + kTile - 1) / kTile;
+    p.by_block = fast_div(a.block_size);
+    p.by_tpp = fast_div(p.tiles_per_page);
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    decode_ws_parts(a.workspace, a.num_seqs, a.num_q_heads, plan, &p.part_o, &p.part_ml);
+    const WsLayout l = ws_layout(a.num_seqs, a.num_q_heads, a.num_kv_heads, a.num_sms);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.o);
+    p.info = reinterpret_cast<int2 *>(ws + l.o + l.ml);
+    p.parts = l.parts;
+    p.out = a.out;
     p.err = a.err;
+    // No more CTAs than the longest allowed lengths would use.
+    const int64_t tiles = (int64_t)a.num_seqs * a.num_kv_heads *
+                          ((int64_t)(a.max_seq_len / a.block_size) * p.tiles_per_page +
+                           (a.max_seq_len % a.block_size + kTile - 1) / kTile);
+    const int grid = (int)std::min<int64_t>(2 * a.num_sms, (tiles + kMinShare - 1) / kMinShare);
     if (a.ev_start && (e = record_event(a.ev_start, stream)) != cudaSuccess) return e;
-    e = launch_pdl(decode_q4_split_kernel, dim3(plan.num_splits, a.num_kv_heads, a.num_seqs),
-                   dim3(kThreads), kSmem, stream, p);
+    e = launch_pdl(decode_q4_stream_kernel, dim3(grid), dim3(kThreads), kSmem, stream, p);
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
-    return launch_decode_combine(p.part_o, p.part_ml, a.num_seqs, a.num_q_heads, plan.num_splits,
-                                 a.out, stream);
+    const int64_t rows = (int64_t)a.num_seqs * a.num_q_heads;
+    if (rows <= 8 * a.num_sms)
+        return launch_pdl(decode_q4_merge_kernel<true>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
+    return launch_pdl(decode_q4_merge_kernel<false>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
 }
 
 }  // namespace pa

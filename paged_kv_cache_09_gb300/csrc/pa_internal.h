@@ -151,13 +151,6 @@ struct DecodeArgs {
 cudaError_t launch_decode(const CUtensorMap *tmaps, const DecodeArgs &a, const DecodePlan &plan,
                           cudaStream_t stream);
 
-// Where a plan's partial sums and (max, sum) pairs lie in the decode workspace, and the
-// launch that merges them into BF16 rows.
-void decode_ws_parts(void *workspace, int num_seqs, int num_q_heads, const DecodePlan &plan,
-                     float **part_o, float2 **part_ml);
-cudaError_t launch_decode_combine(float *part_o, float2 *part_ml, int num_seqs, int num_q_heads,
-                                  int num_splits, uint16_t *out, cudaStream_t stream);
-
 // ----------------------------------------------------------------- 4-bit cache
 // Strides are in BF16 elements for rows, in bytes for cache pages.
 struct Q4WriteArgs {
@@ -225,11 +218,11 @@ struct DecodeQ4Args {
     uint16_t *out;
     void *workspace;
     unsigned *err;
+    int num_sms;
     cudaEvent_t ev_start, ev_stop;
 };
-DecodePlan plan_decode_q4(int num_seqs, int num_kv_heads, int block_size, int max_seq_len,
-                          int num_sms);
-cudaError_t launch_decode_q4(const DecodeQ4Args &a, const DecodePlan &plan, cudaStream_t stream);
+size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms);
+cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream);
 
 // ----------------------------------------------------------------- norm + rotation
 struct RopeArgs {

@@ -87,11 +87,10 @@ def decode(q, kc, vc, bs, table, lens, scale):
     """fp64 outputs, and per element the bound on what the kernel may be off by.
 
     The bound: the output's rounding to BF16 (half a step, 2^-8 of it); FP16 weights (2^-11
-    each, times a value of at most 8 steps; and of those below FP16's normal range, at 2^-29
-    of the largest, nothing that counts); scores in fp32 -- 64 products and an offset of 64 a
-    group, 4 groups: at most 2^-17 of sum |q| (|lo| + 64 s) -- which move a weight by twice
-    their error; the exponential and log2 approximations (2^-21); the sums of both (2^-17 of the
-    largest value)."""
+    each, times codes of at most 15 steps; and of those below FP16's normal range, at 2^-21 of
+    the largest, nothing that counts); scores in fp32 -- 64 products a group, 4 groups: at most
+    2^-17 of sum |q| (|lo| + 64 s) -- which move a weight by twice their error; the exponential's
+    approximation (2^-21); the sums of both (2^-17 of the largest value)."""
     S, hq, _ = q.shape
     G = hq // kc.shape[1]
     out, tol = np.zeros(q.shape), np.full(q.shape, 1e-30)
@@ -106,7 +105,7 @@ def decode(q, kc, vc, bs, table, lens, scale):
             vmax = np.repeat(np.abs(v).reshape(-1, GROUPS, 64).max((0, 2)), 64)
             step = np.repeat(vs.max(0), 64)
             out[s, h] = o
-            tol[s, h] = (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * 8 * step
+            tol[s, h] = (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * 15 * step
                          + (2 * 2.0 ** -17 * big + 2.0 ** -17 + 2.0 ** -21) * vmax) * 1.01
     return out, tol
 

@@ -104,7 +104,7 @@ def test_write_and_gather_padding_bounds_and_strides(cuda_lib):
     vo = ko.clone()
     pa.gather_cache_q4(kc, vc, slots, ko, vo)
     assert pa.device_errors() == pa.DEVERR_SLOT
-    assert (ko[[1, 3, 5]] == 7).all() and (vo[[1, 3, 5]] == 7).all()
+    assert not ko[[1, 3, 5]].any() and not vo[[1, 3, 5]].any()
     k1, v1 = pa.gather_cache_q4(plain_k, plain_v, slots[ok])
     assert torch.equal(ko[ok], k1) and torch.equal(vo[ok], v1)
     pa.reshape_and_cache_q4(key[:0], val[:0], kc, vc, slots[:0])  # no tokens
