@@ -481,9 +481,13 @@ def _device():
 
 def _need(t, name, dtype, ndim, dev):
     """t's shape, if it is a `dtype` tensor of ndim dims on device dev, the current one."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and \
-            t.dim() == ndim:
-        return t.shape
+    try:
+        if t.dtype is dtype and t.get_device() == dev:
+            shape = t.shape
+            if len(shape) == ndim:
+                return shape
+    except AttributeError:  # not a tensor
+        pass
     _check(t, name, dtype, ndim)
     raise ValueError(f"{name} must be on the current CUDA device")
 

@@ -768,6 +768,7 @@ static int rope_impl(pa::RopeArgs &a, void *stream) {
     DeviceInfo dev;
     if (int rc = device_info(&dev)) return rc;
     a.err = dev.err;
+    a.num_sms = dev.num_sms;
     return pa::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;

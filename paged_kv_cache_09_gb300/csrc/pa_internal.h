@@ -243,6 +243,8 @@ struct RopeArgs {
     const int64_t *slot_mapping;
     int block_size;
     unsigned *err;
+    int num_sms;
+    int shift_k, shift_v;  // set by the launch: the warps' rows that keys and values start after
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs &a, cudaStream_t stream);
 

@@ -10,10 +10,15 @@
 // (4-bit cache: the key's BF16 value, so that the result is that of the two calls).
 //
 // Every value is read once and written once; bound by memory for a prompt chunk, by launch
-// and one round trip for a decode batch.  D / 8 lanes hold a row, 8 dims (16 bytes) a lane:
-// the sum of squares is a few shuffles, a half-rotation's partner is the same register of
-// another lane.  A CTA works on one token, so that the warps' cosines and sines come
-// through L1 and stay in registers from row to row.
+// and one round trip for a decode batch.  D / 8 lanes hold a row, 8 dims (16 bytes) a lane.
+// Instructions come close to bounding it too, so the weights are multiplied into the angles once
+// per token and kind of row,
+//     out_j = inv (x_j A_j + x_p B_j),   A_j = w_j cos, B_j = +- w_p sin   (p: j's partner),
+// the partners are exchanged as packed BF16, before any arithmetic, and the arithmetic is on pairs.
+// 4096 tokens of 24 + 4 + 4 heads of 256: 225 instructions a row and 43 us with the weights
+// applied to every row.
+#include <algorithm>
+
 #include "pa_internal.h"
 #include "pa_q4.cuh"
 
@@ -21,170 +26,252 @@ namespace pa {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kBatch = 4;  // rows of a warp whose loads are in flight together
+constexpr int kWarps = 4;
+constexpr int kBatch = 6;  // query rows of a warp that are loaded a token ahead
+
+// Pairs of fp32 in one register pair.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f32x2 pair_bf16(uint32_t w) { return pair(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ f32x2 mul(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack(f32x2 v) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return pack_bf16x2(lo, hi);
+}
 
 template <int kD, bool kNeighbours, int kCache>  // kCache: 0 none, 1 BF16, 2 4-bit
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 4)
     qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kLanes = kD / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp
     static_assert(kCache != 2 || kD == kHeadDim, "the 4-bit cache holds rows of 256");
     const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
-    const int unit = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * kPer + sub;
-    const int step = gridDim.y * kWarps * kPer;
-    const int64_t t = blockIdx.x;
+    const int step = gridDim.y * kWarps * kPer;                              // rows of all warps
+    const int unit = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * kPer + sub;  // this warp's first
+    const int hq = a.num_q_heads, hkv = a.num_kv_heads;
+    // Keys start where the queries' last round ends among the warps, values after them.
+    // (A warp's rows stay together: the shifts, below step, are by whole warps.)
+    int unit_k = unit - a.shift_k, unit_v = unit - a.shift_v;
+    unit_k += unit_k < 0 ? step : 0;
+    unit_v += unit_v < 0 ? step : 0;
+    auto row_of = [&](const uint16_t *p, int r, int n) {
+        return r < n ? *reinterpret_cast<const uint4 *>(p + r * kD + 8 * l) : make_uint4(0, 0, 0, 0);
+    };
     pdl_wait();
     pdl_trigger();
-    const int pos = a.positions[t];
-    if (pos < 0) return;  // padding: the token's rows stay as they are
-    if (pos >= a.max_position) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPosition);
-        return;
+    const int R = a.rotary_dim, half = R / 2;
+    const bool turns = 8 * l < R, second = 8 * l >= half;  // (second: of a pair of halves)
+    const int partner = turns && !kNeighbours ? (second ? l - R / 16 : l + R / 16) : l;
+    // A CTA takes every gridDim.x-th token, and loads ahead: a token's first rows of each kind into
+    // registers and its angles (this lane's, into shared memory) while the token before is worked
+    // on, its position a token earlier still.  (A padding token's rows are read for nothing.)
+    __shared__ float4 angles[kWarps][2][kNeighbours ? 2 : 4][32];
+    uint4 raw[kBatch], raw_k, raw_v;  // each is loaded again as soon as its row is done
+    int64_t slot_next;
+    const uint16_t *q_at, *k_at, *v_at;  // of the token that is loaded
+    auto at = [&](int64_t t) {
+        q_at = a.q + t * a.q_stride;
+        k_at = a.k + t * a.k_stride;
+        if (kCache) v_at = a.v + t * a.v_stride;
+    };
+    auto angles_of = [&](int64_t t, int pos, int buf) {
+        slot_next = kCache ? a.slot_mapping[t] : -1;
+        if (turns && pos >= 0 && pos < a.max_position) {
+            const float *row = a.cos_sin + (int64_t)pos * R +
+                               (kNeighbours ? 4 * l : second ? 8 * l - half : 8 * l);
+            constexpr int kN = kNeighbours ? 1 : 2;
+#pragma unroll
+            for (int e = 0; e < 2 * kN; ++e)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(&angles[threadIdx.x >> 5][buf][e][lane])),
+                             "l"(row + (e / kN) * half + (e % kN) * 4)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto position = [&](int64_t t) { return t < a.num_tokens ? a.positions[t] : -1; };
+    const int64_t stride = gridDim.x;
+    int pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride), buf = 0;
+    at(blockIdx.x);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) raw[b] = row_of(q_at, unit + b * step, hq);
+    raw_k = row_of(k_at, unit_k, hkv);
+    if (kCache) raw_v = row_of(v_at, unit_v, hkv);
+    angles_of(blockIdx.x, pos, 0);
+    for (int64_t t = blockIdx.x; t < a.num_tokens; t += stride, buf ^= 1) {
+    const int pos_now = pos;
+    const int64_t slot = slot_next;
+    const bool more = t + stride < a.num_tokens;
+    pos = pos_next;
+    if (more) {
+        at(t + stride);
+        angles_of(t + stride, pos, buf ^ 1);
+        pos_next = position(t + 2 * stride);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
+    const bool live = pos_now >= 0 && pos_now < a.max_position;  // otherwise its rows stay as they are
+    if (pos_now >= a.max_position && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPosition);
     int64_t run = -1;  // the slot's place in the caches (of head 0)
     int o = 0;
-    if (kCache) {
-        const int64_t slot = a.slot_mapping[t];
-        if (slot >= 0) {
-            const int64_t page = slot / a.block_size;
-            o = (int)(slot - page * a.block_size);
-            if (page < a.num_pages)
-                run = kCache == 1
-                          ? page * a.page_stride + (int64_t)o * a.num_kv_heads * kD
-                          : page * a.page_stride;
-            else if (threadIdx.x == 0 && blockIdx.y == 0)
-                atomicOr(a.err, kErrSlot);
+    if (kCache && live && slot >= 0) {
+        // (A 64-bit division is a hundred instructions for every warp.)
+        const int64_t page = slot >> 31 ? slot / a.block_size : (uint32_t)slot / (uint32_t)a.block_size;
+        o = (int)(slot - page * a.block_size);
+        if (page < a.num_pages)
+            run = kCache == 1 ? page * a.page_stride + (int64_t)o * hkv * kD : page * a.page_stride;
+        else if (threadIdx.x == 0 && blockIdx.y == 0)
+            atomicOr(a.err, kErrSlot);
+    }
+    // A and B of this lane's dims for rows with these weights.
+    f32x2 A[4], B[4];
+    auto factors = [&](const uint16_t *w) {
+        float wo[8], wp[8], c[8], s[8];
+        const uint4 own = __ldg(reinterpret_cast<const uint4 *>(w) + l);
+        const uint4 other = __ldg(reinterpret_cast<const uint4 *>(w) + partner);
+        const uint32_t x[4] = {own.x, own.y, own.z, own.w}, y[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wo[2 * i] = bf16_lo(x[i]) + a.weight_bias;
+            wo[2 * i + 1] = bf16_hi(x[i]) + a.weight_bias;
+            wp[2 * i + (kNeighbours ? 1 : 0)] = bf16_lo(y[i]) + a.weight_bias;
+            wp[2 * i + (kNeighbours ? 0 : 1)] = bf16_hi(y[i]) + a.weight_bias;
         }
-    }
-    // This lane's angles: dims 8l .. 8l + 7.
-    const int R = a.rotary_dim, half = R / 2;
-    const bool turns = 8 * l < R;
-    const bool second = 8 * l >= half;  // of a pair of halves
-    float c[8], s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        c[j] = 1.f;
-        s[j] = 0.f;
-    }
-    if (turns) {
-        const float *row = a.cos_sin + (int64_t)pos * R;
-        if (kNeighbours) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + 4 * l));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + 4 * l));
-            c[0] = c[1] = cv.x; c[2] = c[3] = cv.y; c[4] = c[5] = cv.z; c[6] = c[7] = cv.w;
-            s[1] = sv.x; s[3] = sv.y; s[5] = sv.z; s[7] = sv.w;
-            s[0] = -sv.x; s[2] = -sv.y; s[4] = -sv.z; s[6] = -sv.w;
-        } else {
-            const int i = second ? 8 * l - half : 8 * l;
-            const float sign = second ? 1.f : -1.f;
+        for (int j = 0; j < 8; ++j) {
+            c[j] = 1.f;
+            s[j] = 0.f;
+        }
+        if (turns) {
+            const float4 (*mine)[32] = angles[threadIdx.x >> 5][buf];
+            if (kNeighbours) {
+                const float4 cv = mine[0][lane], sv = mine[1][lane];
+                c[0] = c[1] = cv.x; c[2] = c[3] = cv.y; c[4] = c[5] = cv.z; c[6] = c[7] = cv.w;
+                s[1] = sv.x; s[3] = sv.y; s[5] = sv.z; s[7] = sv.w;
+                s[0] = -sv.x; s[2] = -sv.y; s[4] = -sv.z; s[6] = -sv.w;
+            } else {
+                const float sign = second ? 1.f : -1.f;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + i) + v);
-                const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + i) + v);
-                c[4 * v] = cv.x; c[4 * v + 1] = cv.y; c[4 * v + 2] = cv.z; c[4 * v + 3] = cv.w;
-                s[4 * v] = sign * sv.x; s[4 * v + 1] = sign * sv.y;
-                s[4 * v + 2] = sign * sv.z; s[4 * v + 3] = sign * sv.w;
+                for (int e = 0; e < 2; ++e) {
+                    const float4 cv = mine[e][lane], sv = mine[2 + e][lane];
+                    c[4 * e] = cv.x; c[4 * e + 1] = cv.y; c[4 * e + 2] = cv.z; c[4 * e + 3] = cv.w;
+                    s[4 * e] = sign * sv.x; s[4 * e + 1] = sign * sv.y;
+                    s[4 * e + 2] = sign * sv.z; s[4 * e + 3] = sign * sv.w;
+                }
             }
         }
-    }
-    const int partner = sub * kLanes + (second ? l - R / 16 : l + R / 16) % kLanes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            A[i] = pair(wo[2 * i] * c[2 * i], wo[2 * i + 1] * c[2 * i + 1]);
+            B[i] = pair(wp[2 * i] * s[2 * i], wp[2 * i + 1] * s[2 * i + 1]);
+        }
+    };
 
-    const int rows = a.num_q_heads + (kCache ? 2 : 1) * a.num_kv_heads;
-    // Rows of all warps of the token in steps; the shuffles need whole warps, so a warp
-    // goes on while any of its rows is left.
-    for (int r0 = unit - sub; r0 < rows; r0 += kBatch * step) {
-        uint4 raw[kBatch];
+    auto turned = [&](const uint4 &row) {  // (all lanes of the warp)
+        const uint32_t w[4] = {row.x, row.y, row.z, row.w};
+        f32x2 x[4], ss = pair(0.f, 0.f);
+        uint32_t res[4];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * step + sub;
-            raw[b] = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const uint16_t *src;
-                if (r < a.num_q_heads)
-                    src = a.q + t * a.q_stride + r * kD;
-                else if (r < a.num_q_heads + a.num_kv_heads)
-                    src = a.k + t * a.k_stride + (r - a.num_q_heads) * kD;
-                else
-                    src = a.v + t * a.v_stride + (r - a.num_q_heads - a.num_kv_heads) * kD;
-                raw[b] = *(reinterpret_cast<const uint4 *>(src) + l);
-            }
+        for (int i = 0; i < 4; ++i) {
+            x[i] = pair_bf16(w[i]);
+            ss = fma(x[i], x[i], ss);
         }
+        float sum, odd;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(sum), "=f"(odd) : "l"(ss));
+        sum += odd;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * step + sub;
-            if (r0 + b * step >= rows) break;  // warp-uniform
-            const bool is_q = r < a.num_q_heads;
-            const int h = is_q ? r : (r - a.num_q_heads) % a.num_kv_heads;
-            const bool is_v = r >= a.num_q_heads + a.num_kv_heads;
+        for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        // (rsqrt: within 2 units in the last place of fp32)
+        const float inv = rsqrtf(sum * (1.f / kD) + a.eps);
+        const f32x2 inv2 = pair(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t y = kNeighbours ? __byte_perm(w[i], 0, 0x1032)
+                                           : __shfl_sync(0xffffffffu, w[i], sub * kLanes + partner);
+            res[i] = pack(mul(inv2, fma(pair_bf16(y), B[i], mul(x[i], A[i]))));
+        }
+        return make_uint4(res[0], res[1], res[2], res[3]);
+    };
+    auto to_cache = [&](uint8_t *cache, int h, const uint4 &row) {
+        if (run < 0) return;
+        if (kCache == 1) {
+            *reinterpret_cast<uint4 *>(cache + 2 * (run + h * kD + 8 * l)) = row;
+        } else {  // one row a warp: warp-uniform
             float x[8];
-            {
-                const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+            const uint32_t w[4] = {row.x, row.y, row.z, row.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = bf16_lo(w[i]);
-                    x[2 * i + 1] = bf16_hi(w[i]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
             }
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            if (!is_v) {
-                const float inv = 1.f / sqrtf(ss * (1.f / kD) + a.eps);
-                const uint4 wr = __ldg(reinterpret_cast<const uint4 *>(is_q ? a.q_weight : a.k_weight) + l);
-                const uint32_t w[4] = {wr.x, wr.y, wr.z, wr.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] *= inv * (bf16_lo(w[i]) + a.weight_bias);
-                    x[2 * i + 1] *= inv * (bf16_hi(w[i]) + a.weight_bias);
-                }
-            }
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[j] = kNeighbours ? x[j ^ 1] : __shfl_sync(0xffffffffu, x[j], partner);
-            if (!is_v && turns) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], c[j], y[j] * s[j]);
-            }
-            const uint4 out = is_v ? raw[b]
-                                   : make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-            if (is_q) {
-                if (r < rows)
-                    *(reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + h * kD) + l) = out;
-            } else if (kCache == 0) {
-                if (r < rows)
-                    *(reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + h * kD) + l) = out;
-            } else if (kCache == 1) {
-                if (r < rows && run >= 0)
-                    *(reinterpret_cast<uint4 *>((is_v ? a.v_cache : a.k_cache) + 2 * (run + h * kD)) + l) = out;
-            } else if (run >= 0) {  // one row a warp: warp-uniform
-                const uint32_t w[4] = {out.x, out.y, out.z, out.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = bf16_lo(w[i]);
-                    x[2 * i + 1] = bf16_hi(w[i]);
-                }
-                q4_store_row(x, lane,
-                             (is_v ? a.v_cache : a.k_cache) + run +
-                                 (int64_t)h * a.block_size * kQ4RowBytes,
-                             a.block_size, o);
-            }
+            q4_store_row(x, lane, cache + run + (int64_t)h * a.block_size * kQ4RowBytes, a.block_size, o);
         }
+    };
+
+    // The shuffles need whole warps, so a warp goes on while any of its rows is left.
+    factors(a.q_weight);
+    uint16_t *q_out = a.q_out + t * a.q_out_stride + 8 * l;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+        const int r = unit + b * step;
+        if (r - sub >= hq) break;  // warp-uniform
+        const uint4 out = turned(raw[b]);
+        if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
+        if (more) raw[b] = row_of(q_at, r, hq);
+    }
+    for (int r = unit + kBatch * step; r - sub < hq; r += step) {  // many heads
+        const uint4 out = turned(row_of(a.q + t * a.q_stride, r, hq));
+        if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
+    }
+    if (unit_k - sub < hkv) factors(a.k_weight);
+    for (int r = unit_k; r - sub < hkv; r += step) {
+        const uint4 out = turned(r == unit_k ? raw_k : row_of(a.k + t * a.k_stride, r, hkv));
+        if (live && r < hkv) {
+            if (kCache == 0)
+                *reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + r * kD + 8 * l) = out;
+            else
+                to_cache(a.k_cache, r, out);
+        }
+    }
+    if (kCache)
+        for (int r = unit_v; r < hkv; r += step)
+            to_cache(a.v_cache, r, r == unit_v ? raw_v : row_of(a.v + t * a.v_stride, r, hkv));
+    if (more) {
+        raw_k = row_of(k_at, unit_k, hkv);
+        if (kCache) raw_v = row_of(v_at, unit_v, hkv);
+    }
     }
 }
 
 template <int kD>
-cudaError_t launch_dim(const RopeArgs &a, cudaStream_t stream) {
+cudaError_t launch_dim(RopeArgs a, cudaStream_t stream) {
     const int rows = a.num_q_heads + (a.cache ? 2 : 1) * a.num_kv_heads;
     constexpr int per = kWarps * (256 / kD);
-    // A large call: the token's rows over one CTA, kBatch a warp.  A small one: more CTAs a
-    // token, one row a warp.
-    const int y = a.num_tokens >= 512 ? (rows + per * kBatch - 1) / (per * kBatch)
+    // A large call: a token over as few CTAs as give each warp kBatch query rows.  A small one:
+    // more CTAs a token, one row a warp.
+    const int y = a.num_tokens >= 512 ? (a.num_q_heads + per * kBatch - 1) / (per * kBatch)
                                       : (rows + per - 1) / per;
-    const dim3 grid(a.num_tokens, y), block(kWarps * 32);
+    constexpr int one = 256 / kD;  // rows of a warp
+    const int step = y * per;
+    a.shift_k = (a.num_q_heads + one - 1) / one * one % step;
+    a.shift_v = (a.shift_k + (a.num_kv_heads + one - 1) / one * one) % step;
+    // (Four resident CTAs an SM.)
+    const int x = a.num_tokens >= 512 ? std::min(a.num_tokens, std::max(1, 4 * a.num_sms / y)) : a.num_tokens;
+    const dim3 grid(x, y), block(kWarps * 32);
     if (a.interleaved) {
         if (a.cache == 0) return launch_pdl(qk_norm_rope_kernel<kD, true, 0>, grid, block, 0, stream, a);
         if (a.cache == 1) return launch_pdl(qk_norm_rope_kernel<kD, true, 1>, grid, block, 0, stream, a);
