@@ -22,55 +22,51 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
     }
 }
 
-// KV write: warp per (token, head), K and V of it.
+// KV write: warp per (token, head), K and V of it; the warps of a CTA on one head.
 __global__ void __launch_bounds__(kWarps * 32) write_q4_kernel(const Q4WriteArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, h = blockIdx.y;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_trigger();
-    const int64_t t = row / a.num_kv_heads;
-    const int h = (int)(row - t * a.num_kv_heads);
     if (t >= a.num_tokens) return;
     const int64_t slot = a.slot_mapping[t];
-    const uint4 kr = __ldg(reinterpret_cast<const uint4 *>(a.key + t * a.key_stride + h * kHeadDim) + lane);
-    const uint4 vr = __ldg(reinterpret_cast<const uint4 *>(a.value + t * a.value_stride + h * kHeadDim) + lane);
+    const uint4 k = __ldg(reinterpret_cast<const uint4 *>(a.key + t * a.key_stride + h * kHeadDim) + lane);
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.value + t * a.value_stride + h * kHeadDim) + lane);
     if (slot < 0) return;
-    const int64_t page = slot / a.block_size;
+    const int64_t page = page_of(slot, a.block_size);
     if (page >= a.num_pages) {
         if (lane == 0) atomicOr(a.err, kErrSlot);
         return;
     }
     const int o = (int)(slot - page * a.block_size);
     const int64_t run = page * a.page_stride + (int64_t)h * a.block_size * kQ4RowBytes;
-    float x[8];
-    unpack8(kr, x);
-    q4_store_row(x, lane, a.k_cache + run, a.block_size, o);
-    unpack8(vr, x);
-    q4_store_row(x, lane, a.v_cache + run, a.block_size, o);
+    q4_store_row(k, lane, a.k_cache + run, a.block_size, o);
+    q4_store_row(v, lane, a.v_cache + run, a.block_size, o);
 }
 
 // Read back by slots: warp per (token, head), K and V of it.
 __global__ void __launch_bounds__(kWarps * 32) gather_q4_kernel(const Q4GatherArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, h = blockIdx.y;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     pdl_wait();
     pdl_trigger();
-    const int64_t t = row / a.num_kv_heads;
-    const int h = (int)(row - t * a.num_kv_heads);
     if (t >= a.num_tokens) return;
     const int64_t slot = a.slot_mapping[t];
-    const int64_t page = slot / a.block_size;
     uint4 k = make_uint4(0, 0, 0, 0), v = k;  // padding, and a slot outside the pool
-    if (slot >= 0 && page < a.num_pages) {
-        const int o = (int)(slot - page * a.block_size);
-        const int64_t run = page * a.page_stride + (int64_t)h * a.block_size * kQ4RowBytes;
-        k = q4_load_row(a.k_cache + run, a.block_size, o, lane);
-        v = q4_load_row(a.v_cache + run, a.block_size, o, lane);
-    } else if (slot >= 0 && lane == 0) {
-        atomicOr(a.err, kErrSlot);
+    if (slot >= 0) {
+        const int64_t page = page_of(slot, a.block_size);
+        if (page < a.num_pages) {
+            const int o = (int)(slot - page * a.block_size);
+            const int64_t run = page * a.page_stride + (int64_t)h * a.block_size * kQ4RowBytes;
+            k = q4_load_row(a.k_cache + run, a.block_size, o, lane);
+            v = q4_load_row(a.v_cache + run, a.block_size, o, lane);
+        } else if (lane == 0) {
+            atomicOr(a.err, kErrSlot);
+        }
     }
-    reinterpret_cast<uint4 *>(a.k_out + row * kHeadDim)[lane] = k;
-    reinterpret_cast<uint4 *>(a.v_out + row * kHeadDim)[lane] = v;
+    const int64_t row = (t * a.num_kv_heads + h) * kHeadDim;
+    reinterpret_cast<uint4 *>(a.k_out + row)[lane] = k;
+    reinterpret_cast<uint4 *>(a.v_out + row)[lane] = v;
 }
 
 // ---- prefill: FP16 operands from the 4-bit cache and BF16 queries
@@ -235,20 +231,20 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
-unsigned row_blocks(int num_tokens, int num_kv_heads) {
-    return (unsigned)(((int64_t)num_tokens * num_kv_heads + kWarps - 1) / kWarps);
+dim3 row_grid(int num_tokens, int num_kv_heads) {
+    return dim3((unsigned)((num_tokens - 1) / kWarps + 1), num_kv_heads);
 }
 
 }  // namespace
 
 cudaError_t launch_write_q4(const Q4WriteArgs &a, cudaStream_t stream) {
-    return launch_pdl(write_q4_kernel, dim3(row_blocks(a.num_tokens, a.num_kv_heads)),
-                      dim3(kWarps * 32), 0, stream, a);
+    return launch_pdl(write_q4_kernel, row_grid(a.num_tokens, a.num_kv_heads), dim3(kWarps * 32), 0,
+                      stream, a);
 }
 
 cudaError_t launch_gather_q4(const Q4GatherArgs &a, cudaStream_t stream) {
-    return launch_pdl(gather_q4_kernel, dim3(row_blocks(a.num_tokens, a.num_kv_heads)),
-                      dim3(kWarps * 32), 0, stream, a);
+    return launch_pdl(gather_q4_kernel, row_grid(a.num_tokens, a.num_kv_heads), dim3(kWarps * 32), 0,
+                      stream, a);
 }
 
 cudaError_t launch_expand_q4(const Q4ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream) {

@@ -157,11 +157,6 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int g) {
     return g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w;
 }
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));

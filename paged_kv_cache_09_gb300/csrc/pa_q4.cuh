@@ -44,62 +44,77 @@ __device__ __forceinline__ int q4_pair_offset(int block_size, int o, int g) {
 __device__ __forceinline__ float q4_step(uint32_t pair) { return bf16_lo(pair); }
 __device__ __forceinline__ float q4_low(uint32_t pair) { return bf16_hi(pair); }
 
-// Quantises one row held by a warp, lane l holding dims 8l .. 8l + 7 (BF16 values as
-// floats), and stores it at offset o of the (page, head) run `run`.  A lane's dims are
-// word g = l / 8 of unit l % 8.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Quantises one row held by a warp, lane l holding dims 8l .. 8l + 7 (BF16 pairs), and stores it
+// at offset o of the (page, head) run `run`.  A lane's dims are word g = l / 8 of unit l % 8.
 //
-// Codes are those of exact arithmetic (ties to even): the quotient's rounding in fp32 can
-// be one off at a border, so the remainder x - lo - n s is formed exactly (the difference
-// and its rounding error; n s has 12 bits) and compared with half a step.
+// Codes are those of exact arithmetic (ties to even).  q = (x - lo) / s by a product with the
+// reciprocal and one correction from the exact remainder: a quotient that is a tie k + 1/2 comes
+// out exactly, and no other quotient reaches one (x - lo is a multiple of its last place, so the
+// quotient keeps further from a tie than fp32 rounds).  x - lo itself can round only where x is
+// tiny beside lo, and that matters only where the value 0 lies on a tie: then the sign of x
+// decides.
 // A group with a NaN or an infinity, or whose range overflows fp32, gets s = NaN: all of
 // it reads back as NaN.
-__device__ __forceinline__ void q4_store_row(const float (&x)[8], int lane, uint8_t *run,
+__device__ __forceinline__ void q4_store_row(const uint4 &row, int lane, uint8_t *run,
                                              int block_size, int o) {
-    float lo = x[0], hi = x[0];
-    bool bad = !(fabsf(x[0]) <= 3.4028235e38f);
-#pragma unroll
-    for (int j = 1; j < 8; ++j) {
-        lo = fminf(lo, x[j]);
-        hi = fmaxf(hi, x[j]);
-        bad |= !(fabsf(x[j]) <= 3.4028235e38f);
-    }
-#pragma unroll
-    for (int sh = 1; sh < 8; sh <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, sh));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, sh));
-    }
-    const unsigned bad_lanes = __ballot_sync(0xffffffffu, bad);
+    const uint32_t w[4] = {row.x, row.y, row.z, row.w};
     const int g = lane >> 3, u = lane & 7;
-    const float range = __fsub_rn(hi, lo);
-    bad = ((bad_lanes >> (g * 8)) & 0xffu) != 0 || !(range <= 3.4028235e38f);
+    // (minimum, -maximum) of the group: one register, one kind of minimum
+    uint32_t lows = min_bf16x2(min_bf16x2(w[0], w[1]), min_bf16x2(w[2], w[3]));
+    uint32_t highs = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+    highs ^= 0x80008000u;
+    uint32_t ends = min_bf16x2(__byte_perm(lows, highs, 0x5410), __byte_perm(lows, highs, 0x7632));
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+#pragma unroll
+    for (int sh = 1; sh < 8; sh <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, sh));
+    float lo = bf16_lo(ends), range = __fsub_rn(-bf16_hi(ends), lo);
+    bad = ((__ballot_sync(0xffffffffu, bad) >> (g * 8)) & 0xffu) != 0 || !(range <= 3.4028235e38f);
+    const uint32_t lo_bits = ends & 0xffffu;
     const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.f)));
-    uint32_t word = 0;
+    uint32_t codes = 0;
     if (!bad && s > 0.f) {
         // Steps near the subnormals: the same quotients from values 2^64 times as large.
         const float up = s < 1e-30f ? 0x1p64f : 1.f;
-        const float st = s * up, rcp = __frcp_rn(st), half = 0.5f * st, l = lo * up;
+        const float st = s * up, rcp = __frcp_rn(st), l = lo * up;
+        auto quotient = [&](float d) {
+            const float t = d * rcp;
+            return __fmaf_rn(__fmaf_rn(-t, st, d), rcp, t);
+        };
+        const float zero = quotient(-l);
+        const bool tie = zero - floorf(zero) == 0.5f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = x[j] * up;
-            const float d = __fsub_rn(v, l);
-            const float b = __fsub_rn(d, v);  // two-sum: v - l = d + e exactly
-            const float e = __fadd_rn(__fsub_rn(v, __fsub_rn(d, b)), __fsub_rn(-l, b));
-            float n = fminf(rintf(d * rcp), 15.f);
-            const float r = __fmaf_rn(-n, st, d);
-            const bool odd = (static_cast<int>(n) & 1) != 0;
-            if (r > half || (r == half && (e > 0.f || (e == 0.f && odd))))
-                n += 1.f;
-            else if (r < -half || (r == -half && (e < 0.f || (e == 0.f && odd))))
-                n -= 1.f;
-            word |= static_cast<uint32_t>(fminf(n, 15.f)) << (4 * j);
+            const float x = (j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1])) * up;
+            const float d = __fsub_rn(x, l);
+            // (adding 1.5 * 2^23 rounds to an integer, ties to even, in the low bits)
+            uint32_t n = __float_as_uint(__fadd_rn(quotient(d), 12582912.f)) & 31u;
+            if (tie && d == -l && x != 0.f) n = (uint32_t)floorf(zero) + (x > 0.f ? 1u : 0u);
+            codes |= min(n, 15u) << (4 * j);
         }
     }
-    *reinterpret_cast<uint32_t *>(run + q4_word_offset(o, u, g)) = word;
-    if (u == 0) {
-        const uint32_t sb = bad ? 0x7fc0u : (__float_as_uint(s) >> 16);
+    *reinterpret_cast<uint32_t *>(run + q4_word_offset(o, u, g)) = codes;
+    if (u == 0)
         *reinterpret_cast<uint32_t *>(run + q4_pair_offset(block_size, o, g)) =
-            sb | (__float_as_uint(lo) & 0xffff0000u);
-    }
+            (bad ? 0x7fc0u : (__float_as_uint(s) >> 16)) | (lo_bits << 16);
+}
+
+// Page of a slot (>= 0).  (A 64-bit division is a hundred instructions for every warp.)
+__device__ __forceinline__ int64_t page_of(int64_t slot, int block_size) {
+    return slot >> 31 ? slot / block_size : (uint32_t)slot / (uint32_t)block_size;
 }
 
 // Lane l's dims 8l .. 8l + 7 of the row at offset o of `run`, rounded to BF16: two per

@@ -129,8 +129,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     int64_t run = -1;  // the slot's place in the caches (of head 0)
     int o = 0;
     if (kCache && live && slot >= 0) {
-        // (A 64-bit division is a hundred instructions for every warp.)
-        const int64_t page = slot >> 31 ? slot / a.block_size : (uint32_t)slot / (uint32_t)a.block_size;
+        const int64_t page = page_of(slot, a.block_size);
         o = (int)(slot - page * a.block_size);
         if (page < a.num_pages)
             run = kCache == 1 ? page * a.page_stride + (int64_t)o * hkv * kD : page * a.page_stride;
@@ -211,14 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         if (kCache == 1) {
             *reinterpret_cast<uint4 *>(cache + 2 * (run + h * kD + 8 * l)) = row;
         } else {  // one row a warp: warp-uniform
-            float x[8];
-            const uint32_t w[4] = {row.x, row.y, row.z, row.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_lo(w[i]);
-                x[2 * i + 1] = bf16_hi(w[i]);
-            }
-            q4_store_row(x, lane, cache + run + (int64_t)h * a.block_size * kQ4RowBytes, a.block_size, o);
+            q4_store_row(row, lane, cache + run + (int64_t)h * a.block_size * kQ4RowBytes, a.block_size, o);
         }
     };
 
