@@ -615,10 +615,14 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos_sin, positions, eps, k_c
         pages, ps, bs, heads = _q4_cache(k_cache, v_cache, dev)
         dim = 256
     else:
-        ps = _check_cache(k_cache, v_cache)
-        pages, bs, heads, dim = k_cache.shape
-        if k_cache.get_device() != dev or v_cache.get_device() != dev:
-            raise ValueError("the caches must be on the current CUDA device")
+        shape = _need(k_cache, "k_cache", _BF16, 4, dev)
+        pages, bs, heads, dim = shape
+        strides = k_cache.stride()
+        ps = strides[0]
+        if _need(v_cache, "v_cache", _BF16, 4, dev) != shape or v_cache.stride() != strides or \
+                strides[1:] != (heads * dim, dim, 1):
+            _check_cache(k_cache, v_cache)  # says what is wrong
+            raise ValueError("k_cache and v_cache must have the same shape and strides")
     if heads != hkv or dim != d:
         raise ValueError("the caches' heads must be k's")
     if q_out is None:
