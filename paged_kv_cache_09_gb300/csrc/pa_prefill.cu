@@ -49,7 +49,6 @@
 //             item's last PV is done, they load O into registers (BF16, normalised),
 //             release O to the next item's PVs, then store the rows to out (a piece of a
 //             split item: fp32 partials to the workspace).
-// (FP16 operands: P in one part, see kHalf below.)
 // TMEM columns: O [0, 256), S [256, 512); P of quarter q: hi at 256+64q, lo at +32.
 //
 // Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT, flags the CTA to
@@ -101,7 +100,9 @@ enum Bar {
     kEpiReady,            // the softmax warps handed an item's row sums to the epilogue
     kDrain,
     kPair,                // [4] the two softmax warps of a lane quarter meet here
-    kNumBars = kPair + 4
+    kSum = kPair + 4,     // [4] FP16 operands only: one group's row sums, to the other
+    kSFull1 = kSum + 4,   // FP16 operands only: the second score buffer
+    kNumBars
 };
 constexpr int kSmemBytes = kOffBars + kNumBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -248,6 +249,11 @@ __device__ __forceinline__ bool item_of(const TcParams<kSeqs, kExt, kHalf> &p, i
     return true;
 }
 
+// The 128-key halves of the item's tiles (FP16 operands), up to its last key block.
+__device__ __forceinline__ int halves_of(const Item &it) {
+    return min(2 * it.je, (it.nblocks + 1) / 2) - 2 * it.jb;
+}
+
 #ifdef PA_TEST_HOOKS
 // Test build only: the K/V ring unit (counted over the CTA's whole run) whose loads the
 // producer leaves out (-1: none), so that the MMA thread's wait for it runs out.  Set by
@@ -257,9 +263,23 @@ __device__ int g_test_skip_unit = -1;
 
 // kHalf: Q, K and V are FP16, each row of Q and each KV head of a sequence scaled by a power
 // of two (the 4-bit cache's prefill makes them so).  With 11 significant bits P needs one
-// part instead of two, so a tile takes 32 MMAs instead of 48, and K and V lose an eighth of
-// what they would in BF16.  P is kept 2^7 times as large (at most 2^15): full precision down
-// to 2^-21 of a row's largest weight.
+// part instead of two, and K and V lose an eighth of what they would in BF16.  P is kept 2^7
+// times as large (at most 2^15): full precision down to 2^-21 of a row's largest weight.
+//
+// One part of P takes a quarter of the score's columns, and an MMA over N = 128 keys takes
+// half the time of one over 256 (64 cycles; a step of 128 keys is 16 + 8 MMAs, 2048 cycles),
+// so the scores are double-buffered in halves of 128 keys: S of half G + 1 is issued before
+// O += P V of half G, and the tensor core works on it while the softmax of G runs.  Softmax
+// warps 2-5 take the even halves of the CTA's run and warps 6-9 the odd ones, whole rows:
+// each reads its scores twice (row max, then weights; 64 columns at a time).  The row's
+// reference passes from group to group through shared memory, once a half, and the group
+// that moves it rescales O after the last half's PV.  P of a half goes out in two 64-key
+// parts.  Measured on 1685 queries over 12288 keys (24 heads, 4 KV heads): 3350 cycles of a
+// group's time per half, 2 x 2700 per pair of halves for the whole kernel; the same softmax
+// on one score buffer (64-key quarters, warp pairs meeting on the max) took 7300 per 256
+// keys.  The two issuing warps' single lanes come from elect.sync: chosen by lane == 0, the
+// compiler cannot see that one lane runs the code, and an MMA took 74 cycles to issue
+// instead of 24, more than it takes to run (508 against 381 us for the case above).
 constexpr float kHalfHeadroom = 7.f;
 
 template <int kSeqs, bool kExt, bool kHalf>
@@ -291,10 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars[kQEmpty], 1);
         mbar_init(&bars[kSFull], 1);
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&bars[kPFull + i], kSoftmaxWarps);  // one elected lane per warp
+            // one elected lane per warp that takes part
+            mbar_init(&bars[kPFull + i], kHalf ? kSoftmaxWarps / 2 : kSoftmaxWarps);
             mbar_init(&bars[kPvDone + i], 1);
-            mbar_init(&bars[kPair + i], 2);
+            mbar_init(&bars[kPair + i], kHalf ? 1 : 2);
+            mbar_init(&bars[kSum + i], 1);
         }
+        mbar_init(&bars[kSFull1], 1);
         mbar_init(&bars[kOEmpty], kEpilogueWarps);
         mbar_init(&bars[kEpiReady], kSoftmaxWarps / 2);  // one warp of each pair
         mbar_init(&bars[kDrain], 1);
@@ -322,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0) {
+        if (kHalf ? elect_one() : lane == 0) {
 #ifdef PA_TEST_HOOKS
             const int skip_unit = *reinterpret_cast<volatile int *>(&g_test_skip_unit);
 #endif
@@ -334,6 +357,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             int q_loads = 0;
             Item it;
             bool stop = false;
+            // FP16 operands: a half's two K units (two 64-dim chunks x 128 keys each) and its
+            // two V units (64 keys x 256 dims), in the order the MMA thread takes them: the
+            // K of half G + 1, of the next item's first half too, comes before the V of G.
+            struct Half {
+                int g, pg[2], of[2], last[2];  // last: the sequence whose cut maps apply, or -1
+            };
+            Half prev;
+            bool held = false;  // prev's V is still to be loaded
+            auto next_slot = [&]() -> int {
+                const int s = u % kRing;
+                if (u >= kRing &&
+                    !mbar_wait_abort(&bars[kRingEmpty + s], ((u / kRing) - 1) & 1, p.err, abort))
+                    return -1;
+                issued |= 1u << s;
+                par = (par & ~(1u << s)) | (((u / kRing) & 1u) << s);
+                mbar_arrive_expect_tx(&bars[kRingFull + s], kUnit);
+                ++u;
+                return s;
+            };
+            auto load_k = [&](const Half &x) -> bool {
+                for (int y = 0; y < 2; ++y) {
+                    const int s = next_slot();
+                    if (s < 0) return false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tma_load_4d(ring + s * kUnit + i * kBlkBytes,
+                                    x.last[i & 1] < 0 ? &maps.k : &maps.k_last[x.last[i & 1]],
+                                    &bars[kRingFull + s], (2 * y + i / 2) * kChunkElems, x.g,
+                                    x.of[i & 1], x.pg[i & 1]);
+                }
+                return true;
+            };
+            auto load_v = [&](const Half &x) -> bool {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int s = next_slot();
+                    if (s < 0) return false;
+                    const CUtensorMap *m = x.last[y] < 0 ? &maps.v : &maps.v_last[x.last[y]];
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        tma_load_4d(ring + s * kUnit + c * kBlkBytes, m, &bars[kRingFull + s],
+                                    c * kChunkElems, x.g, x.of[y], x.pg[y]);
+                }
+                return true;
+            };
             for (int k = 0; !stop && (item_of<kSeqs, kExt, kHalf>(p, k, it)); ++k) {
                 if (k > 0 && !mbar_wait_abort(&bars[kQEmpty], (k - 1) & 1, p.err, abort)) break;
                 ++q_loads;
@@ -344,6 +412,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(qs + c * kQChunk, pk ? &maps.qp[it.qpi] : &maps.q,
                                 &bars[kQFull], c * kChunkElems, it.h, it.q_off + it.r0);
                 const int32_t *bt = p.block_table + (int64_t)it.bt_row * p.bt_stride;
+                if constexpr (kHalf) {
+                    const int nh = halves_of(it);
+                    int lp = 4 * it.jb / p.blocks_per_page;
+                    int in = 4 * it.jb - lp * p.blocks_per_page;
+                    for (int r = 0; r < nh; ++r) {
+                        Half x;
+                        x.g = it.g;
+#pragma unroll
+                        for (int bb = 0; bb < 2; ++bb) {
+                            x.of[bb] = 0;  // a block past the last: zeros, and masked
+                            x.pg[bb] = (int)p.num_pages;
+                            x.last[bb] = -1;
+                            if (4 * it.jb + 2 * r + bb < it.nblocks) {
+                                x.of[bb] = in * kBlk;
+                                x.pg[bb] = bt[lp];
+                                if (x.pg[bb] < 0 || x.pg[bb] >= p.num_pages)
+                                    atomicOr(p.err, kErrPage);
+                                if (lp == it.last_page) x.last[bb] = it.b;
+                            }
+                            if (++in == p.blocks_per_page) {
+                                in = 0;
+                                ++lp;
+                            }
+                        }
+                        if (!load_k(x) || (held && !load_v(prev))) {
+                            stop = true;
+                            break;
+                        }
+                        prev = x;
+                        held = true;
+                    }
+                    continue;
+                }
                 // Page and in-page index of block kb, advanced block by block: a division
                 // per block would take the MUFU, which the softmax warps keep busy (one
                 // per item places the first block of a piece).
@@ -407,6 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            if constexpr (kHalf) {
+                if (held && !stop && *abort == 0) load_v(prev);
+            }
             // Loads always complete, so these waits end; in a normal run every unit and Q
             // tile was consumed and they return at once.
             for (int s = 0; s < kRing; ++s)
@@ -415,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (kHalf ? elect_one() : lane == 0) {
             constexpr uint32_t kIdQK = umma_idesc(kHalf, kBM, kBN, 0, 0);
             constexpr uint32_t kIdPV = umma_idesc(kHalf, kBM, kHeadDim, 0, 1);
             const uint32_t q_addr = smem_u32(qs), ring_addr = smem_u32(ring);
@@ -423,7 +527,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t u = 0, jt = 0;
             Item it;
             bool stop = false;
-            for (int k = 0; !stop && (item_of<kSeqs, kExt, kHalf>(p, k, it)); ++k) {
+            if constexpr (kHalf) {
+                // QK of half G + 1 goes ahead of PV of half G (across items too), so that the
+                // tensor core has the one while the softmax of G makes the other's P.
+                constexpr uint32_t kIdHalf = umma_idesc(true, kBM, kBN / 2, 0, 0);
+                // Descriptors of the buffers' starts: the address is their low field, in units
+                // of 16 bytes, so an offset within shared memory is added to it.
+                const uint64_t q_desc = umma_sdesc_sw128(q_addr);
+                const uint64_t k_desc = umma_sdesc_sw128(ring_addr);
+                const uint64_t v_desc = umma_sdesc_sw128(ring_addr, kBlkBytes);
+                auto qk = [&](uint32_t G, bool last) -> bool {
+                    const uint32_t sb = sbuf + (kBN / 2) * (G & 1);
+                    for (int y = 0; y < 2; ++y, ++u) {
+                        const int s = u % kRing;
+                        if (!mbar_wait_abort(&bars[kRingFull + s], (u / kRing) & 1, p.err, abort))
+                            return false;
+                        tc_fence_after();
+                        const uint64_t dq = q_desc + y * (2 * kQChunk / 16);
+                        const uint64_t dk = k_desc + s * (kUnit / 16);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            umma_ss(sb, dq + ((i / 4) * kQChunk + (i & 3) * 32) / 16,
+                                    dk + ((i / 4) * (kUnit / 2) + (i & 3) * 32) / 16, kIdHalf,
+                                    (y | i) != 0);
+                        umma_commit(&bars[kRingEmpty + s]);
+                    }
+                    if (last) umma_commit(&bars[kQEmpty]);
+                    umma_commit(&bars[(G & 1) ? kSFull1 : kSFull]);
+                    return true;
+                };
+                auto pv = [&](uint32_t G, bool first, int k) -> bool {
+                    const uint32_t sb = sbuf + (kBN / 2) * (G & 1);
+                    for (int y = 0; y < 2; ++y, ++u) {
+                        const int s = u % kRing;
+                        if (!mbar_wait_abort(&bars[kRingFull + s], (u / kRing) & 1, p.err, abort) ||
+                            (first && y == 0 && k > 0 &&
+                             !mbar_wait_abort(&bars[kOEmpty], (k - 1) & 1, p.err, abort)))
+                            return false;
+                        const uint64_t dv = v_desc + s * (kUnit / 16);
+                        const int qq = 2 * (G & 1) + y;
+                        if (!mbar_wait_abort(&bars[kPFull + qq], (G >> 1) & 1, p.err, abort))
+                            return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < kBlk / 16; ++ks)
+                            umma_ts(obuf, sb + 32 * y + 8 * ks, dv + ks * (2048 / 16), kIdPV,
+                                    !first || (y | ks) != 0);
+                        umma_commit(&bars[kRingEmpty + s]);
+                    }
+                    umma_commit(&bars[kPvDone + (G & 1)]);
+                    return true;
+                };
+                uint32_t G = 0;
+                bool more = item_of<kSeqs, kExt, kHalf>(p, 0, it);
+                stop = !more || !mbar_wait_abort(&bars[kQFull], 0, p.err, abort) ||
+                       !qk(0, halves_of(it) == 1);
+                for (int k = 0; more && !stop; ++k) {
+                    const int nh = halves_of(it);
+                    for (int r = 0; r < nh && !stop; ++r, ++G) {
+                        if (r + 1 < nh) {
+                            stop = !qk(G + 1, r + 2 == nh);
+                        } else {
+                            more = item_of<kSeqs, kExt, kHalf>(p, k + 1, it);
+                            if (more)
+                                stop = !mbar_wait_abort(&bars[kQFull], (k + 1) & 1, p.err, abort) ||
+                                       !qk(G + 1, halves_of(it) == 1);
+                        }
+                        if (!stop) stop = !pv(G, r == 0, k);
+                    }
+                }
+            }
+            for (int k = 0; !kHalf && !stop && (item_of<kSeqs, kExt, kHalf>(p, k, it)); ++k) {
                 if (!mbar_wait_abort(&bars[kQFull], k & 1, p.err, abort)) break;
                 tc_fence_after();
                 for (int j = it.jb; j < it.je && !stop; ++j) {
@@ -475,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int ks = 0; ks < kBlk / 16; ++ks) {
                             umma_ts(obuf, phi + 8 * ks, vd[ks], kIdPV, (jr | qq | ks) != 0);
-                            if (!kHalf) umma_ts(obuf, phi + 32 + 8 * ks, vd[ks], kIdPV, 1);
+                            umma_ts(obuf, phi + 32 + 8 * ks, vd[ks], kIdPV, 1);
                         }
                         umma_commit(&bars[kRingEmpty + s]);
                         umma_commit(&bars[kPvDone + qq]);
@@ -498,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hf = (warp - 2) >> 2;
         const int row = lq * 32 + lane;
         const uint32_t lane_off = (uint32_t)(lq * 32) << 16;
-        const uint32_t obase = tmem + lane_off + kColO + 128 * hf;
+        const uint32_t obase = tmem + lane_off + kColO + (kHalf ? 0 : 128 * hf);
         const uint32_t sbase = tmem + lane_off + kColS;
         float *xq = xchg + lq * 128;  // [phase][half][lane]
         // Loop-invariant parameters, read once into registers.
@@ -533,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it.hp > 1) rpos = row / it.hp;
             }
             const int qpos = it.q_start + it.r0 + rpos;
+            float m_used = -CUDART_INF_F, l = 0.f;
             if constexpr (kHalf) {
                 const int rh = it.h + (it.hp > 1 ? row - rpos * it.hp : 0);
                 const float fq =
@@ -541,8 +716,151 @@ __global__ void __launch_bounds__(kThreads, 1)
                         : 1.f;
                 // (never 0, as p.sc: a masked score is -inf and stays that)
                 sc = fmaxf(p.sc * fq * p.f.kv[it.b * p.f.num_kv_heads + it.g].x, FLT_MIN);
+                // Half r of the item is half jt + r of the CTA; those of this group's parity
+                // are its own, whole rows of 128 keys.
+                const int nh = halves_of(it);
+                for (int r = (int)(jt ^ (uint32_t)hf) & 1; r < nh; r += 2) {
+                    const uint32_t G = jt + r;
+                    const int key0 = 2 * kBlk * (2 * it.jb + r);
+                    int lim = it.seq_len_k - key0;  // its valid keys are a prefix
+                    if (causal) lim = min(lim, qpos - key0 + 1);
+                    const bool ragged = !__all_sync(0xffffffffu, lim >= 2 * kBlk);
+                    const uint32_t sb = sbase + 2 * kBlk * hf;
+                    if (!__all_sync(0xffffffffu, mbar_wait_abort(&bars[hf ? kSFull1 : kSFull],
+                                                                 (G >> 1) & 1, p.err, abort))) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    // 64 scores from column 64 * y on: sign of the scale, mask.
+                    uint32_t s0[32], s1[32];
+                    auto scores = [&](int y) {
+                        tmem_ld32(sb + kBlk * y, s0);
+                        tmem_ld32(sb + kBlk * y + 32, s1);
+                        tc_wait_ld();
+                        if (neg) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                s0[i] ^= 0x80000000u;
+                                s1[i] ^= 0x80000000u;
+                            }
+                        }
+                        if (ragged) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                s0[i] = kBlk * y + i < lim ? s0[i] : 0xff800000u;
+                                s1[i] = kBlk * y + 32 + i < lim ? s1[i] : 0xff800000u;
+                            }
+                        }
+                    };
+                    float mp[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y) {
+                        scores(y);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            mp[i & 3] = fmax3(mp[i & 3], __uint_as_float(s0[i]),
+                                              __uint_as_float(s1[i]));
+                    }
+                    const float mx =
+                        fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sc;
+                    // The row's reference as the other group left it, and this half's move.
+                    float m_prev = -CUDART_INF_F;
+                    if (r > 0) {
+                        if (!__all_sync(0xffffffffu,
+                                        mbar_wait_abort(pair, (G - 1) & 1, p.err, abort))) {
+                            stop = true;
+                            break;
+                        }
+                        m_prev = xq[(hf ^ 1) * 32 + lane];
+                    }
+                    const float m_new = fmaxf(m_prev, mx);
+                    const bool need = m_new > m_prev + 8.f;  // also for the first finite max
+                    const float m = need ? m_new : m_prev;
+                    xq[hf * 32 + lane] = m;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pair);
+                    if (m != m_used) l *= ex2_approx(m_used - m);
+                    m_used = m;
+                    const float nmu = m == -CUDART_INF_F ? 0.f : kHalfHeadroom - m;
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y) {
+                        scores(y);
+                        float sa[2] = {0.f, 0.f}, sc2[2] = {0.f, 0.f};
+                        uint32_t pk[16];
+                        auto weights = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float e0, e1;
+                                fma2_bc(e0, e1, __uint_as_float(x[2 * i]),
+                                        __uint_as_float(x[2 * i + 1]), sc, nmu);
+                                const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+                                add2(sa[i & 1], sc2[i & 1], sa[i & 1], sc2[i & 1], p0, p1);
+                                pk[i] = pack_f16x2(p0, p1);
+                            }
+                        };
+                        weights(s0);
+                        tmem_st16(sb + 32 * y, pk);
+                        weights(s1);
+                        tmem_st16(sb + 32 * y + 16, pk);
+                        l += (sa[0] + sc2[0]) + (sa[1] + sc2[1]);
+                        // The reference moved: rescale the row of O, once the PVs up to the
+                        // last half's are done (its barrier cannot run two phases ahead:
+                        // PV G + 1 waits for this half's weights).
+                        if (y == 0 && r > 0 && __any_sync(0xffffffffu, need)) {
+                            if (!__all_sync(
+                                    0xffffffffu,
+                                    mbar_wait_abort(&bars[kPvDone + (hf ^ 1)],
+                                                    ((G - 1) >> 1) & 1, p.err, abort))) {
+                                stop = true;
+                                break;
+                            }
+                            tc_fence_after();
+                            const float alpha = need ? ex2_approx(m_prev - m) : 1.f;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(obase + 32 * c, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                tmem_st32(obase + 32 * c, o);
+                            }
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[kPFull + 2 * hf + y]);
+                    }
+                    if (stop) break;
+                }
+                if (stop) break;
+                // The group with the last half writes the row sum; the other brings its part
+                // to the final reference and hands it over.  The sums of the item before
+                // have been read once its O was released.
+                jt += nh;
+                bool ok = true;
+                if (((jt - 1) & 1) != (uint32_t)hf) {
+                    ok = mbar_wait_abort(pair, (jt - 1) & 1, p.err, abort);
+                    const float m = xq[(hf ^ 1) * 32 + lane];
+                    if (m != m_used) l *= ex2_approx(m_used - m);
+                    xq[64 + lane] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kSum + lq]);
+                } else {
+                    ok = mbar_wait_abort(&bars[kSum + lq], k & 1, p.err, abort) &&
+                         (k == 0 || mbar_wait_abort(&bars[kOEmpty], (k - 1) & 1, p.err, abort));
+                    const float lt = l + xq[64 + lane];
+                    rowsum[row] = lt;
+                    if (kExt && it.slot >= 0 && rpos < it.rows)
+                        p.ws_ml[(int64_t)it.slot * kBM + row] = make_float2(m_used, lt);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kEpiReady]);
+                }
+                if (!__all_sync(0xffffffffu, ok)) break;
+                continue;
             }
-            float m_used = -CUDART_INF_F, l = 0.f;
             // First token of block kb = 4j + qq and its in-page index, advanced quarter by
             // quarter (no division: it would wait behind the partner warp's exps on the MUFU).
             int blk_in = 0, blk_tok0 = 0;
@@ -618,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float nmu = m_used == -CUDART_INF_F
                                           ? 0.f
-                                          : (kHalf ? kHalfHeadroom - m_used : -m_used);
+                                          : -m_used;
                     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
                     uint32_t hi[16], lo[16];
 #pragma unroll
@@ -627,17 +945,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fma2_bc(e0, e1, x[2 * i], x[2 * i + 1], sc, nmu);
                         const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
                         add2(sa[i & 3], sb[i & 3], sa[i & 3], sb[i & 3], p0, p1);
-                        if constexpr (kHalf) {
-                            hi[i] = pack_f16x2(p0, p1);
-                        } else {
-                            hi[i] = pack_bf16x2(p0, p1);
-                            float r0, r1;
-                            sub2(r0, r1, p0, p1, bf16_lo(hi[i]), bf16_hi(hi[i]));
-                            lo[i] = pack_bf16x2(r0, r1);
-                        }
+                        hi[i] = pack_bf16x2(p0, p1);
+                        float r0, r1;
+                        sub2(r0, r1, p0, p1, bf16_lo(hi[i]), bf16_hi(hi[i]));
+                        lo[i] = pack_bf16x2(r0, r1);
                     }
                     tmem_st16(sbase + 64 * qq + 16 * hf, hi);
-                    if constexpr (!kHalf) tmem_st16(sbase + 64 * qq + 32 + 16 * hf, lo);
+                    tmem_st16(sbase + 64 * qq + 32 + 16 * hf, lo);
                     l += ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
                     // Moving the running max rescales this row of O (this warp's half of the
                     // columns), which the PVs of the tile's earlier quarters may still be
@@ -707,10 +1021,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t jt = 0;
         Item it;
         for (int k = 0; item_of<kSeqs, kExt, kHalf>(p, k, it); ++k) {
+            // its last PV: of its last tile's last quarter, or of its last half
+            const int steps = kHalf ? halves_of(it) : it.je - it.jb;
+            const uint32_t end = jt + steps - 1;
             if (!__all_sync(0xffffffffu,
                             mbar_wait_abort(&bars[kEpiReady], k & 1, p.err, abort) &&
-                                mbar_wait_abort(&bars[kPvDone + 3],
-                                                (jt + (it.je - it.jb) - 1) & 1, p.err, abort)))
+                                (kHalf ? mbar_wait_abort(&bars[kPvDone + (end & 1)], (end >> 1) & 1,
+                                                         p.err, abort)
+                                       : mbar_wait_abort(&bars[kPvDone + 3], end & 1, p.err,
+                                                         abort))))
                 break;
             tc_fence_after();
             const float lt = rowsum[row];
@@ -778,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             b[4 * q4 + 3]);
                 }
             }
-            jt += it.je - it.jb;
+            jt += steps;
         }
     }
 
