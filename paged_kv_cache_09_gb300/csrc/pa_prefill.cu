@@ -271,15 +271,17 @@ __device__ int g_test_skip_unit = -1;
 // so the scores are double-buffered in halves of 128 keys: S of half G + 1 is issued before
 // O += P V of half G, and the tensor core works on it while the softmax of G runs.  Softmax
 // warps 2-5 take the even halves of the CTA's run and warps 6-9 the odd ones, whole rows:
-// each reads its scores twice (row max, then weights; 64 columns at a time).  The row's
-// reference passes from group to group through shared memory, once a half, and the group
-// that moves it rescales O after the last half's PV.  P of a half goes out in two 64-key
-// parts.  Measured on 1685 queries over 12288 keys (24 heads, 4 KV heads): 3350 cycles of a
-// group's time per half, 2 x 2700 per pair of halves for the whole kernel; the same softmax
-// on one score buffer (64-key quarters, warp pairs meeting on the max) took 7300 per 256
-// keys.  The two issuing warps' single lanes come from elect.sync: chosen by lane == 0, the
-// compiler cannot see that one lane runs the code, and an MMA took 74 cycles to issue
-// instead of 24, more than it takes to run (508 against 381 us for the case above).
+// each reads its first 64 scores and its last 64 for the row's max, makes P of the last ones,
+// which are still in registers, and reads the first ones again for theirs; each 64-key part
+// goes to the tensor core at once.  The row's reference passes from group to group through
+// shared memory, once a half, and the group that moves it rescales O after the last half's
+// PV.  The time of a half is half of: its softmax up to the second part, that part's PV and
+// the next S in the same buffer.  Measured on 1685 queries over 12288 keys (24 heads, 4 KV
+// heads) with the kernels around it: 355 us, 1.53 PFLOP/s; the same softmax on one score
+// buffer (64-key quarters, warp pairs meeting on the max) took 548.  The two issuing warps'
+// single lanes come from elect.sync: chosen by lane == 0, the compiler does not see that one
+// lane runs the code, and an MMA took 74 cycles to issue instead of 24, more than it takes
+// to run (508 against 381 us, before the steps that led to 355).
 constexpr float kHalfHeadroom = 7.f;
 
 template <int kSeqs, bool kExt, bool kHalf>
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto load_v = [&](const Half &x) -> bool {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
+                for (int y = 1; y >= 0; --y) {
                     const int s = next_slot();
                     if (s < 0) return false;
                     const CUtensorMap *m = x.last[y] < 0 ? &maps.v : &maps.v_last[x.last[y]];
@@ -558,10 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 auto pv = [&](uint32_t G, bool first, int k) -> bool {
                     const uint32_t sb = sbuf + (kBN / 2) * (G & 1);
-                    for (int y = 0; y < 2; ++y, ++u) {
+                    for (int y = 1; y >= 0; --y, ++u) {  // keys 64.. 127 come first
                         const int s = u % kRing;
                         if (!mbar_wait_abort(&bars[kRingFull + s], (u / kRing) & 1, p.err, abort) ||
-                            (first && y == 0 && k > 0 &&
+                            (first && y == 1 && k > 0 &&
                              !mbar_wait_abort(&bars[kOEmpty], (k - 1) & 1, p.err, abort)))
                             return false;
                         const uint64_t dv = v_desc + s * (kUnit / 16);
@@ -571,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 0; ks < kBlk / 16; ++ks)
-                            umma_ts(obuf, sb + 32 * y + 8 * ks, dv + ks * (2048 / 16), kIdPV,
-                                    !first || (y | ks) != 0);
+                            umma_ts(obuf, sb + kBlk * y + 8 * ks, dv + ks * (2048 / 16), kIdPV,
+                                    !first || y == 0 || ks != 0);
                         umma_commit(&bars[kRingEmpty + s]);
                     }
                     umma_commit(&bars[kPvDone + (G & 1)]);
@@ -732,11 +734,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    // 64 scores from column 64 * y on: sign of the scale, mask.
+                    // 64 scores from column 64 * y on: loaded; sign of the scale and mask.
                     uint32_t s0[32], s1[32];
-                    auto scores = [&](int y) {
+                    auto load = [&](int y) {
                         tmem_ld32(sb + kBlk * y, s0);
                         tmem_ld32(sb + kBlk * y + 32, s1);
+                    };
+                    auto finish = [&](int y) {
                         tc_wait_ld();
                         if (neg) {
 #pragma unroll
@@ -753,27 +757,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     };
-                    float mp[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll 1
-                    for (int y = 0; y < 2; ++y) {
-                        scores(y);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            mp[i & 3] = fmax3(mp[i & 3], __uint_as_float(s0[i]),
-                                              __uint_as_float(s1[i]));
-                    }
-                    const float mx =
-                        fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sc;
-                    // The row's reference as the other group left it, and this half's move.
+                    load(0);
+                    // The row's reference as the other group left it.
                     float m_prev = -CUDART_INF_F;
                     if (r > 0) {
                         if (!__all_sync(0xffffffffu,
-                                        mbar_wait_abort(pair, (G - 1) & 1, p.err, abort))) {
+                                        mbar_wait_abort(pair, (G - 1) & 1, p.err, abort)))
                             stop = true;
-                            break;
-                        }
                         m_prev = xq[(hf ^ 1) * 32 + lane];
                     }
+                    finish(0);
+                    if (stop) break;
+                    float mp[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mp[i] = fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i]));
+#pragma unroll
+                    for (int i = 4; i < 32; ++i)
+                        mp[i & 3] = fmax3(mp[i & 3], __uint_as_float(s0[i]),
+                                          __uint_as_float(s1[i]));
+                    load(1);
+                    finish(1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        mp[i & 3] = fmax3(mp[i & 3], __uint_as_float(s0[i]),
+                                          __uint_as_float(s1[i]));
+                    const float mx =
+                        fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sc;
                     const float m_new = fmaxf(m_prev, mx);
                     const bool need = m_new > m_prev + 8.f;  // also for the first finite max
                     const float m = need ? m_new : m_prev;
@@ -783,12 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (m != m_used) l *= ex2_approx(m_used - m);
                     m_used = m;
                     const float nmu = m == -CUDART_INF_F ? 0.f : kHalfHeadroom - m;
-#pragma unroll 1
-                    for (int y = 0; y < 2; ++y) {
-                        scores(y);
+                    // The weights of the 64 scores at hand: P over the first half of their
+                    // columns, and their sum.
+                    auto weights = [&](int y) {
                         float sa[2] = {0.f, 0.f}, sc2[2] = {0.f, 0.f};
                         uint32_t pk[16];
-                        auto weights = [&](const uint32_t (&x)[32]) {
+                        auto part = [&](const uint32_t (&x)[32]) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 float e0, e1;
@@ -799,41 +809,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pk[i] = pack_f16x2(p0, p1);
                             }
                         };
-                        weights(s0);
-                        tmem_st16(sb + 32 * y, pk);
-                        weights(s1);
-                        tmem_st16(sb + 32 * y + 16, pk);
+                        part(s0);
+                        tmem_st16(sb + kBlk * y, pk);
+                        part(s1);
+                        tmem_st16(sb + kBlk * y + 16, pk);
                         l += (sa[0] + sc2[0]) + (sa[1] + sc2[1]);
-                        // The reference moved: rescale the row of O, once the PVs up to the
-                        // last half's are done (its barrier cannot run two phases ahead:
-                        // PV G + 1 waits for this half's weights).
-                        if (y == 0 && r > 0 && __any_sync(0xffffffffu, need)) {
-                            if (!__all_sync(
-                                    0xffffffffu,
-                                    mbar_wait_abort(&bars[kPvDone + (hf ^ 1)],
-                                                    ((G - 1) >> 1) & 1, p.err, abort))) {
-                                stop = true;
-                                break;
-                            }
-                            tc_fence_after();
-                            const float alpha = need ? ex2_approx(m_prev - m) : 1.f;
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(obase + 32 * c, o);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                                tmem_st32(obase + 32 * c, o);
-                            }
-                        }
+                    };
+                    auto hand_over = [&](int y) {
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars[kPFull + 2 * hf + y]);
+                    };
+                    weights(1);  // still in registers
+                    // The reference moved: rescale the row of O, once the PVs up to the last
+                    // half's are done (its barrier cannot run two phases ahead: PV G + 1
+                    // waits for this half's weights).
+                    if (r > 0 && __any_sync(0xffffffffu, need)) {
+                        if (!__all_sync(0xffffffffu,
+                                        mbar_wait_abort(&bars[kPvDone + (hf ^ 1)],
+                                                        ((G - 1) >> 1) & 1, p.err, abort))) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float alpha = need ? ex2_approx(m_prev - m) : 1.f;
+#pragma unroll 1
+                        for (int c = 0; c < kHeadDim; c += 64) {
+                            tmem_ld32(obase + c, s0);
+                            tmem_ld32(obase + c + 32, s1);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                s0[i] = __float_as_uint(__uint_as_float(s0[i]) * alpha);
+                                s1[i] = __float_as_uint(__uint_as_float(s1[i]) * alpha);
+                            }
+                            tmem_st32(obase + c, s0);
+                            tmem_st32(obase + c + 32, s1);
+                        }
                     }
-                    if (stop) break;
+                    load(0);
+                    hand_over(1);
+                    finish(0);
+                    weights(0);
+                    hand_over(0);
                 }
                 if (stop) break;
                 // The group with the last half writes the row sum; the other brings its part
