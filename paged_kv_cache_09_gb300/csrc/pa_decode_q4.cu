@@ -33,6 +33,11 @@
 //
 // Work split: the tiles of all (sequence, KV head) pairs in a row, cut evenly over two CTAs an
 // SM, so that uneven lengths leave no SM idle; each CTA finds its share from the lengths.  A pair
+// also costs its beginning (table, q, the first loads' way, the merge): it counts as kPairCost
+// tiles, half a share at most, ahead of the pair's first, so that CTAs with many short pairs get
+// fewer tiles (64 sequences of 1..2048 keys, 8 KV heads: 62 us without it, 53.5, 46, 42 and 44 us
+// with 4, 8, 16 and 28).  Shares below two rounds of the warps' tiles stay even: there a CTA's
+// time is its rounds (one sequence of 1701 keys, shares of 8).  A pair
 // that one CTA holds whole is finished there; the others leave a part per CTA (sums relative to
 // their reference), which a second kernel merges.
 // Within a CTA each warp streams pairs of 16-token tiles of its own (every kW-th pair) through a
@@ -71,6 +76,7 @@ constexpr int kOffQ = kOffMl + kW * kDecMaxGroup * 8, kOffBars = kOffQ + 9 * 512
 constexpr int kSmem = kOffBars + kW * kDepth * 16 + 16;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 constexpr int kMinShare = 2 * kW;                     // tiles of the smallest share
+constexpr int kPairCost = 16;                         // of beginning a pair, in tiles
 constexpr float kHeadroom = 7.f, kLag = 8.f;          // log2 units: p s <= 2^(kHeadroom + kLag)
 
 // Division of n < 2^31 by a constant of the launch.
@@ -210,25 +216,32 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     // g of sequence seq (every warp finds the same)
     const int tpp = p.tiles_per_page;
     Shares shares;
-    uint32_t at, end;  // the next tile of all, and the share's end
+    uint32_t at, end;  // the next place in the row of all pairs, and the share's end
+    // Places before each pair's tiles, and the segment's first place in its pair.
+    int lead, v0;
     int seq, g, t0, seq_len, tiles;
     // Finds them, with the tiles and lengths of the first 32 sequences given; false: no share.
     auto place = [&](int first_tiles, int first_len) {
-        uint64_t all = 0;
+        uint64_t all = 0, used = 0;
         for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
             int len;
             uint64_t t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, blockIdx.x == 0 && warp == 0);
+            used += __popc(__ballot_sync(0xffffffffu, t > 0));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
             all += t;
         }
         all *= p.num_kv_heads;
+        const uint32_t ctas = (uint32_t)min((uint64_t)gridDim.x, (all + kMinShare - 1) / kMinShare);
+        lead = 0;
+        if (all >= 2 * kMinShare * (uint64_t)ctas)
+            lead = (int)min((uint32_t)kPairCost, (uint32_t)min(all, (uint64_t)0xffffffffu) / (2 * ctas));
+        all += lead * used * p.num_kv_heads;
         if (all > 0x7fffffffu) {  // (as many tiles as 600 GB of cache hold, counting shared pages again)
             if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
             return false;
         }
         const uint32_t total = (uint32_t)all;
-        const uint32_t ctas = min(gridDim.x, (total + kMinShare - 1) / kMinShare);
         if (blockIdx.x >= ctas) return false;
         shares.q = total / ctas;
         shares.r = total - shares.q * ctas;
@@ -238,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
             int len = first_len;
             const int t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, false);
-            uint32_t sum = t;
+            const uint32_t span = t > 0 ? t + lead : 0;  // a pair's places
+            uint32_t sum = span;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const uint32_t o = __shfl_up_sync(0xffffffffu, sum, d);
@@ -250,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                 seq = s0 + l;
                 seq_len = __shfl_sync(0xffffffffu, len, l);
                 tiles = __shfl_sync(0xffffffffu, t, l);
-                const uint32_t rem = at - (before + __shfl_sync(0xffffffffu, sum - t, l)) * p.num_kv_heads;
-                g = (int)(rem / (uint32_t)tiles);
-                t0 = (int)(rem - (uint32_t)g * tiles);
+                const uint32_t rem = at - (before + __shfl_sync(0xffffffffu, sum - span, l)) * p.num_kv_heads;
+                g = (int)(rem / (uint32_t)(tiles + lead));
+                v0 = (int)(rem - (uint32_t)g * (tiles + lead));
                 return true;
             }
             before += __shfl_sync(0xffffffffu, sum, 31);
@@ -273,9 +287,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     uint32_t it = 0;  // the warp's steps: slots and phases go on from segment to segment
     bool gave_up;  // a wait ran out: this and the CTA's remaining segments contribute nothing
 
-    // Starts a segment: tiles [t0, t1) of KV head g of sequence seq.
+    // Starts a segment: tiles [t0, t1) of KV head g of sequence seq, at least one.
     auto begin_segment = [&]() {
-        t1 = (int)min((uint32_t)tiles, t0 + (end - at));
+        t0 = max(0, v0 - lead);
+        t1 = (int)min((uint32_t)tiles, v0 + (end - at) - lead);
         n = !*abort && t0 + 2 * warp < t1 ? (t1 - t0 - 2 * warp + 2 * kW - 1) / (2 * kW) : 0;
         bt = p.block_table + (int64_t)seq * p.bt_stride;
         j_in = t0 + 2 * warp + l_tile;  // this lane's next tile
@@ -597,12 +612,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         const int64_t pair = (int64_t)seq * p.num_kv_heads + g, part = blockIdx.x + pair;
         const bool whole = t0 == 0 && t1 == tiles;
         if (threadIdx.x == 0 && t0 == 0)
-            p.info[pair] = make_int2((int)part, whole ? 0 : (int)(shares.owner(at + tiles - 1) - blockIdx.x) + 1);
+            p.info[pair] = make_int2((int)part, whole ? 0 : (int)(shares.owner(at - v0 + lead + tiles - 1) - blockIdx.x) + 1);
         uint16_t *out_rows = p.out + ((int64_t)seq * p.num_q_heads + g * p.group) * kHeadDim;
-        at += t1 - t0;
-        const bool more = at < end;
+        at += lead + t1 - v0;
+        const bool more = end > at + lead;  // (a share that ends before the next pair's first tile is done)
         if (more) {
-            t0 = 0;
+            v0 = 0;
             if (++g == p.num_kv_heads) {
                 g = 0;
                 do tiles = seq_tiles(p, ++seq, &seq_len, false);
