@@ -176,6 +176,20 @@ def test_decode_matches_plain(cuda_lib, bs, hq, hkv, lens):
     assert pa.device_errors() == 0
 
 
+# Shares long enough that a pair's beginning counts (16 tiles and more a CTA): many pairs a CTA,
+# empty and one-token sequences between them, and a few pairs that many CTAs share.
+@pytest.mark.parametrize("bs,hq,hkv,lens", [
+    (16, 16, 8, [(i * 389) % 601 for i in range(33)] + [0, 0, 1, 1, 2, 0, 599, 0]),
+    (48, 8, 8, [(i * 577) % 1201 for i in range(34)] + [1, 0]),
+    (64, 16, 4, [0, 20001, 0]),
+    (832, 8, 2, [15000, 1, 30000, 33]),
+])
+def test_decode_long_shares(cuda_lib, bs, hq, hkv, lens):
+    c = _case(cuda_lib, lens, bs, hq, hkv, seed=bs)
+    _check_decode(_decode(cuda_lib, c), c)
+    assert cuda_lib.device_errors() == 0
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
 def test_decode_scales(cuda_lib, scale):
     c = _case(cuda_lib, [300, 17], 64, 6, 1, seed=9)
@@ -376,6 +390,38 @@ def test_prefill_split_items_and_less_workspace(cuda_lib):
     with pytest.raises(pa.PAError):
         pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], 8940, True, 0.0625,
                             workspace=torch.empty(9000 * 4 * 1024, dtype=torch.uint8, device="cuda"))
+    assert pa.device_errors() == 0
+
+
+def test_prefill_many_short_items_a_cta(cuda_lib):
+    # Several items a CTA, of one, two and three 128-key halves each, so that items begin on
+    # either parity; chunk lengths at and around a query tile's rows.
+    pa = cuda_lib
+    rows = [1, 127, 128, 129, 130, 2, 64, 200, 16, 17, 96, 128] * 2
+    lens = [r + 61 * (i % 5) for i, r in enumerate(rows)]
+    cu = [0] + np.cumsum(rows).tolist()
+    c = _case(pa, lens, 16, 32, 8, seed=50, rows=cu[-1])
+    out = pa.prefill_varlen_q4(c["q"], c["kc"], c["vc"], c["bt"], cu, lens, True, 0.0625)
+    _check_prefill(out, c, cu, lens)
+    assert torch.equal(out, pa.prefill_varlen_q4(c["q"], c["kc"], c["vc"], c["bt"], cu, lens, True, 0.0625))
+    assert pa.device_errors() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0625, 0.0625])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_scores_that_grow_along_the_keys(cuda_lib, scale, causal):
+    # Keys up to 16 times as long at the end as at the start: the row's reference moves again
+    # and again, in both directions of the scores, and rows end in any half.
+    pa = cuda_lib
+    n, rows = 1500, 400
+    c = _case(pa, [n], 64, 8, 2, seed=51, rows=rows)
+    k = torch.randn(n, 2, 256, device="cuda") * torch.linspace(1, 16, n, device="cuda")[:, None, None]
+    v = torch.randn(n, 2, 256, device="cuda") + 3
+    pa.reshape_and_cache_q4(k.to(torch.bfloat16), v.to(torch.bfloat16), c["kc"], c["vc"], c["slots"])
+    out = pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], n - rows, causal, scale)
+    ref, tol = _q4.prefill(_q4.f64(c["q"]), c["kc"].cpu().numpy(), c["vc"].cpu().numpy(), 64,
+                           c["table"], [0, rows], [n], causal, scale)
+    assert (np.abs(_q4.f64(out) - ref) <= tol).all()
     assert pa.device_errors() == 0
 
 
