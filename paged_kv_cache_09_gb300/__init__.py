@@ -494,10 +494,14 @@ def _need(t, name, dtype, ndim, dev):
 
 def _vector(t, name, dtype, n, dev):
     """Checks a contiguous vector of n entries (any number for None); returns its address."""
-    shape = _need(t, name, dtype, 1, dev)
-    if (n is not None and shape[0] != n) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and have {n} entries")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.is_contiguous() and \
+                (n is None or t.numel() == n):
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _need(t, name, dtype, 1, dev)
+    raise ValueError(f"{name} must be contiguous" + (f" and have {n} entries" if n is not None else ""))
 
 
 def _table(t, name, rows, dev):
@@ -516,6 +520,10 @@ def _token_rows(t, name, tokens, heads, dim, dev):
     shape = _need(t, name, _BF16, 3, dev)
     if shape != (tokens, heads, dim):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {tuple(shape)}")
+    return _row_stride(t, name, tokens, heads, dim)
+
+
+def _row_stride(t, name, tokens, heads, dim):
     a, b, c = t.stride()
     if (c != 1 and dim > 1) or (b != dim and heads > 1):
         raise ValueError(f"{name}: each token's rows must be contiguous")
@@ -534,8 +542,8 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     G, T = len(block_tables), int(num_tokens)
     if len(block_sizes) != G or len(free_pages) != G or not 1 <= G <= 8:
         raise ValueError("one block size and one free list per group, 1..8 groups")
-    S = _need(num_computed, "num_computed", _I32, 1, dev)[0]
-    computed = _vector(num_computed, "num_computed", _I32, S, dev)
+    computed = _vector(num_computed, "num_computed", _I32, None, dev)
+    S = num_computed.shape[0]
     new = _vector(num_new, "num_new", _I32, S, dev)
     widths, strides = zip(*[_table(t, "block_table", S, dev) for t in block_tables])
     free = [_vector(f, "free_pages", _I32, None, dev) for f in free_pages]
@@ -569,8 +577,10 @@ def _rope_args(q, k, q_weight, k_weight, cos_sin, positions, dev):
     """(tokens, query heads, KV heads, head_dim, token strides of q and k, the addresses of the
     weights, the table's sizes, the address of the positions)"""
     T, hq, d = _need(q, "q", _BF16, 3, dev)
-    hkv = _need(k, "k", _BF16, 3, dev)[1]
-    qs, ks = _token_rows(q, "q", T, hq, d, dev), _token_rows(k, "k", T, hkv, d, dev)
+    kt, hkv, kd = _need(k, "k", _BF16, 3, dev)
+    if kt != T or kd != d:
+        raise ValueError(f"k must be [{T}, {hkv}, {d}], got [{kt}, {hkv}, {kd}]")
+    qs, ks = _row_stride(q, "q", T, hq, d), _row_stride(k, "k", T, hkv, d)
     rows, rot = _need(cos_sin, "cos_sin", _F32, 2, dev)
     if not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous")
@@ -592,11 +602,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved=
         q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
     if k_out is None:
         k_out = torch.empty((T, hkv, d), dtype=_BF16, device=k.device)
+    qos = _token_rows(q_out, "q_out", T, hq, d, dev)
+    kos = _token_rows(k_out, "k_out", T, hkv, d, dev)
     _raise(lib.pa_qk_norm_rope(
         q.data_ptr(), qs, k.data_ptr(), ks, qw, kw, float(weight_bias), float(eps),
         cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, pos, T, hq, hkv, d,
-        q_out.data_ptr(), _token_rows(q_out, "q_out", T, hq, d, dev), k_out.data_ptr(),
-        _token_rows(k_out, "k_out", T, hkv, d, dev), _stream()), "pa_qk_norm_rope")
+        q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream()), "pa_qk_norm_rope")
     return q_out, k_out
 
 
@@ -662,12 +673,23 @@ def reshape_and_cache_q4(key, value, k_cache, v_cache, slot_mapping):
     """Quantise key/value [T, Hkv, 256] into the 4-bit caches at slot_mapping (in place)."""
     lib, dev = _lib or load(), _device()
     pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
-    T = _need(key, "key", _BF16, 3, dev)[0]
+    T, heads, dim = _need(key, "key", _BF16, 3, dev)
+    if heads != hkv or dim != 256:
+        raise ValueError(f"key must be [{T}, {hkv}, 256], got [{T}, {heads}, {dim}]")
+    ks = _row_stride(key, "key", T, hkv, 256)
+    vs = _token_rows(value, "value", T, hkv, 256, dev)
     _raise(lib.pa_reshape_and_cache_q4(
-        key.data_ptr(), _token_rows(key, "key", T, hkv, 256, dev), value.data_ptr(),
-        _token_rows(value, "value", T, hkv, 256, dev), k_cache.data_ptr(), v_cache.data_ptr(), ps,
+        key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), ps,
         pages, _vector(slot_mapping, "slot_mapping", _I64, T, dev), T, hkv, 256, bs, _stream()),
         "pa_reshape_and_cache_q4")
+
+
+def _gather_out(t, name, tokens, heads, like, dev):
+    if t is None:
+        return torch.empty((tokens, heads, 256), dtype=_BF16, device=like.device)
+    if _need(t, name, _BF16, 3, dev) != (tokens, heads, 256) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [T, Hkv, 256] tensor")
+    return t
 
 
 def gather_cache_q4(k_cache, v_cache, slot_mapping, k_out=None, v_out=None):
@@ -677,13 +699,8 @@ def gather_cache_q4(k_cache, v_cache, slot_mapping, k_out=None, v_out=None):
     pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
     slots = _vector(slot_mapping, "slot_mapping", _I64, None, dev)
     T = slot_mapping.shape[0]
-    if k_out is None:
-        k_out = torch.empty((T, hkv, 256), dtype=_BF16, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty((T, hkv, 256), dtype=_BF16, device=k_cache.device)
-    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        if _need(t, nm, _BF16, 3, dev) != (T, hkv, 256) or not t.is_contiguous():
-            raise ValueError(f"{nm} must be a contiguous [T, Hkv, 256] tensor")
+    k_out = _gather_out(k_out, "k_out", T, hkv, k_cache, dev)
+    v_out = _gather_out(v_out, "v_out", T, hkv, v_cache, dev)
     _raise(lib.pa_gather_cache_q4(k_cache.data_ptr(), v_cache.data_ptr(), ps, pages, slots, T, hkv,
                                   256, bs, k_out.data_ptr(), v_out.data_ptr(), _stream()),
            "pa_gather_cache_q4")
