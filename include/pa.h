@@ -439,11 +439,12 @@ int pa_qk_norm_rope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, 
  * holds a NaN or an infinity (or spans more than fp32 does) reads back as NaN.
  *
  * K and V caches are separate arrays of pages, page_stride bytes apart (a multiple of 16,
- * at least num_kv_heads * block_size * PA_Q4_ROW_BYTES); block_size is at most 2^20.  A page holds for each KV head
- * first its tokens' codes, 128 bytes each, then their pairs (s, lo of group 0, s, lo of
- * group 1, ...), 16 bytes each.  Dim 64g + 8u + j of the token at offset o of its page is
- * in byte o * 128 + (u ^ (o % 8)) * 16 + 4g + j / 2 of the head's bytes, in the lower half
- * for even j.  Block tables, slots and errors are those of the BF16 cache.
+ * at least num_kv_heads * block_size * PA_Q4_ROW_BYTES); block_size is at most 2^20.  A
+ * page holds for each KV head first its tokens' codes, 128 bytes each, then their pairs (s,
+ * lo of group 0, s, lo of group 1, ...), 16 bytes each.  Dim 64g + 8u + j of the token at
+ * offset o of its page is in byte o * 128 + (u ^ (o % 8)) * 16 + 4g + j / 2 of the head's
+ * bytes, in the lower half for even j.  Block tables, slots and errors are those of the BF16
+ * cache.
  */
 #define PA_Q4_ROW_BYTES 144
 
@@ -476,7 +477,10 @@ int pa_gather_cache_q4(const void *k_cache, const void *v_cache, int64_t page_st
  * of pa_decode (without the fused write and with out on the device), but: page_stride is in
  * bytes; seq_lens[s] may be 0, a padding entry, whose rows of out become zeros; the
  * workspace is sized by pa_decode_q4_workspace_size.  A page outside the pool sets
- * PA_DEVERR_PAGE and its tokens read as zeros.  Steps of V count as at most 2^80.
+ * PA_DEVERR_PAGE and its tokens read as zeros.  Steps of V count as at most 2^80; |scale * q|
+ * of 2^116 and more is not representable and gives NaN.  Lengths that come to more than 2^31
+ * tiles of 16 tokens over all sequences and KV heads set PA_DEVERR_SEQLEN, and out is not
+ * written.
  */
 size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                    int block_size, int max_seq_len);
@@ -489,14 +493,17 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
 
 /*
  * pa_prefill_chunk_q4, pa_prefill_varlen_q4 -- pa_prefill_chunk and pa_prefill_varlen over
- * the 4-bit cache (the chunk's own tokens included, which must be in it).  The sequences are
- * and the queries are first expanded into FP16 in the workspace (each query row and each KV
- * head of a sequence scaled by a power of two: values are rounded to 2^-12, an eighth of
- * BF16's step), which the prefill kernel then reads as pages.  The expansion is linear in the
- * keys, the attention quadratic.  Arguments and errors are those of the BF16 calls, but: page_stride is in bytes, and the
- * workspace is required.  With the bytes that the size functions give (1 KB per key and KV
- * head, 0.5 KB per query row and head, and room for split items) items may be split; with
- * less than the expansion needs the call is refused (PA_ERR_INVALID_ARG).
+ * the 4-bit cache (the chunk's own tokens included, which must be in it).  The sequences'
+ * keys and values and the queries are first expanded into FP16 in the workspace (each query
+ * row and each KV head of a sequence scaled by a power of two: values are rounded to 2^-12,
+ * an eighth of BF16's step), which the prefill kernel then reads as pages.  The expansion is
+ * linear in the keys, the attention quadratic.  Arguments and errors are those of the BF16
+ * calls, but: page_stride is in bytes, and the workspace is required.  With the bytes that
+ * the size functions give (1 KB per key and KV head, 0.5 KB per query row and head, and room
+ * for split items) items may be split; with less than the expansion needs the call is
+ * refused (PA_ERR_INVALID_ARG).  As in the BF16 calls, a value of V that is NaN reaches every
+ * row of the chunk whose last tile of keys holds its token, rows before it among them; such a
+ * key reaches only the rows that attend to it.
  */
 size_t pa_prefill_q4_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
                                     int num_kv_heads, int head_dim, int block_size);

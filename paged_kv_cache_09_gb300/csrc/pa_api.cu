@@ -942,15 +942,12 @@ struct PrefillQ4Layout {
     int table_stride = 0;   // pages of its longest sequence
     int ranges = 0;         // entries of the ranges, per KV head
     size_t q = 0, kv = 0, q_factor = 0, kv_factor = 0, range = 0, table = 0;  // bytes
-    size_t pieces = 0;
     size_t fixed() const { return q + q_factor + 2 * kv + kv_factor + range + table; }
 };
 static size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 static PrefillQ4Layout prefill_q4_layout(const pa::PrefillSeq *seqs, int cnt, int total_q,
-                                         int causal, int num_q_heads, int num_kv_heads,
-                                         int num_sms) {
-    static thread_local pa::PrefillSchedule sched;
+                                         int num_q_heads, int num_kv_heads) {
     PrefillQ4Layout l;
     for (int b = 0; b < cnt; ++b) {
         const int keys = seqs[b].q_start + seqs[b].q_len;
@@ -965,10 +962,6 @@ static PrefillQ4Layout prefill_q4_layout(const pa::PrefillSeq *seqs, int cnt, in
     l.kv_factor = up256((size_t)cnt * num_kv_heads * sizeof(float2));
     l.range = up256((size_t)l.ranges * num_kv_heads * sizeof(float2));
     l.table = up256((size_t)cnt * l.table_stride * 4);
-    if (prefill_schedule(seqs, cnt, causal, num_q_heads, num_q_heads / num_kv_heads,
-                         pa::kQ4PrefillPage, num_sms, (size_t)pa::kPfMaxPieces * pa::kPfSlotBytes,
-                         &sched))
-        l.pieces = (size_t)sched.num_pieces * pa::kPfSlotBytes;
     return l;
 }
 
@@ -982,13 +975,17 @@ size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const in
         return 0;
     DeviceInfo dev;
     if (device_info(&dev)) return 0;
+    static thread_local pa::PrefillSchedule sched;
     size_t need = 0;
     for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
         const int cnt = (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0);
-        const PrefillQ4Layout l =
-            prefill_q4_layout(&seqs[s0], cnt, cu_seqlens_q[num_seqs], causal ? 1 : 0, num_q_heads,
-                              num_kv_heads, dev.num_sms);
-        need = std::max(need, l.fixed() + l.pieces);
+        size_t bytes = prefill_q4_layout(&seqs[s0], cnt, cu_seqlens_q[num_seqs], num_q_heads,
+                                         num_kv_heads).fixed();
+        if (prefill_schedule(&seqs[s0], cnt, causal ? 1 : 0, num_q_heads, num_q_heads / num_kv_heads,
+                             pa::kQ4PrefillPage, dev.num_sms,
+                             (size_t)pa::kPfMaxPieces * pa::kPfSlotBytes, &sched))
+            bytes += (size_t)sched.num_pieces * pa::kPfSlotBytes;
+        need = std::max(need, bytes);
     }
     return need;
 } catch (...) {  // out of host memory
@@ -1022,8 +1019,7 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
     for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
         layouts.push_back(prefill_q4_layout(&seqs[s0],
                                             (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0),
-                                            cu_seqlens_q[num_seqs], causal, num_q_heads,
-                                            num_kv_heads, dev.num_sms));
+                                            cu_seqlens_q[num_seqs], num_q_heads, num_kv_heads));
         // Split items are an option (as in pa_prefill_varlen); the pages are not.
         if (workspace_bytes < layouts.back().fixed()) return PA_ERR_INVALID_ARG;
     }
@@ -1130,6 +1126,7 @@ int pa_get_device_errors(unsigned int *bits, int clear, void *stream) {
 int pa_test_hook(int decode_skip_stage, int prefill_skip_unit, int decode_consumer_delay_ns) {
     if (decode_consumer_delay_ns < 0 || decode_consumer_delay_ns > 1000000) return PA_ERR_INVALID_ARG;
     if (pa::set_decode_test_hook(decode_skip_stage, decode_consumer_delay_ns) != cudaSuccess ||
+        pa::set_decode_q4_test_hook(decode_skip_stage) != cudaSuccess ||
         pa::set_prefill_test_hook(prefill_skip_unit) != cudaSuccess)
         return PA_ERR_CUDA;
     return PA_OK;

@@ -195,6 +195,12 @@ struct Shares {
     }
 };
 
+#ifdef PA_TEST_HOOKS
+// Test build only: the pair of tiles (counted over each warp's run) whose loads are left out (-1:
+// none), so that the warp's wait runs out.
+__device__ int g_test_skip_pair = -1;
+#endif
+
 __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -331,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         const bool joined = __shfl_sync(0xffffffffu, (int)(mine == kTile && other > 0 && next == off + kTile), 0);
         if (joined) mine = l_tile ? 0 : total;
         __syncwarp();  // zeros go before the arrival
+#ifdef PA_TEST_HOOKS
+        if ((int)i == *reinterpret_cast<volatile int *>(&g_test_skip_pair)) return;
+#endif
         if (lane == 0) mbar_arrive_expect_tx(&full[s], total * 2 * kQ4RowBytes);
         __syncwarp();
         if (lane < 8 && mine) bulk_load(dst, src, mine * l_bytes, &full[s], l2_evict_first_policy());
@@ -812,6 +821,12 @@ size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads
     const WsLayout l = ws_layout(num_seqs, num_q_heads, num_kv_heads, num_sms);
     return l.o + l.ml + l.info;
 }
+
+#ifdef PA_TEST_HOOKS
+cudaError_t set_decode_q4_test_hook(int skip_pair) {
+    return cudaMemcpyToSymbol(g_test_skip_pair, &skip_pair, sizeof skip_pair);
+}
+#endif
 
 cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream) {
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_q4_stream_kernel), kSmem, 6);

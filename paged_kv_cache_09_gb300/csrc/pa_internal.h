@@ -426,6 +426,7 @@ cudaError_t launch_prefill(const CUtensorMap *tmaps, const PrefillArgs &a, cudaS
 //                                 int decode_consumer_delay_ns);
 // The product library has neither the hooks nor this entry point.
 cudaError_t set_decode_test_hook(int skip_stage, int consumer_delay_ns);
+cudaError_t set_decode_q4_test_hook(int skip_pair);
 cudaError_t set_prefill_test_hook(int skip_unit);
 #endif
 

@@ -372,6 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (u >= kRing &&
                     !mbar_wait_abort(&bars[kRingEmpty + s], ((u / kRing) - 1) & 1, p.err, abort))
                     return -1;
+#ifdef PA_TEST_HOOKS
+                if ((int)u == skip_unit) {  // the MMA thread's wait runs out
+                    ++u;
+                    return kRing;
+                }
+#endif
                 issued |= 1u << s;
                 par = (par & ~(1u << s)) | (((u / kRing) & 1u) << s);
                 mbar_arrive_expect_tx(&bars[kRingFull + s], kUnit);
@@ -382,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = 0; y < 2; ++y) {
                     const int s = next_slot();
                     if (s < 0) return false;
+                    if (s == kRing) continue;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tma_load_4d(ring + s * kUnit + i * kBlkBytes,
@@ -396,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = 1; y >= 0; --y) {
                     const int s = next_slot();
                     if (s < 0) return false;
+                    if (s == kRing) continue;
                     const CUtensorMap *m = x.last[y] < 0 ? &maps.v : &maps.v_last[x.last[y]];
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c)
