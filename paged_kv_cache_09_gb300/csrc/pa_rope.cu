@@ -15,8 +15,9 @@
 // per token and kind of row,
 //     out_j = inv (x_j A_j + x_p B_j),   A_j = w_j cos, B_j = +- w_p sin   (p: j's partner),
 // the partners are exchanged as packed BF16, before any arithmetic, and the arithmetic is on pairs.
-// 4096 tokens of 24 + 4 + 4 heads of 256: 225 instructions a row and 43 us with the weights
-// applied to every row.
+// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 28.7 us, 4.8 TB/s (43 with the
+// weights applied to every row, 29.6 with the rows summed one by one).  16 warps an SM with 8 rows
+// each on their way move more than 20 or 24 with fewer (33 and 40 us).  16 tokens: 2.4 us.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -180,28 +181,36 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         }
     };
 
-    auto turned = [&](const uint4 &row) {  // (all lanes of the warp)
+    auto squares = [&](const uint4 &row) {  // of this lane's dims
         const uint32_t w[4] = {row.x, row.y, row.z, row.w};
-        f32x2 x[4], ss = pair(0.f, 0.f);
-        uint32_t res[4];
+        f32x2 ss = pair(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[i] = pair_bf16(w[i]);
-            ss = fma(x[i], x[i], ss);
+            const f32x2 x = pair_bf16(w[i]);
+            ss = fma(x, x, ss);
         }
-        float sum, odd;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(sum), "=f"(odd) : "l"(ss));
-        sum += odd;
+        float even, odd;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(even), "=f"(odd) : "l"(ss));
+        return even + odd;
+    };
+    auto inverse = [&](float sum) {  // (rsqrt: within 2 units in the last place of fp32)
+        return rsqrtf(sum * (1.f / kD) + a.eps);
+    };
+    auto inverse_of = [&](const uint4 &row) {  // (all lanes of the warp)
+        float sum = squares(row);
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        // (rsqrt: within 2 units in the last place of fp32)
-        const float inv = rsqrtf(sum * (1.f / kD) + a.eps);
+        return inverse(sum);
+    };
+    auto turned = [&](const uint4 &row, float inv) {  // (all lanes of the warp)
+        const uint32_t w[4] = {row.x, row.y, row.z, row.w};
         const f32x2 inv2 = pair(inv, inv);
+        uint32_t res[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t y = kNeighbours ? __byte_perm(w[i], 0, 0x1032)
                                            : __shfl_sync(0xffffffffu, w[i], sub * kLanes + partner);
-            res[i] = pack(mul(inv2, fma(pair_bf16(y), B[i], mul(x[i], A[i]))));
+            res[i] = pack(mul(inv2, fma(pair_bf16(y), B[i], mul(pair_bf16(w[i]), A[i]))));
         }
         return make_uint4(res[0], res[1], res[2], res[3]);
     };
@@ -216,22 +225,48 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 
     // The shuffles need whole warps, so a warp goes on while any of its rows is left.
     factors(a.q_weight);
+    // A warp with several whole rows sums them together: each step of the reduction halves the
+    // rows that a lane has (9 exchanges and 7 for the results, instead of 5 a row), and every
+    // lane takes one row's root.
+    const bool joint = kD == 256 && unit + step < hq;
+    float inv[kBatch + 1];
+    if (joint) {
+        static_assert(kBatch + 1 <= 8, "eight sums a warp");
+        float v[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            v[b] = b < kBatch ? squares(raw[b]) : b == kBatch ? squares(raw_k) : 0.f;
+#pragma unroll
+        for (int n = 4, d = 16; n > 0; n >>= 1, d >>= 1)
+#pragma unroll
+            for (int b = 0; b < n; ++b) {
+                const bool up = (lane & d) != 0;
+                const float send = up ? v[b] : v[b + n], keep = up ? v[b + n] : v[b];
+                v[b] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+            }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        const float mine = inverse(v[0]);
+#pragma unroll
+        for (int b = 0; b <= kBatch; ++b) inv[b] = __shfl_sync(0xffffffffu, mine, 4 * b);
+    }
     uint16_t *q_out = a.q_out + t * a.q_out_stride + 8 * l;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
         const int r = unit + b * step;
         if (r - sub >= hq) break;  // warp-uniform
-        const uint4 out = turned(raw[b]);
+        const uint4 out = turned(raw[b], joint ? inv[b] : inverse_of(raw[b]));
         if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
         if (more) raw[b] = row_of(q_at, r, hq);
     }
     for (int r = unit + kBatch * step; r - sub < hq; r += step) {  // many heads
-        const uint4 out = turned(row_of(a.q + t * a.q_stride, r, hq));
+        const uint4 row = row_of(a.q + t * a.q_stride, r, hq), out = turned(row, inverse_of(row));
         if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
     }
     if (unit_k - sub < hkv) factors(a.k_weight);
     for (int r = unit_k; r - sub < hkv; r += step) {
-        const uint4 out = turned(r == unit_k ? raw_k : row_of(a.k + t * a.k_stride, r, hkv));
+        const uint4 row = r == unit_k ? raw_k : row_of(a.k + t * a.k_stride, r, hkv);
+        const uint4 out = turned(row, joint && r == unit_k ? inv[kBatch] : inverse_of(row));
         if (live && r < hkv) {
             if (kCache == 0)
                 *reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + r * kD + 8 * l) = out;
