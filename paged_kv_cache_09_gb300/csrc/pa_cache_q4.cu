@@ -1,9 +1,11 @@
 // pa_cache_q4.cu -- writes into and reads from the 4-bit cache (format: pa_q4.cuh).
 //
 // One warp per row (a token's 256 dims of one KV head), 8 dims a lane: a row is one
-// 16-byte load per lane of BF16, one 4-byte word per lane of codes.  All three kernels
-// move bytes and are bound by memory (large calls) or by launch and one round trip
-// (a decode batch's).
+// 16-byte load per lane of BF16, one 4-byte word per lane of codes.  The kernels move bytes and
+// are bound by memory (large calls) or by launch and one round trip (a decode batch's); the
+// write also by its instructions (a group's bounds and 8 codes a lane, about 150).
+// Measured with 4 KV heads: 4096 tokens written in 9.5 us and read back in 6.7 (2.3 and 3.2
+// TB/s); 16 tokens written and read in 3.7 us together.
 #include "pa_internal.h"
 #include "pa_q4.cuh"
 
@@ -84,6 +86,7 @@ __device__ __forceinline__ float scale_for(float top) {
 
 // Blocks [0, num_ranges * num_kv_heads): bounds of |K| and |V| over kQ4RangeKeys keys of one
 // head, from the groups' minima and steps alone.  The other blocks: kWarps rows of Q each.
+// 13973 keys of 4 heads and 1685 x 24 query rows: 8.2 us (43 MB, nearly all of it the queries).
 __global__ void __launch_bounds__(kWarps * 32)
     range_q4_kernel(const __grid_constant__ Q4ExpandArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -160,7 +163,8 @@ __device__ __forceinline__ uint4 widen_word(uint32_t w, float s, float lo) {
 }
 
 // Warp per (key, head), the warps of a CTA on consecutive keys of one head, whose codes are
-// one contiguous run; kWarps keys' loads in flight a round.
+// one contiguous run; kWarps keys' loads in flight a round.  13973 keys of 4 heads: 15.6 us (16 MB
+// read, 57 MB written: 4.7 TB/s).
 __global__ void __launch_bounds__(kWarps * 32)
     expand_q4_kernel(const __grid_constant__ Q4ExpandArgs a) {
     constexpr int kRows = kQ4ExpandKeys / kWarps;  // keys of a warp
