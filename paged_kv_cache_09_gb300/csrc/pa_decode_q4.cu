@@ -50,7 +50,7 @@
 // because the extra warps cost instructions (spills, exchanges, loads), and issue is what bounds.
 //
 // Measured, calls one after another, 4 KV heads of 6 query heads unless said: 16 sequences of
-// 4K..32K keys 69 us (streaming kernel 5.1 TB/s, issue slots 51% used with 8 warps an SM); 64 of
+// 4K..32K keys 67 us (streaming kernel 5.1 TB/s, issue slots 51% used with 8 warps an SM); 64 of
 // 1..2048 keys, 8 KV heads of 4, pages of 16: 42 us; one of 32768 keys 16.5 us; one of 1701 keys
 // 10.2 us.  The short ones are latency: finding the share 1.5 us, q 1.2, one step 1.3, the CTA's
 // merge 1, and the second kernel.
@@ -711,17 +711,24 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
 }
 
 // Merges a row's parts: sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j, M = max m_j; an empty
-// part has m = -inf.  All loads of a round are in
-// flight together.
-//   few rows:  8 warps and 4 CTAs a row (64 dims each), for the latency of many parts
-//   many rows: two warps a row (128 dims each), 4 rows a CTA
-template <bool kFew>
+// part has m = -inf.  All loads of a round are in flight together.
+//   kSplit > 1: that many warps for each 64 dims of a row take its parts in turn, for the
+//               latency of many parts
+//   kSplit = 1: two warps a row (128 dims each), 4 rows a CTA
+// The fewer the rows, the more parts each may have: 8 up to a row an SM (24 rows of 76 parts: a
+// step of 16.5 us, 26.3 with 1), 4 up to 8 rows an SM (384 rows of 5 parts: 67.2 us, 69.5 with 8,
+// 67.3 with 1, but one long sequence among short ones has many parts again), 1 beyond (2048
+// rows: 42 us, 53 with 8).
+template <int kSplit>
 __global__ void __launch_bounds__(256) decode_q4_merge_kernel(const __grid_constant__ Params p) {
-    constexpr int kWarps = kFew ? 8 : 1, kRound = 4;
+    constexpr bool kFew = kSplit > 1;
+    constexpr int kWarps = kSplit, kRound = 4;
+    constexpr int kBlocks = 8 / kSplit;  // of 64 dims, in a CTA
     constexpr int kVec = kFew ? 1 : 2;  // float2 a lane
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = kFew ? blockIdx.x >> 2 : (int64_t)blockIdx.x * 4 + (warp >> 1);
-    const int d0 = kFew ? (blockIdx.x & 3) * 64 : (warp & 1) * 128;
+    const int lane = threadIdx.x & 31, all = threadIdx.x >> 5;
+    const int warp = kFew ? all % kWarps : all, block = kFew ? all / kWarps : 0;
+    const int64_t row = kFew ? blockIdx.x / (4 / kBlocks) : (int64_t)blockIdx.x * 4 + (warp >> 1);
+    const int d0 = kFew ? (blockIdx.x % (4 / kBlocks) * kBlocks + block) * 64 : (warp & 1) * 128;
     pdl_wait();
     pdl_trigger();
     if (row >= (int64_t)p.num_seqs * p.num_q_heads) return;  // (warp-uniform; kFew: never)
@@ -779,7 +786,8 @@ __global__ void __launch_bounds__(256) decode_q4_merge_kernel(const __grid_const
         }
     }
     if (kFew) {
-        __shared__ float2 so[kWarps][32], sml[kWarps];
+        __shared__ float2 sums[kBlocks][kWarps][32], refs[kBlocks][kWarps];
+        float2 (*so)[32] = sums[block], *sml = refs[block];
         so[warp][lane] = acc[0];
         if (lane == 0) sml[warp] = make_float2(M, L);
         __syncthreads();
@@ -874,9 +882,11 @@ cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.num_seqs * a.num_q_heads;
+    if (rows <= a.num_sms)
+        return launch_pdl(decode_q4_merge_kernel<8>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
     if (rows <= 8 * a.num_sms)
-        return launch_pdl(decode_q4_merge_kernel<true>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
-    return launch_pdl(decode_q4_merge_kernel<false>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+        return launch_pdl(decode_q4_merge_kernel<4>, dim3((unsigned)(rows * 2)), dim3(256), 0, stream, p);
+    return launch_pdl(decode_q4_merge_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
 }
 
 }  // namespace pa
