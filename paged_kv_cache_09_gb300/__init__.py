@@ -530,6 +530,10 @@ def _row_stride(t, name, tokens, heads, dim):
     return a if tokens > 1 else heads * dim
 
 
+# (void *, int, int64_t) arrays of each length up to the number of groups
+_ARRAYS = [(ctypes.c_void_p * n, ctypes.c_int * n, ctypes.c_int64 * n) for n in range(9)]
+
+
 def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_pages, num_tokens,
                      out=None):
     """One mixed step's inputs from the requests' lengths (see pa_batch_input_prep).
@@ -558,10 +562,10 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     slots = out["slot_mappings"]
     if len(slots) != G:
         raise ValueError("out: one slot mapping per group")
-    pointers, ints = ctypes.c_void_p * G, ctypes.c_int * G
+    pointers, ints, longs = _ARRAYS[G]
     _raise(lib.pa_batch_input_prep(
         computed, new, S, G, pointers(*[t.data_ptr() for t in block_tables]),
-        (ctypes.c_int64 * G)(*strides), ints(*widths), ints(*map(int, block_sizes)),
+        longs(*strides), ints(*widths), ints(*map(int, block_sizes)),
         pointers(*free), ints(*[f.shape[0] for f in free_pages]), T,
         _vector(out["seq_lens"], "seq_lens", _I32, S, dev),
         _vector(out["query_start_loc"], "query_start_loc", _I32, S + 1, dev),
