@@ -477,10 +477,12 @@ int pa_gather_cache_q4(const void *k_cache, const void *v_cache, int64_t page_st
  * of pa_decode (without the fused write and with out on the device), but: page_stride is in
  * bytes; seq_lens[s] may be 0, a padding entry, whose rows of out become zeros; the
  * workspace is sized by pa_decode_q4_workspace_size.  A page outside the pool sets
- * PA_DEVERR_PAGE and its tokens read as zeros.  Steps of V count as at most 2^80; |scale * q|
- * of 2^116 and more is not representable and gives NaN.  Lengths that come to more than 2^31
- * tiles of 16 tokens over all sequences and KV heads set PA_DEVERR_SEQLEN, and out is not
- * written.
+ * PA_DEVERR_PAGE and its tokens read as zeros.  Weights times steps of V are rounded to FP16, each
+ * head's and group's relative to the largest of its own, so that groups and tokens of V may be of
+ * any sizes; a head's q is FP16 relative to its largest value (values down to 2^-24 of it exact,
+ * smaller ones off by up to 2^-34 of it).  |scale * q| of 2^116 and more is not representable and
+ * gives NaN.  Lengths that come to more than 2^31 tiles of 16 tokens over all sequences and KV
+ * heads set PA_DEVERR_SEQLEN, and out is not written.
  */
 size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                    int block_size, int max_seq_len);

@@ -24,20 +24,24 @@
 // q becomes FP16 after scaling each head by a power of two (largest value in [2^13, 2^14)):
 // exact for values down to 2^-24 of the head's largest, and below that off by less than
 // 2^-34 of it.
-// The weights p s become FP16 (2^-12 relative): an eighth of the output's own rounding to BF16.
-// So that they neither overflow nor vanish, p is taken relative to 2^M, M = running largest
-// score + log2 of the running largest step of V - 7, both at most 2^8 behind the true ones:
-// p s <= 2^15, and weights down to 2^-21 of the largest keep 11 bits.  The reference moves
-// (and the sums are rescaled) only when a score passes it by more than 8, which needs one
-// vote a step instead of a reduction over the tokens.  Steps are taken as at most 2^80.
-//
+// The weights p s become FP16 (off by 2^-11 of them at most), scaled so that they neither overflow
+// nor vanish: p = 2^(x - m - kLag), m the largest score rounded up to a whole number and at most
+// kLag behind, so p <= 1; and p s F, F a power of two for each head and group that leaves the
+// group's largest p s at 2^-1 at least, so that the smallest FP16 is 2^-23 of it, whatever the
+// other groups and the tokens without weight hold.  (One reference for all groups, from the
+// largest score and the largest step taken apart, left groups 2^24 apart 5% off.)  While steps are
+// alike F comes from them alone, for all heads; where they are not, from the scores too.  One vote
+// a step finds whether anything moves: a score above m + kLag, or a step that could give a weight
+// above 2^15.  s and F are applied to both heads of a lane by products of pairs (1% of the time less
+// than one by one).  Against a form without F, all of this costs 2% of a long batch's time (16
+// sequences: 67.2 us) and 0.8 us of a short sequence's.
 // Work split: the tiles of all (sequence, KV head) pairs in a row, cut evenly over two CTAs an
 // SM, so that uneven lengths leave no SM idle; each CTA finds its share from the lengths.  A pair
 // also costs its beginning (table, q, the first loads' way, the merge): it counts as kPairCost
 // tiles, half a share at most, ahead of the pair's first, so that CTAs with many short pairs get
-// fewer tiles (64 sequences of 1..2048 keys, 8 KV heads: 62 us without it, 53.5, 46, 42 and 44 us
-// with 4, 8, 16 and 28).  Shares below two rounds of the warps' tiles stay even: there a CTA's
-// time is its rounds (one sequence of 1701 keys, shares of 8).  A pair
+// fewer tiles (64 sequences of 1..2048 keys, 8 KV heads, in a form without F: 62 us without it, 53.5,
+// 46, 42 and 44 us with 4, 8, 16 and 28).  Shares below two rounds of the warps' tiles stay even:
+// there a CTA's time is its rounds (one sequence of 1701 keys, shares of 8).  A pair
 // that one CTA holds whole is finished there; the others leave a part per CTA (sums relative to
 // their reference), which a second kernel merges.
 // Within a CTA each warp streams pairs of 16-token tiles of its own (every kW-th pair) through a
@@ -50,10 +54,9 @@
 // because the extra warps cost instructions (spills, exchanges, loads), and issue is what bounds.
 //
 // Measured, calls one after another, 4 KV heads of 6 query heads unless said: 16 sequences of
-// 4K..32K keys 67 us (streaming kernel 5.1 TB/s, issue slots 51% used with 8 warps an SM); 64 of
-// 1..2048 keys, 8 KV heads of 4, pages of 16: 42 us; one of 32768 keys 16.5 us; one of 1701 keys
-// 10.2 us.  The short ones are latency: finding the share 1.5 us, q 1.2, one step 1.3, the CTA's
-// merge 1, and the second kernel.
+// 4K..32K keys 68.4 us (streaming kernel 5.0 TB/s); 64 of 1..2048 keys, 8 KV heads of 4, pages of
+// 16: 43.5 us; one of 32768 keys 17.3 us; one of 1701 keys 11.1 us.  The short ones are latency:
+// finding the share 1.5 us, q 1.2, one step 2, the CTA's merge 1, and the second kernel.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -83,7 +86,9 @@ constexpr int kSmem = kOffBars + kW * kDepth * 16 + 16;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 constexpr int kMinShare = 2 * kW;                     // tiles of the smallest share
 constexpr int kPairCost = 16;                         // of beginning a pair, in tiles
-constexpr float kHeadroom = 7.f, kLag = 8.f;          // log2 units: p s <= 2^(kHeadroom + kLag)
+constexpr float kLag = 8.f;  // log2 units: a score may pass the reference by it
+constexpr float kTop = 4.f;  // where F follows the scores, the largest weight is 2^(kTop - 1) .. 2^(kTop + 1)
+constexpr int kSpare = 2;    // where it follows the steps, they may grow by 2^kSpare unexamined
 
 // Division of n < 2^31 by a constant of the launch.
 struct FastDiv {
@@ -156,6 +161,15 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t (&x)[4]) {
     x[1] = w & 0x00f000f0u;
     x[2] = high & 0x000f000fu;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(x[3]) : "r"(high), "r"(x[2]));
+}
+
+// 2^e of a whole number e <= 127; 0 below the normal range.
+__device__ __forceinline__ float exp2_whole(float e) {
+    return e < -126.f ? 0.f : __uint_as_float((uint32_t)((int)e + 127) << 23);
+}
+// log2 of a power of two.
+__device__ __forceinline__ float log2_whole(float f) {
+    return (float)((int)(__float_as_uint(f) >> 23) - 127);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -444,9 +458,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[gg][k][0] = o[gg][k][1] = o[gg][k][2] = o[gg][k][3] = 0.f;
         }
-        // Running references: largest scores (of heads 2c, 2c + 1) and largest step, the latter a
-        // power of two 2^eb.
-        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, eb = 0.f, big = 0.f, l0 = 0.f, l1 = 0.f;
+        // Running references of heads 2c and 2c + 1, and their groups' factors.
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+        float f0[4], f1[4];
+#pragma unroll
+        for (int gg = 0; gg < 4; ++gg) f0[gg] = f1[gg] = 0x1p126f;
+        uint32_t safe01 = 0, safe23 = 0;  // steps up to these (of groups 0, 1 and 2, 3) give at most 2^15
 
         for (int i = 0; i < n; ++i) {
             if (loaded < n) load(it + loaded++);  // into the slot that the previous pair has left
@@ -460,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
             // ---- scores of tokens r and r + 8 of each tile, heads 2c and 2c + 1: 8 accumulators
             // (tile, group) in turn
             float x[2][4];
-            uint32_t steps = 0;  // the largest step of V, a BF16 in the lower half
+            uint32_t big01 = 0, big23 = 0;  // the largest steps of V, of groups 0, 1 and 2, 3
             {
                 const uint4 qa = lds128(q_frag + 8 * 512);  // sums of (head r, group c); scales
                 const uint32_t ka = base + r * 128 + (((2 * c) ^ r) << 4);
@@ -497,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                     const uint32_t lo1 = __byte_perm(lds32(kp + c * 4 + 128), 0, 0x3232);
                     const uint4 pr0 = lds128(kp), pr1 = lds128(kp + 128);
                     const uint4 vp0 = lds128(kp + 2 * kTilePairs), vp1 = lds128(kp + 2 * kTilePairs + 128);
-                    uint32_t b0 = max_bf16x2(max_bf16x2(vp0.x, vp0.y), max_bf16x2(vp0.z, vp0.w));
-                    uint32_t b1 = max_bf16x2(max_bf16x2(vp1.x, vp1.y), max_bf16x2(vp1.z, vp1.w));
+                    uint32_t a01 = __byte_perm(vp0.x, vp0.y, 0x5410), a23 = __byte_perm(vp0.z, vp0.w, 0x5410);
+                    uint32_t b01 = __byte_perm(vp1.x, vp1.y, 0x5410), b23 = __byte_perm(vp1.z, vp1.w, 0x5410);
                     x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
                     mma_bf16_16816(x[t], lo0, lo1, lo0, lo1, qa.x, qa.y);
 #pragma unroll
@@ -517,55 +534,149 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                     if (nvalid < kTile) {  // what lies behind the valid rows may be anything
                         if (r >= nvalid) {
                             x[t][0] = x[t][1] = -CUDART_INF_F;
-                            b0 = 0;
+                            a01 = a23 = 0;
                         }
                         if (r + 8 >= nvalid) {
                             x[t][2] = x[t][3] = -CUDART_INF_F;
-                            b1 = 0;
+                            b01 = b23 = 0;
                         }
                     }
-                    steps = max_bf16x2(steps, max_bf16x2(b0, b1));
+                    big01 = max_bf16x2(big01, max_bf16x2(a01, b01));
+                    big23 = max_bf16x2(big23, max_bf16x2(a23, b23));
                 }
             }
 
-            // ---- references: moved when a score passes by more than kLag, or a step at all
+            // The pairs of V of tokens r and r + 8 of tile t.
+            auto v_pairs = [&](int t, uint4 &vp0, uint4 &vp1) {
+                const uint32_t vp = base + kOffVPairs + t * kTilePairs + r * 16;
+                vp0 = lds128(vp);
+                vp1 = lds128(vp + 128);
+                const int nvalid = t ? nv.y : nv.x;
+                if (nvalid < kTile) {
+                    if (r >= nvalid) vp0 = make_uint4(0, 0, 0, 0);
+                    if (r + 8 >= nvalid) vp1 = make_uint4(0, 0, 0, 0);
+                }
+            };
+
+            // ---- references: moved (in the first step always) when a score passes by more than
+            // kLag, or when a step is large enough for a weight to pass 2^15
             float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
             float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-            float step = bf16_lo(steps);
-            if (__any_sync(0xffffffffu, mx0 > m0 + kLag || mx1 > m1 + kLag || step > big)) {
+            const bool large = max_bf16x2(big01, safe01) != safe01 || max_bf16x2(big23, safe23) != safe23;
+            if (__any_sync(0xffffffffu, mx0 > m0 + kLag || mx1 > m1 + kLag || large)) {
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) {
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
-                    step = fmaxf(step, __shfl_xor_sync(0xffffffffu, step, sh));
                 }
-                const float old0 = m0 + eb, old1 = m1 + eb;
-                m0 = fmaxf(m0, mx0);
-                m1 = fmaxf(m1, mx1);
-                if (step > big) {  // the next power of two (within [2^-80, 2^80])
-                    const int e = min(80, max(-80, (int)(__float_as_uint(step) >> 23) - 126));
-                    eb = (float)e;
-                    big = e == 80 ? CUDART_INF_F : __uint_as_float((uint32_t)(e + 127) << 23);
-                }
-                const float al0 = old0 == -CUDART_INF_F ? 0.f : ex2_approx(old0 - (m0 + eb));
-                const float al1 = old1 == -CUDART_INF_F ? 0.f : ex2_approx(old1 - (m1 + eb));
-                l0 *= al0;
-                l1 *= al1;
+                const float n0 = fmaxf(m0, ceilf(mx0)), n1 = fmaxf(m1, ceilf(mx1));
+                const float d0 = n0 == m0 ? 0.f : n0 - m0, d1 = n1 == m1 ? 0.f : n1 - m1;
+                m0 = n0;
+                m1 = n1;
+                const float al0 = ex2_approx(-d0), al1 = ex2_approx(-d1);
+                float g0[4], g1[4];  // what the sums of each group are multiplied by
 #pragma unroll
                 for (int gg = 0; gg < 4; ++gg) {
-                    low0[gg] *= al0;
-                    low1[gg] *= al1;
+                    g0[gg] = al0;
+                    g1[gg] = al1;
+                }
+                if (i == 0) {  // room for steps 2^kSpare times the largest
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[gg][k][0] *= al0;
-                        o[gg][k][1] *= al1;
-                        o[gg][k][2] *= al0;
-                        o[gg][k][3] *= al1;
+                    for (int sh = 4; sh < 32; sh <<= 1) {
+                        big01 = max_bf16x2(big01, __shfl_xor_sync(0xffffffffu, big01, sh));
+                        big23 = max_bf16x2(big23, __shfl_xor_sync(0xffffffffu, big23, sh));
+                    }
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) {
+                        const int e = ((gg < 2 ? big01 : big23) >> (gg & 1 ? 23 : 7)) & 255;
+                        f0[gg] = f1[gg] = __uint_as_float(min(253, 2 * 127 + 14 - kSpare - e) << 23);
+                    }
+                }
+                // While every step times F is 2^8 at least, the token that moved m (p > 2^-9) gives the
+                // group a weight above 2^-1, and F can stay.
+                uint32_t low01 = 0x7f807f80u, low23 = low01;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int nvalid = t ? nv.y : nv.x;
+                    uint4 vp0, vp1;
+                    v_pairs(t, vp0, vp1);
+                    if (r < nvalid) {
+                        low01 = min_bf16x2(low01, __byte_perm(vp0.x, vp0.y, 0x5410));
+                        low23 = min_bf16x2(low23, __byte_perm(vp0.z, vp0.w, 0x5410));
+                    }
+                    if (r + 8 < nvalid) {
+                        low01 = min_bf16x2(low01, __byte_perm(vp1.x, vp1.y, 0x5410));
+                        low23 = min_bf16x2(low23, __byte_perm(vp1.z, vp1.w, 0x5410));
+                    }
+                }
+                const bool even = bf16_lo(low01) * fminf(f0[0], f1[0]) >= 256.f &&
+                                  bf16_hi(low01) * fminf(f0[1], f1[1]) >= 256.f &&
+                                  bf16_lo(low23) * fminf(f0[2], f1[2]) >= 256.f &&
+                                  bf16_hi(low23) * fminf(f0[3], f1[3]) >= 256.f;
+                if (!__all_sync(0xffffffffu, even && (i == 0 || !large))) {
+                    // The groups' largest x + floor(log2 s): p s is 2^(t - m - kLag) to twice that.
+                    float t0[4], t1[4];
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) t0[gg] = t1[gg] = -CUDART_INF_F;
+#pragma unroll 1
+                    for (int t = 0; t < 2; ++t) {
+                        uint4 vp0, vp1;
+                        v_pairs(t, vp0, vp1);
+#pragma unroll
+                        for (int gg = 0; gg < 4; ++gg) {
+                            const float s0 = q4_step(word(vp0, gg)), s1 = q4_step(word(vp1, gg));
+                            const float e0 = s0 > 0.f ? log2_whole(s0) : -CUDART_INF_F;
+                            const float e1 = s1 > 0.f ? log2_whole(s1) : -CUDART_INF_F;
+                            t0[gg] = fmaxf(t0[gg], fmaxf((t ? x[1][0] : x[0][0]) + e0,
+                                                         (t ? x[1][2] : x[0][2]) + e1));
+                            t1[gg] = fmaxf(t1[gg], fmaxf((t ? x[1][1] : x[0][1]) + e0,
+                                                         (t ? x[1][3] : x[0][3]) + e1));
+                        }
+                    }
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) {
+#pragma unroll 1
+                        for (int sh = 4; sh < 32; sh <<= 1) {
+                            t0[gg] = fmaxf(t0[gg], __shfl_xor_sync(0xffffffffu, t0[gg], sh));
+                            t1[gg] = fmaxf(t1[gg], __shfl_xor_sync(0xffffffffu, t1[gg], sh));
+                        }
+                        // F goes up only to follow m, and down where this step's largest needs it.
+                        auto moved = [&](float &f, float n, float d, float top) {
+                            const float old = i == 0 ? 126.f : log2_whole(f) + d;
+                            const float e = fmaxf(-122.f, fminf(fminf(old, 126.f),
+                                                                n + kLag + kTop - 1.f - floorf(top)));
+                            f = exp2_whole(e);
+                            return exp2_whole(e - old);
+                        };
+                        g0[gg] = moved(f0[gg], n0, d0, t0[gg]);
+                        g1[gg] = moved(f1[gg], n1, d1, t1[gg]);
+                    }
+                }
+                // Steps that cannot give a weight above 2^15 (p is 1 at most) with this lane's heads.
+                auto safe = [&](int gg) {
+                    return min(254u, 2 * 127 + 15 - (__float_as_uint(fmaxf(f0[gg], f1[gg])) >> 23)) << 7;
+                };
+                safe01 = safe(0) | safe(1) << 16;
+                safe23 = safe(2) | safe(3) << 16;
+                if (i > 0) {
+                    l0 *= al0;
+                    l1 *= al1;
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) {
+                        low0[gg] *= al0;
+                        low1[gg] *= al1;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            o[gg][k][0] *= g0[gg];
+                            o[gg][k][1] *= g1[gg];
+                            o[gg][k][2] *= g0[gg];
+                            o[gg][k][3] *= g1[gg];
+                        }
                     }
                 }
             }
-            const float mu0 = m0 == -CUDART_INF_F ? 0.f : m0 + eb - kHeadroom;
-            const float mu1 = m1 == -CUDART_INF_F ? 0.f : m1 + eb - kHeadroom;
+            const float mu0 = m0 == -CUDART_INF_F ? 0.f : m0 + kLag;
+            const float mu1 = m1 == -CUDART_INF_F ? 0.f : m1 + kLag;
 
             // ---- O^T += V^T (p s)^T, two tokens' codes a register
 #pragma unroll
@@ -578,21 +689,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                 const uint32_t v0 = vt + 2 * c * 128 + ((r ^ (2 * c)) << 4), v1 = (v0 ^ 16) + 128;
                 const uint4 va = lds128(v0), vb = lds128(v1);                // tokens 2c, 2c + 1
                 const uint4 vc = lds128(v0 + 1024), vd = lds128(v1 + 1024);  // tokens 2c + 8, 2c + 9
-                const uint32_t vp = base + kOffVPairs + t * kTilePairs + r * 16;
-                uint4 vp0 = lds128(vp), vp1 = lds128(vp + 128);
-                const int nvalid = t ? nv.y : nv.x;
-                if (nvalid < kTile) {
-                    if (r >= nvalid) vp0 = make_uint4(0, 0, 0, 0);
-                    if (r + 8 >= nvalid) vp1 = make_uint4(0, 0, 0, 0);
-                }
+                uint4 vp0, vp1;
+                v_pairs(t, vp0, vp1);
 #pragma unroll
                 for (int gg = 0; gg < 4; ++gg) {
-                    const float s0 = q4_step(word(vp0, gg)), s1 = q4_step(word(vp1, gg));
                     const float lo0 = q4_low(word(vp0, gg)), lo1 = q4_low(word(vp1, gg));
                     low0[gg] = fmaf(p00, lo0, fmaf(p10, lo1, low0[gg]));
                     low1[gg] = fmaf(p01, lo0, fmaf(p11, lo1, low1[gg]));
-                    const uint32_t b0 = movmatrix_t(pack_f16x2(p00 * s0, p01 * s0));
-                    const uint32_t b1 = movmatrix_t(pack_f16x2(p10 * s1, p11 * s1));
+                    const float s0 = q4_step(word(vp0, gg)), s1 = q4_step(word(vp1, gg));
+                    float a0, a1, c0, c1;  // (p s is in fp32's range whatever F is)
+                    mul2(a0, a1, p00, p01, s0, s0);
+                    mul2(c0, c1, p10, p11, s1, s1);
+                    mul2(a0, a1, a0, a1, f0[gg], f1[gg]);
+                    mul2(c0, c1, c0, c1, f0[gg], f1[gg]);
+                    const uint32_t b0 = movmatrix_t(pack_f16x2(a0, a1));
+                    const uint32_t b1 = movmatrix_t(pack_f16x2(c0, c1));
                     uint32_t u[4], v[4];
                     widen(__byte_perm(word(va, gg), word(vb, gg), 0x5410), u);
                     widen(__byte_perm(word(vc, gg), word(vd, gg), 0x5410), v);
@@ -610,8 +721,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         for (uint32_t i = it + max(0, loaded - kDepth); i < it + loaded; ++i)
             mbar_wait(&full[i % kDepth], (i / kDepth) & 1, p.err);
         it += n;
-        m0 += eb;
-        m1 += eb;
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
@@ -653,18 +762,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         {
             float *row0 = red_o + (warp * kDecMaxGroup + 2 * c) * kMergeRow + 8 * r;
 #pragma unroll
-            for (int gg = 0; gg < 4; ++gg)
+            for (int gg = 0; gg < 4; ++gg) {
+                const float u0 = __uint_as_float((254u << 23) - __float_as_uint(f0[gg]));  // 1 / F
+                const float u1 = __uint_as_float((254u << 23) - __float_as_uint(f1[gg]));
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    auto row = [&](int h, float low) {
-                        return make_float4(
-                            fmaf(o[gg][2 * k][h], 0x1p24f, low), fmaf(o[gg][2 * k][2 + h], 0x1p20f, low),
-                            fmaf(o[gg][2 * k + 1][h], 0x1p24f, low),
-                            fmaf(o[gg][2 * k + 1][2 + h], 0x1p20f, low));
+                    auto row = [&](int h, float low, float u) {
+                        return make_float4(fmaf(o[gg][2 * k][h] * 0x1p24f, u, low),
+                                           fmaf(o[gg][2 * k][2 + h] * 0x1p20f, u, low),
+                                           fmaf(o[gg][2 * k + 1][h] * 0x1p24f, u, low),
+                                           fmaf(o[gg][2 * k + 1][2 + h] * 0x1p20f, u, low));
                     };
-                    *reinterpret_cast<float4 *>(row0 + gg * 64 + k * 4) = row(0, low0[gg]);
-                    *reinterpret_cast<float4 *>(row0 + kMergeRow + gg * 64 + k * 4) = row(1, low1[gg]);
+                    *reinterpret_cast<float4 *>(row0 + gg * 64 + k * 4) = row(0, low0[gg], u0);
+                    *reinterpret_cast<float4 *>(row0 + kMergeRow + gg * 64 + k * 4) = row(1, low1[gg], u1);
                 }
+            }
         }
         __syncthreads();  // every warp's rows are there, and q is no longer read
         gave_up = *abort != 0;

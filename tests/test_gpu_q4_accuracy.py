@@ -1,0 +1,129 @@
+"""Decode over the 4-bit cache against 64 bits under a bound on each head's and group's error norm
+(_q4_bounds): ordinary data, values of V of very uneven size, and scores that are all alike, where
+every token counts the same and one left out or counted twice shows."""
+import numpy as np
+import pytest
+import torch
+
+import _q4
+import _q4_bounds
+from test_gpu_q4 import _case, _decode
+
+pytestmark = pytest.mark.gpu
+
+
+def _check(out, c, scale=0.0625):
+    ref, bound = _q4_bounds.decode(_q4.f64(c["q"]), c["kc"].cpu().numpy(), c["vc"].cpu().numpy(), c["bs"],
+                                   c["table"], c["lens"].cpu().numpy(), scale)
+    return _q4_bounds.check(_q4.f64(out), ref, bound)
+
+
+def _bf(x):
+    return x.to(torch.bfloat16).contiguous()
+
+
+@pytest.mark.parametrize("bs,hq,hkv,lens", [
+    (832, 24, 4, [1701]),
+    (784, 6, 1, [783, 785, 1568]),
+    (16, 32, 8, [1, 2, 15, 16, 17, 0, 31, 33, 200]),
+    (7, 5, 1, [1, 6, 7, 8, 99]),
+    (100, 14, 2, [99, 100, 101, 350]),
+    (16, 16, 8, [(i * 389) % 601 for i in range(33)] + [0, 0, 1, 1, 2, 0, 599, 0]),
+    (64, 16, 4, [0, 20001, 0]),
+])
+def test_decode_within_the_norm_bound(cuda_lib, bs, hq, hkv, lens):
+    c = _case(cuda_lib, lens, bs, hq, hkv, seed=3 * len(lens) + bs)
+    _check(_decode(cuda_lib, c), c)
+    assert cuda_lib.device_errors() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+def test_decode_scales_within_the_norm_bound(cuda_lib, scale):
+    c = _case(cuda_lib, [300, 17], 64, 6, 1, seed=9)
+    _check(_decode(cuda_lib, c, scale), c, scale)
+
+
+@pytest.mark.parametrize("bs,hq,hkv,lens", [
+    (832, 24, 4, [1701]), (16, 6, 1, [5000]), (784, 8, 8, [785, 0, 1, 2999]), (7, 5, 1, [333, 6]),
+    (16, 8, 8, [(i * 577) % 1201 for i in range(34)]), (48, 16, 4, [20001, 17]),
+])
+def test_decode_flat_scores_count_every_token(cuda_lib, bs, hq, hkv, lens):
+    # Token t has one value, 15 in dim t % 256 (a step of 1, exact): dim d of the mean counts the
+    # tokens of that dim, so that one token more or less moves it by 256 / length of it at least.
+    pa = cuda_lib
+    c = _case(pa, lens, bs, hq, hkv, seed=bs)
+    c["q"].zero_()
+    v = torch.zeros(sum(lens), hkv, 256, device="cuda")
+    t = torch.cat([torch.arange(n) for n in lens]).cuda()
+    v[torch.arange(sum(lens), device="cuda"), :, t % 256] = 15
+    k = torch.randn(sum(lens), hkv, 256, device="cuda")
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    out = _q4.f64(_decode(pa, c))
+    for s, n in enumerate(lens):
+        want = 15.0 * np.bincount(np.arange(n) % 256, minlength=256) / max(n, 1)
+        # a rounding to BF16 (2^-8), and to FP16 the same weight for all (2^-11)
+        assert (np.abs(out[s] - want) <= want * (2.0 ** -8 + 2.0 ** -10)).all(), (s, n)
+
+
+@pytest.mark.parametrize("apart", [2.0 ** 20, 2.0 ** 24, 2.0 ** 28, 2.0 ** 60])
+@pytest.mark.parametrize("lens", [[500], [9000, 40]])
+def test_decode_uneven_groups(cuda_lib, apart, lens):
+    # Groups of V whose sizes are far apart: each keeps the precision of its own.
+    pa = cuda_lib
+    c = _case(pa, lens, 64, 6, 1, seed=11)
+    N = sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    v = torch.randn(N, 1, 4, 64, generator=g, device="cuda")
+    v *= torch.tensor([apart, 1.0, 1 / apart, apart ** 0.5], device="cuda")[:, None]
+    k = torch.randn(N, 1, 256, generator=g, device="cuda")
+    pa.reshape_and_cache_q4(_bf(k), _bf(v.flatten(-2)), c["kc"], c["vc"], c["slots"])
+    _check(_decode(pa, c), c)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 24, 2.0 ** 28, 2.0 ** 60])
+@pytest.mark.parametrize("at", [0, 250, 499])
+def test_decode_large_token_of_negligible_weight(cuda_lib, size, at):
+    # One token whose V is far larger than the others' and whose weight is e^-60 or so.
+    pa = cuda_lib
+    c = _case(pa, [500], 64, 4, 1, seed=12)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    u = torch.randn(256, generator=g, device="cuda")
+    c["q"] = _bf(u + 0.05 * torch.randn(1, 4, 256, generator=g, device="cuda"))
+    k = torch.randn(500, 1, 256, generator=g, device="cuda")
+    v = torch.randn(500, 1, 256, generator=g, device="cuda")
+    k[at] = -u * (60 / 0.0625 / float(u @ u))
+    v[at] *= size
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    _check(_decode(pa, c), c)
+
+
+@pytest.mark.parametrize("small,large", [(1e-24, 1e15), (1e-30, 1e30)])
+def test_decode_tiny_steps_beside_a_large_constant_group(cuda_lib, small, large):
+    pa = cuda_lib
+    c = _case(pa, [300], 64, 6, 1, seed=13)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.randn(300, 1, 256, generator=g, device="cuda") * small
+    v[:, :, 64:128] = torch.randn(300, 1, 1, generator=g, device="cuda") * large
+    k = torch.randn(300, 1, 256, generator=g, device="cuda")
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    _check(_decode(pa, c), c)
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e-30, 1e30, 3e36])
+def test_decode_sizes_of_v(cuda_lib, size):
+    c = _case(cuda_lib, [700, 3], 64, 6, 1, seed=14, scale_v=size)
+    _check(_decode(cuda_lib, c), c)
+
+
+def test_decode_scores_that_grow_along_the_keys(cuda_lib):
+    # The largest score moves again and again, and with it the sums of every group.
+    pa = cuda_lib
+    n = 3000
+    c = _case(pa, [n], 64, 6, 1, seed=15)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    grow = torch.linspace(0, 24, n, device="cuda")[:, None, None]
+    k = torch.randn(n, 1, 256, generator=g, device="cuda") * (1 + grow)
+    v = torch.randn(n, 1, 256, generator=g, device="cuda") * torch.exp2(2 * grow)
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    for scale in (0.0625, 0.01, -0.03):
+        _check(_decode(pa, c, scale), c, scale)
