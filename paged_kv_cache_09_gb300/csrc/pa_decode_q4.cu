@@ -887,8 +887,8 @@ __global__ void __launch_bounds__(256) decode_q4_merge_kernel(const __grid_const
         }
 #pragma unroll
         for (int k = 0; k < kRound; ++k) {
+            // (an empty part is zeros; one of weight 0 counts too: its sums may be NaN)
             const float e = ml[k].x == -CUDART_INF_F ? 0.f : ex2_approx(ml[k].x - M);
-            if (e == 0.f) continue;  // an empty part's sums are not used
             L = fmaf(e, ml[k].y, L);
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {

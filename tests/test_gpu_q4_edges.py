@@ -1,0 +1,45 @@
+"""Decode over the 4-bit cache at the ends of its range."""
+import pytest
+import torch
+
+from test_gpu_q4 import _bf, _case, _decode
+from test_gpu_q4_accuracy import _check
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------ NaN
+def test_decode_nan_value_of_vanishing_weight(cuda_lib):
+    # The first keys outweigh the rest by e^200: the NaN is in another part, of weight 0 in fp32.
+    pa = cuda_lib
+    c = _case(pa, [9000], 64, 8, 2, seed=1)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(256, generator=g)
+    c["q"] = _bf(q.expand(1, 8, 256))
+    x = torch.randn(9000, 2, 256, generator=g)
+    x[:8] += (q * (200 / 0.0625 / float(q @ q)))[None, None]
+    y = torch.randn(9000, 2, 256, generator=g)
+    pa.reshape_and_cache_q4(_bf(x), _bf(y), c["kc"], c["vc"], c["slots"])
+    fine = c["vc"].clone()
+    for at in range(100, 9000, 300):
+        y[at, 1, 70] = float("nan")
+        c["vc"].copy_(fine)
+        pa.reshape_and_cache_q4(_bf(x[at:at + 1]), _bf(y[at:at + 1]), c["kc"], c["vc"], c["slots"][at:at + 1])
+        nan = torch.isnan(_decode(pa, c)[0])
+        assert nan[4:, 64:128].all(), at
+        assert not nan[:4].any() and not nan[4:, :64].any() and not nan[4:, 128:].any(), at
+
+
+@pytest.mark.parametrize("n,first,last", [(9000, 4000, 5000), (9000, 0, 9000), (300, 128, 256), (40, 0, 40)])
+def test_decode_nan_keys(cuda_lib, n, first, last):
+    # Whole shares of NaN keys in head 1: its query heads are NaN, head 0's as they are without.
+    pa = cuda_lib
+    c = _case(pa, [n], 64, 8, 2, seed=2)
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(n, 2, 256, generator=g) for _ in range(2))
+    k[first:last, 1] = float("nan")
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    out = _decode(pa, c)
+    assert torch.isnan(out[0, 4:]).all()
+    one = dict(c, q=c["q"][:, :4], kc=c["kc"][:, :1].contiguous(), vc=c["vc"][:, :1].contiguous())
+    _check(out[:, :4], one)
