@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
             all += t;
         }
         all *= p.num_kv_heads;
+        if (all == 0) return false;  // padding entries only
         const uint32_t ctas = (uint32_t)min((uint64_t)gridDim.x, (all + kMinShare - 1) / kMinShare);
         lead = 0;
         if (all >= 2 * kMinShare * (uint64_t)ctas)

@@ -43,3 +43,21 @@ def test_decode_nan_keys(cuda_lib, n, first, last):
     assert torch.isnan(out[0, 4:]).all()
     one = dict(c, q=c["q"][:, :4], kc=c["kc"][:, :1].contiguous(), vc=c["vc"][:, :1].contiguous())
     _check(out[:, :4], one)
+
+
+# ------------------------------------------------------------------------------ lengths
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [0] * 40])
+@pytest.mark.parametrize("max_len", [1, 100, 9000])
+def test_decode_of_padding_entries_alone(cuda_lib, lens, max_len):
+    pa = cuda_lib
+    c = _case(pa, [64], 64, 8, 2, seed=3)
+    S = len(lens)
+    q = torch.randn(S, 8, 256, device="cuda").to(torch.bfloat16)
+    need = pa.decode_q4_workspace_size(S, 8, 2, 256, 64, max_len)
+    for fill in (0, 0xFF):
+        out = torch.full_like(q, 3.0)
+        pa.decode_q4(q, c["kc"], c["vc"], torch.full((S, 141), -1, dtype=torch.int32, device="cuda"),
+                     torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.0625, max_len, out=out,
+                     workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+        assert not out.any()
+    assert pa.device_errors() == 0
