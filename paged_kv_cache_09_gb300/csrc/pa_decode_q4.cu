@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     // Places before each pair's tiles, and the segment's first place in its pair.
     int lead, v0;
     int seq, g, t0, seq_len, tiles;
+    bool refused = false;  // more tiles than a share can be found of
     // Finds them, with the tiles and lengths of the first 32 sequences given; false: no share.
     auto place = [&](int first_tiles, int first_len) {
         uint64_t all = 0, used = 0;
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         all += lead * used * p.num_kv_heads;
         if (all > 0x7fffffffu) {  // (as many tiles as 600 GB of cache hold, counting shared pages again)
             if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
+            refused = true;
             return false;
         }
         const uint32_t total = (uint32_t)all;
@@ -444,7 +446,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
         guess = false;
     }
-    if (!placed) return;
+    if (!placed) {
+        if (refused) {  // tells the merge so: the pairs have no parts
+            const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
+            for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < pairs; x += gridDim.x * kThreads)
+                p.info[x] = make_int2(0, 0);
+        }
+        return;
+    }
     first_loads();
     make_q();
     __syncthreads();  // q is ready

@@ -61,3 +61,23 @@ def test_decode_of_padding_entries_alone(cuda_lib, lens, max_len):
                      workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
         assert not out.any()
     assert pa.device_errors() == 0
+
+
+def test_decode_lengths_past_the_limit_leave_the_output(cuda_lib):
+    # 16 x 2^27 tiles: refused on the device, with the parts of an earlier call in the workspace.
+    pa = cuda_lib
+    bs, S = 1 << 20, 16
+    kc, vc = (torch.zeros(pa.q4_cache_shape(1, bs, 1), dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = torch.zeros(S, 2048, dtype=torch.int32, device="cuda")
+    q = torch.randn(S, 4, 256, device="cuda").to(torch.bfloat16)
+    most = 2**31 - 1
+    ws = torch.zeros(pa.decode_q4_workspace_size(S, 4, 1, 256, bs, most), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 3.0)
+    lens = torch.full((S,), 5000, dtype=torch.int32, device="cuda")
+    pa.decode_q4(q, kc, vc, table, lens, 0.0625, most, out=out, workspace=ws)
+    assert pa.device_errors() == 0 and not out.any()
+    out.fill_(3.0)
+    lens.fill_(most)
+    pa.decode_q4(q, kc, vc, table, lens, 0.0625, most, out=out, workspace=ws)
+    assert pa.device_errors() == pa.DEVERR_SEQLEN
+    assert (out == 3.0).all()
