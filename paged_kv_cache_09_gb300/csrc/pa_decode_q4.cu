@@ -266,7 +266,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
             lead = (int)min((uint32_t)kPairCost, (uint32_t)min(all, (uint64_t)0xffffffffu) / (2 * ctas));
         all += lead * used * p.num_kv_heads;
         if (all > 0x7fffffffu) {  // (as many tiles as 600 GB of cache hold, counting shared pages again)
-            if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
             refused = true;
             return false;
         }
@@ -437,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     const int actual = seq_tiles(p, lane, &len, blockIdx.x == 0 && warp == 0);
     bool guess = p.num_seqs == 1, placed;
     for (;;) {
+        refused = false;
         placed = guess ? place(lane == 0 ? tiles_of(p, p.max_seq_len) : 0, p.max_seq_len)
                        : place(actual, len);
         if (placed) {
@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         guess = false;
     }
     if (!placed) {
-        if (refused) {  // tells the merge so: the pairs have no parts
+        if (refused) {  // (not by a guess) tells the merge so: the pairs have no parts
+            if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
             const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
             for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < pairs; x += gridDim.x * kThreads)
                 p.info[x] = make_int2(0, 0);

@@ -81,3 +81,18 @@ def test_decode_lengths_past_the_limit_leave_the_output(cuda_lib):
     pa.decode_q4(q, kc, vc, table, lens, 0.0625, most, out=out, workspace=ws)
     assert pa.device_errors() == pa.DEVERR_SEQLEN
     assert (out == 3.0).all()
+
+
+def test_decode_short_sequence_under_the_largest_length(cuda_lib):
+    # One sequence of 100 keys whose table has room for 2^31 - 1: no error.
+    pa = cuda_lib
+    bs, hkv = 1 << 16, 16
+    kc, vc = (torch.zeros(pa.q4_cache_shape(1, bs, hkv), dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = torch.zeros(1, 1 << 15, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 16, 256, device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn(100, hkv, 256, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pa.reshape_and_cache_q4(k, v, kc, vc, torch.arange(100, device="cuda"))
+    lens = torch.tensor([100], dtype=torch.int32, device="cuda")
+    out = pa.decode_q4(q, kc, vc, table, lens, 0.0625, 2**31 - 1)
+    assert pa.device_errors() == 0
+    assert torch.equal(out, pa.decode_q4(q, kc, vc, table, lens, 0.0625, 100))
