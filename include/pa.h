@@ -481,8 +481,8 @@ int pa_gather_cache_q4(const void *k_cache, const void *v_cache, int64_t page_st
  * head's and group's relative to the largest of its own, so that groups and tokens of V may be of
  * any sizes; a head's q is FP16 relative to its largest value (values down to 2^-24 of it exact,
  * smaller ones off by up to 2^-34 of it).  |scale * q| of 2^116 and more is not representable and
- * gives NaN.  Lengths that come to more than 2^31 tiles of 16 tokens over all sequences and KV
- * heads set PA_DEVERR_SEQLEN, and only the rows of padding entries are written.
+ * gives NaN.  Lengths that come to 2^31 tiles of 16 tokens or more over all sequences and KV heads
+ * set PA_DEVERR_SEQLEN, and only the rows of padding entries are written.
  */
 size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                    int block_size, int max_seq_len);

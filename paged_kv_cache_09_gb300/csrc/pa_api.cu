@@ -1131,6 +1131,9 @@ int pa_test_hook(int decode_skip_stage, int prefill_skip_unit, int decode_consum
         return PA_ERR_CUDA;
     return PA_OK;
 }
+int pa_test_decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas) {
+    return pa::decode_q4_pair_lead(tiles, pairs, ctas);
+}
 #endif
 
 }  // extern "C"

@@ -205,6 +205,17 @@ __device__ __forceinline__ int seq_tiles(const Params &p, int s, int *len, bool 
     return tiles_of(p, L);
 }
 
+constexpr uint32_t kMaxTiles = 0x7fffffffu;  // of all pairs, with their leads (9.9 TB, shared pages counted again)
+
+// Places ahead of each of `pairs` pairs' tiles, when `tiles` (at most kMaxTiles) are cut over `ctas`
+// shares: half a share at most, and none where they would not be numbered in 31 bits.
+__host__ __device__ __forceinline__ int pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas) {
+    if (tiles < (uint64_t)2 * kMinShare * ctas) return 0;
+    const uint32_t half = tiles / (2 * ctas);
+    const uint32_t lead = half < (uint32_t)kPairCost ? half : (uint32_t)kPairCost;
+    return tiles + lead * pairs > kMaxTiles ? 0 : (int)lead;
+}
+
 // CTA b's first tile when `total` tiles are cut over `ctas`: the first r shares have one more.
 struct Shares {
     uint32_t q, r;
@@ -260,16 +271,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
         }
         all *= p.num_kv_heads;
         if (all == 0) return false;  // padding entries only
-        const uint32_t ctas = (uint32_t)min((uint64_t)gridDim.x, (all + kMinShare - 1) / kMinShare);
-        lead = 0;
-        if (all >= 2 * kMinShare * (uint64_t)ctas)
-            lead = (int)min((uint32_t)kPairCost, (uint32_t)min(all, (uint64_t)0xffffffffu) / (2 * ctas));
-        all += lead * used * p.num_kv_heads;
-        if (all > 0x7fffffffu) {  // (as many tiles as 600 GB of cache hold, counting shared pages again)
+        if (all > kMaxTiles) {
             refused = true;
             return false;
         }
-        const uint32_t total = (uint32_t)all;
+        const uint32_t ctas = min(gridDim.x, ((uint32_t)all + kMinShare - 1) / kMinShare);
+        lead = pair_lead((uint32_t)all, used * p.num_kv_heads, ctas);
+        const uint32_t total = (uint32_t)(all + lead * used * p.num_kv_heads);
         if (blockIdx.x >= ctas) return false;
         shares.q = total / ctas;
         shares.r = total - shares.q * ctas;
@@ -963,6 +971,7 @@ size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads
 cudaError_t set_decode_q4_test_hook(int skip_pair) {
     return cudaMemcpyToSymbol(g_test_skip_pair, &skip_pair, sizeof skip_pair);
 }
+int decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas) { return pair_lead(tiles, pairs, ctas); }
 #endif
 
 cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream) {

@@ -424,9 +424,12 @@ cudaError_t launch_prefill(const CUtensorMap *tmaps, const PrefillArgs &a, cudaS
 // Exported to the failure-path tests as
 //     extern "C" int pa_test_hook(int decode_skip_stage, int prefill_skip_unit,
 //                                 int decode_consumer_delay_ns);
-// The product library has neither the hooks nor this entry point.
+// and, for a host test of the 4-bit decode's work split,
+//     extern "C" int pa_test_decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas);
+// The product library has neither the hooks nor these entry points.
 cudaError_t set_decode_test_hook(int skip_stage, int consumer_delay_ns);
 cudaError_t set_decode_q4_test_hook(int skip_pair);
+int decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas);  // (host only)
 cudaError_t set_prefill_test_hook(int skip_unit);
 #endif
 
