@@ -737,22 +737,23 @@ def _q4_workspace(workspace, need, dev, device):
 
 def decode_q4(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, out=None,
               workspace=None):
-    """q=1 decode over the 4-bit cache (see pa_decode_q4).  Returns out [S, Hq, 256] BF16;
-    rows of sequences of length 0 are zeros."""
+    """q=1 decode over the 4-bit cache (see pa_decode_q4): row s of q [S, Hq, 256] attends to
+    sequence s of seq_lens [S] and of block_table (S rows or more).  Returns out [S, Hq, 256]
+    BF16; rows of sequences of length 0 are zeros.  (A step's tokens are packed: with idle entries
+    before others, row t belongs to sequence seq_idx[t] instead, and is moved there first.)"""
     lib, dev = _lib or load(), _device()
     S, hq, d = _need(q, "q", _BF16, 3, dev)
     q = q.contiguous()
     pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
     width, row = _table(block_table, "block_table", S, dev)
-    if _need(seq_lens, "seq_lens", _I32, 1, dev)[0] < S or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be contiguous, one entry per sequence")
+    lens = _vector(seq_lens, "seq_lens", _I32, S, dev)  # one entry per row of q
     if width * bs < max_seq_len:
         raise ValueError("block_table rows are too short for max_seq_len")
     out = _q4_out(out, q, dev)
     _keep, ws, ws_bytes = _q4_workspace(
         workspace, lambda: decode_q4_workspace_size(S, hq, hkv, d, bs, max_seq_len), dev, q.device)
     _raise(lib.pa_decode_q4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ps, pages,
-                            block_table.data_ptr(), row, seq_lens.data_ptr(), S, int(max_seq_len),
+                            block_table.data_ptr(), row, lens, S, int(max_seq_len),
                             hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes, _stream()),
            "pa_decode_q4")
     return out

@@ -96,3 +96,50 @@ def test_decode_short_sequence_under_the_largest_length(cuda_lib):
     out = pa.decode_q4(q, kc, vc, table, lens, 0.0625, 2**31 - 1)
     assert pa.device_errors() == 0
     assert torch.equal(out, pa.decode_q4(q, kc, vc, table, lens, 0.0625, 100))
+
+
+# ------------------------------------------------------------------------------ steps with idle entries
+def _step(pa, new, num_tokens, seed):
+    """Prep, norm + rotation and write of one token for each live entry over filled caches."""
+    S, bs, pages = len(new), 16, 60
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+    computed = [70, 0, 33, 48, 15][:S]
+    table = torch.arange(S * 8, device="cuda", dtype=torch.int32).view(S, 8)
+    kc, vc = (torch.zeros(pa.q4_cache_shape(pages, bs, 2), dtype=torch.uint8, device="cuda") for _ in range(2))
+    slots = torch.arange(S * 8 * bs, device="cuda")
+    pa.reshape_and_cache_q4(rn(S * 8 * bs, 2, 256), rn(S * 8 * bs, 2, 256), kc, vc, slots)
+    tensor = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    step = pa.batch_input_prep(tensor(computed), tensor(new), [table], [bs],
+                               [torch.arange(S * 8, pages, device="cuda", dtype=torch.int32)], num_tokens)
+    q, k, v = rn(num_tokens, 8, 256), rn(num_tokens, 2, 256), rn(num_tokens, 2, 256)
+    angle = torch.arange(100, device="cuda")[:, None] * 10000.0 ** (-torch.arange(32, device="cuda") / 32)
+    w = rn(256)
+    q = pa.qk_norm_rope_cache(q, k, v, w, w, torch.cat([angle.cos(), angle.sin()], 1), step["positions"], 1e-6,
+                              kc, vc, step["slot_mappings"][0])
+    return dict(q=q, kc=kc, vc=vc, bt=table, table=table.cpu().numpy(), lens=step["seq_lens"], bs=bs), step
+
+
+def test_decode_step_with_idle_entries_behind(cuda_lib):
+    pa = cuda_lib
+    c, _ = _step(pa, [1, 1, 1, 0, 0], 5, 1)
+    out = _decode(pa, c)
+    assert not out[3:].any()
+    live = dict(c, q=c["q"][:3], table=c["table"][:3], bt=c["bt"][:3], lens=c["lens"][:3])
+    _check(out[:3], live)
+    assert pa.device_errors() == 0
+
+
+def test_decode_step_with_an_idle_entry_between(cuda_lib):
+    # Row 1 of the packed q belongs to entry 2: refused as it is, right when moved there.
+    pa = cuda_lib
+    c, step = _step(pa, [1, 0, 1, 1, 0], 3, 2)
+    packed = c["q"]
+    for rows in (packed, torch.cat([packed] * 2)):
+        with pytest.raises(ValueError):
+            pa.decode_q4(rows, c["kc"], c["vc"], c["bt"], c["lens"], 0.0625, 100)
+    c["q"] = torch.zeros(5, 8, 256, dtype=torch.bfloat16, device="cuda")
+    c["q"][step["seq_idx"].long()] = packed
+    out = _decode(pa, c)
+    _check(out, c)
+    assert not out[[1, 4]].any() and pa.device_errors() == 0
