@@ -496,10 +496,14 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
 /*
  * pa_prefill_chunk_q4, pa_prefill_varlen_q4 -- pa_prefill_chunk and pa_prefill_varlen over
  * the 4-bit cache (the chunk's own tokens included, which must be in it).  The sequences'
- * keys and values and the queries are first expanded into FP16 in the workspace (each query
- * row and each KV head of a sequence scaled by a power of two: values are rounded to 2^-12,
- * an eighth of BF16's step), which the prefill kernel then reads as pages.  The expansion is
- * linear in the keys, the attention quadratic.  Arguments and errors are those of the BF16
+ * keys and values and the queries are first expanded into FP16 in the workspace, each query row
+ * and K and V of each KV head of a sequence scaled by a power of two, which the prefill kernel
+ * then reads as pages.  The expansion is linear in the keys, the attention quadratic.
+ * Precision: values are off by up to 2^-11 of themselves (BF16: 2^-8) while they are at least
+ * 2^-28 of the largest of their query row, or of the KV head's K or V in that sequence, and by up
+ * to 2^-39 of that largest below; weights by up to 2^-11 of themselves, and by up to 2^-32 of the
+ * row's largest below 2^-21 of it.  (So dims or tokens of V 2^-28 times as large as others lose
+ * bits here, which they do not in pa_decode_q4.)  Arguments and errors are those of the BF16
  * calls, but: page_stride is in bytes, and the workspace is required.  With the bytes that
  * the size functions give (1 KB per key and KV head, 0.5 KB per query row and head, and room
  * for split items) items may be split; with less than the expansion needs the call is

@@ -73,9 +73,10 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q4_kernel(const Q4GatherAr
 
 // ---- prefill: FP16 operands from the 4-bit cache and BF16 queries
 //
-// FP16 holds the values to 2^-12 (BF16 to 2^-9) but spans fewer binades, so each query row and
+// FP16 holds the values to 2^-11 (BF16 to 2^-8) but spans fewer binades, so each query row and
 // each KV head of a sequence is scaled by the power of two that brings its largest magnitude
-// to [2^14, 2^15).  Values down to 2^-28 of the largest keep 11 bits.
+// to [2^14, 2^15).  Values down to 2^-28 of the largest keep 11 bits; smaller ones are off by up
+// to 2^-39 of it.
 
 // The power of two that brings magnitudes up to `top` below 2^15 (1 for 0 and non-finite).
 __device__ __forceinline__ float scale_for(float top) {

@@ -127,3 +127,64 @@ def test_decode_scores_that_grow_along_the_keys(cuda_lib):
     pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
     for scale in (0.0625, 0.01, -0.03):
         _check(_decode(pa, c, scale), c, scale)
+
+
+# ------------------------------------------------------------------------------ prefill
+def _prefill_uneven(pa, rows, n, v, seed=0, scale=0.0625, far=None):
+    """A causal chunk over values v [n, 2, 256]; returns its outputs and the plain ones."""
+    c = _case(pa, [n], 64, 12, 2, seed=seed, rows=rows)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = torch.randn(n, 2, 256, generator=g, device="cuda")
+    if far is not None:  # a key that outweighs no other: scores 60 below in every row
+        u = torch.randn(256, generator=g, device="cuda")
+        c["q"] = _bf(u + 0.05 * torch.randn(rows, 12, 256, generator=g, device="cuda"))
+        k[far] = -u * (60 / 0.0625 / float(u @ u))
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    out = pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], n - rows, True, scale)
+    ref, tol = _q4.prefill(_q4.f64(c["q"]), c["kc"].cpu().numpy(), c["vc"].cpu().numpy(), 64, c["table"],
+                           [0, rows], [n], True, scale)
+    assert pa.device_errors() == 0
+    return _q4.f64(out), ref, tol
+
+
+def _group_errors(out, ref):
+    """Error norm over reference norm of each group of 64 dims, all rows and heads together."""
+    norm = lambda x: np.linalg.norm(x.reshape(-1, 4, 64), axis=(0, 2))
+    return norm(out - ref) / norm(ref)
+
+
+# The whole of a group's errors: a rounding to BF16, at most 2^-8 / sqrt(3) where errors are spread
+# evenly over half a step, and a fifth for the FP16 operands (2^-11 / sqrt(3) each).
+GROUP = 2.0 ** -8 / 3 ** 0.5 * 1.2
+
+
+@pytest.mark.parametrize("apart", [2.0 ** 8, 2.0 ** 16, 2.0 ** 22])
+def test_prefill_uneven_groups(cuda_lib, apart):
+    # Down to 2^-28 of the head's largest value FP16 keeps its 11 bits.
+    g = torch.Generator(device="cuda").manual_seed(5)
+    v = torch.randn(700, 2, 4, 64, generator=g, device="cuda")
+    v *= torch.tensor([apart, 1.0, 4.0, apart ** 0.5], device="cuda")[:, None]
+    out, ref, tol = _prefill_uneven(cuda_lib, 200, 700, v.flatten(-2), seed=21)
+    assert (np.abs(out - ref) <= tol).all()
+    assert (_group_errors(out, ref) <= GROUP).all(), _group_errors(out, ref)
+
+
+@pytest.mark.parametrize("at", [0, 300, 499])
+def test_prefill_large_token_of_negligible_weight(cuda_lib, at):
+    g = torch.Generator(device="cuda").manual_seed(6)
+    v = torch.randn(700, 2, 256, generator=g, device="cuda")
+    v[at] *= 2.0 ** 20
+    out, ref, _ = _prefill_uneven(cuda_lib, 200, 700, v, seed=22, far=at)
+    assert (_group_errors(out, ref) <= GROUP).all(), _group_errors(out, ref)
+
+
+def test_prefill_values_below_the_range_of_their_head(cuda_lib):
+    # A group 2^-36 times as large as another: off by up to 2^-39 of the head's largest value, and
+    # the others keep their own.
+    g = torch.Generator(device="cuda").manual_seed(7)
+    v = torch.randn(700, 2, 4, 64, generator=g, device="cuda")
+    v *= torch.tensor([1.0, 2.0 ** -36, 0.5, 2.0 ** -10], device="cuda")[:, None]
+    out, ref, tol = _prefill_uneven(cuda_lib, 200, 700, v.flatten(-2), seed=23)
+    largest = float(v.abs().max()) * 1.1  # (and what the quantiser adds)
+    assert (np.abs(out - ref) <= tol + 2.0 ** -39 * largest).all()
+    assert (_group_errors(out, ref)[[0, 2, 3]] <= GROUP).all(), _group_errors(out, ref)
