@@ -479,6 +479,14 @@ def _device():
         return -2
 
 
+def _i32(x, name):
+    """x as an int that a C int holds (ctypes would wrap it)."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must be within 32 bits, got {x}")
+    return x
+
+
 def _need(t, name, dtype, ndim, dev):
     """t's shape, if it is a `dtype` tensor of ndim dims on device dev, the current one."""
     try:
@@ -543,7 +551,7 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     query_start_loc, positions, seq_idx, slot_mappings (one per group) and pages_taken (int32
     [groups]); `out` may pass that dict back in to reuse its tensors."""
     lib, dev = _lib or load(), _device()
-    G, T = len(block_tables), int(num_tokens)
+    G, T = len(block_tables), _i32(num_tokens, "num_tokens")
     if len(block_sizes) != G or len(free_pages) != G or not 1 <= G <= 8:
         raise ValueError("one block size and one free list per group, 1..8 groups")
     computed = _vector(num_computed, "num_computed", _I32, None, dev)
@@ -565,7 +573,7 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     pointers, ints, longs = _ARRAYS[G]
     _raise(lib.pa_batch_input_prep(
         computed, new, S, G, pointers(*[t.data_ptr() for t in block_tables]),
-        longs(*strides), ints(*widths), ints(*map(int, block_sizes)),
+        longs(*strides), ints(*widths), ints(*[_i32(b, "block size") for b in block_sizes]),
         pointers(*free), ints(*[f.shape[0] for f in free_pages]), T,
         _vector(out["seq_lens"], "seq_lens", _I32, S, dev),
         _vector(out["query_start_loc"], "query_start_loc", _I32, S + 1, dev),
@@ -714,7 +722,7 @@ def gather_cache_q4(k_cache, v_cache, slot_mapping, k_out=None, v_out=None):
 def decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                              max_seq_len) -> int:
     return int(load().pa_decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                  block_size, max_seq_len))
+                                                  block_size, _i32(max_seq_len, "max_seq_len")))
 
 
 def _q4_out(out, q, dev):
@@ -747,13 +755,14 @@ def decode_q4(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, ou
     pages, ps, bs, hkv = _q4_cache(k_cache, v_cache, dev)
     width, row = _table(block_table, "block_table", S, dev)
     lens = _vector(seq_lens, "seq_lens", _I32, S, dev)  # one entry per row of q
+    max_seq_len = _i32(max_seq_len, "max_seq_len")
     if width * bs < max_seq_len:
         raise ValueError("block_table rows are too short for max_seq_len")
     out = _q4_out(out, q, dev)
     _keep, ws, ws_bytes = _q4_workspace(
         workspace, lambda: decode_q4_workspace_size(S, hq, hkv, d, bs, max_seq_len), dev, q.device)
     _raise(lib.pa_decode_q4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ps, pages,
-                            block_table.data_ptr(), row, lens, S, int(max_seq_len),
+                            block_table.data_ptr(), row, lens, S, max_seq_len,
                             hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes, _stream()),
            "pa_decode_q4")
     return out
@@ -762,7 +771,8 @@ def decode_q4(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, ou
 def prefill_q4_workspace_size(q_len, q_start, causal, num_q_heads, num_kv_heads, head_dim,
                               block_size) -> int:
     """Bytes of workspace for prefill_chunk_q4 (the expanded operands, and room for split items)."""
-    return int(load().pa_prefill_q4_workspace_size(int(q_len), int(q_start), int(bool(causal)),
+    return int(load().pa_prefill_q4_workspace_size(_i32(q_len, "q_len"), _i32(q_start, "q_start"),
+                                                   int(bool(causal)),
                                                    num_q_heads, num_kv_heads, head_dim,
                                                    block_size))
 
@@ -772,6 +782,8 @@ def prefill_chunk_q4(q, k_cache, v_cache, block_table, q_start, causal, scale, o
     """Causal (or full) chunk attention of one sequence over the 4-bit cache (see
     pa_prefill_chunk_q4).  Without a workspace, one of prefill_q4_workspace_size bytes is
     allocated for the call."""
+    _check(q, "q", _BF16, 3)
+    _check(block_table, "block_table", _I32)
     bt = block_table.reshape(1, -1)
     return prefill_varlen_q4(q, k_cache, v_cache, bt, [0, q.shape[0]],
                              [int(q_start) + q.shape[0]], causal, scale, out, workspace)
@@ -781,8 +793,8 @@ def _varlen_lens(cu_seqlens_q, seq_lens_k):
     B = len(seq_lens_k)
     if len(cu_seqlens_q) != B + 1:
         raise ValueError("cu_seqlens_q: num_seqs + 1 offsets")
-    return ((ctypes.c_int32 * (B + 1))(*[int(x) for x in cu_seqlens_q]),
-            (ctypes.c_int32 * max(B, 1))(*[int(x) for x in seq_lens_k]), B)
+    return ((ctypes.c_int32 * (B + 1))(*[_i32(x, "cu_seqlens_q") for x in cu_seqlens_q]),
+            (ctypes.c_int32 * max(B, 1))(*[_i32(x, "seq_lens_k") for x in seq_lens_k]), B)
 
 
 def prefill_varlen_q4_workspace_size(cu_seqlens_q, seq_lens_k, causal, num_q_heads, num_kv_heads,

@@ -143,3 +143,15 @@ def test_decode_step_with_an_idle_entry_between(cuda_lib):
     out = _decode(pa, c)
     _check(out, c)
     assert not out[[1, 4]].any() and pa.device_errors() == 0
+
+
+def test_lengths_past_32_bits_are_refused(cuda_lib):
+    pa = cuda_lib
+    c = _case(pa, [20], 1 << 16, 6, 1, seed=9, max_blocks=(1 << 16) + 1)
+    with pytest.raises(ValueError):
+        _decode(pa, c, max_len=2**32 + 20)
+    for q_start in (2**32 + 19, 2**31 - 1):
+        with pytest.raises(ValueError):
+            pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], q_start, True, 0.0625)
+    with pytest.raises(pa.PAError):
+        pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], -1, True, 0.0625)
