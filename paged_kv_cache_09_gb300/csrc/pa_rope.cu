@@ -16,8 +16,11 @@
 //     out_j = inv (x_j A_j + x_p B_j),   A_j = w_j cos, B_j = +- w_p sin   (p: j's partner),
 // the partners are exchanged as packed BF16, before any arithmetic, and the arithmetic is on pairs.
 // 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 28.7 us, 4.8 TB/s (43 with the
-// weights applied to every row, 29.6 with the rows summed one by one).  16 warps an SM with 8 rows
-// each on their way move more than 20 or 24 with fewer (33 and 40 us).  16 tokens: 2.4 us.
+// weights applied to every row, 29.6 with the rows summed one by one); into a 4-bit cache 33.6 us,
+// without a cache 26.3.  32 + 8 + 8 heads 45.9 us, 16 + 4 + 4 24.8, 12 + 2 + 2 20.5 (4.5, 4.2 and
+// 3.5 TB/s: warps with fewer rows of a token on their way).  16 warps an SM with 8 rows each on
+// their way move more than 20 or 24 with fewer (33 and 40 us): a row on its way is registers.
+// 16 tokens: 2.3 us.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -28,7 +31,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBatch = 6;  // query rows of a warp that are loaded a token ahead
+constexpr int kBatch = 6;  // query rows of a warp that are loaded a token ahead (24 heads over 4 warps)
 
 // Pairs of fp32 in one register pair.
 typedef unsigned long long f32x2;
@@ -286,18 +289,22 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 
 template <int kD>
 cudaError_t launch_dim(RopeArgs a, cudaStream_t stream) {
-    const int rows = a.num_q_heads + (a.cache ? 2 : 1) * a.num_kv_heads;
     constexpr int per = kWarps * (256 / kD);
-    // A large call: a token over as few CTAs as give each warp kBatch query rows.  A small one:
-    // more CTAs a token, one row a warp.
-    const int y = a.num_tokens >= 512 ? (a.num_q_heads + per * kBatch - 1) / (per * kBatch)
-                                      : (rows + per - 1) / per;
+    // A small call: a row a warp, as many CTAs a token as that takes.  A large one: a token over as
+    // few CTAs as give each warp kBatch query rows, and four CTAs an SM that go from token to token.
+    // Small is what is resident at once, with the rows of a call that writes the cache (so that the
+    // calls with and without a cache sum a row in the same order).  24 + 4 + 4 heads of 256, 8 CTAs
+    // a token, small and large: 16 tokens 2.3 and 2.9 us, 64 2.7 and 3.0, 128 4.5 and 2.9, 256 7.3
+    // and 3.4, 512 14.3 and 5.5; 32 + 8 + 8 heads, 12 CTAs: 16 tokens 2.3 and 2.8, 64 4.2 and 2.8;
+    // 16 + 4 + 4 of 64, 2 CTAs: 128 tokens 2.3 and 2.3, 384 4.0 and 2.8.
+    const int y_small = (a.num_q_heads + 2 * a.num_kv_heads + per - 1) / per;
+    const bool small = (int64_t)a.num_tokens * y_small <= 4 * a.num_sms;
+    const int y = small ? y_small : (a.num_q_heads + per * kBatch - 1) / (per * kBatch);
     constexpr int one = 256 / kD;  // rows of a warp
     const int step = y * per;
     a.shift_k = (a.num_q_heads + one - 1) / one * one % step;
     a.shift_v = (a.shift_k + (a.num_kv_heads + one - 1) / one * one) % step;
-    // (Four resident CTAs an SM.)
-    const int x = a.num_tokens >= 512 ? std::min(a.num_tokens, std::max(1, 4 * a.num_sms / y)) : a.num_tokens;
+    const int x = small ? a.num_tokens : std::min(a.num_tokens, std::max(1, 4 * a.num_sms / y));
     const dim3 grid(x, y), block(kWarps * 32);
     if (a.interleaved) {
         if (a.cache == 0) return launch_pdl(qk_norm_rope_kernel<kD, true, 0>, grid, block, 0, stream, a);
