@@ -24,17 +24,20 @@
 // q becomes FP16 after scaling each head by a power of two (largest value in [2^13, 2^14)):
 // exact for values down to 2^-24 of the head's largest, and below that off by less than
 // 2^-34 of it.
-// The weights p s become FP16 (off by 2^-11 of them at most), scaled so that they neither overflow
-// nor vanish: p = 2^(x - m - kLag), m the largest score rounded up to a whole number and at most
-// kLag behind, so p <= 1; and p s F, F a power of two for each head and group that leaves the
-// group's largest p s at 2^-1 at least, so that the smallest FP16 is 2^-23 of it, whatever the
-// other groups and the tokens without weight hold.  (One reference for all groups, from the
-// largest score and the largest step taken apart, left groups 2^24 apart 5% off.)  While steps are
-// alike F comes from them alone, for all heads; where they are not, from the scores too.  One vote
-// a step finds whether anything moves: a score above m + kLag, or a step that could give a weight
-// above 2^15.  s and F are applied to both heads of a lane by products of pairs (1% of the time less
-// than one by one).  Against a form without F, all of this costs 2% of a long batch's time (16
-// sequences: 67.2 us) and 0.8 us of a short sequence's.
+// The weights p s become FP16 (off by 2^-11 of them at most), scaled so that they neither
+// overflow nor vanish: p = 2^(x - m - kLag), m the largest score and at most kLag behind, so p <=
+// 1, and the p of a token that outweighs all others is a power of two, which leaves p s as exact
+// as s; and p s F, F for each head and group, that leaves the group's largest weight at 1 at
+// least, so that the smallest FP16 is 2^-24 of it, whatever the other groups and the tokens
+// without weight hold.  (One reference for all groups, from the largest score and the largest
+// step taken apart, left groups 2^24 apart 5% off.)  While steps are alike F comes from them
+// alone, for all heads; where they are not, from the scores too.  It is a power of two but where
+// it follows m over tokens that are not alike.  One vote a step finds whether anything moves: a
+// score above m + kLag, or a step that could give a weight above 2^15.  s and F are applied to
+// both heads of a lane by products of pairs (1% of the time less than one by one).  Against a
+// form without F, all of this costs 2% of a long batch's time (16 sequences: 67.2 us) and 0.8 us
+// of a short sequence's.
+//
 // Work split: the tiles of all (sequence, KV head) pairs in a row, cut evenly over two CTAs an
 // SM, so that uneven lengths leave no SM idle; each CTA finds its share from the lengths.  A pair
 // also costs its beginning (table, q, the first loads' way, the merge): it counts as kPairCost
@@ -167,9 +170,15 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t (&x)[4]) {
 __device__ __forceinline__ float exp2_whole(float e) {
     return e < -126.f ? 0.f : __uint_as_float((uint32_t)((int)e + 127) << 23);
 }
-// log2 of a power of two.
+// floor(log2) of a positive number.
 __device__ __forceinline__ float log2_whole(float f) {
     return (float)((int)(__float_as_uint(f) >> 23) - 127);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
                 }
-                const float n0 = fmaxf(m0, ceilf(mx0)), n1 = fmaxf(m1, ceilf(mx1));
+                const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
                 const float d0 = n0 == m0 ? 0.f : n0 - m0, d1 = n1 == m1 ? 0.f : n1 - m1;
                 m0 = n0;
                 m1 = n1;
@@ -611,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                         f0[gg] = f1[gg] = __uint_as_float(min(253, 2 * 127 + 14 - kSpare - e) << 23);
                     }
                 }
-                // While every step times F is 2^8 at least, the token that moved m (p > 2^-9) gives the
-                // group a weight above 2^-1, and F can stay.
+                // While every step times F is 2^8 at least, the token that moved m (p = 2^-8) gives the
+                // group a weight of 1 at least, and F can stay.
                 uint32_t low01 = 0x7f807f80u, low23 = low01;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -633,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                                   bf16_lo(low23) * fminf(f0[2], f1[2]) >= 256.f &&
                                   bf16_hi(low23) * fminf(f0[3], f1[3]) >= 256.f;
                 if (!__all_sync(0xffffffffu, even && (i == 0 || !large))) {
-                    // The groups' largest x + floor(log2 s): p s is 2^(t - m - kLag) to twice that.
+                    // The groups' largest x + floor(log2 s): their p s is 2^(t - m - kLag) to twice that.
                     float t0[4], t1[4];
 #pragma unroll
                     for (int gg = 0; gg < 4; ++gg) t0[gg] = t1[gg] = -CUDART_INF_F;
@@ -659,21 +668,24 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
                             t0[gg] = fmaxf(t0[gg], __shfl_xor_sync(0xffffffffu, t0[gg], sh));
                             t1[gg] = fmaxf(t1[gg], __shfl_xor_sync(0xffffffffu, t1[gg], sh));
                         }
-                        // F goes up only to follow m, and down where this step's largest needs it.
-                        auto moved = [&](float &f, float n, float d, float top) {
-                            const float old = i == 0 ? 126.f : log2_whole(f) + d;
-                            const float e = fmaxf(-122.f, fminf(fminf(old, 126.f),
-                                                                n + kLag + kTop - 1.f - floorf(top)));
-                            f = exp2_whole(e);
-                            return exp2_whole(e - old);
+                        // F goes up only to follow m (it need not be a power of two then), and down
+                        // where this step's largest needs it.
+                        auto moved = [&](float &f, float n, float d, float al, float top) {
+                            const float keep = i == 0 ? 0x1p126f : f * ex2_approx(d);
+                            const float e = floorf(n + kLag + kTop - 1.f - top);
+                            const float to = fminf(keep, exp2_whole(fmaxf(-122.f, fminf(126.f, e))));
+                            const float g = to == keep ? 1.f : al * fminf(to / f, 0x1p127f);
+                            f = to;
+                            return g;
                         };
-                        g0[gg] = moved(f0[gg], n0, d0, t0[gg]);
-                        g1[gg] = moved(f1[gg], n1, d1, t1[gg]);
+                        g0[gg] = moved(f0[gg], n0, d0, al0, t0[gg]);
+                        g1[gg] = moved(f1[gg], n1, d1, al1, t1[gg]);
                     }
                 }
                 // Steps that cannot give a weight above 2^15 (p is 1 at most) with this lane's heads.
                 auto safe = [&](int gg) {
-                    return min(254u, 2 * 127 + 15 - (__float_as_uint(fmaxf(f0[gg], f1[gg])) >> 23)) << 7;
+                    const uint32_t up = (__float_as_uint(fmaxf(f0[gg], f1[gg])) + 0x7fffff) >> 23;
+                    return min(254u, 2 * 127 + 15 - up) << 7;
                 };
                 safe01 = safe(0) | safe(1) << 16;
                 safe23 = safe(2) | safe(3) << 16;
@@ -782,8 +794,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
             float *row0 = red_o + (warp * kDecMaxGroup + 2 * c) * kMergeRow + 8 * r;
 #pragma unroll
             for (int gg = 0; gg < 4; ++gg) {
-                const float u0 = __uint_as_float((254u << 23) - __float_as_uint(f0[gg]));  // 1 / F
-                const float u1 = __uint_as_float((254u << 23) - __float_as_uint(f1[gg]));
+                const float u0 = rcp_approx(f0[gg]), u1 = rcp_approx(f1[gg]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     auto row = [&](int h, float low, float u) {

@@ -188,3 +188,34 @@ def test_prefill_values_below_the_range_of_their_head(cuda_lib):
     largest = float(v.abs().max()) * 1.1  # (and what the quantiser adds)
     assert (np.abs(out - ref) <= tol + 2.0 ** -39 * largest).all()
     assert (_group_errors(out, ref)[[0, 2, 3]] <= GROUP).all(), _group_errors(out, ref)
+
+
+# ------------------------------------------------------------------------------ one token alone
+@pytest.mark.parametrize("scale_v", [1e-30, 1.0, 1e30])
+def test_decode_of_one_token_is_its_row(cuda_lib, scale_v):
+    # Its weight p is a power of two but for the rounding of the exponent's argument (m + 8, so 2^-21
+    # where m is below 8), and p s in FP16 is exact: before its rounding the result is off by 2^-20
+    # of |lo| + s n at most.
+    pa = cuda_lib
+    c = _case(pa, [1] * 40, 16, 16, 4, seed=24, scale_v=scale_v)
+    out, cache = _q4.f64(_decode(pa, c)), c["vc"].cpu().numpy()
+    for s in range(40):
+        for g in range(4):
+            n, step, lo = (x[0] for x in _q4_bounds.parts(cache, 16, c["table"][s], 1, g))
+            want = _q4.value(n[None], step[None], lo[None])
+            size = np.abs(lo).repeat(64) + step.repeat(64) * n
+            assert (_q4_bounds.excess(out[s, 4 * g:4 * g + 4], want) <= 2.0 ** -20 * size).all(), (s, g)
+
+
+@pytest.mark.parametrize("n,at", [(3000, 0), (3000, 1777), (3000, 2999), (40, 20), (9000, 8190)])
+def test_decode_of_a_token_that_outweighs_the_others_is_its_row(cuda_lib, n, at):
+    pa = cuda_lib
+    c = _case(pa, [n], 64, 8, 2, seed=25)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    u = torch.randn(256, generator=g, device="cuda")
+    c["q"] = _bf(u.expand(1, 8, 256))
+    k, v = (torch.randn(n, 2, 256, generator=g, device="cuda") for _ in range(2))
+    k[at] += u * (200 / 0.0625 / float(u @ u))  # e^200: the others' weights are 0 in fp32
+    pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
+    row = pa.gather_cache_q4(c["kc"], c["vc"], c["slots"][at:at + 1])[1]
+    assert torch.equal(_decode(pa, c), row.repeat_interleave(4, 1))
