@@ -560,10 +560,12 @@ int pa_get_device_errors(unsigned int *bits, int clear, void *stream);
 
 /*
  * pa_set_kernel_events -- measurement hook.  The next pa_decode, pa_decode_append,
- * pa_prefill_chunk or pa_prefill_varlen call (or 4-bit decode or prefill call) made by this host thread records `start` on
- * its stream immediately before it launches its main kernel (the split-context decode
- * kernel, or the prefill kernel) and `stop` immediately after that launch, then forgets
- * both.  Inside a stream capture the records carry cudaEventRecordExternal, so they
+ * pa_prefill_chunk or pa_prefill_varlen call, or 4-bit decode or prefill call, made by this
+ * host thread records `start` on its stream immediately before it launches its main kernel
+ * (the split-context or streaming decode kernel, or the prefill kernel) and `stop` immediately
+ * after that launch, then forgets both.  A 4-bit prefill's expansion, two kernels before the
+ * main one, is not between them (that of later batches is, when a call has more than 32
+ * chunks).  Inside a stream capture the records carry cudaEventRecordExternal, so they
  * become event record nodes that every replay of the graph records.  The arguments are
  * cudaEvent_t handles owned by the caller; passing NULL, NULL cancels a pending hook.
  * Both or neither must be NULL.

@@ -42,8 +42,9 @@
 // SM, so that uneven lengths leave no SM idle; each CTA finds its share from the lengths.  A pair
 // also costs its beginning (table, q, the first loads' way, the merge): it counts as kPairCost
 // tiles, half a share at most, ahead of the pair's first, so that CTAs with many short pairs get
-// fewer tiles (64 sequences of 1..2048 keys, 8 KV heads, in a form without F: 62 us without it, 53.5,
-// 46, 42 and 44 us with 4, 8, 16 and 28).  Shares below two rounds of the warps' tiles stay even:
+// fewer tiles (with 0, 4, 8, 16 and 28: 64 sequences of 1..2048 keys, 8 KV heads, 69, 65, 54, 44
+// and 45 us; 16 of 1..4096, 4 KV heads, 29, 22, 18, 17 and 17; 64 of which one has 32768 and the
+// others up to 200, 60, 38, 31, 26 and 26).  Shares below two rounds of the warps' tiles stay even:
 // there a CTA's time is its rounds (one sequence of 1701 keys, shares of 8).  A pair
 // that one CTA holds whole is finished there; the others leave a part per CTA (sums relative to
 // their reference), which a second kernel merges.
@@ -857,10 +858,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
 //   kSplit > 1: that many warps for each 64 dims of a row take its parts in turn, for the
 //               latency of many parts
 //   kSplit = 1: two warps a row (128 dims each), 4 rows a CTA
-// The fewer the rows, the more parts each may have: 8 up to a row an SM (24 rows of 76 parts: a
-// step of 16.5 us, 26.3 with 1), 4 up to 8 rows an SM (384 rows of 5 parts: 67.2 us, 69.5 with 8,
-// 67.3 with 1, but one long sequence among short ones has many parts again), 1 beyond (2048
-// rows: 42 us, 53 with 8).
+// The fewer the rows, the more parts each may have: 8 up to a row an SM, 4 up to 8 rows an SM, 1
+// beyond.  A step's us with 8, 4 and 1 (6 query heads a KV head):
+//   sequences of 1..4096 keys    24 rows 11.1 11.3 12.5   144 14.3 15.3 16.7   192 18.9 18.6 19.2
+//     384 19.3 17.5 17.8   768 27.8 24.7 23.1   1200 39.8 35.1 31.9   1536 48.1 42.2 38.2
+//   one of 32768, others to 200   192 17.5 20.4 24.9   384 18.7 21.0 24.4   768 22.0 22.7 24.8
+//     1200 24.2 22.9 25.0   1536 27.1 23.6 26.0   3072 38.4 31.2 29.3
+// so between 2 and 8 rows an SM 4 loses up to 9% to 1 where lengths are alike, and gains as much
+// where one is long.
 template <int kSplit>
 __global__ void __launch_bounds__(256) decode_q4_merge_kernel(const __grid_constant__ Params p) {
     constexpr bool kFew = kSplit > 1;

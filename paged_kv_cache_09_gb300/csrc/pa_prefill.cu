@@ -961,9 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l *= alpha;
                         m_used = m_new;
                     }
-                    const float nmu = m_used == -CUDART_INF_F
-                                          ? 0.f
-                                          : -m_used;
+                    const float nmu = m_used == -CUDART_INF_F ? 0.f : -m_used;
                     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
                     uint32_t hi[16], lo[16];
 #pragma unroll
