@@ -58,8 +58,8 @@
 // because the extra warps cost instructions (spills, exchanges, loads), and issue is what bounds.
 //
 // Measured, calls one after another, 4 KV heads of 6 query heads unless said: 16 sequences of
-// 4K..32K keys 68.4 us (streaming kernel 5.0 TB/s); 64 of 1..2048 keys, 8 KV heads of 4, pages of
-// 16: 43.5 us; one of 32768 keys 17.3 us; one of 1701 keys 11.1 us.  The short ones are latency:
+// 4K..32K keys 68.8 us (streaming kernel 4.9 TB/s); 64 of 1..2048 keys, 8 KV heads of 4, pages of
+// 16: 43.7 us; one of 32768 keys 17.3 us; one of 1701 keys 11.0 us.  The short ones are latency:
 // finding the share 1.5 us, q 1.2, one step 2, the CTA's merge 1, and the second kernel.
 #include <math_constants.h>
 
