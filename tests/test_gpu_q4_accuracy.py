@@ -219,3 +219,26 @@ def test_decode_of_a_token_that_outweighs_the_others_is_its_row(cuda_lib, n, at)
     pa.reshape_and_cache_q4(_bf(k), _bf(v), c["kc"], c["vc"], c["slots"])
     row = pa.gather_cache_q4(c["kc"], c["vc"], c["slots"][at:at + 1])[1]
     assert torch.equal(_decode(pa, c), row.repeat_interleave(4, 1))
+
+
+@pytest.mark.parametrize("bs,hq,hkv,rows,lens", [
+    (64, 12, 2, [300], [1500]), (832, 24, 4, [40], [9000]), (16, 16, 8, [1, 129, 0, 64, 200], [700, 129, 33, 65, 1300]),
+    (7, 5, 1, [128, 17], [128, 300])])
+def test_prefill_flat_scores_count_every_token(cuda_lib, bs, hq, hkv, rows, lens):
+    # As the decode's: dim d of row i counts the tokens t <= its position with t % 256 == d.
+    pa = cuda_lib
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    c = _case(pa, lens, bs, hq, hkv, seed=bs, rows=cu[-1])
+    c["q"].zero_()
+    v = torch.zeros(sum(lens), hkv, 256, device="cuda")
+    t = torch.cat([torch.arange(n) for n in lens]).cuda()
+    v[torch.arange(sum(lens), device="cuda"), :, t % 256] = 15
+    pa.reshape_and_cache_q4(_bf(torch.randn(sum(lens), hkv, 256, device="cuda")), _bf(v), c["kc"], c["vc"], c["slots"])
+    out = _q4.f64(pa.prefill_varlen_q4(c["q"], c["kc"], c["vc"], c["bt"], cu, lens, True, 0.0625))
+    for b, n in enumerate(lens):
+        seen = n - rows[b] + 1 + np.arange(rows[b])  # keys of each row
+        count = (seen[:, None] + 255 - np.arange(256)) // 256
+        want = (15.0 * count / seen[:, None])[:, None]
+        got = out[cu[b]:cu[b + 1]]
+        assert (np.abs(got - want) <= want * (2.0 ** -8 + 2.0 ** -10)).all(), b
+    assert pa.device_errors() == 0
