@@ -369,6 +369,8 @@ int pa_prefill_plan_pieces(int q_len, int q_start, int causal, int num_q_heads,
  *                      HOST arrays of num_groups entries (1 <= num_groups <= 8), holding
  *                      device pointers and sizes; read during the call only
  *   pages_taken        int32 [num_groups], device
+ * Outputs and tables must not overlap the lengths, the free lists or one another (the seq_lens of
+ * one step are not the num_computed of the next in place: PA_ERR_INVALID_ARG).
  * Errors on the device: a free list that runs out gives entries and slots of -1 and sets
  * PA_DEVERR_NO_PAGES; a logical page >= max_blocks[g] takes no page, gives slot -1 and sets
  * PA_DEVERR_POSITION, as does a negative entry of a page held before or of the free list;

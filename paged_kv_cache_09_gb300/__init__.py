@@ -549,7 +549,8 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     receives the new pages, a block size and an int32 list of free pages.  num_tokens: rows
     of the per-token outputs, at least the step's tokens.  Returns a dict with seq_lens,
     query_start_loc, positions, seq_idx, slot_mappings (one per group) and pages_taken (int32
-    [groups]); `out` may pass that dict back in to reuse its tensors."""
+    [groups]); `out` may pass that dict back in to reuse its tensors, but none of them may be an
+    input (the seq_lens of one step are copied to be the num_computed of the next)."""
     lib, dev = _lib or load(), _device()
     G, T = len(block_tables), _i32(num_tokens, "num_tokens")
     if len(block_sizes) != G or len(free_pages) != G or not 1 <= G <= 8:

@@ -711,6 +711,32 @@ int pa_batch_input_prep(const int32_t *num_computed, const int32_t *num_new, int
     if (!query_start_loc || (num_seqs > 0 && (!num_computed || !num_new || !seq_lens)) ||
         (num_tokens > 0 && (!positions || !seq_idx)))
         return PA_ERR_INVALID_ARG;
+    // Every CTA reads the lengths and the free lists for itself, so nothing may be written over
+    // them, nor may an entry of one group's table be another's.
+    const auto meet = [](const void *p, int64_t n, const void *q, int64_t m) {  // n and m bytes
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(p), b0 = reinterpret_cast<uintptr_t>(q);
+        return p && q && n > 0 && m > 0 && a0 < b0 + m && b0 < a0 + n;
+    };
+    const auto written = [&](const void *p, int64_t n) {
+        bool hit = meet(p, n, seq_lens, 4LL * num_seqs) || meet(p, n, query_start_loc, 4LL * num_seqs + 4) ||
+                   meet(p, n, positions, 4LL * num_tokens) || meet(p, n, seq_idx, 4LL * num_tokens) ||
+                   meet(p, n, pages_taken, 4LL * num_groups);
+        for (int g = 0; g < num_groups; ++g) hit = hit || meet(p, n, slot_mappings[g], 8LL * num_tokens);
+        return hit;
+    };
+    if (written(num_computed, 4LL * num_seqs) || written(num_new, 4LL * num_seqs)) return PA_ERR_INVALID_ARG;
+    for (int g = 0; g < num_groups; ++g) {
+        // (of a table whose rows lie apart, the first: other tensors may lie between them)
+        const int64_t bytes = num_seqs < 1 ? 0 : 4LL * max_blocks[g] * (bt_strides[g] == max_blocks[g] ? num_seqs : 1);
+        if (written(free_pages[g], 4LL * num_free[g]) || written(block_tables[g], bytes) ||
+            meet(block_tables[g], bytes, num_computed, 4LL * num_seqs) ||
+            meet(block_tables[g], bytes, num_new, 4LL * num_seqs))
+            return PA_ERR_INVALID_ARG;
+        for (int h = 0; h < num_groups; ++h)
+            if (meet(block_tables[g], bytes, free_pages[h], 4LL * num_free[h]) ||
+                (h != g && bytes > 0 && block_tables[g] == block_tables[h]))
+                return PA_ERR_INVALID_ARG;
+    }
     DeviceInfo dev;
     if (int rc = device_info(&dev)) return rc;
     a.num_computed = num_computed;

@@ -155,3 +155,21 @@ def test_lengths_past_32_bits_are_refused(cuda_lib):
             pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], q_start, True, 0.0625)
     with pytest.raises(pa.PAError):
         pa.prefill_chunk_q4(c["q"], c["kc"], c["vc"], c["bt"][0], -1, True, 0.0625)
+
+
+def test_prep_lengths_of_the_step_before(cuda_lib):
+    # Many CTAs read the lengths: in place they are refused, a copy is taken.
+    pa = cuda_lib
+    S, T = 600, 9000
+    new = torch.full((S,), 15, dtype=torch.int32, device="cuda")
+    table = torch.full((S, 8), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(4 * S, dtype=torch.int32, device="cuda")
+    out = pa.batch_input_prep(torch.zeros_like(new), new, [table], [16], [free], T)
+    assert out["pages_taken"].tolist() == [S]
+    with pytest.raises(pa.PAError):
+        pa.batch_input_prep(out["seq_lens"], new, [table], [16], [free[S:]], T, out=out)
+    out = pa.batch_input_prep(out["seq_lens"].clone(), new, [table], [16], [free[S:]], T, out=out)
+    assert out["seq_lens"].tolist() == [30] * S and out["pages_taken"].tolist() == [S]
+    assert out["positions"].view(S, 15)[:, 0].tolist() == [15] * S
+    assert torch.equal(table[:, :2], torch.stack([free[:S], free[S:2 * S]], 1))
+    assert pa.device_errors() == 0
