@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
 //   sequences of 1..4096 keys    24 rows 11.1 11.3 12.5   144 14.3 15.3 16.7   192 18.9 18.6 19.2
 //     384 19.3 17.5 17.8   768 27.8 24.7 23.1   1200 39.8 35.1 31.9   1536 48.1 42.2 38.2
 //   one of 32768, others to 200   192 17.5 20.4 24.9   384 18.7 21.0 24.4   768 22.0 22.7 24.8
-//     1200 24.2 22.9 25.0   1536 27.1 23.6 26.0   3072 38.4 31.2 29.3
+//     1200 24.2 22.9 25.0   1536 27.1 23.6 26.0
 // so between 2 and 8 rows an SM 4 loses up to 9% to 1 where lengths are alike, and gains as much
 // where one is long.
 template <int kSplit>
