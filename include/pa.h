@@ -434,6 +434,38 @@ int pa_qk_norm_rope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, 
                           void *stream);
 
 /*
+ * pa_qk_norm_mrope, pa_qk_norm_mrope_cache -- pa_qk_norm_rope and pa_qk_norm_rope_cache with a
+ * position on each of several axes (time, height and width of an image's or a video's tokens; text
+ * tokens have the same on all).  Frequency i turns by the position on axis axes[i]: the pair it
+ * turns takes cos_sin[positions[axes[i]][t]][i] and [rotary_dim / 2 + i].
+ *   positions   int32 [num_axes, num_tokens], axes position_stride elements apart (at least
+ *               num_tokens).  A token with a negative one on any axis is padding; otherwise one >=
+ *               max_position leaves the token's outputs as they were and sets PA_DEVERR_POSITION.
+ *   num_axes    1 .. PA_MAX_AXES
+ *   axes        HOST array of rotary_dim / 2 entries below num_axes, read during the call only
+ * All other arguments, checks and errors are those of the calls with one position.
+ */
+#define PA_MAX_AXES 4
+
+int pa_qk_norm_mrope(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                     const pa_bf16 *q_weight, const pa_bf16 *k_weight, float weight_bias, float eps,
+                     const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                     const int32_t *positions, int64_t position_stride, int num_axes,
+                     const uint8_t *axes, int num_tokens, int num_q_heads, int num_kv_heads,
+                     int head_dim, pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out,
+                     int64_t k_out_stride, void *stream);
+
+int pa_qk_norm_mrope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                           const pa_bf16 *v, int64_t v_stride, const pa_bf16 *q_weight,
+                           const pa_bf16 *k_weight, float weight_bias, float eps,
+                           const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                           const int32_t *positions, int64_t position_stride, int num_axes,
+                           const uint8_t *axes, int num_tokens, int num_q_heads, int num_kv_heads,
+                           int head_dim, pa_bf16 *q_out, int64_t q_out_stride, int cache_format,
+                           void *k_cache, void *v_cache, int64_t page_stride, int64_t num_pages,
+                           const int64_t *slot_mapping, int block_size, void *stream);
+
+/*
  * The 4-bit cache.  A row (one token of one KV head, 256 values) takes PA_Q4_ROW_BYTES
  * instead of 512: it is cut into 4 groups of 64 dims, and group g keeps its minimum lo and
  * a step s = bf16((max - lo) / 15), both BF16, and a code n = clamp(rint((x - lo) / s), 0,
@@ -528,6 +560,106 @@ size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const in
 
 int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
                          int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                         int64_t bt_stride, const int32_t *cu_seqlens_q,
+                         const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The 8-bit cache.  A value is a code c, an 8-bit float e4m3 (4 bits of exponent, bias 7, 3 of
+ * fraction; 0x7f and 0xff are NaN, no infinities), times a power of two that PA_Q8_TOKENS
+ * tokens of a page and one KV head share, K and V apart: c * 2^(b - 127), b the block's scale
+ * byte (255: the block reads as NaN).  257/512 of the bytes of BF16, nearly.
+ *
+ * K and V caches are separate arrays of codes, [num_pages, block_size, num_kv_heads, 256] bytes in
+ * the last three dimensions, page_stride bytes apart (a multiple of 16, at least block_size *
+ * num_kv_heads * 256, below 2^40), 16-byte aligned; block_size is at most 2^20.  Their scales are
+ * [num_pages, ceil(block_size / PA_Q8_TOKENS), num_kv_heads] bytes, scale_stride bytes apart (at
+ * most page_stride): block i of a page holds its offsets PA_Q8_TOKENS * i and following.  Block
+ * tables, slots and errors are those of the BF16 cache.
+ */
+#define PA_Q8_TOKENS 16
+
+/*
+ * pa_reshape_and_cache_q8 -- KV write of new tokens into the 8-bit cache.  key, value BF16
+ * [num_tokens, num_kv_heads, 256], tokens key_stride / value_stride elements apart (multiples of
+ * 8).  For each block that new tokens fall into, and each KV head, K and V apart:
+ *   - the scale byte becomes the smallest with every new finite value within 448 * 2^(b - 127),
+ *     1 at least, but not less than it was;
+ *   - new values are rounded to the nearest code (ties to even); infinities and NaN give NaN codes;
+ *   - where the byte has grown, the codes of the block's other rows are rounded to the new
+ *     scale (exact, but for codes that fall below 2^-6).
+ * A write to a block's first row begins the block anew, as does one to a block whose byte is 255:
+ * its byte follows from the new values alone, and the codes of the rows that are not written are
+ * left as they are, without meaning until they are written.  (So tokens of a sequence are
+ * written in order, as a serving layer does; a page needs no clearing before its next use.)
+ * Tokens may stand in the call in any order; of several with one slot the last one counts and the
+ * others are ignored.  A negative slot is skipped; one outside the pool is skipped and sets
+ * PA_DEVERR_SLOT.  The caches, the scales and the new rows must not overlap one another.
+ */
+int pa_reshape_and_cache_q8(const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value,
+                            int64_t value_stride, void *k_cache, void *v_cache, uint8_t *k_scales,
+                            uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                            int64_t num_pages, const int64_t *slot_mapping, int num_tokens,
+                            int num_kv_heads, int head_dim, int block_size, void *stream);
+
+/*
+ * pa_gather_cache_q8 -- reads tokens back by slot: k_out, v_out BF16 [num_tokens, num_kv_heads,
+ * 256], contiguous, receive c * 2^(b - 127) rounded to BF16 (exact within BF16's normal range);
+ * zeros for a negative slot, and for one outside the pool, which sets PA_DEVERR_SLOT.
+ */
+int pa_gather_cache_q8(const void *k_cache, const void *v_cache, const uint8_t *k_scales,
+                       const uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                       int64_t num_pages, const int64_t *slot_mapping, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, pa_bf16 *k_out,
+                       pa_bf16 *v_out, void *stream);
+
+/*
+ * pa_decode_q8 -- pa_decode over the 8-bit cache: the attention of q over the values that the
+ * cache's codes stand for, accumulated in fp32.  The newest tokens must be in the cache
+ * (pa_reshape_and_cache_q8 first).  Arguments and errors are those of pa_decode_q4: seq_lens[s] may
+ * be 0, a padding entry, whose rows of out become zeros; the workspace is sized by
+ * pa_decode_q8_workspace_size.  Weights times scales of V are rounded to FP16 relative to each
+ * head's largest (2^-11 of them at most down to 2^-20 of that largest); a head's q is FP16 relative
+ * to its largest value (values down to 2^-24 of it exact, smaller ones off by up to 2^-34 of it).
+ * Values of V of 2^100 and more may overflow, and outputs below 2^-110 may come out as 0.
+ */
+size_t pa_decode_q8_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_seq_len);
+
+int pa_decode_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache, const uint8_t *k_scales,
+                 const uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                 int64_t num_pages, const int32_t *block_table, int64_t bt_stride,
+                 const int32_t *seq_lens, int num_seqs, int max_seq_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * pa_prefill_chunk_q8, pa_prefill_varlen_q8 -- pa_prefill_chunk and pa_prefill_varlen over the
+ * 8-bit cache (the chunk's own tokens included, which must be in it).  As in the 4-bit calls the
+ * sequences' keys and values and the queries are first expanded into FP16 in the required
+ * workspace, each query row and K and V of each KV head of a sequence scaled by a power of two.
+ * Precision: K and V are exact while a block's scale is at least 2^-15 of the head's largest in that
+ * sequence (smaller values lose bits below 2^-39 of the largest); queries and weights as in the
+ * 4-bit calls, as are the other arguments, errors and what a NaN in V reaches.
+ */
+size_t pa_prefill_q8_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size);
+
+int pa_prefill_chunk_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                        const uint8_t *k_scales, const uint8_t *v_scales, int64_t page_stride,
+                        int64_t scale_stride, int64_t num_pages, const int32_t *block_table,
+                        int q_len, int q_start, int causal, int num_q_heads, int num_kv_heads,
+                        int head_dim, int block_size, float scale, pa_bf16 *out, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+size_t pa_prefill_varlen_q8_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
+                                           int num_seqs, int causal, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size);
+
+int pa_prefill_varlen_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                         const uint8_t *k_scales, const uint8_t *v_scales, int64_t page_stride,
+                         int64_t scale_stride, int64_t num_pages, const int32_t *block_table,
                          int64_t bt_stride, const int32_t *cu_seqlens_q,
                          const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
                          int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,

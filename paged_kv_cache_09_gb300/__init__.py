@@ -26,6 +26,12 @@ Functions (names follow the C ABI):
     reshape_and_cache_q4(...) (in place), gather_cache_q4(...) -> key, value
     decode_q4(...), prefill_chunk_q4(...), prefill_varlen_q4(...) and their
     *_workspace_size functions: as the calls without _q4
+    8-bit cache (float8_e4m3fn codes and uint8 scales, shapes of q8_cache_shapes(...)):
+    reshape_and_cache_q8(...) (in place), gather_cache_q8(...) -> key, value
+    decode_q8(...), prefill_chunk_q8(...), prefill_varlen_q8(...) and their
+    *_workspace_size functions: as the calls without _q8
+    qk_norm_mrope(...), qk_norm_mrope_cache(...): qk_norm_rope(_cache) with positions on several
+    axes; mrope_axes(sections, ...) -> the axis of each frequency
     device_errors(clear=True)
 """
 from __future__ import annotations
@@ -47,12 +53,17 @@ __all__ = ["load", "build", "slot_mapping", "decode_input_prep", "reshape_and_ca
            "qk_norm_rope_cache", "q4_cache_shape", "reshape_and_cache_q4", "gather_cache_q4",
            "decode_q4", "decode_q4_workspace_size", "prefill_chunk_q4",
            "prefill_q4_workspace_size", "prefill_varlen_q4", "prefill_varlen_q4_workspace_size",
+           "Q8_TOKENS", "q8_cache_shapes", "reshape_and_cache_q8", "gather_cache_q8", "decode_q8",
+           "decode_q8_workspace_size", "prefill_chunk_q8", "prefill_q8_workspace_size",
+           "prefill_varlen_q8", "prefill_varlen_q8_workspace_size", "mrope_axes", "qk_norm_mrope",
+           "qk_norm_mrope_cache",
            "LIB_PATH"]
 
 LIB_PATH = _build.LIB
 DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_POSITION = 1, 2, 4, 8, 16
 DEVERR_LAYOUT, DEVERR_NO_PAGES = 32, 64
 Q4_ROW_BYTES = 144  # PA_Q4_ROW_BYTES: a token of one KV head in the 4-bit cache
+Q8_TOKENS = 16  # PA_Q8_TOKENS: tokens of a page under one scale of the 8-bit cache
 ERR_TIMEOUT = 4  # PA_ERR_TIMEOUT
 
 _lib = None
@@ -122,6 +133,24 @@ def load():
             "pa_prefill_varlen_q4_workspace_size": ([P, P, i32, i32, i32, i32, i32, i32], sz),
             "pa_prefill_varlen_q4": ([P, P, P, i64, i64, P, i64, P, P, i32, i32, i32, i32, i32,
                                       i32, f32, P, P, sz, P], i32),
+            "pa_reshape_and_cache_q8": ([P, i64, P, i64, P, P, P, P, i64, i64, i64, P, i32, i32,
+                                         i32, i32, P], i32),
+            "pa_gather_cache_q8": ([P, P, P, P, i64, i64, i64, P, i32, i32, i32, i32, P, P, P],
+                                   i32),
+            "pa_decode_q8_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
+            "pa_decode_q8": ([P, P, P, P, P, i64, i64, i64, P, i64, P, i32, i32, i32, i32, i32,
+                              i32, f32, P, P, sz, P], i32),
+            "pa_prefill_q8_workspace_size": ([i32, i32, i32, i32, i32, i32, i32], sz),
+            "pa_prefill_chunk_q8": ([P, P, P, P, P, i64, i64, i64, P, i32, i32, i32, i32, i32,
+                                     i32, i32, f32, P, P, sz, P], i32),
+            "pa_prefill_varlen_q8_workspace_size": ([P, P, i32, i32, i32, i32, i32, i32], sz),
+            "pa_prefill_varlen_q8": ([P, P, P, P, P, i64, i64, i64, P, i64, P, P, i32, i32, i32,
+                                      i32, i32, i32, f32, P, P, sz, P], i32),
+            "pa_qk_norm_mrope": ([P, i64, P, i64, P, P, f32, f32, P, i32, i32, i32, P, i64, i32,
+                                  ctypes.c_char_p, i32, i32, i32, i32, P, i64, P, i64, P], i32),
+            "pa_qk_norm_mrope_cache": ([P, i64, P, i64, P, i64, P, P, f32, f32, P, i32, i32, i32,
+                                        P, i64, i32, ctypes.c_char_p, i32, i32, i32, i32, P, i64,
+                                        i32, P, P, i64, i64, P, i32, P], i32),
             "pa_copy": ([P, P, sz, P], i32),
             "pa_get_device_errors": ([ctypes.POINTER(ctypes.c_uint), i32, P], i32),
             "pa_set_kernel_events": ([P, P], i32),
@@ -469,6 +498,7 @@ def prefill_plan_pieces(q_len, q_start, causal, num_q_heads, num_kv_heads, block
 
 _BF16, _I32, _I64, _U8, _F32 = (torch.bfloat16, torch.int32, torch.int64, torch.uint8,
                                 torch.float32)
+_E4M3 = torch.float8_e4m3fn
 
 
 def _device():
@@ -586,9 +616,9 @@ def batch_input_prep(num_computed, num_new, block_tables, block_sizes, free_page
     return out
 
 
-def _rope_args(q, k, q_weight, k_weight, cos_sin, positions, dev):
+def _rope_args(q, k, q_weight, k_weight, cos_sin, dev):
     """(tokens, query heads, KV heads, head_dim, token strides of q and k, the addresses of the
-    weights, the table's sizes, the address of the positions)"""
+    weights, the table's sizes)"""
     T, hq, d = _need(q, "q", _BF16, 3, dev)
     kt, hkv, kd = _need(k, "k", _BF16, 3, dev)
     if kt != T or kd != d:
@@ -598,8 +628,35 @@ def _rope_args(q, k, q_weight, k_weight, cos_sin, positions, dev):
     if not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous")
     return (T, hq, hkv, d, qs, ks, _vector(q_weight, "q_weight", _BF16, d, dev),
-            _vector(k_weight, "k_weight", _BF16, d, dev), rows, rot,
-            _vector(positions, "positions", _I32, T, dev))
+            _vector(k_weight, "k_weight", _BF16, d, dev), rows, rot)
+
+
+def _rope_cache(v, k_cache, v_cache, slot_mapping, T, hkv, d, dev):
+    """(token stride of v, address of the slots, cache format, pages, page stride, block size)"""
+    vs = _token_rows(v, "v", T, hkv, d, dev)
+    slots = _vector(slot_mapping, "slot_mapping", _I64, T, dev)
+    fmt = 1 if isinstance(k_cache, torch.Tensor) and k_cache.dtype is _U8 else 0
+    if fmt:
+        pages, ps, bs, heads = _q4_cache(k_cache, v_cache, dev)
+        dim = 256
+    else:
+        shape = _need(k_cache, "k_cache", _BF16, 4, dev)
+        pages, bs, heads, dim = shape
+        strides = k_cache.stride()
+        ps = strides[0]
+        if _need(v_cache, "v_cache", _BF16, 4, dev) != shape or v_cache.stride() != strides or \
+                strides[1:] != (heads * dim, dim, 1):
+            _check_cache(k_cache, v_cache)  # says what is wrong
+            raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if heads != hkv or dim != d:
+        raise ValueError("the caches' heads must be k's")
+    return vs, slots, fmt, pages, ps, bs
+
+
+def _rope_q_out(q_out, q, T, hq, d, dev):
+    if q_out is None:
+        return torch.empty((T, hq, d), dtype=_BF16, device=q.device), hq * d
+    return q_out, _token_rows(q_out, "q_out", T, hq, d, dev)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved=False,
@@ -609,8 +666,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved=
     fp32 [max_position, rotary_dim], cosines then sines.  q_out / k_out may be q / k.  Rows of
     negative positions are left as they were.  Returns (q_out, k_out)."""
     lib, dev = _lib or load(), _device()
-    T, hq, hkv, d, qs, ks, qw, kw, rows, rot, pos = _rope_args(q, k, q_weight, k_weight, cos_sin,
-                                                               positions, dev)
+    T, hq, hkv, d, qs, ks, qw, kw, rows, rot = _rope_args(q, k, q_weight, k_weight, cos_sin, dev)
+    pos = _vector(positions, "positions", _I32, T, dev)
     if q_out is None:
         q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
     if k_out is None:
@@ -630,35 +687,72 @@ def qk_norm_rope_cache(q, k, v, q_weight, k_weight, cos_sin, positions, eps, k_c
     are, go to their slots of the caches (see pa_qk_norm_rope_cache), BF16 [num_pages,
     block_size, Hkv, D] or 4-bit (uint8, q4_cache_shape).  Returns q_out."""
     lib, dev = _lib or load(), _device()
-    T, hq, hkv, d, qs, ks, qw, kw, rows, rot, pos = _rope_args(q, k, q_weight, k_weight, cos_sin,
-                                                               positions, dev)
-    vs = _token_rows(v, "v", T, hkv, d, dev)
-    slots = _vector(slot_mapping, "slot_mapping", _I64, T, dev)
-    fmt = 1 if isinstance(k_cache, torch.Tensor) and k_cache.dtype is _U8 else 0
-    if fmt:
-        pages, ps, bs, heads = _q4_cache(k_cache, v_cache, dev)
-        dim = 256
-    else:
-        shape = _need(k_cache, "k_cache", _BF16, 4, dev)
-        pages, bs, heads, dim = shape
-        strides = k_cache.stride()
-        ps = strides[0]
-        if _need(v_cache, "v_cache", _BF16, 4, dev) != shape or v_cache.stride() != strides or \
-                strides[1:] != (heads * dim, dim, 1):
-            _check_cache(k_cache, v_cache)  # says what is wrong
-            raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if heads != hkv or dim != d:
-        raise ValueError("the caches' heads must be k's")
-    if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
-        qos = hq * d
-    else:
-        qos = _token_rows(q_out, "q_out", T, hq, d, dev)
+    T, hq, hkv, d, qs, ks, qw, kw, rows, rot = _rope_args(q, k, q_weight, k_weight, cos_sin, dev)
+    pos = _vector(positions, "positions", _I32, T, dev)
+    vs, slots, fmt, pages, ps, bs = _rope_cache(v, k_cache, v_cache, slot_mapping, T, hkv, d, dev)
+    q_out, qos = _rope_q_out(q_out, q, T, hq, d, dev)
     _raise(lib.pa_qk_norm_rope_cache(
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, float(weight_bias),
         float(eps), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, pos, T, hq, hkv, d,
         q_out.data_ptr(), qos, fmt, k_cache.data_ptr(), v_cache.data_ptr(), ps, pages, slots, bs,
         _stream()), "pa_qk_norm_rope_cache")
+    return q_out
+
+
+def mrope_axes(sections, in_turn=False):
+    """The axis of each frequency, for qk_norm_mrope: sections[a] frequencies turn by axis a.
+    In runs, axis after axis; or in turn, frequency i by axis i % len(sections) while that axis
+    has frequencies left, and by axis 0 afterwards."""
+    n, count = sum(sections), len(sections)
+    if in_turn:
+        return bytes(i % count if i // count < sections[i % count] else 0 for i in range(n))
+    return bytes(a for a, m in enumerate(sections) for _ in range(m))
+
+
+def _axis_rows(positions, axes, T, rot, dev):
+    """(address of the positions, distance between axes, axes, the frequencies' axes as bytes)"""
+    n, tokens = _need(positions, "positions", _I32, 2, dev)
+    row, col = positions.stride()
+    if tokens != T or not 1 <= n <= 4 or (col != 1 and T > 1):
+        raise ValueError(f"positions must be [axes, {T}], 1 to 4 axes, each row contiguous")
+    axes = bytes(axes)
+    if len(axes) != rot // 2:
+        raise ValueError(f"axes must have an entry for each of {rot // 2} frequencies")
+    return positions.data_ptr(), row if n > 1 else T, n, axes
+
+
+def qk_norm_mrope(q, k, q_weight, k_weight, cos_sin, positions, axes, eps, interleaved=False,
+                  weight_bias=0.0, q_out=None, k_out=None):
+    """qk_norm_rope with positions on several axes (see pa_qk_norm_mrope): positions int32 [axes,
+    T], axes the axis of each of the rotary_dim / 2 frequencies (bytes or ints, see mrope_axes).
+    Returns (q_out, k_out)."""
+    lib, dev = _lib or load(), _device()
+    T, hq, hkv, d, qs, ks, qw, kw, rows, rot = _rope_args(q, k, q_weight, k_weight, cos_sin, dev)
+    pos, stride, n, axes = _axis_rows(positions, axes, T, rot, dev)
+    q_out, qos = _rope_q_out(q_out, q, T, hq, d, dev)
+    if k_out is None:
+        k_out = torch.empty((T, hkv, d), dtype=_BF16, device=k.device)
+    kos = _token_rows(k_out, "k_out", T, hkv, d, dev)
+    _raise(lib.pa_qk_norm_mrope(
+        q.data_ptr(), qs, k.data_ptr(), ks, qw, kw, float(weight_bias), float(eps),
+        cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, pos, stride, n, axes, T, hq, hkv, d,
+        q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream()), "pa_qk_norm_mrope")
+    return q_out, k_out
+
+
+def qk_norm_mrope_cache(q, k, v, q_weight, k_weight, cos_sin, positions, axes, eps, k_cache,
+                        v_cache, slot_mapping, interleaved=False, weight_bias=0.0, q_out=None):
+    """qk_norm_rope_cache with positions on several axes (see qk_norm_mrope).  Returns q_out."""
+    lib, dev = _lib or load(), _device()
+    T, hq, hkv, d, qs, ks, qw, kw, rows, rot = _rope_args(q, k, q_weight, k_weight, cos_sin, dev)
+    pos, stride, n, axes = _axis_rows(positions, axes, T, rot, dev)
+    vs, slots, fmt, pages, ps, bs = _rope_cache(v, k_cache, v_cache, slot_mapping, T, hkv, d, dev)
+    q_out, qos = _rope_q_out(q_out, q, T, hq, d, dev)
+    _raise(lib.pa_qk_norm_mrope_cache(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, float(weight_bias),
+        float(eps), cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, pos, stride, n, axes, T,
+        hq, hkv, d, q_out.data_ptr(), qos, fmt, k_cache.data_ptr(), v_cache.data_ptr(), ps, pages,
+        slots, bs, _stream()), "pa_qk_norm_mrope_cache")
     return q_out
 
 
@@ -831,6 +925,154 @@ def prefill_varlen_q4(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens_k
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ps, pages, block_table.data_ptr(),
         stride, cu, sk, B, causal, hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes,
         _stream()), "pa_prefill_varlen_q4")
+    return out
+
+
+def q8_cache_shapes(num_pages, block_size, num_kv_heads):
+    """Shapes of an 8-bit K or V cache: its codes (float8_e4m3fn) and its scales (uint8)."""
+    return ((num_pages, block_size, num_kv_heads, 256),
+            (num_pages, -(-block_size // Q8_TOKENS), num_kv_heads))
+
+
+def _q8_cache(k_cache, v_cache, k_scales, v_scales, dev):
+    """(the four addresses, page stride and scale stride in bytes, pages), block size, KV heads of
+    an 8-bit cache."""
+    shape = _need(k_cache, "k_cache", _E4M3, 4, dev)
+    pages, bs, heads, dim = shape
+    stride = k_cache.stride()
+    if _need(v_cache, "v_cache", _E4M3, 4, dev) != shape or \
+            (v_cache.stride() != stride and not (k_cache.is_contiguous() and
+                                                 v_cache.is_contiguous())):
+        raise ValueError("k_cache and v_cache must have the same shape and page stride")
+    if dim != 256 or stride[3] != 1 or (heads > 1 and stride[2] != 256) or \
+            (bs > 1 and stride[1] != heads * 256):
+        raise ValueError("each page of an 8-bit cache must be a contiguous [block_size, Hkv, 256] "
+                         "block of codes")
+    want = (pages, (bs - 1) // Q8_TOKENS + 1, heads)
+    got = _need(k_scales, "k_scales", _U8, 3, dev)
+    sstride = k_scales.stride()
+    if got != want or _need(v_scales, "v_scales", _U8, 3, dev) != want or \
+            (v_scales.stride() != sstride and not (k_scales.is_contiguous() and
+                                                   v_scales.is_contiguous())) or \
+            (heads > 1 and sstride[2] != 1) or (want[1] > 1 and sstride[1] != heads):
+        raise ValueError(f"k_scales and v_scales must be {want}, each page contiguous, with the "
+                         "same page stride")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            stride[0] if pages > 1 else bs * heads * 256, sstride[0] if pages > 1 else want[1] * heads,
+            pages), bs, heads
+
+
+def reshape_and_cache_q8(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping):
+    """Quantise key/value [T, Hkv, 256] into the 8-bit caches at slot_mapping (in place; see
+    pa_reshape_and_cache_q8 for how a block's scale follows its tokens)."""
+    lib, dev = _lib or load(), _device()
+    cache, bs, hkv = _q8_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    T, heads, dim = _need(key, "key", _BF16, 3, dev)
+    if heads != hkv or dim != 256:
+        raise ValueError(f"key must be [{T}, {hkv}, 256], got [{T}, {heads}, {dim}]")
+    ks = _row_stride(key, "key", T, hkv, 256)
+    vs = _token_rows(value, "value", T, hkv, 256, dev)
+    _raise(lib.pa_reshape_and_cache_q8(
+        key.data_ptr(), ks, value.data_ptr(), vs, *cache,
+        _vector(slot_mapping, "slot_mapping", _I64, T, dev), T, hkv, 256, bs, _stream()),
+        "pa_reshape_and_cache_q8")
+
+
+def gather_cache_q8(k_cache, v_cache, k_scales, v_scales, slot_mapping, k_out=None, v_out=None):
+    """The tokens at slot_mapping [T] as BF16 (k, v), each [T, Hkv, 256]; zeros for negative
+    slots."""
+    lib, dev = _lib or load(), _device()
+    cache, bs, hkv = _q8_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    slots = _vector(slot_mapping, "slot_mapping", _I64, None, dev)
+    T = slot_mapping.shape[0]
+    k_out = _gather_out(k_out, "k_out", T, hkv, k_cache, dev)
+    v_out = _gather_out(v_out, "v_out", T, hkv, v_cache, dev)
+    _raise(lib.pa_gather_cache_q8(*cache, slots, T, hkv, 256, bs, k_out.data_ptr(),
+                                  v_out.data_ptr(), _stream()), "pa_gather_cache_q8")
+    return k_out, v_out
+
+
+def decode_q8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                             max_seq_len) -> int:
+    return int(load().pa_decode_q8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                  block_size, _i32(max_seq_len, "max_seq_len")))
+
+
+def decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, scale, max_seq_len,
+              out=None, workspace=None):
+    """q=1 decode over the 8-bit cache (see pa_decode_q8): row s of q [S, Hq, 256] attends to
+    sequence s of seq_lens [S] and of block_table (S rows or more).  Returns out [S, Hq, 256]
+    BF16; rows of sequences of length 0 are zeros."""
+    lib, dev = _lib or load(), _device()
+    S, hq, d = _need(q, "q", _BF16, 3, dev)
+    q = q.contiguous()
+    cache, bs, hkv = _q8_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    width, row = _table(block_table, "block_table", S, dev)
+    lens = _vector(seq_lens, "seq_lens", _I32, S, dev)  # one entry per row of q
+    max_seq_len = _i32(max_seq_len, "max_seq_len")
+    if width * bs < max_seq_len:
+        raise ValueError("block_table rows are too short for max_seq_len")
+    out = _q4_out(out, q, dev)
+    _keep, ws, ws_bytes = _q4_workspace(
+        workspace, lambda: decode_q8_workspace_size(S, hq, hkv, d, bs, max_seq_len), dev, q.device)
+    _raise(lib.pa_decode_q8(q.data_ptr(), *cache, block_table.data_ptr(), row, lens, S, max_seq_len,
+                            hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes, _stream()),
+           "pa_decode_q8")
+    return out
+
+
+def prefill_q8_workspace_size(q_len, q_start, causal, num_q_heads, num_kv_heads, head_dim,
+                              block_size) -> int:
+    """Bytes of workspace for prefill_chunk_q8 (the expanded operands, and room for split items)."""
+    return int(load().pa_prefill_q8_workspace_size(_i32(q_len, "q_len"), _i32(q_start, "q_start"),
+                                                   int(bool(causal)), num_q_heads, num_kv_heads,
+                                                   head_dim, block_size))
+
+
+def prefill_chunk_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, q_start, causal, scale,
+                     out=None, workspace=None):
+    """Causal (or full) chunk attention of one sequence over the 8-bit cache (see
+    pa_prefill_chunk_q8).  Without a workspace, one of prefill_q8_workspace_size bytes is
+    allocated for the call."""
+    _check(q, "q", _BF16, 3)
+    _check(block_table, "block_table", _I32)
+    bt = block_table.reshape(1, -1)
+    return prefill_varlen_q8(q, k_cache, v_cache, k_scales, v_scales, bt, [0, q.shape[0]],
+                             [int(q_start) + q.shape[0]], causal, scale, out, workspace)
+
+
+def prefill_varlen_q8_workspace_size(cu_seqlens_q, seq_lens_k, causal, num_q_heads, num_kv_heads,
+                                     head_dim, block_size) -> int:
+    """Bytes of workspace for prefill_varlen_q8 (the expanded operands, and room for split items)."""
+    cu, sk, B = _varlen_lens(cu_seqlens_q, seq_lens_k)
+    return int(load().pa_prefill_varlen_q8_workspace_size(cu, sk, B, int(bool(causal)),
+                                                          num_q_heads, num_kv_heads, head_dim,
+                                                          block_size))
+
+
+def prefill_varlen_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_seqlens_q,
+                      seq_lens_k, causal, scale, out=None, workspace=None):
+    """Chunks of several sequences stacked row-wise in q, over the 8-bit cache (see
+    pa_prefill_varlen_q8).  cu_seqlens_q and seq_lens_k are host sequences of ints.  Without a
+    workspace, one of prefill_varlen_q8_workspace_size bytes is allocated for the call."""
+    lib, dev = _lib or load(), _device()
+    rows, hq, d = _need(q, "q", _BF16, 3, dev)
+    q = q.contiguous()
+    cache, bs, hkv = _q8_cache(k_cache, v_cache, k_scales, v_scales, dev)
+    cu, sk, B = _varlen_lens(cu_seqlens_q, seq_lens_k)
+    if cu[B] != rows:
+        raise ValueError("cu_seqlens_q must end at q's row count")
+    width, stride = _table(block_table, "block_table", B, dev)
+    if B and width * bs < max(sk):
+        raise ValueError("block_table rows are too short for the sequences' keys")
+    out = _q4_out(out, q, dev)
+    causal = 1 if causal else 0
+    _keep, ws, ws_bytes = _q4_workspace(
+        workspace, lambda: int(lib.pa_prefill_varlen_q8_workspace_size(cu, sk, B, causal, hq, hkv,
+                                                                       d, bs)), dev, q.device)
+    _raise(lib.pa_prefill_varlen_q8(
+        q.data_ptr(), *cache, block_table.data_ptr(), stride, cu, sk, B, causal, hq, hkv, d, bs,
+        float(scale), out.data_ptr(), ws, ws_bytes, _stream()), "pa_prefill_varlen_q8")
     return out
 
 

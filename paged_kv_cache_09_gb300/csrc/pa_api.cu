@@ -120,6 +120,26 @@ bool make_tile_map(CUtensorMap *m, const void *base, int head_dim, int num_kv_he
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The codes of an 8-bit cache likewise: 128 dims of a byte each instead of 64 of two, so two
+// chunks; a tile of one KV head is 4 KB.
+bool make_code_map(CUtensorMap *m, const void *base, int head_dim, int num_kv_heads, int rows,
+                   int64_t num_pages, int64_t page_stride, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    constexpr int span = 2 * pa::kChunkElems;
+    const int chunks = head_dim / span;
+    cuuint64_t dims[5] = {(cuuint64_t)span, (cuuint64_t)rows, (cuuint64_t)chunks,
+                          (cuuint64_t)num_kv_heads, (cuuint64_t)num_pages};
+    cuuint64_t strides[4] = {(cuuint64_t)num_kv_heads * head_dim, (cuuint64_t)span,
+                             (cuuint64_t)head_dim, (cuuint64_t)page_stride};
+    cuuint32_t box[5] = {(cuuint32_t)span, (cuuint32_t)box_rows, (cuuint32_t)chunks, 1, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Query rows [q_len, Hq, D] as {D, Hq, q_len}; boxes of 64 dims x box_heads heads x
 // box_rows rows (in shared memory: box_heads * box_rows rows of 128 bytes, heads fastest).
 bool make_rows_map(CUtensorMap *m, const void *base, int head_dim, int num_heads, int rows,
@@ -143,10 +163,11 @@ struct MapKey {
     const void *base;
     int head_dim, num_kv_heads, rows, box_rows;
     int64_t num_pages, page_stride;
+    int elem_bytes = 2;  // 2: BF16, 1: codes
     bool operator==(const MapKey &o) const {
         return base == o.base && head_dim == o.head_dim && num_kv_heads == o.num_kv_heads &&
                rows == o.rows && box_rows == o.box_rows && num_pages == o.num_pages &&
-               page_stride == o.page_stride;
+               page_stride == o.page_stride && elem_bytes == o.elem_bytes;
     }
 };
 
@@ -163,8 +184,9 @@ bool cached_cache_map(CUtensorMap *m, const MapKey &k) {
             *m = e.map;
             return true;
         }
-    if (!make_tile_map(m, k.base, k.head_dim, k.num_kv_heads, k.rows, k.num_pages,
-                       k.page_stride, k.box_rows))
+    const auto make = k.elem_bytes == 1 ? make_code_map : make_tile_map;
+    if (!make(m, k.base, k.head_dim, k.num_kv_heads, k.rows, k.num_pages, k.page_stride,
+              k.box_rows))
         return false;
     entries[next] = Entry{k, *m, true};
     next = (next + 1) % 16;
@@ -767,6 +789,8 @@ static int rope_impl(pa::RopeArgs &a, void *stream) {
         !(a.eps >= 0.f) || !isfinite(a.eps) || !isfinite(a.weight_bias))
         return PA_ERR_INVALID_ARG;
     if (a.rotary_dim % 16 || a.rotary_dim > a.head_dim) return PA_ERR_INVALID_ARG;
+    if (a.num_axes && (a.num_axes < 1 || a.num_axes > PA_MAX_AXES || a.position_stride < a.num_tokens))
+        return PA_ERR_INVALID_ARG;
     if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return PA_ERR_UNSUPPORTED;
     if (a.cache == 2 && a.head_dim != pa::kHeadDim) return PA_ERR_UNSUPPORTED;
     if (a.num_tokens == 0) return PA_OK;
@@ -831,6 +855,66 @@ int pa_qk_norm_rope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, 
     a.q_weight = q_weight; a.k_weight = k_weight; a.weight_bias = weight_bias; a.eps = eps;
     a.cos_sin = cos_sin; a.max_position = max_position; a.rotary_dim = rotary_dim;
     a.interleaved = interleaved; a.positions = positions; a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads; a.num_kv_heads = num_kv_heads; a.head_dim = head_dim;
+    a.q_out = q_out; a.q_out_stride = q_out_stride;
+    a.cache = cache_format == PA_CACHE_BF16 ? 1 : 2;
+    a.k_cache = static_cast<uint8_t *>(k_cache); a.v_cache = static_cast<uint8_t *>(v_cache);
+    a.page_stride = page_stride; a.num_pages = num_pages; a.slot_mapping = slot_mapping;
+    a.block_size = block_size;
+    return rope_impl(a, stream);
+}
+
+// The axis of each frequency, two bits each, into a; false: one out of range.
+static bool pack_axes(const uint8_t *axes, int num_axes, int rotary_dim, uint32_t (&packed)[8]) {
+    const int n = rotary_dim / 2;
+    if (n < 0 || n > 128 || (n > 0 && !axes)) return false;
+    for (int i = 0; i < n; ++i) {
+        if (axes[i] >= num_axes) return false;
+        packed[i / 16] |= (uint32_t)axes[i] << (2 * (i % 16));
+    }
+    return true;
+}
+
+int pa_qk_norm_mrope(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                     const pa_bf16 *q_weight, const pa_bf16 *k_weight, float weight_bias, float eps,
+                     const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                     const int32_t *positions, int64_t position_stride, int num_axes,
+                     const uint8_t *axes, int num_tokens, int num_q_heads, int num_kv_heads,
+                     int head_dim, pa_bf16 *q_out, int64_t q_out_stride, pa_bf16 *k_out,
+                     int64_t k_out_stride, void *stream) {
+    pa::RopeArgs a = {};
+    if (num_axes < 1 || num_axes > PA_MAX_AXES || rotary_dim > head_dim ||
+        (head_dim <= 256 && !pack_axes(axes, num_axes, rotary_dim, a.axes)))
+        return PA_ERR_INVALID_ARG;
+    a.q = q; a.q_stride = q_stride; a.k = k; a.k_stride = k_stride;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.weight_bias = weight_bias; a.eps = eps;
+    a.cos_sin = cos_sin; a.max_position = max_position; a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved; a.positions = positions; a.num_tokens = num_tokens;
+    a.position_stride = position_stride; a.num_axes = num_axes;
+    a.num_q_heads = num_q_heads; a.num_kv_heads = num_kv_heads; a.head_dim = head_dim;
+    a.q_out = q_out; a.q_out_stride = q_out_stride; a.k_out = k_out; a.k_out_stride = k_out_stride;
+    return rope_impl(a, stream);
+}
+
+int pa_qk_norm_mrope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_t k_stride,
+                           const pa_bf16 *v, int64_t v_stride, const pa_bf16 *q_weight,
+                           const pa_bf16 *k_weight, float weight_bias, float eps,
+                           const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+                           const int32_t *positions, int64_t position_stride, int num_axes,
+                           const uint8_t *axes, int num_tokens, int num_q_heads, int num_kv_heads,
+                           int head_dim, pa_bf16 *q_out, int64_t q_out_stride, int cache_format,
+                           void *k_cache, void *v_cache, int64_t page_stride, int64_t num_pages,
+                           const int64_t *slot_mapping, int block_size, void *stream) {
+    pa::RopeArgs a = {};
+    if (cache_format != PA_CACHE_BF16 && cache_format != PA_CACHE_Q4) return PA_ERR_INVALID_ARG;
+    if (num_axes < 1 || num_axes > PA_MAX_AXES || rotary_dim > head_dim ||
+        (head_dim <= 256 && !pack_axes(axes, num_axes, rotary_dim, a.axes)))
+        return PA_ERR_INVALID_ARG;
+    a.q = q; a.q_stride = q_stride; a.k = k; a.k_stride = k_stride; a.v = v; a.v_stride = v_stride;
+    a.q_weight = q_weight; a.k_weight = k_weight; a.weight_bias = weight_bias; a.eps = eps;
+    a.cos_sin = cos_sin; a.max_position = max_position; a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved; a.positions = positions; a.num_tokens = num_tokens;
+    a.position_stride = position_stride; a.num_axes = num_axes;
     a.num_q_heads = num_q_heads; a.num_kv_heads = num_kv_heads; a.head_dim = head_dim;
     a.q_out = q_out; a.q_out_stride = q_out_stride;
     a.cache = cache_format == PA_CACHE_BF16 ? 1 : 2;
@@ -958,12 +1042,12 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
                                                                                      : PA_ERR_CUDA;
 }
 
-// Workspace of the 4-bit prefill: the batch's K, then its V, as FP16 pages, the queries as
+// Workspace of the 4-bit and the 8-bit prefill: the batch's K, then its V, as FP16 pages, the queries as
 // FP16, the factors that undo their scaling, the heads' ranges, the pages' block tables, and
 // the room for split items; each part 256-byte aligned.  Batches are of kPfMaxSeqs chunks,
 // one after another in the same workspace (the queries of all of them are converted with the
 // first).
-struct PrefillQ4Layout {
+struct ExpandLayout {
     int64_t pages = 0;      // output pages of the batch
     int table_stride = 0;   // pages of its longest sequence
     int ranges = 0;         // entries of the ranges, per KV head
@@ -972,28 +1056,28 @@ struct PrefillQ4Layout {
 };
 static size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-static PrefillQ4Layout prefill_q4_layout(const pa::PrefillSeq *seqs, int cnt, int total_q,
+static ExpandLayout expand_layout(const pa::PrefillSeq *seqs, int cnt, int total_q,
                                          int num_q_heads, int num_kv_heads) {
-    PrefillQ4Layout l;
+    ExpandLayout l;
     for (int b = 0; b < cnt; ++b) {
         const int keys = seqs[b].q_start + seqs[b].q_len;
-        const int pages = (keys - 1) / pa::kQ4PrefillPage + 1;
+        const int pages = (keys - 1) / pa::kExpandPage + 1;
         l.pages += pages;
         l.table_stride = std::max(l.table_stride, pages);
-        l.ranges += (keys - 1) / pa::kQ4RangeKeys + 1;
+        l.ranges += (keys - 1) / pa::kExpandRange + 1;
     }
     l.q = (size_t)total_q * num_q_heads * pa::kHeadDim * 2;
     l.q_factor = up256((size_t)total_q * num_q_heads * 4);
-    l.kv = (size_t)l.pages * pa::kQ4PrefillPage * num_kv_heads * pa::kHeadDim * 2;
+    l.kv = (size_t)l.pages * pa::kExpandPage * num_kv_heads * pa::kHeadDim * 2;
     l.kv_factor = up256((size_t)cnt * num_kv_heads * sizeof(float2));
     l.range = up256((size_t)l.ranges * num_kv_heads * sizeof(float2));
     l.table = up256((size_t)cnt * l.table_stride * 4);
     return l;
 }
 
-size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
-                                           int num_seqs, int causal, int num_q_heads,
-                                           int num_kv_heads, int head_dim, int block_size) try {
+static size_t expanded_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
+                                      int num_seqs, int causal, int num_q_heads, int num_kv_heads,
+                                      int head_dim, int block_size) try {
     std::vector<pa::PrefillSeq> seqs;
     if (!varlen_chunks(cu_seqlens_q, seq_lens_k, num_seqs, &seqs) || num_q_heads < 1 ||
         num_kv_heads < 1 || num_q_heads % num_kv_heads || head_dim != pa::kHeadDim ||
@@ -1005,10 +1089,10 @@ size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const in
     size_t need = 0;
     for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
         const int cnt = (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0);
-        size_t bytes = prefill_q4_layout(&seqs[s0], cnt, cu_seqlens_q[num_seqs], num_q_heads,
+        size_t bytes = expand_layout(&seqs[s0], cnt, cu_seqlens_q[num_seqs], num_q_heads,
                                          num_kv_heads).fixed();
         if (prefill_schedule(&seqs[s0], cnt, causal ? 1 : 0, num_q_heads, num_q_heads / num_kv_heads,
-                             pa::kQ4PrefillPage, dev.num_sms,
+                             pa::kExpandPage, dev.num_sms,
                              (size_t)pa::kPfMaxPieces * pa::kPfSlotBytes, &sched))
             bytes += (size_t)sched.num_pieces * pa::kPfSlotBytes;
         need = std::max(need, bytes);
@@ -1018,19 +1102,20 @@ size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const in
     return 0;
 }
 
-int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
-                         int64_t page_stride, int64_t num_pages, const int32_t *block_table,
-                         int64_t bt_stride, const int32_t *cu_seqlens_q,
-                         const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
-                         int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
-                         void *workspace, size_t workspace_bytes, void *stream) try {
+// The prefill over a cache whose format `launch_expand` expands; `cache` holds its checked
+// pointers and sizes (cache_status: what the check found).
+static int prefill_expanded(const pa::ExpandArgs &cache, int cache_status,
+                            cudaError_t (*launch_expand)(const pa::ExpandArgs &, int64_t, cudaStream_t),
+                            const pa_bf16 *q, const int32_t *block_table, int64_t bt_stride,
+                            const int32_t *cu_seqlens_q, const int32_t *seq_lens_k, int num_seqs,
+                            int causal, int num_q_heads, int head_dim, float scale, pa_bf16 *out,
+                            void *workspace, size_t workspace_bytes, void *stream) try {
+    const int num_kv_heads = cache.num_kv_heads, block_size = cache.block_size;
     std::vector<pa::PrefillSeq> seqs;
     if (!varlen_chunks(cu_seqlens_q, seq_lens_k, num_seqs, &seqs)) return PA_ERR_INVALID_ARG;
     if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads > 65535 || num_q_heads % num_kv_heads)
         return PA_ERR_INVALID_ARG;
-    if (int rc = check_q4_cache(k_cache, v_cache, page_stride, num_pages, num_kv_heads, head_dim,
-                                block_size))
-        return rc;
+    if (cache_status) return cache_status;
     if (num_q_heads / num_kv_heads > pa::kDecMaxGroup) return PA_ERR_UNSUPPORTED;
     if (seqs.empty()) return PA_OK;
     if (!q || !block_table || !out || !workspace || !isfinite(scale) || !aligned16(q) ||
@@ -1041,11 +1126,11 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
     DeviceInfo dev;
     if (int rc = device_info(&dev)) return rc;
     causal = causal ? 1 : 0;
-    std::vector<PrefillQ4Layout> layouts;
+    std::vector<ExpandLayout> layouts;
     for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
-        layouts.push_back(prefill_q4_layout(&seqs[s0],
-                                            (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0),
-                                            cu_seqlens_q[num_seqs], num_q_heads, num_kv_heads));
+        layouts.push_back(expand_layout(&seqs[s0],
+                                        (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0),
+                                        cu_seqlens_q[num_seqs], num_q_heads, num_kv_heads));
         // Split items are an option (as in pa_prefill_varlen); the pages are not.
         if (workspace_bytes < layouts.back().fixed()) return PA_ERR_INVALID_ARG;
     }
@@ -1055,19 +1140,13 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
     const int total_q = cu_seqlens_q[num_seqs];
     for (size_t i = 0, s0 = 0; s0 < seqs.size(); ++i, s0 += pa::kPfMaxSeqs) {
         const int cnt = (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0);
-        const PrefillQ4Layout &l = layouts[i];
+        const ExpandLayout &l = layouts[i];
         uint8_t *ws = static_cast<uint8_t *>(workspace);
-        pa::Q4ExpandArgs x = {};
+        pa::ExpandArgs x = cache;
         x.q = q;
         x.q_rows = s0 == 0 ? (int64_t)total_q * num_q_heads : 0;
-        x.k_cache = static_cast<const uint8_t *>(k_cache);
-        x.v_cache = static_cast<const uint8_t *>(v_cache);
-        x.page_stride = page_stride;
-        x.num_pages = num_pages;
         x.block_table = block_table;
         x.bt_stride = bt_stride;
-        x.num_kv_heads = num_kv_heads;
-        x.block_size = block_size;
         x.num_seqs = cnt;
         x.num_ranges = l.ranges;
         x.q_out = reinterpret_cast<uint16_t *>(ws);
@@ -1084,17 +1163,17 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
         int page = 0, range = 0;
         for (int b = 0; b < cnt; ++b) {
             const pa::PrefillSeq &s = seqs[s0 + b];
-            x.seq[b] = pa::Q4ExpandSeq{page, range, s.q_start + s.q_len, s.bt_row};
-            range += (s.q_start + s.q_len - 1) / pa::kQ4RangeKeys + 1;
+            x.seq[b] = pa::ExpandSeq{page, range, s.q_start + s.q_len, s.bt_row};
+            range += (s.q_start + s.q_len - 1) / pa::kExpandRange + 1;
             chunk[b] = s;
             chunk[b].bt_row = b;
-            page += (s.q_start + s.q_len - 1) / pa::kQ4PrefillPage + 1;
+            page += (s.q_start + s.q_len - 1) / pa::kExpandPage + 1;
         }
-        if (pa::launch_expand_q4(x, l.pages, st) != cudaSuccess) return PA_ERR_CUDA;
+        if (launch_expand(x, l.pages, st) != cudaSuccess) return PA_ERR_CUDA;
         if (int rc = prefill_launch(
-                x.q_out, total_q, x.k_out, x.v_out, (int64_t)pa::kQ4PrefillPage * num_kv_heads * head_dim,
+                x.q_out, total_q, x.k_out, x.v_out, (int64_t)pa::kExpandPage * num_kv_heads * head_dim,
                 l.pages, x.table_out, l.table_stride, chunk, cnt, causal, num_q_heads, num_kv_heads,
-                head_dim, pa::kQ4PrefillPage, scale, out,
+                head_dim, pa::kExpandPage, scale, out,
                 workspace_bytes > l.fixed() ? ws : nullptr, workspace_bytes - l.fixed(), dev,
                 s0 == 0 ? e0 : nullptr, s0 + cnt == seqs.size() ? e1 : nullptr, st, x.q_factor,
                 x.kv_factor))
@@ -1103,6 +1182,33 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
     return PA_OK;
 } catch (...) {  // out of host memory
     return PA_ERR_INVALID_ARG;
+}
+
+size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
+                                           int num_seqs, int causal, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size) {
+    return expanded_workspace_size(cu_seqlens_q, seq_lens_k, num_seqs, causal, num_q_heads,
+                                   num_kv_heads, head_dim, block_size);
+}
+
+int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                         int64_t page_stride, int64_t num_pages, const int32_t *block_table,
+                         int64_t bt_stride, const int32_t *cu_seqlens_q,
+                         const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+    const int rc = check_q4_cache(k_cache, v_cache, page_stride, num_pages, num_kv_heads, head_dim,
+                                  block_size);
+    pa::ExpandArgs x = {};
+    x.k_cache = static_cast<const uint8_t *>(k_cache);
+    x.v_cache = static_cast<const uint8_t *>(v_cache);
+    x.page_stride = page_stride;
+    x.num_pages = num_pages;
+    x.num_kv_heads = num_kv_heads;
+    x.block_size = block_size;
+    return prefill_expanded(x, rc, pa::launch_expand_q4, q, block_table, bt_stride, cu_seqlens_q, seq_lens_k,
+                            num_seqs, causal, num_q_heads, head_dim, scale, out, workspace,
+                            workspace_bytes, stream);
 }
 
 size_t pa_prefill_q4_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
@@ -1124,6 +1230,191 @@ int pa_prefill_chunk_q4(const pa_bf16 *q, const void *k_cache, const void *v_cac
     return pa_prefill_varlen_q4(q, k_cache, v_cache, page_stride, num_pages, block_table,
                                 (len - 1) / block_size + 1, cu, &len, 1, causal, num_q_heads,
                                 num_kv_heads, head_dim, block_size, scale, out, workspace,
+                                workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------- 8-bit cache
+// The cache arguments shared by the 8-bit calls.
+static int check_q8_cache(const void *k_cache, const void *v_cache, const uint8_t *k_scales,
+                          const uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                          int64_t num_pages, int num_kv_heads, int head_dim, int block_size) {
+    if (num_kv_heads < 1 || num_kv_heads > 65535 || head_dim < 1 || block_size < 1 ||
+        block_size > kQ4MaxBlock || num_pages < 1 || num_pages > 0x7fffffffLL)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != pa::kHeadDim) return PA_ERR_UNSUPPORTED;
+    const int64_t blocks = (block_size - 1) / PA_Q8_TOKENS + 1;
+    // (a tensor map's strides are below 2^40 bytes)
+    if (page_stride < (int64_t)block_size * num_kv_heads * head_dim || page_stride % 16 ||
+        page_stride >= (int64_t)1 << 40 || scale_stride < blocks * num_kv_heads ||
+        scale_stride > page_stride)
+        return PA_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !k_scales || !v_scales || !aligned16(k_cache) || !aligned16(v_cache))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+int pa_reshape_and_cache_q8(const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value,
+                            int64_t value_stride, void *k_cache, void *v_cache, uint8_t *k_scales,
+                            uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                            int64_t num_pages, const int64_t *slot_mapping, int num_tokens,
+                            int num_kv_heads, int head_dim, int block_size, void *stream) {
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (int rc = check_q8_cache(k_cache, v_cache, k_scales, v_scales, page_stride, scale_stride,
+                                num_pages, num_kv_heads, head_dim, block_size))
+        return rc;
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    if (!rows_ok(key, key_stride, row) || !rows_ok(value, value_stride, row) || !slot_mapping ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    const pa::Q8WriteArgs a{key, value, key_stride, value_stride, static_cast<uint8_t *>(k_cache),
+                            static_cast<uint8_t *>(v_cache), k_scales, v_scales, page_stride,
+                            scale_stride, num_pages, slot_mapping, num_tokens, num_kv_heads,
+                            block_size, dev.err, 0};
+    return pa::launch_write_q8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                    : PA_ERR_CUDA;
+}
+
+int pa_gather_cache_q8(const void *k_cache, const void *v_cache, const uint8_t *k_scales,
+                       const uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                       int64_t num_pages, const int64_t *slot_mapping, int num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, pa_bf16 *k_out,
+                       pa_bf16 *v_out, void *stream) {
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (int rc = check_q8_cache(k_cache, v_cache, k_scales, v_scales, page_stride, scale_stride,
+                                num_pages, num_kv_heads, head_dim, block_size))
+        return rc;
+    if (!slot_mapping || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || !k_out || !v_out ||
+        !aligned16(k_out) || !aligned16(v_out))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    const pa::Q8GatherArgs a{static_cast<const uint8_t *>(k_cache),
+                             static_cast<const uint8_t *>(v_cache), k_scales, v_scales, page_stride,
+                             scale_stride, num_pages, slot_mapping, num_tokens, num_kv_heads,
+                             block_size, k_out, v_out, dev.err};
+    return pa::launch_gather_q8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                     : PA_ERR_CUDA;
+}
+
+size_t pa_decode_q8_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_seq_len) {
+    if (num_seqs < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_dim != pa::kHeadDim ||
+        block_size < 1 || max_seq_len < 1 || num_q_heads % num_kv_heads)
+        return 0;
+    DeviceInfo dev;
+    if (device_info(&dev)) return 0;
+    return pa::decode_q8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, dev.num_sms);
+}
+
+int pa_decode_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache, const uint8_t *k_scales,
+                 const uint8_t *v_scales, int64_t page_stride, int64_t scale_stride,
+                 int64_t num_pages, const int32_t *block_table, int64_t bt_stride,
+                 const int32_t *seq_lens, int num_seqs, int max_seq_len, int num_q_heads,
+                 int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !block_table || !seq_lens || !out || !workspace) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 1 || num_seqs > 65535 || max_seq_len < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
+        num_q_heads > 65535 || num_q_heads % num_kv_heads)
+        return PA_ERR_INVALID_ARG;
+    if (int rc = check_q8_cache(k_cache, v_cache, k_scales, v_scales, page_stride, scale_stride,
+                                num_pages, num_kv_heads, head_dim, block_size))
+        return rc;
+    if (num_q_heads / num_kv_heads > pa::kDecMaxGroup) return PA_ERR_UNSUPPORTED;
+    if (bt_stride < ((int64_t)max_seq_len + block_size - 1) / block_size) return PA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return PA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = device_info(&dev)) return rc;
+    if (workspace_bytes <
+        pa::decode_q8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, dev.num_sms))
+        return PA_ERR_INVALID_ARG;
+    CUtensorMap maps[2];
+    for (int i = 0; i < 2; ++i)
+        if (!cached_cache_map(&maps[i], MapKey{i ? v_cache : k_cache, head_dim, num_kv_heads, block_size,
+                                               pa::kDecTile, num_pages, page_stride, 1}))
+            return PA_ERR_CUDA;
+    pa::DecodeQ8Args a = {};
+    a.num_sms = dev.num_sms;
+    a.q = q;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.scale_stride = scale_stride;
+    a.num_pages = num_pages;
+    a.block_table = block_table;
+    a.bt_stride = bt_stride;
+    a.seq_lens = seq_lens;
+    a.num_seqs = num_seqs;
+    a.max_seq_len = max_seq_len;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.scale = scale;
+    a.out = out;
+    a.workspace = workspace;
+    a.err = dev.err;
+    take_kernel_events(&a.ev_start, &a.ev_stop);
+    if (diag_enabled())
+        fprintf(stderr, "[pa] decode_q8: seqs=%d max_seq_len=%d bs=%d\n", num_seqs, max_seq_len,
+                block_size);
+    return pa::launch_decode_q8(maps, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_prefill_varlen_q8_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
+                                           int num_seqs, int causal, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size) {
+    return expanded_workspace_size(cu_seqlens_q, seq_lens_k, num_seqs, causal, num_q_heads,
+                                   num_kv_heads, head_dim, block_size);
+}
+
+int pa_prefill_varlen_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                         const uint8_t *k_scales, const uint8_t *v_scales, int64_t page_stride,
+                         int64_t scale_stride, int64_t num_pages, const int32_t *block_table,
+                         int64_t bt_stride, const int32_t *cu_seqlens_q,
+                         const int32_t *seq_lens_k, int num_seqs, int causal, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale, pa_bf16 *out,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+    const int rc = check_q8_cache(k_cache, v_cache, k_scales, v_scales, page_stride, scale_stride,
+                                  num_pages, num_kv_heads, head_dim, block_size);
+    pa::ExpandArgs x = {};
+    x.k_cache = static_cast<const uint8_t *>(k_cache);
+    x.v_cache = static_cast<const uint8_t *>(v_cache);
+    x.k_scales = k_scales;
+    x.v_scales = v_scales;
+    x.page_stride = page_stride;
+    x.scale_stride = scale_stride;
+    x.num_pages = num_pages;
+    x.num_kv_heads = num_kv_heads;
+    x.block_size = block_size;
+    return prefill_expanded(x, rc, pa::launch_expand_q8, q, block_table, bt_stride, cu_seqlens_q, seq_lens_k,
+                            num_seqs, causal, num_q_heads, head_dim, scale, out, workspace,
+                            workspace_bytes, stream);
+}
+
+size_t pa_prefill_q8_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size) {
+    return pa_prefill_q4_workspace_size(q_len, q_start, causal, num_q_heads, num_kv_heads, head_dim,
+                                        block_size);
+}
+
+int pa_prefill_chunk_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache,
+                        const uint8_t *k_scales, const uint8_t *v_scales, int64_t page_stride,
+                        int64_t scale_stride, int64_t num_pages, const int32_t *block_table,
+                        int q_len, int q_start, int causal, int num_q_heads, int num_kv_heads,
+                        int head_dim, int block_size, float scale, pa_bf16 *out, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    if (q_len < 1 || q_start < 0 || (int64_t)q_start + q_len > 0x7fffffffLL || block_size < 1)
+        return PA_ERR_INVALID_ARG;
+    const int32_t cu[2] = {0, q_len}, len = q_start + q_len;
+    return pa_prefill_varlen_q8(q, k_cache, v_cache, k_scales, v_scales, page_stride, scale_stride,
+                                num_pages, block_table, (len - 1) / block_size + 1, cu, &len, 1, causal,
+                                num_q_heads, num_kv_heads, head_dim, block_size, scale, out, workspace,
                                 workspace_bytes, stream);
 }
 
@@ -1153,6 +1444,7 @@ int pa_test_hook(int decode_skip_stage, int prefill_skip_unit, int decode_consum
     if (decode_consumer_delay_ns < 0 || decode_consumer_delay_ns > 1000000) return PA_ERR_INVALID_ARG;
     if (pa::set_decode_test_hook(decode_skip_stage, decode_consumer_delay_ns) != cudaSuccess ||
         pa::set_decode_q4_test_hook(decode_skip_stage) != cudaSuccess ||
+        pa::set_decode_q8_test_hook(decode_skip_stage) != cudaSuccess ||
         pa::set_prefill_test_hook(prefill_skip_unit) != cudaSuccess)
         return PA_ERR_CUDA;
     return PA_OK;

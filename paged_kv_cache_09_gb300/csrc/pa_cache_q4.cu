@@ -6,7 +6,7 @@
 // write also by its instructions (a group's bounds and 8 codes a lane, about 150).
 // Measured with 4 KV heads: 4096 tokens written in 9.5 us and read back in 6.7 (2.3 and 3.2
 // TB/s); 16 tokens written and read in 3.7 us together.
-#include "pa_internal.h"
+#include "pa_expand.cuh"
 #include "pa_q4.cuh"
 
 namespace pa {
@@ -14,15 +14,6 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 8;  // rows in flight per CTA
-
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
 
 // KV write: warp per (token, head), K and V of it; the warps of a CTA on one head.
 __global__ void __launch_bounds__(kWarps * 32) write_q4_kernel(const Q4WriteArgs a) {
@@ -72,51 +63,28 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q4_kernel(const Q4GatherAr
 }
 
 // ---- prefill: FP16 operands from the 4-bit cache and BF16 queries
-//
-// FP16 holds the values to 2^-11 (BF16 to 2^-8) but spans fewer binades, so each query row and
-// each KV head of a sequence is scaled by the power of two that brings its largest magnitude
-// to [2^14, 2^15).  Values down to 2^-28 of the largest keep 11 bits; smaller ones are off by up
-// to 2^-39 of it.
 
-// The power of two that brings magnitudes up to `top` below 2^15 (1 for 0 and non-finite).
-__device__ __forceinline__ float scale_for(float top) {
-    const int e = (int)(__float_as_uint(top) >> 23) & 255;
-    if (e == 255 || top == 0.f) return 1.f;
-    return __uint_as_float((uint32_t)min(254, max(1, 127 + 14 - (e - 127))) << 23);
-}
-
-// Blocks [0, num_ranges * num_kv_heads): bounds of |K| and |V| over kQ4RangeKeys keys of one
+// Blocks [0, num_ranges * num_kv_heads): bounds of |K| and |V| over kExpandRange keys of one
 // head, from the groups' minima and steps alone.  The other blocks: kWarps rows of Q each.
 // 13973 keys of 4 heads and 1685 x 24 query rows: 8.2 us (43 MB, nearly all of it the queries).
 __global__ void __launch_bounds__(kWarps * 32)
-    range_q4_kernel(const __grid_constant__ Q4ExpandArgs a) {
+    range_q4_kernel(const __grid_constant__ ExpandArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
     const int nr = a.num_ranges * a.num_kv_heads;
     if ((int)blockIdx.x >= nr) {
         const int64_t row = (int64_t)(blockIdx.x - nr) * kWarps + warp;
-        if (row >= a.q_rows) return;
-        float x[8], top = 0.f;
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(a.q + row * kHeadDim) + lane), x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float f = scale_for(top);
-        reinterpret_cast<uint4 *>(a.q_out + row * kHeadDim)[lane] =
-            make_uint4(pack_f16x2(x[0] * f, x[1] * f), pack_f16x2(x[2] * f, x[3] * f),
-                       pack_f16x2(x[4] * f, x[5] * f), pack_f16x2(x[6] * f, x[7] * f));
-        if (lane == 0) a.q_factor[row] = 1.f / f;
+        if (row < a.q_rows) expand_query(a, row, lane);
         return;
     }
     const int h = blockIdx.x / a.num_ranges, range = blockIdx.x - h * a.num_ranges;
     int b = 0;
     while (b + 1 < a.num_seqs && range >= a.seq[b + 1].range0) ++b;
-    const Q4ExpandSeq s = a.seq[b];
+    const ExpandSeq s = a.seq[b];
     const int32_t *bt = a.block_table + (int64_t)s.bt_row * a.bt_stride;
-    const int k0 = (range - s.range0) * kQ4RangeKeys;
-    const int k1 = min(s.num_keys, k0 + kQ4RangeKeys);
+    const int k0 = (range - s.range0) * kExpandRange;
+    const int k1 = min(s.num_keys, k0 + kExpandRange);
     float top[2] = {0.f, 0.f};
     for (int k = k0 + threadIdx.x; k < k1; k += kWarps * 32) {
         const int lp = k / a.block_size, o = k - lp * a.block_size, page = bt[lp];
@@ -167,20 +135,20 @@ __device__ __forceinline__ uint4 widen_word(uint32_t w, float s, float lo) {
 // one contiguous run; kWarps keys' loads in flight a round.  13973 keys of 4 heads: 15.6 us (16 MB
 // read, 57 MB written: 4.7 TB/s).
 __global__ void __launch_bounds__(kWarps * 32)
-    expand_q4_kernel(const __grid_constant__ Q4ExpandArgs a) {
-    constexpr int kRows = kQ4ExpandKeys / kWarps;  // keys of a warp
+    expand_q4_kernel(const __grid_constant__ ExpandArgs a) {
+    constexpr int kRows = kExpandKeys / kWarps;  // keys of a warp
     __shared__ float2 part[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-    const int64_t key0 = (int64_t)blockIdx.x * kQ4ExpandKeys;  // of the stacked, page-padded keys
+    const int64_t key0 = (int64_t)blockIdx.x * kExpandKeys;  // of the stacked, page-padded keys
     int b = 0;
-    while (b + 1 < a.num_seqs && key0 >= (int64_t)a.seq[b + 1].page0 * kQ4PrefillPage) ++b;
-    const Q4ExpandSeq sq = a.seq[b];
-    const int k0 = (int)(key0 - (int64_t)sq.page0 * kQ4PrefillPage);  // key of the sequence
+    while (b + 1 < a.num_seqs && key0 >= (int64_t)a.seq[b + 1].page0 * kExpandPage) ++b;
+    const ExpandSeq sq = a.seq[b];
+    const int k0 = (int)(key0 - (int64_t)sq.page0 * kExpandPage);  // key of the sequence
     const int g = lane >> 3, u = lane & 7;
     pdl_wait();
     pdl_trigger();
-    if (h == 0 && k0 % kQ4PrefillPage == 0 && threadIdx.x == 0)
-        a.table_out[(int64_t)b * a.table_stride + k0 / kQ4PrefillPage] = sq.page0 + k0 / kQ4PrefillPage;
+    if (h == 0 && k0 % kExpandPage == 0 && threadIdx.x == 0)
+        a.table_out[(int64_t)b * a.table_stride + k0 / kExpandPage] = sq.page0 + k0 / kExpandPage;
     // This warp's words and pairs, all loads in flight.
     const int32_t *bt = a.block_table + (int64_t)sq.bt_row * a.bt_stride;
     uint32_t kw[kRows], vw[kRows], kp[kRows], vp[kRows];
@@ -203,7 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     // The head's scales, from all of its sequence's ranges.
     float2 top = make_float2(0.f, 0.f);
-    const int nr = (sq.num_keys - 1) / kQ4RangeKeys + 1;
+    const int nr = (sq.num_keys - 1) / kExpandRange + 1;
     for (int i = threadIdx.x; i < nr; i += kWarps * 32) {
         const float2 t = a.ranges[(int64_t)h * a.num_ranges + sq.range0 + i];
         top.x = fmaxf(top.x, t.x);
@@ -252,12 +220,12 @@ cudaError_t launch_gather_q4(const Q4GatherArgs &a, cudaStream_t stream) {
                       stream, a);
 }
 
-cudaError_t launch_expand_q4(const Q4ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream) {
+cudaError_t launch_expand_q4(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream) {
     const int64_t blocks = (int64_t)a.num_ranges * a.num_kv_heads + (a.q_rows + kWarps - 1) / kWarps;
     cudaError_t e = launch_pdl(range_q4_kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(expand_q4_kernel,
-                      dim3((unsigned)(num_pages_out * (kQ4PrefillPage / kQ4ExpandKeys)),
+                      dim3((unsigned)(num_pages_out * (kExpandPage / kExpandKeys)),
                            a.num_kv_heads),
                       dim3(kWarps * 32), 0, stream, a);
 }

@@ -61,18 +61,13 @@
 // 4K..32K keys 68.8 us (streaming kernel 4.9 TB/s); 64 of 1..2048 keys, 8 KV heads of 4, pages of
 // 16: 43.7 us; one of 32768 keys 17.3 us; one of 1701 keys 11.0 us.  The short ones are latency:
 // finding the share 1.5 us, q 1.2, one step 2, the CTA's merge 1, and the second kernel.
-#include <math_constants.h>
-
-#include <algorithm>
-
-#include "pa_internal.h"
+#include "pa_decode_split.cuh"
 #include "pa_q4.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kTile = kDecTile;                       // 16 tokens
 constexpr int kW = 4, kThreads = kW * 32;             // warps of a CTA
 constexpr int kDepth = 2;                             // pairs of tiles in a warp's ring
 constexpr int kTileCodes = kTile * kQ4CodeBytes;      // 2 KB
@@ -94,38 +89,9 @@ constexpr float kLag = 8.f;  // log2 units: a score may pass the reference by it
 constexpr float kTop = 4.f;  // where F follows the scores, the largest weight is 2^(kTop - 1) .. 2^(kTop + 1)
 constexpr int kSpare = 2;    // where it follows the steps, they may grow by 2^kSpare unexamined
 
-// Division of n < 2^31 by a constant of the launch.
-struct FastDiv {
-    uint32_t d, mul, shift;
-    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-        return (__umulhi(n, mul) + n) >> shift;
-    }
-};
-FastDiv fast_div(uint32_t d) {
-    FastDiv f{d, 0, 0};
-    while ((1ull << f.shift) < d) ++f.shift;
-    f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
-    return f;
-}
-
-struct Params {
-    const uint16_t *q;
+struct Params : SplitParams {
     const uint8_t *k_cache, *v_cache;
-    int64_t page_stride, num_pages;
-    const int32_t *block_table;
-    int64_t bt_stride;
-    const int32_t *seq_lens;
-    int num_seqs, max_seq_len, num_q_heads, num_kv_heads, group, block_size, tiles_per_page;
-    FastDiv by_block, by_tpp;
-    float scale_log2;
-    // Part i: fp32 sums [group, 256] and (reference, sum of weights) [group].  CTA b's part of
-    // pair x is part b + x (one of the two grows from part to part, so no two are the same).
-    float *part_o;
-    float2 *part_ml;
-    int2 *info;  // [pairs]: a pair's first part and how many (0: finished by one CTA)
-    int64_t parts;
-    uint16_t *out;
-    unsigned *err;
+    int64_t page_stride;
 };
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
@@ -135,25 +101,6 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
-}
-
-// D += A (16x16, row) * B (16x8, col), FP16 in, fp32 accumulate.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same from D = 0.
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The four pairs (codes k, k + 4) of a word as FP16 subnormals: k
@@ -176,12 +123,6 @@ __device__ __forceinline__ float log2_whole(float f) {
     return (float)((int)(__float_as_uint(f) >> 23) - 127);
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -198,43 +139,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
-
-__device__ __forceinline__ int tiles_of(const Params &p, int len) {
-    const int full = (int)p.by_block(len);
-    return full * p.tiles_per_page + ((len - full * p.block_size + kTile - 1) >> 4);
-}
-
-// Tiles of sequence s (none past the last); lengths out of range are cut to it.
-__device__ __forceinline__ int seq_tiles(const Params &p, int s, int *len, bool report) {
-    int L = s < p.num_seqs ? p.seq_lens[s] : 0;
-    if (L < 0 || L > p.max_seq_len) {
-        if (report) atomicOr(p.err, kErrSeqLen);
-        L = L < 0 ? 0 : p.max_seq_len;
-    }
-    *len = L;
-    return tiles_of(p, L);
-}
-
-constexpr uint32_t kMaxTiles = 0x7fffffffu;  // of all pairs, with their leads (9.9 TB, shared pages counted again)
-
-// Places ahead of each of `pairs` pairs' tiles, when `tiles` (at most kMaxTiles) are cut over `ctas`
-// shares: half a share at most, and none where they would not be numbered in 31 bits.
-__host__ __device__ __forceinline__ int pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas) {
-    if (tiles < (uint64_t)2 * kMinShare * ctas) return 0;
-    const uint32_t half = tiles / (2 * ctas);
-    const uint32_t lead = half < (uint32_t)kPairCost ? half : (uint32_t)kPairCost;
-    return tiles + lead * pairs > kMaxTiles ? 0 : (int)lead;
-}
-
-// CTA b's first tile when `total` tiles are cut over `ctas`: the first r shares have one more.
-struct Shares {
-    uint32_t q, r;
-    __device__ __forceinline__ uint32_t begin(uint32_t b) const { return b * q + min(b, r); }
-    __device__ __forceinline__ uint32_t owner(uint32_t tile) const {
-        const uint32_t big = r * (q + 1);
-        return tile < big ? tile / (q + 1) : r + (tile - big) / q;
-    }
-};
 
 #ifdef PA_TEST_HOOKS
 // Test build only: the pair of tiles (counted over each warp's run) whose loads are left out (-1:
@@ -262,63 +166,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     // ---- this CTA's share of all tiles, and the segment that it begins with: tile t0 of KV head
     // g of sequence seq (every warp finds the same)
     const int tpp = p.tiles_per_page;
-    Shares shares;
-    uint32_t at, end;  // the next place in the row of all pairs, and the share's end
-    // Places before each pair's tiles, and the segment's first place in its pair.
-    int lead, v0;
-    int seq, g, t0, seq_len, tiles;
-    bool refused = false;  // more tiles than a share can be found of
-    // Finds them, with the tiles and lengths of the first 32 sequences given; false: no share.
-    auto place = [&](int first_tiles, int first_len) {
-        uint64_t all = 0, used = 0;
-        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-            int len;
-            uint64_t t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, blockIdx.x == 0 && warp == 0);
-            used += __popc(__ballot_sync(0xffffffffu, t > 0));
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-            all += t;
-        }
-        all *= p.num_kv_heads;
-        if (all == 0) return false;  // padding entries only
-        if (all > kMaxTiles) {
-            refused = true;
-            return false;
-        }
-        const uint32_t ctas = min(gridDim.x, ((uint32_t)all + kMinShare - 1) / kMinShare);
-        lead = pair_lead((uint32_t)all, used * p.num_kv_heads, ctas);
-        const uint32_t total = (uint32_t)(all + lead * used * p.num_kv_heads);
-        if (blockIdx.x >= ctas) return false;
-        shares.q = total / ctas;
-        shares.r = total - shares.q * ctas;
-        at = shares.begin(blockIdx.x);
-        end = shares.begin(blockIdx.x + 1);
-        uint32_t before = 0;
-        for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-            int len = first_len;
-            const int t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, false);
-            const uint32_t span = t > 0 ? t + lead : 0;  // a pair's places
-            uint32_t sum = span;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, (before + sum) * p.num_kv_heads > at);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                seq = s0 + l;
-                seq_len = __shfl_sync(0xffffffffu, len, l);
-                tiles = __shfl_sync(0xffffffffu, t, l);
-                const uint32_t rem = at - (before + __shfl_sync(0xffffffffu, sum - span, l)) * p.num_kv_heads;
-                g = (int)(rem / (uint32_t)(tiles + lead));
-                v0 = (int)(rem - (uint32_t)g * (tiles + lead));
-                return true;
-            }
-            before += __shfl_sync(0xffffffffu, sum, 31);
-        }
-        return false;  // (not reached: at < total)
-    };
+    Start st;
+    Shares &shares = st.shares;
+    uint32_t &at = st.at, &end = st.end;
+    int &lead = st.lead, &v0 = st.v0, &seq = st.seq, &g = st.g, &seq_len = st.seq_len, &tiles = st.tiles;
+    int t0;  // the segment's first tile
 
     const int r = lane >> 2, c = lane & 3;
     const uint32_t q_frag = smem_u32(smem + kOffQ) + lane * 16;
@@ -452,20 +304,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     // then read beside the length instead of after it.
     int len;
     const int actual = seq_tiles(p, lane, &len, blockIdx.x == 0 && warp == 0);
-    bool guess = p.num_seqs == 1, placed;
+    bool guess = p.num_seqs == 1;
+    Found found;
     for (;;) {
-        refused = false;
-        placed = guess ? place(lane == 0 ? tiles_of(p, p.max_seq_len) : 0, p.max_seq_len)
-                       : place(actual, len);
-        if (placed) {
+        found = guess ? find_start<kMinShare, kPairCost>(p, lane, false, lane == 0 ? tiles_of(p, p.max_seq_len) : 0,
+                                                         p.max_seq_len, st)
+                      : find_start<kMinShare, kPairCost>(p, lane, blockIdx.x == 0 && warp == 0, actual, len, st);
+        if (found == Found::kShare) {
             begin_segment();
             load_q();
         }
         if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
         guess = false;
     }
-    if (!placed) {
-        if (refused) {  // (not by a guess) tells the merge so: the pairs have no parts
+    if (found != Found::kShare) {
+        if (found == Found::kRefused) {  // (not by a guess) tells the merge so: the pairs have no parts
             if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
             const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
             for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < pairs; x += gridDim.x * kThreads)
@@ -853,129 +706,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
     }
 }
 
-// Merges a row's parts: sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j, M = max m_j; an empty
-// part has m = -inf.  All loads of a round are in flight together.
-//   kSplit > 1: that many warps for each 64 dims of a row take its parts in turn, for the
-//               latency of many parts
-//   kSplit = 1: two warps a row (128 dims each), 4 rows a CTA
-// The fewer the rows, the more parts each may have: 8 up to a row an SM, 4 up to 8 rows an SM, 1
-// beyond.  A step's us with 8, 4 and 1 (6 query heads a KV head):
-//   sequences of 1..4096 keys    24 rows 11.1 11.3 12.5   144 14.3 15.3 16.7   192 18.9 18.6 19.2
-//     384 19.3 17.5 17.8   768 27.8 24.7 23.1   1200 39.8 35.1 31.9   1536 48.1 42.2 38.2
-//   one of 32768, others to 200   192 17.5 20.4 24.9   384 18.7 21.0 24.4   768 22.0 22.7 24.8
-//     1200 24.2 22.9 25.0   1536 27.1 23.6 26.0
-// so between 2 and 8 rows an SM 4 loses up to 9% to 1 where lengths are alike, and gains as much
-// where one is long.
-template <int kSplit>
-__global__ void __launch_bounds__(256) decode_q4_merge_kernel(const __grid_constant__ Params p) {
-    constexpr bool kFew = kSplit > 1;
-    constexpr int kWarps = kSplit, kRound = 4;
-    constexpr int kBlocks = 8 / kSplit;  // of 64 dims, in a CTA
-    constexpr int kVec = kFew ? 1 : 2;  // float2 a lane
-    const int lane = threadIdx.x & 31, all = threadIdx.x >> 5;
-    const int warp = kFew ? all % kWarps : all, block = kFew ? all / kWarps : 0;
-    const int64_t row = kFew ? blockIdx.x / (4 / kBlocks) : (int64_t)blockIdx.x * 4 + (warp >> 1);
-    const int d0 = kFew ? (blockIdx.x % (4 / kBlocks) * kBlocks + block) * 64 : (warp & 1) * 128;
-    pdl_wait();
-    pdl_trigger();
-    if (row >= (int64_t)p.num_seqs * p.num_q_heads) return;  // (warp-uniform; kFew: never)
-    const int seq = (int)(row / p.num_q_heads), h = (int)(row - (int64_t)seq * p.num_q_heads);
-    const int len = p.seq_lens[seq];
-    const int2 info = p.info[(int64_t)seq * p.num_kv_heads + h / p.group];
-    uint16_t *out = p.out + row * kHeadDim + d0;
-    if (len <= 0) {
-        if (kFew ? warp == 0 : true)
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) reinterpret_cast<uint32_t *>(out)[v * 32 + lane] = 0;
-        return;
-    }
-    const int count = info.y;
-    if (count <= 0 || info.x < 0 || info.x + (int64_t)count > p.parts) return;
-    const int64_t first = (int64_t)info.x * p.group + h % p.group;  // parts are p.group rows apart
-    float M = -CUDART_INF_F, L = 0.f;
-    float2 acc[kVec];
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) acc[v] = make_float2(0.f, 0.f);
-    for (int j0 = kFew ? warp : 0; j0 < count; j0 += kWarps * kRound) {
-        float2 o[kRound][kVec], ml[kRound];
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            const int j = j0 + k * kWarps;
-            const int64_t at = first + (int64_t)j * p.group;
-            ml[k] = j < count ? ld_f2_ordered(p.part_ml + at) : make_float2(-CUDART_INF_F, 0.f);
-#pragma unroll
-            for (int v = 0; v < kVec; ++v)
-                o[k][v] = j < count ? ld_f2_ordered(reinterpret_cast<const float2 *>(
-                                          p.part_o + at * kHeadDim + d0) + v * 32 + lane)
-                                    : make_float2(0.f, 0.f);
-        }
-        float mn = M;
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) mn = fmaxf(mn, ml[k].x);
-        const float f = M == -CUDART_INF_F ? 0.f : ex2_approx(M - mn);
-        M = mn;
-        L *= f;
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            acc[v].x *= f;
-            acc[v].y *= f;
-        }
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            // (an empty part is zeros; one of weight 0 counts too: its sums may be NaN)
-            const float e = ml[k].x == -CUDART_INF_F ? 0.f : ex2_approx(ml[k].x - M);
-            L = fmaf(e, ml[k].y, L);
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                acc[v].x = fmaf(e, o[k][v].x, acc[v].x);
-                acc[v].y = fmaf(e, o[k][v].y, acc[v].y);
-            }
-        }
-    }
-    if (kFew) {
-        __shared__ float2 sums[kBlocks][kWarps][32], refs[kBlocks][kWarps];
-        float2 (*so)[32] = sums[block], *sml = refs[block];
-        so[warp][lane] = acc[0];
-        if (lane == 0) sml[warp] = make_float2(M, L);
-        __syncthreads();
-        if (warp) return;
-        M = -CUDART_INF_F;
-        L = 0.f;
-        acc[0] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w].x);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float e = sml[w].x == -CUDART_INF_F ? 0.f : ex2_approx(sml[w].x - M);
-            L = fmaf(e, sml[w].y, L);
-            acc[0].x = fmaf(e, so[w][lane].x, acc[0].x);
-            acc[0].y = fmaf(e, so[w][lane].y, acc[0].y);
-        }
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-    for (int v = 0; v < kVec; ++v)
-        reinterpret_cast<uint32_t *>(out)[v * 32 + lane] = pack_bf16x2(acc[v].x * inv, acc[v].y * inv);
-}
-
-}  // namespace
-
-// Workspace: the parts' sums, their (reference, sum) pairs, and the pairs' info, each
-// 256-byte aligned.  A part is numbered CTA + pair, so there are at most CTAs + pairs.
-namespace {
-struct WsLayout {
-    int64_t parts;
-    size_t o, ml, info;
-};
-WsLayout ws_layout(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms) {
-    WsLayout l;
-    const int64_t pairs = (int64_t)num_seqs * num_kv_heads, group = num_q_heads / num_kv_heads;
-    l.parts = pairs + 2 * num_sms;
-    l.o = (size_t)l.parts * group * kHeadDim * 4;
-    l.ml = ((size_t)l.parts * group * sizeof(float2) + 255) & ~size_t(255);
-    l.info = ((size_t)pairs * sizeof(int2) + 255) & ~size_t(255);
-    return l;
-}
 }  // namespace
 
 size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms) {
@@ -987,54 +717,23 @@ size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads
 cudaError_t set_decode_q4_test_hook(int skip_pair) {
     return cudaMemcpyToSymbol(g_test_skip_pair, &skip_pair, sizeof skip_pair);
 }
-int decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas) { return pair_lead(tiles, pairs, ctas); }
+int decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas) { return pair_lead<kMinShare, kPairCost>(tiles, pairs, ctas); }
 #endif
 
 cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream) {
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_q4_stream_kernel), kSmem, 6);
     if (e != cudaSuccess) return e;
     Params p;
-    p.q = a.q;
+    fill_split(p, a);
     p.k_cache = a.k_cache;
     p.v_cache = a.v_cache;
     p.page_stride = a.page_stride;
-    p.num_pages = a.num_pages;
-    p.block_table = a.block_table;
-    p.bt_stride = a.bt_stride;
-    p.seq_lens = a.seq_lens;
-    p.num_seqs = a.num_seqs;
-    p.max_seq_len = a.max_seq_len;
-    p.num_q_heads = a.num_q_heads;
-    p.num_kv_heads = a.num_kv_heads;
-    p.group = a.num_q_heads / a.num_kv_heads;
-    p.block_size = a.block_size;
-    p.tiles_per_page = (a.block_size + kTile - 1) / kTile;
-    p.by_block = fast_div(a.block_size);
-    p.by_tpp = fast_div(p.tiles_per_page);
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    const WsLayout l = ws_layout(a.num_seqs, a.num_q_heads, a.num_kv_heads, a.num_sms);
-    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    p.part_o = reinterpret_cast<float *>(ws);
-    p.part_ml = reinterpret_cast<float2 *>(ws + l.o);
-    p.info = reinterpret_cast<int2 *>(ws + l.o + l.ml);
-    p.parts = l.parts;
-    p.out = a.out;
-    p.err = a.err;
-    // No more CTAs than the longest allowed lengths would use.
-    const int64_t tiles = (int64_t)a.num_seqs * a.num_kv_heads *
-                          ((int64_t)(a.max_seq_len / a.block_size) * p.tiles_per_page +
-                           (a.max_seq_len % a.block_size + kTile - 1) / kTile);
-    const int grid = (int)std::min<int64_t>(2 * a.num_sms, (tiles + kMinShare - 1) / kMinShare);
+    const int grid = split_grid<kMinShare>(p, a);
     if (a.ev_start && (e = record_event(a.ev_start, stream)) != cudaSuccess) return e;
     e = launch_pdl(decode_q4_stream_kernel, dim3(grid), dim3(kThreads), kSmem, stream, p);
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
-    const int64_t rows = (int64_t)a.num_seqs * a.num_q_heads;
-    if (rows <= a.num_sms)
-        return launch_pdl(decode_q4_merge_kernel<8>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
-    if (rows <= 8 * a.num_sms)
-        return launch_pdl(decode_q4_merge_kernel<4>, dim3((unsigned)(rows * 2)), dim3(256), 0, stream, p);
-    return launch_pdl(decode_q4_merge_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+    return launch_merge(p, a.num_sms, stream);
 }
 
 }  // namespace pa

@@ -1,0 +1,478 @@
+// pa_decode_q8.cu -- q=1 decode over the 8-bit cache (format: pa_q8.cuh): a kernel that streams the
+// cache, and one that merges the parts of sequences that it cut (pa_decode_split.cuh).
+//
+// For query head h of KV head g, over the sequence's tokens t < seq_len,
+//     out = softmax_t(scale q . k_t) . v_t,   k_t = c_t 2^ek, v_t = d_t 2^ev,
+// with one ek and one ev for each 16-token tile of a page: the tile of the matrix products.  So
+// the products are of codes, which are exact in FP16:
+//     x_t = (scale log2(e) 2^ek) (q . c_t),   out = sum_t 2^(x_t + ev - M') d_t / (2^-M' sum_t 2^x_t)
+// and the scales cost an addition and a product per (token, head).
+//
+// q becomes FP16 after scaling each head by a power of two (largest value in [2^13, 2^14)):
+// exact for values down to 2^-24 of the head's largest, and below that off by less than 2^-34 of
+// it.  The weights 2^(x + ev - M') become FP16 (off by 2^-11 of them at most); M' follows the
+// largest x + ev, the reference m of the weights' sum the largest x, each at most kLag behind: a
+// weight is 2^(kTop + kLag) at most, and those down to 2^(-14 - kTop) = 2^-20 of the largest keep
+// all of FP16's bits, whatever the scales of tokens without weight are.
+//
+// Bytes: 512 and 2 of scales for a 16-token tile's token and KV head; at the copy bandwidth an SM
+// has to take a tile (8 KB) about every 185 ns (370 cycles).
+#include "pa_decode_split.cuh"
+#include "pa_q8.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kW = 4, kThreads = kW * 32;             // warps of a CTA
+constexpr int kDepth = 3;                             // tiles in a warp's ring
+constexpr int kTileCodes = kTile * kHeadDim;          // 4 KB: [2 halves of the dims][16 tokens][128 bytes]
+constexpr int kSlotBytes = 2 * kTileCodes;            // K, V
+// Shared memory: rings (whose slots also take a warp's sums for the CTA's merge); q's fragments
+// and scales; the warps' references; barriers and the slots of the sums.
+constexpr int kOffQ = kW * kDepth * kSlotBytes, kOffMl = kOffQ + 9 * 512;
+constexpr int kOffBars = kOffMl + kW * kDecMaxGroup * 8, kOffMisc = kOffBars + kW * kDepth * 8;
+constexpr int kSmem = kOffMisc + 32 + 1024;           // (the rings start at a multiple of 1024)
+static_assert(kDecMaxGroup * kHeadDim * 4 == kSlotBytes, "a slot holds a warp's sums");
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(kTile == kQ8Tokens, "a tile has one scale");
+constexpr int kMinShare = kW;                         // tiles of the smallest share
+constexpr int kPairCost = 8;                          // of beginning a pair, in tiles
+constexpr float kLag = 8.f;  // log2 units: a score may pass the reference by it
+constexpr float kTop = 6.f;  // log2 of the weight at the reference M'
+
+struct Params : SplitParams {
+    const uint8_t *k_scales, *v_scales;
+    int64_t scale_stride;
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+#ifdef PA_TEST_HOOKS
+// Test build only: the tile (counted over each warp's run) whose loads are left out (-1: none),
+// so that the warp's wait runs out.
+__device__ int g_test_skip_tile = -1;
+#endif
+
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_q8_stream_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                            const __grid_constant__ Params p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars) + warp * kDepth;  // this warp's ring
+    volatile int *sum_slot = reinterpret_cast<volatile int *>(smem + kOffMisc);      // [warp]
+    volatile int *abort = sum_slot + kW;
+    uint8_t *ring = smem + warp * kDepth * kSlotBytes;
+
+    if (lane == 0) {
+        for (int s = 0; s < kDepth; ++s) mbar_init(&full[s], 1);
+        if (warp == 0) {
+            *abort = 0;
+            tma_prefetch_desc(&k_map);
+            tma_prefetch_desc(&v_map);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's share of all tiles, and the segment that it begins with
+    const int tpp = p.tiles_per_page;
+    Start st;
+    uint32_t &at = st.at, &end = st.end;
+    int &lead = st.lead, &v0 = st.v0, &seq = st.seq, &g = st.g, &seq_len = st.seq_len, &tiles = st.tiles;
+    const int r = lane >> 2, c = lane & 3;
+    const uint32_t q_frag = smem_u32(smem + kOffQ) + lane * 16;
+    const int32_t *bt;
+    int t0, t1, n;                          // the segment's tiles [t0, t1), this warp's count of them
+    int j_in, lp_in, tip_in, page_in;       // the warp's next tile to load
+    uint32_t it = 0;  // the warp's steps: slots and phases go on from segment to segment
+
+    auto begin_segment = [&]() {
+        t0 = max(0, v0 - lead);
+        t1 = (int)min((uint32_t)tiles, v0 + (end - at) - lead);
+        n = !*abort && t0 + warp < t1 ? (t1 - t0 - warp + kW - 1) / kW : 0;
+        bt = p.block_table + (int64_t)seq * p.bt_stride;
+        j_in = t0 + warp;
+        lp_in = (int)p.by_tpp(j_in);
+        tip_in = j_in - lp_in * tpp;
+        page_in = j_in < t1 ? bt[lp_in] : 0;
+    };
+    // Loads the warp's tile i, its next, into slot i % kDepth; its scale bytes, and its valid rows.
+    struct Tile {
+        uint32_t k_scale, v_scale;
+        int rows;
+    };
+    auto load = [&](uint32_t i) {
+        const uint32_t s = i % kDepth;
+        const int page = page_in, off = tip_in * kTile;
+        Tile t;
+        t.rows = min(kTile, min(p.block_size - off, seq_len - lp_in * p.block_size - off));
+        t.k_scale = t.v_scale = 127;
+        // A page outside the pool is reported, and its box, which lies outside the map, reads as zeros.
+        if (page >= 0 && page < p.num_pages) {
+            const int64_t o = page * p.scale_stride + (int64_t)tip_in * p.num_kv_heads + g;
+            t.k_scale = __ldg(p.k_scales + o);
+            t.v_scale = __ldg(p.v_scales + o);
+        } else if (lane == 0) {
+            atomicOr(p.err, kErrPage);
+        }
+        // The next tile's table entry, read ahead of its use.
+        j_in += kW;
+        for (tip_in += kW; tip_in >= tpp; tip_in -= tpp) ++lp_in;
+        if (j_in < t1) page_in = bt[lp_in];
+#ifdef PA_TEST_HOOKS
+        if ((int)i == *reinterpret_cast<volatile int *>(&g_test_skip_tile)) return t;
+#endif
+        if (lane == 0) {
+            uint8_t *dst = ring + s * kSlotBytes;
+            const uint64_t policy = l2_evict_first_policy();
+            mbar_arrive_expect_tx(&full[s], kSlotBytes);
+            tma_load_5d_hint(dst, &k_map, &full[s], 0, off, 0, g, page, policy);
+            tma_load_5d_hint(dst + kTileCodes, &v_map, &full[s], 0, off, 0, g, page, policy);
+        }
+        return t;
+    };
+    int loaded = 0;
+    Tile next0{}, next1{};  // of the next tiles
+    auto first_loads = [&]() {
+        loaded = min(n, kDepth - 1);
+        if (n > 0) next0 = load(it);
+        if (n > 1) next1 = load(it + 1);
+    };
+    static_assert(kDepth == 3, "two tiles ahead");
+    // q as FP16 B fragments in shared memory: lane (head r, column c) holds dims 128a + 32c + 16b +
+    // {0..15} (a, b = 0, 1) as two 16-byte words, word w of which are dims 4w and 4w + 1 (or + 2, + 3).
+    // Each warp loads all of q (for the heads' largest values) and makes a quarter.
+    uint4 raw[8];
+    auto load_q = [&]() {
+        const uint4 *qrow = reinterpret_cast<const uint4 *>(
+            p.q + ((int64_t)seq * p.num_q_heads + g * p.group + (r < p.group ? r : 0)) * kHeadDim);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            raw[k] = r < p.group ? qrow[(k >> 2) * 16 + 4 * c + (k & 3)] : make_uint4(0, 0, 0, 0);
+    };
+    auto make_q = [&]() {
+        uint4 *own = reinterpret_cast<uint4 *>(smem + kOffQ) + lane;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                amax = max(amax, max((word(raw[k], i) << 16) & 0x7fff0000u, word(raw[k], i) & 0x7fff0000u));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // A power of two f that brings the head's largest value to [2^13, 2^14).
+        const int e = (int)(amax >> 23);
+        const float f = e == 255 ? 1.f : __uint_as_float((uint32_t)min(254, max(1, 267 - e)) << 23);
+        static_assert(kW == 4, "a warp a quarter");
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 mine = raw[h];
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                if (warp == k) mine = raw[2 * k + h];
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = pack_f16x2(bf16_lo(word(mine, i)) * f, bf16_hi(word(mine, i)) * f);
+            own[(2 * warp + h) * 32] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        const float sc = p.scale_log2 / f;
+        const float sc0 = __shfl_sync(0xffffffffu, sc, 8 * c), sc1 = __shfl_sync(0xffffffffu, sc, 8 * c + 4);
+        if (warp == 0) own[8 * 32] = make_uint4(__float_as_uint(sc0), __float_as_uint(sc1), 0, 0);
+    };
+
+    // With one sequence, its length is nearly always the longest allowed: the table entry and q are
+    // then read beside the length instead of after it.
+    int len;
+    const int actual = seq_tiles(p, lane, &len, blockIdx.x == 0 && warp == 0);
+    bool guess = p.num_seqs == 1;
+    Found found;
+    for (;;) {
+        found = guess ? find_start<kMinShare, kPairCost>(p, lane, false, lane == 0 ? tiles_of(p, p.max_seq_len) : 0,
+                                                         p.max_seq_len, st)
+                      : find_start<kMinShare, kPairCost>(p, lane, blockIdx.x == 0 && warp == 0, actual, len, st);
+        if (found == Found::kShare) {
+            begin_segment();
+            load_q();
+        }
+        if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
+        guess = false;
+    }
+    if (found != Found::kShare) {
+        if (found == Found::kRefused) {  // (not by a guess) tells the merge so: the pairs have no parts
+            if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
+            const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
+            for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < pairs; x += gridDim.x * kThreads)
+                p.info[x] = make_int2(0, 0);
+        }
+        return;
+    }
+    first_loads();
+    make_q();
+    __syncthreads();  // q is ready
+    for (;;) {
+        float o[2][4][2][4];  // [half][word][dim pair][(dim, head) of the pairs], relative to M'
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) o[a][w][k][0] = o[a][w][k][1] = o[a][w][k][2] = o[a][w][k][3] = 0.f;
+        // References of heads 2c and 2c + 1: m of the sums l, v (M') of o.
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+        float v_ref0 = -CUDART_INF_F, v_ref1 = -CUDART_INF_F;
+
+        for (int i = 0; i < n; ++i) {
+            const Tile now = next0;
+            next0 = next1;
+            if (loaded < n) next1 = load(it + loaded++);  // into the slot that the previous tile has left
+            const uint32_t s = (it + i) % kDepth;
+            if (!__all_sync(0xffffffffu, mbar_wait_abort(&full[s], ((it + i) / kDepth) & 1, p.err, abort))) break;
+            const uint32_t base = smem_u32(ring) + s * kSlotBytes;
+
+            // ---- scores of tokens r and r + 8, heads 2c and 2c + 1: 4 accumulators in turn
+            float x[4];
+            {
+                const uint32_t ka = base + r * 128 + (((2 * c) ^ r) << 4);
+                float acc[4][4];
+#pragma unroll
+                for (int ab = 0; ab < 4; ++ab) {  // (half a of the dims, unit b of the lane's two)
+                    const uint32_t k_at = (ab & 1 ? ka ^ 16 : ka) + (ab >> 1) * 2048;
+                    const uint4 k0 = lds128(k_at), k1 = lds128(k_at + 1024);
+                    const uint4 qa = lds128(q_frag + 2 * ab * 512), qb = lds128(q_frag + (2 * ab + 1) * 512);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t a0 = f16x2_of_e4m3(word(k0, w)), a1 = f16x2_of_e4m3(word(k1, w));
+                        const uint32_t a2 = f16x2_of_e4m3_hi(word(k0, w)), a3 = f16x2_of_e4m3_hi(word(k1, w));
+                        const uint4 &q = w < 2 ? qa : qb;
+                        const uint32_t b0 = w & 1 ? q.z : q.x, b1 = w & 1 ? q.w : q.y;
+                        if (w == 0)
+                            mma_f16_zero(acc[ab], a0, a1, a2, a3, b0, b1);
+                        else
+                            mma_f16(acc[ab], a0, a1, a2, a3, b0, b1);
+                    }
+                }
+                const uint4 sc = lds128(q_frag + 8 * 512);
+                const float ek = q8_scale(now.k_scale);
+                const float f0 = __uint_as_float(sc.x) * ek, f1 = __uint_as_float(sc.y) * ek;
+                x[0] = ((acc[0][0] + acc[1][0]) + (acc[2][0] + acc[3][0])) * f0;
+                x[1] = ((acc[0][1] + acc[1][1]) + (acc[2][1] + acc[3][1])) * f1;
+                x[2] = ((acc[0][2] + acc[1][2]) + (acc[2][2] + acc[3][2])) * f0;
+                x[3] = ((acc[0][3] + acc[1][3]) + (acc[2][3] + acc[3][3])) * f1;
+                if (now.rows < kTile) {  // what lies behind the valid rows may be anything
+                    if (r >= now.rows) x[0] = x[1] = -CUDART_INF_F;
+                    if (r + 8 >= now.rows) x[2] = x[3] = -CUDART_INF_F;
+                }
+            }
+            const float ev = now.v_scale == 255 ? CUDART_NAN_F : (float)((int)now.v_scale - 127);
+
+            // ---- references, moved when a score passes one by more than kLag
+            float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+            if (__any_sync(0xffffffffu, mx0 > m0 + kLag || mx1 > m1 + kLag || mx0 + ev > v_ref0 + kLag ||
+                                            mx1 + ev > v_ref1 + kLag)) {
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+                }
+                auto moved = [](float &ref, float to) {  // what sums relative to it are multiplied by
+                    const float n = fmaxf(ref, to), f = n == ref ? 1.f : ex2_approx(ref - n);
+                    ref = n;
+                    return f;
+                };
+                l0 *= moved(m0, mx0);
+                l1 *= moved(m1, mx1);
+                const float g0 = moved(v_ref0, mx0 + ev), g1 = moved(v_ref1, mx1 + ev);
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            o[a][w][k][0] *= g0;
+                            o[a][w][k][1] *= g1;
+                            o[a][w][k][2] *= g0;
+                            o[a][w][k][3] *= g1;
+                        }
+            }
+            // (a reference is -inf while there has been no score above it: all of them NaN or -inf)
+            const float mu0 = m0 == -CUDART_INF_F ? 0.f : m0, mu1 = m1 == -CUDART_INF_F ? 0.f : m1;
+            const float ve0 = (v_ref0 == -CUDART_INF_F ? 0.f : v_ref0) - kTop;
+            const float ve1 = (v_ref1 == -CUDART_INF_F ? 0.f : v_ref1) - kTop;
+            l0 += ex2_approx(x[0] - mu0) + ex2_approx(x[2] - mu0);
+            l1 += ex2_approx(x[1] - mu1) + ex2_approx(x[3] - mu1);
+            const float e0 = ev - ve0, e1 = ev - ve1;
+            const uint32_t b0 = movmatrix_t(pack_f16x2(ex2_approx(x[0] + e0), ex2_approx(x[1] + e1)));
+            const uint32_t b1 = movmatrix_t(pack_f16x2(ex2_approx(x[2] + e0), ex2_approx(x[3] + e1)));
+
+            // ---- O^T += V^T W^T: two tokens' codes of a dim a register
+            const uint32_t va = base + kTileCodes + 2 * c * 128 + ((r ^ (2 * c)) << 4);
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const uint32_t v_at = va + a * 2048, v_at1 = (v_at ^ 16) + 128;
+                uint4 t0v = lds128(v_at), t1v = lds128(v_at1);                // tokens 2c, 2c + 1
+                uint4 t8v = lds128(v_at + 1024), t9v = lds128(v_at1 + 1024);  // tokens 2c + 8, 2c + 9
+                if (now.rows < kTile) {
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    if (2 * c >= now.rows) t0v = zero;
+                    if (2 * c + 1 >= now.rows) t1v = zero;
+                    if (2 * c + 8 >= now.rows) t8v = zero;
+                    if (2 * c + 9 >= now.rows) t9v = zero;
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t sel = k ? 0x7362 : 0x5140;
+                        const uint32_t lo = __byte_perm(word(t0v, w), word(t1v, w), sel);
+                        const uint32_t hi = __byte_perm(word(t8v, w), word(t9v, w), sel);
+                        mma_f16(o[a][w][k], f16x2_of_e4m3(lo), f16x2_of_e4m3_hi(lo), f16x2_of_e4m3(hi),
+                                f16x2_of_e4m3_hi(hi), b0, b1);
+                    }
+            }
+            __syncwarp();  // the slot is free
+        }
+        // Every load lands before its slot is loaded again or left (when a wait gave up).
+        for (uint32_t i = it + max(0, loaded - kDepth); i < it + loaded; ++i)
+            mbar_wait(&full[i % kDepth], (i / kDepth) & 1, p.err);
+        it += n;
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
+        }
+
+        // ---- the next segment's first loads and its q, before this one's merge
+        const int64_t pair = (int64_t)seq * p.num_kv_heads + g, part = blockIdx.x + pair;
+        const bool whole = t0 == 0 && t1 == tiles;
+        if (threadIdx.x == 0 && t0 == 0)
+            p.info[pair] =
+                make_int2((int)part, whole ? 0 : (int)(st.shares.owner(at - v0 + lead + tiles - 1) - blockIdx.x) + 1);
+        uint16_t *out_rows = p.out + ((int64_t)seq * p.num_q_heads + g * p.group) * kHeadDim;
+        at += lead + t1 - v0;
+        const bool more = end > at + lead;  // (a share that ends before the next pair's first tile is done)
+        const uint32_t spare = (it + kDepth - 1) % kDepth;  // the slot that the next segment loads last
+        if (more) {
+            v0 = 0;
+            if (++g == p.num_kv_heads) {
+                g = 0;
+                do tiles = seq_tiles(p, ++seq, &seq_len, false);
+                while (tiles == 0 && seq < p.num_seqs);
+            }
+            begin_segment();
+            load_q();
+            first_loads();
+        }
+
+        // ------------------------------------------------------------ merge of the warps
+        // A warp's sums, relative to m, as rows of 64 units of 16 bytes, unit u of head h at place
+        // u ^ (h / 2).
+        float2 *red_ml = reinterpret_cast<float2 *>(smem + kOffMl);  // [warp][head]
+        if (lane < 4) {
+            red_ml[warp * kDecMaxGroup + 2 * c] = make_float2(m0, l0);
+            red_ml[warp * kDecMaxGroup + 2 * c + 1] = make_float2(m1, l1);
+        }
+        if (lane == 0) sum_slot[warp] = (int)(warp * kDepth + spare);
+        {
+            float4 *rows = reinterpret_cast<float4 *>(ring + spare * kSlotBytes) + 2 * c * 64;
+            // (without a score above -inf the sums are 0, or NaN)
+            const float u0 = m0 == -CUDART_INF_F ? 0.f : ex2_approx(v_ref0 - kTop - m0);
+            const float u1 = m1 == -CUDART_INF_F ? 0.f : ex2_approx(v_ref1 - kTop - m1);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int unit = (32 * a + 4 * r + w) ^ c;
+                    const float(&x)[2][4] = o[a][w];
+                    rows[unit] = make_float4(x[0][0] * u0, x[0][2] * u0, x[1][0] * u0, x[1][2] * u0);
+                    rows[64 + unit] = make_float4(x[0][1] * u1, x[0][3] * u1, x[1][1] * u1, x[1][3] * u1);
+                }
+        }
+        fence_proxy_async_smem();  // (the slot's next contents come by a bulk copy)
+        __syncthreads();  // every warp's rows are there, and q is no longer read
+        const bool gave_up = *abort != 0;  // a wait ran out: this and the CTA's remaining segments contribute nothing
+        if (more) make_q();
+        for (int qd = threadIdx.x; qd < p.group * (kHeadDim / 4); qd += kThreads) {
+            const int h = qd / (kHeadDim / 4), u = qd - h * (kHeadDim / 4), d = u * 4;
+            float M = -CUDART_INF_F;
+            float2 ml[kW];
+#pragma unroll
+            for (int v = 0; v < kW; ++v) {
+                ml[v] = red_ml[v * kDecMaxGroup + h];
+                M = fmaxf(M, ml[v].x);
+            }
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < kW; ++v) {
+                const float e = M == -CUDART_INF_F ? 0.f : ex2_approx(ml[v].x - M);
+                const float4 f = reinterpret_cast<const float4 *>(smem + sum_slot[v] * kSlotBytes)[h * 64 + (u ^ (h >> 1))];
+                L += e * ml[v].y;
+                O.x += e * f.x;
+                O.y += e * f.y;
+                O.z += e * f.z;
+                O.w += e * f.w;
+            }
+            if (gave_up) {  // an empty part, or zeros
+                O = make_float4(0.f, 0.f, 0.f, 0.f);
+                M = -CUDART_INF_F;
+                L = 0.f;
+            }
+            if (whole) {
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                *reinterpret_cast<uint2 *>(out_rows + h * kHeadDim + d) =
+                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+            } else {
+                *reinterpret_cast<float4 *>(p.part_o + (part * p.group + h) * kHeadDim + d) = O;
+                if (d == 0) p.part_ml[part * p.group + h] = make_float2(M, L);
+            }
+        }
+
+        if (!more) return;
+        __syncthreads();  // q is ready, and the merge's rows are free
+    }
+}
+
+}  // namespace
+
+size_t decode_q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms) {
+    const WsLayout l = ws_layout(num_seqs, num_q_heads, num_kv_heads, num_sms);
+    return l.o + l.ml + l.info;
+}
+
+#ifdef PA_TEST_HOOKS
+cudaError_t set_decode_q8_test_hook(int skip_tile) {
+    return cudaMemcpyToSymbol(g_test_skip_tile, &skip_tile, sizeof skip_tile);
+}
+#endif
+
+cudaError_t launch_decode_q8(const CUtensorMap *tmaps, const DecodeQ8Args &a, cudaStream_t stream) {
+    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_q8_stream_kernel), kSmem, 9);
+    if (e != cudaSuccess) return e;
+    Params p;
+    fill_split(p, a);
+    p.k_scales = a.k_scales;
+    p.v_scales = a.v_scales;
+    p.scale_stride = a.scale_stride;
+    if (a.ev_start && (e = record_event(a.ev_start, stream)) != cudaSuccess) return e;
+    e = launch_pdl(decode_q8_stream_kernel, dim3(split_grid<kMinShare>(p, a)), dim3(kThreads), kSmem, stream,
+                   tmaps[0], tmaps[1], p);
+    if (e != cudaSuccess) return e;
+    if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
+    return launch_merge(p, a.num_sms, stream);
+}
+
+}  // namespace pa

@@ -17,7 +17,7 @@ uintptr_t current_context();
 // Raises a kernel's dynamic shared-memory limit once per (kernel slot, device context),
 // so that later launches (possibly under stream capture) make no attribute call.  Slots:
 // 0 and 3 the two decode kernel shapes, 1, 2, 4, 5 the four prefill kernel variants with
-// BF16 operands, 7, 8, 10, 11 those with FP16 operands, 6 the 4-bit decode.
+// BF16 operands, 7, 8, 10, 11 those with FP16 operands, 6 the 4-bit decode, 9 the 8-bit one.
 constexpr int kSmemSlots = 12;
 cudaError_t set_smem_once(const void *kernel, int bytes, int slot);
 
@@ -174,38 +174,6 @@ struct Q4GatherArgs {
 };
 cudaError_t launch_gather_q4(const Q4GatherArgs &a, cudaStream_t stream);
 
-// Sequences of the 4-bit cache as FP16 pages of kQ4PrefillPage tokens (a multiple of the
-// prefill kernel's 64-key blocks) beside FP16 queries, for the prefill kernel.
-constexpr int kQ4PrefillPage = 256;
-constexpr int kQ4ExpandKeys = 64;  // keys of one head per CTA of the expansion
-constexpr int kQ4RangeKeys = 1024; // keys of one head per CTA of the range pass
-struct Q4ExpandSeq {
-    int page0;     // its first output page; its keys fill ceil(num_keys / kQ4PrefillPage)
-    int range0;    // its first entry of `ranges` (per KV head, ceil(num_keys / kQ4RangeKeys))
-    int num_keys;
-    int bt_row;    // its row of the block table
-};
-struct Q4ExpandArgs {
-    const uint16_t *q;       // BF16 [q_rows], q_rows = tokens * num_q_heads rows of 256
-    int64_t q_rows;
-    const uint8_t *k_cache, *v_cache;
-    int64_t page_stride, num_pages;
-    const int32_t *block_table;
-    int64_t bt_stride;
-    int num_kv_heads, block_size, num_seqs, num_ranges;
-    Q4ExpandSeq seq[32];
-    uint16_t *q_out;         // FP16 rows, each scaled by a power of two, and what undoes it
-    float *q_factor;
-    float2 *ranges;          // [num_kv_heads, num_ranges]: bounds of |K| and |V|
-    float2 *kv_factor;       // [num_seqs, num_kv_heads]
-    uint16_t *k_out, *v_out;
-    int32_t *table_out;      // [num_seqs, table_stride]: the output pages of each sequence
-    int64_t table_stride;
-    unsigned *err;
-};
-// Two launches: ranges and queries, then keys and values.
-cudaError_t launch_expand_q4(const Q4ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
-
 struct DecodeQ4Args {
     const uint16_t *q;
     const uint8_t *k_cache, *v_cache;
@@ -224,6 +192,84 @@ struct DecodeQ4Args {
 size_t decode_q4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms);
 cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream);
 
+// ----------------------------------------------------------------- 8-bit cache
+// Row strides in BF16 elements; page and scale strides (between pages) in bytes.
+struct Q8WriteArgs {
+    const uint16_t *key, *value;
+    int64_t key_stride, value_stride;  // between tokens
+    uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+    int64_t page_stride, scale_stride, num_pages;
+    const int64_t *slot_mapping;
+    int num_tokens, num_kv_heads, block_size;
+    unsigned *err;
+    int range;  // set by the launch: tokens of a CTA
+};
+cudaError_t launch_write_q8(const Q8WriteArgs &a, cudaStream_t stream);
+
+struct Q8GatherArgs {
+    const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+    int64_t page_stride, scale_stride, num_pages;
+    const int64_t *slot_mapping;
+    int num_tokens, num_kv_heads, block_size;
+    uint16_t *k_out, *v_out;
+    unsigned *err;
+};
+cudaError_t launch_gather_q8(const Q8GatherArgs &a, cudaStream_t stream);
+
+struct DecodeQ8Args {
+    const uint16_t *q;
+    const uint8_t *k_scales, *v_scales;
+    int64_t scale_stride, num_pages;
+    const int32_t *block_table;
+    int64_t bt_stride;
+    const int32_t *seq_lens;
+    int num_seqs, max_seq_len, num_q_heads, num_kv_heads, block_size;
+    float scale;
+    uint16_t *out;
+    void *workspace;
+    unsigned *err;
+    int num_sms;
+    cudaEvent_t ev_start, ev_stop;
+};
+size_t decode_q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int num_sms);
+// tmaps: the codes of K and V, whose boxes hold one 16-token tile of one KV head.
+cudaError_t launch_decode_q8(const CUtensorMap *tmaps, const DecodeQ8Args &a, cudaStream_t stream);
+
+// ----------------------------------------------------------------- expansion for the prefill
+// Sequences of the 4-bit or the 8-bit cache as FP16 pages of kExpandPage tokens (a multiple of the
+// prefill kernel's 64-key blocks) beside FP16 queries, for the prefill kernel.
+constexpr int kExpandPage = 256;
+constexpr int kExpandKeys = 64;    // keys of one head per CTA of the expansion
+constexpr int kExpandRange = 1024; // keys of one head per CTA of the range pass
+struct ExpandSeq {
+    int page0;     // its first output page; its keys fill ceil(num_keys / kExpandPage)
+    int range0;    // its first entry of `ranges` (per KV head, ceil(num_keys / kExpandRange))
+    int num_keys;
+    int bt_row;    // its row of the block table
+};
+struct ExpandArgs {
+    const uint16_t *q;       // BF16 [q_rows], q_rows = tokens * num_q_heads rows of 256
+    int64_t q_rows;
+    const uint8_t *k_cache, *v_cache;
+    const uint8_t *k_scales, *v_scales;  // (8-bit cache)
+    int64_t page_stride, scale_stride, num_pages;
+    const int32_t *block_table;
+    int64_t bt_stride;
+    int num_kv_heads, block_size, num_seqs, num_ranges;
+    ExpandSeq seq[32];
+    uint16_t *q_out;         // FP16 rows, each scaled by a power of two, and what undoes it
+    float *q_factor;
+    float2 *ranges;          // [num_kv_heads, num_ranges]: bounds of |K| and |V|
+    float2 *kv_factor;       // [num_seqs, num_kv_heads]
+    uint16_t *k_out, *v_out;
+    int32_t *table_out;      // [num_seqs, table_stride]: the output pages of each sequence
+    int64_t table_stride;
+    unsigned *err;
+};
+// Two launches each: ranges and queries, then keys and values.
+cudaError_t launch_expand_q4(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
+cudaError_t launch_expand_q8(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
+
 // ----------------------------------------------------------------- norm + rotation
 struct RopeArgs {
     const uint16_t *q, *k, *v;
@@ -231,8 +277,11 @@ struct RopeArgs {
     const uint16_t *q_weight, *k_weight;
     float weight_bias, eps;
     const float *cos_sin;                  // [max_position, rotary_dim]
-    const int32_t *positions;
+    const int32_t *positions;              // [num_tokens], or [num_axes] rows of them
     int max_position, rotary_dim, interleaved;
+    int num_axes;                          // 0: one position a token
+    int64_t position_stride;               // between axes
+    uint32_t axes[8];                      // the axis of each frequency, two bits each
     int num_tokens, num_q_heads, num_kv_heads, head_dim;
     uint16_t *q_out, *k_out;
     int64_t q_out_stride, k_out_stride;
@@ -429,6 +478,7 @@ cudaError_t launch_prefill(const CUtensorMap *tmaps, const PrefillArgs &a, cudaS
 // The product library has neither the hooks nor these entry points.
 cudaError_t set_decode_test_hook(int skip_stage, int consumer_delay_ns);
 cudaError_t set_decode_q4_test_hook(int skip_pair);
+cudaError_t set_decode_q8_test_hook(int skip_tile);
 int decode_q4_pair_lead(uint32_t tiles, uint64_t pairs, uint32_t ctas);  // (host only)
 cudaError_t set_prefill_test_hook(int skip_unit);
 #endif

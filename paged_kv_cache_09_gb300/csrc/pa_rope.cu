@@ -21,7 +21,12 @@
 // 3.5 TB/s: warps with fewer rows of a token on their way).  16 warps an SM with 8 rows each on
 // their way move more than 20 or 24 with fewer (33 and 40 us): a row on its way is registers.
 // 16 tokens: 2.3 us.
+//
+// Positions on several axes (time, height, width of a token): frequency i takes its angle from the
+// position on the axis that the caller gives it.  Only the fetch of the angles differs: four
+// frequencies of one axis come as one 16-byte copy, as with one position, others one by one.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_internal.h"
 #include "pa_q4.cuh"
@@ -57,7 +62,7 @@ __device__ __forceinline__ uint32_t pack(f32x2 v) {
     return pack_bf16x2(lo, hi);
 }
 
-template <int kD, bool kNeighbours, int kCache>  // kCache: 0 none, 1 BF16, 2 4-bit
+template <int kD, bool kNeighbours, int kCache, bool kAxes>  // kCache: 0 none, 1 BF16, 2 4-bit
 __global__ void __launch_bounds__(kWarps * 32, 4)
     qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kLanes = kD / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a warp
@@ -91,24 +96,69 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         k_at = a.k + t * a.k_stride;
         if (kCache) v_at = a.v + t * a.v_stride;
     };
-    auto angles_of = [&](int64_t t, int pos, int buf) {
-        slot_next = kCache ? a.slot_mapping[t] : -1;
-        if (turns && pos >= 0 && pos < a.max_position) {
-            const float *row = a.cos_sin + (int64_t)pos * R +
-                               (kNeighbours ? 4 * l : second ? 8 * l - half : 8 * l);
-            constexpr int kN = kNeighbours ? 1 : 2;
+    // A token's positions on all axes.
+    struct Pos {
+        int at[kAxes ? 4 : 1];
+        __device__ __forceinline__ int lowest() const {
+            if constexpr (kAxes) return min(min(at[0], at[1]), min(at[2], at[3]));
+            return at[0];
+        }
+        __device__ __forceinline__ int highest() const {
+            if constexpr (kAxes) return max(max(at[0], at[1]), max(at[2], at[3]));
+            return at[0];
+        }
+        __device__ __forceinline__ int on(uint32_t axis) const {
+            if constexpr (kAxes) return axis & 2 ? (axis & 1 ? at[3] : at[2]) : axis & 1 ? at[1] : at[0];
+            return at[0];
+        }
+    };
+    constexpr int kN = kNeighbours ? 1 : 2;  // fours of frequencies of a lane
+    const int freq = kNeighbours ? 4 * l : second ? 8 * l - half : 8 * l;  // its first
+    uint32_t axes[kN] = {};  // of each four, two bits each
+    if constexpr (kAxes) {
+        if (turns)
 #pragma unroll
-            for (int e = 0; e < 2 * kN; ++e)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(&angles[threadIdx.x >> 5][buf][e][lane])),
-                             "l"(row + (e / kN) * half + (e % kN) * 4)
-                             : "memory");
+            for (int e = 0; e < kN; ++e) axes[e] = a.axes[(freq + 4 * e) / 16] >> (2 * ((freq + 4 * e) % 16)) & 0xffu;
+    }
+    auto copy = [&](float *dst, const float *src, auto bytes) {
+        if constexpr (decltype(bytes)::value == 16)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    };
+    using Four = std::integral_constant<int, 16>;
+    using One = std::integral_constant<int, 4>;
+    auto angles_of = [&](int64_t t, const Pos &pos, int buf) {
+        slot_next = kCache ? a.slot_mapping[t] : -1;
+        if (turns && pos.lowest() >= 0 && pos.highest() < a.max_position) {
+#pragma unroll
+            for (int e = 0; e < 2 * kN; ++e) {  // cosines, then sines
+                float *dst = &angles[threadIdx.x >> 5][buf][e][lane].x;
+                const float *column = a.cos_sin + freq + (e / kN) * half + (e % kN) * 4;
+                const uint32_t ax = axes[e % kN];
+                if (!kAxes || ax == (ax & 3) * 0x55u) {
+                    copy(dst, column + (int64_t)pos.on(ax & 3) * R, Four());
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        copy(dst + j, column + (int64_t)pos.on(ax >> (2 * j) & 3) * R + j, One());
+                }
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto position = [&](int64_t t) { return t < a.num_tokens ? a.positions[t] : -1; };
+    auto position = [&](int64_t t) {
+        Pos p;
+        p.at[0] = t < a.num_tokens ? a.positions[t] : -1;
+        if constexpr (kAxes)
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                p.at[i] = t < a.num_tokens && i < a.num_axes ? a.positions[i * a.position_stride + t] : p.at[0];
+        return p;
+    };
     const int64_t stride = gridDim.x;
-    int pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride), buf = 0;
+    Pos pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride);
+    int buf = 0;
     at(blockIdx.x);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) raw[b] = row_of(q_at, unit + b * step, hq);
@@ -116,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     if (kCache) raw_v = row_of(v_at, unit_v, hkv);
     angles_of(blockIdx.x, pos, 0);
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += stride, buf ^= 1) {
-    const int pos_now = pos;
+    const Pos pos_now = pos;
     const int64_t slot = slot_next;
     const bool more = t + stride < a.num_tokens;
     pos = pos_next;
@@ -128,8 +178,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     } else {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    const bool live = pos_now >= 0 && pos_now < a.max_position;  // otherwise its rows stay as they are
-    if (pos_now >= a.max_position && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPosition);
+    // (a token that is not live: its rows stay as they are)
+    const bool placed = pos_now.lowest() >= 0, live = placed && pos_now.highest() < a.max_position;
+    if (placed && !live && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPosition);
     int64_t run = -1;  // the slot's place in the caches (of head 0)
     int o = 0;
     if (kCache && live && slot >= 0) {
@@ -306,18 +357,18 @@ cudaError_t launch_dim(RopeArgs a, cudaStream_t stream) {
     a.shift_v = (a.shift_k + (a.num_kv_heads + one - 1) / one * one) % step;
     const int x = small ? a.num_tokens : std::min(a.num_tokens, std::max(1, 4 * a.num_sms / y));
     const dim3 grid(x, y), block(kWarps * 32);
-    if (a.interleaved) {
-        if (a.cache == 0) return launch_pdl(qk_norm_rope_kernel<kD, true, 0>, grid, block, 0, stream, a);
-        if (a.cache == 1) return launch_pdl(qk_norm_rope_kernel<kD, true, 1>, grid, block, 0, stream, a);
+    auto launch = [&](auto neighbours, auto axes) {
+        constexpr bool kN = decltype(neighbours)::value, kA = decltype(axes)::value;
+        if (a.cache == 0) return launch_pdl(qk_norm_rope_kernel<kD, kN, 0, kA>, grid, block, 0, stream, a);
+        if (a.cache == 1) return launch_pdl(qk_norm_rope_kernel<kD, kN, 1, kA>, grid, block, 0, stream, a);
         if constexpr (kD == kHeadDim)
-            return launch_pdl(qk_norm_rope_kernel<kD, true, 2>, grid, block, 0, stream, a);
-    } else {
-        if (a.cache == 0) return launch_pdl(qk_norm_rope_kernel<kD, false, 0>, grid, block, 0, stream, a);
-        if (a.cache == 1) return launch_pdl(qk_norm_rope_kernel<kD, false, 1>, grid, block, 0, stream, a);
-        if constexpr (kD == kHeadDim)
-            return launch_pdl(qk_norm_rope_kernel<kD, false, 2>, grid, block, 0, stream, a);
-    }
-    return cudaErrorInvalidValue;
+            return launch_pdl(qk_norm_rope_kernel<kD, kN, 2, kA>, grid, block, 0, stream, a);
+        return cudaErrorInvalidValue;
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (a.num_axes) return a.interleaved ? launch(yes, yes) : launch(no, yes);
+    return a.interleaved ? launch(yes, no) : launch(no, no);
 }
 
 }  // namespace
