@@ -19,7 +19,9 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMaxRange = 16;      // tokens of a CTA
+constexpr int kWriteWarps = 16;
+constexpr int kMaxRange = 16;      // tokens of a CTA of the write
+constexpr int kScan = 8;           // slots of a thread in flight
 constexpr int kMapBits = 4096;
 
 __device__ __forceinline__ uint32_t map_bit(long long slot) { return (uint32_t)(slot >> 4) % kMapBits; }
@@ -53,33 +55,44 @@ __device__ __forceinline__ uint32_t codes_down(uint32_t c, float f) {
     return e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-__global__ void __launch_bounds__(kWarps * 32) write_q8_kernel(const Q8WriteArgs a) {
+// Two warps for each head of K and of V: the first and the last 8 rows of a block, 8 dims a lane.
+__global__ void __launch_bounds__(kWriteWarps * 32, 2) write_q8_kernel(const Q8WriteArgs a) {
+    constexpr int kThreads = kWriteWarps * 32, kHalf = kQ8Tokens / 2;
     __shared__ long long first[kMaxRange];  // a block's first slot
     __shared__ int rows[kMaxRange];         // its rows in the page (0: no block)
     __shared__ int lowest[kMaxRange];       // its first token
-    __shared__ int token[kMaxRange][kQ8Tokens];
+    __shared__ __align__(16) int token[kMaxRange][kQ8Tokens];
     __shared__ uint32_t map[kMapBits / 32];
+    __shared__ uint32_t tops[2][kWriteWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * a.range, n = min(a.range, a.num_tokens - t0);
-    const int h = blockIdx.y * (kWarps / 2) + (warp >> 1);  // this warp's head, of K or of V
-    const bool is_v = warp & 1;
+    const int h = blockIdx.y * (kWriteWarps / 4) + (warp >> 2);  // this warp's head
+    const bool is_v = warp & 2;                                  // of K or of V
+    const int r0 = (warp & 1) * kHalf;                           // its first row
     const uint16_t *x = (is_v ? a.value : a.key) + (int64_t)h * kHeadDim + 8 * lane;
     const int64_t x_stride = is_v ? a.value_stride : a.key_stride;
     pdl_wait();
     pdl_trigger();
-    for (int i = threadIdx.x; i < kMapBits / 32; i += kWarps * 32) map[i] = 0;
-    for (int i = threadIdx.x; i < kMaxRange * kQ8Tokens; i += kWarps * 32) (&token[0][0])[i] = -1;
+    // The first slots of all, and the rows of this CTA's tokens, are on their way while the
+    // blocks are found.
+    long long s[kScan];
+#pragma unroll
+    for (int k = 0; k < kScan; ++k) {
+        const int j = threadIdx.x + k * kThreads;
+        s[k] = j < a.num_tokens ? a.slot_mapping[j] : -1;
+    }
+    const long long slot = warp == 0 && lane < n ? a.slot_mapping[t0 + lane] : -1;
+    if (h < a.num_kv_heads)
+        for (int i = (lane >> 2) + r0; i < n; i += kQ8Tokens)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (int64_t)(t0 + i) * x_stride - 8 * lane + 64 * (lane & 3)));
+    for (int i = threadIdx.x; i < kMapBits / 32; i += kThreads) map[i] = 0;
+    for (int i = threadIdx.x; i < kMaxRange * kQ8Tokens; i += kThreads) (&token[0][0])[i] = -1;
     if (threadIdx.x < kMaxRange) {
         rows[threadIdx.x] = 0;
         lowest[threadIdx.x] = 0x7fffffff;
     }
-    // The rows are on their way while the blocks are found.
-    if (h < a.num_kv_heads)
-        for (int i = lane >> 2; i < n; i += 8)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (t0 + i) * x_stride - 8 * lane + 64 * (lane & 3)));
     __syncthreads();
     if (warp == 0) {
-        const long long slot = lane < n ? a.slot_mapping[t0 + lane] : -1;
         long long f = -1;
         int count = 0;
         if (slot >= 0) {
@@ -102,21 +115,30 @@ __global__ void __launch_bounds__(kWarps * 32) write_q8_kernel(const Q8WriteArgs
         }
     }
     __syncthreads();
-#pragma unroll 4
-    for (int j = threadIdx.x; j < a.num_tokens; j += kWarps * 32) {
-        const long long s = a.slot_mapping[j];
-        const uint32_t bit = map_bit(s);
-        if (map[bit / 32] >> (bit % 32) & 1)
-            for (int e = 0; e < n; ++e) {
-                const unsigned long long at = (unsigned long long)(s - first[e]);
-                if (rows[e] && at < (unsigned)rows[e]) {
-                    atomicMax(&token[e][at], j);
-                    atomicMin(&lowest[e], j);
+    for (int j0 = 0; j0 < a.num_tokens; j0 += kScan * kThreads) {
+#pragma unroll
+        for (int k = 0; k < kScan; ++k) {
+            const int j = j0 + threadIdx.x + k * kThreads;
+            if (j0 > 0) s[k] = j < a.num_tokens ? a.slot_mapping[j] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kScan; ++k) {
+            const uint32_t bit = map_bit(s[k]);
+            if (map[bit / 32] >> (bit % 32) & 1)
+                for (int e = 0; e < n; ++e) {
+                    const unsigned long long at = (unsigned long long)(s[k] - first[e]);
+                    if (rows[e] && at < (unsigned)rows[e]) {
+                        const int j = j0 + threadIdx.x + k * kThreads;
+                        atomicMax(&token[e][at], j);
+                        atomicMin(&lowest[e], j);
+                    }
                 }
-            }
+        }
     }
     __syncthreads();
     if (h >= a.num_kv_heads) return;
+    const int64_t row_stride = (int64_t)a.num_kv_heads * kHeadDim;
+    int turn = 0;
     for (int e = 0; e < n; ++e) {
         const int in_page = rows[e];
         if (in_page == 0 || lowest[e] < t0) continue;  // none, or another CTA's
@@ -126,24 +148,24 @@ __global__ void __launch_bounds__(kWarps * 32) write_q8_kernel(const Q8WriteArgs
         uint8_t *scale = (is_v ? a.v_scales : a.k_scales) + page * a.scale_stride +
                          (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
         const uint32_t old = *scale;
-        int4 at[kQ8Tokens / 4];
-        uint4 v[kQ8Tokens];
+        const int4 at[2] = {*reinterpret_cast<const int4 *>(&token[e][r0]),
+                            *reinterpret_cast<const int4 *>(&token[e][r0 + 4])};
+        auto token_of = [&](int i) { return (&at[i / 4].x)[i % 4]; };
+        uint4 v[kHalf];
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < kQ8Tokens; ++i) {
-            if (i % 4 == 0) at[i / 4] = reinterpret_cast<const int4 *>(token[e])[i / 4];
-            const int t = (&at[i / 4].x)[i % 4];
+        for (int i = 0; i < kHalf; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
-            if (t >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(x + t * x_stride));
+            if (token_of(i) >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(x + token_of(i) * x_stride));
         }
 #pragma unroll
-        for (int i = 0; i < kQ8Tokens; ++i)
+        for (int i = 0; i < kHalf; ++i)
             top = abs_max2(abs_max2(abs_max2(abs_max2(top, v[i].x), v[i].y), v[i].z), v[i].w);
         uint32_t m = warp_top(top);
         if (m >= 0x7f80u) {  // infinities and NaN: codes of NaN, and no part in the scale
             top = 0;
 #pragma unroll
-            for (int i = 0; i < kQ8Tokens; ++i) {
+            for (int i = 0; i < kHalf; ++i) {
                 top = abs_max2(abs_max2(top, without_inf<true>(v[i].x)), without_inf<true>(v[i].y));
                 top = abs_max2(abs_max2(top, without_inf<true>(v[i].z)), without_inf<true>(v[i].w));
                 v[i].x = without_inf<false>(v[i].x);
@@ -153,60 +175,56 @@ __global__ void __launch_bounds__(kWarps * 32) write_q8_kernel(const Q8WriteArgs
             }
             m = warp_top(top);
         }
+        // The two warps meet; both have read the old byte by then.
+        if (lane == 0) tops[turn][warp] = m;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+        m = max(m, tops[turn][warp ^ 1]);
+        turn ^= 1;
         // m = 1.f 2^(E - 127) <= 448 2^(b - 127) = 1.75 2^8 2^(b - 127): b = E - 8, or one more
         // where f > .75
         const uint32_t need = (uint32_t)max(1, (int)(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0));
-        const bool anew = at[0].x >= 0 || old == 255;
+        const bool anew = token[e][0] >= 0 || old == 255;
         const uint32_t b = anew ? need : max(old, need);
         const float up = b == 254 ? 0x1p-127f : __uint_as_float((254 - b) << 23);
         uint8_t *row = (is_v ? a.v_cache : a.k_cache) + page * a.page_stride +
-                       ((int64_t)o * a.num_kv_heads + h) * kHeadDim + 8 * lane;
-        const int64_t row_stride = (int64_t)a.num_kv_heads * kHeadDim;
-        if (lane == 0 && b != old) *scale = (uint8_t)b;
+                       ((int64_t)(o + r0) * a.num_kv_heads + h) * kHeadDim + 8 * lane;
+        if (lane == 0 && r0 == 0 && b != old) *scale = (uint8_t)b;
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+            if (token_of(i) >= 0) *reinterpret_cast<uint2 *>(row + i * row_stride) = codes_of(v[i], up);
         if (!anew && b > old) {
             const float down = b - old > 126 ? 0.f : __uint_as_float((127 - (b - old)) << 23);
-            uint2 c[kQ8Tokens];
+            uint2 c[kHalf];
 #pragma unroll
-            for (int i = 0; i < kQ8Tokens; ++i)
-                if (i < in_page && (&at[i / 4].x)[i % 4] < 0)
-                    c[i] = *reinterpret_cast<const uint2 *>(row + i * row_stride);
+            for (int i = 0; i < kHalf; ++i)
+                if (r0 + i < in_page && token_of(i) < 0) c[i] = *reinterpret_cast<const uint2 *>(row + i * row_stride);
 #pragma unroll
-            for (int i = 0; i < kQ8Tokens; ++i)
-                if (i < in_page && (&at[i / 4].x)[i % 4] < 0)
+            for (int i = 0; i < kHalf; ++i)
+                if (r0 + i < in_page && token_of(i) < 0)
                     *reinterpret_cast<uint2 *>(row + i * row_stride) =
                         make_uint2(codes_down(c[i].x, down), codes_down(c[i].y, down));
         }
-#pragma unroll
-        for (int i = 0; i < kQ8Tokens; ++i)
-            if ((&at[i / 4].x)[i % 4] >= 0) *reinterpret_cast<uint2 *>(row + i * row_stride) = codes_of(v[i], up);
     }
 }
 
-// Sixteen codes times f, rounded to BF16, to 32 bytes.
-__device__ __forceinline__ void widen16(const uint4 &c, float f, uint16_t *out) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t r[8];
+// Eight codes times f, rounded to BF16.
+__device__ __forceinline__ uint4 widen8(const uint2 &c, float f) {
+    uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = f16x2_of_e4m3(w[i]), hi = f16x2_of_e4m3_hi(w[i]);
-        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-        const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        r[2 * i] = pack_bf16x2(p.x * f, p.y * f);
-        r[2 * i + 1] = pack_bf16x2(q.x * f, q.y * f);
+        const uint32_t w = i < 2 ? c.x : c.y, x = i & 1 ? f16x2_of_e4m3_hi(w) : f16x2_of_e4m3(w);
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+        r[i] = pack_bf16x2(p.x * f, p.y * f);
     }
-    reinterpret_cast<uint4 *>(out)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4 *>(out)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Read back by slots: warp per (token, head), lanes 0 .. 15 K and the others V, 16 dims a lane;
-// the warps of a CTA on one head, kTok tokens each.
+// Read back by slots: warp per (token, head), K and V of it, 8 dims a lane; the warps of a CTA
+// on one head, kTok tokens each.
 template <int kTok>
 __global__ void __launch_bounds__(kWarps * 32) gather_q8_kernel(const Q8GatherArgs a) {
     const int lane = threadIdx.x & 31, h = blockIdx.y;
-    const bool is_v = lane >= 16;
     const int64_t t0 = (int64_t)blockIdx.x * (kWarps * kTok) + (threadIdx.x >> 5);
-    const uint8_t *cache = is_v ? a.v_cache : a.k_cache, *scales = is_v ? a.v_scales : a.k_scales;
-    uint16_t *out = is_v ? a.v_out : a.k_out;
     pdl_wait();
     pdl_trigger();
     int64_t slot[kTok];
@@ -215,20 +233,22 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q8_kernel(const Q8GatherAr
         const int64_t t = t0 + k * kWarps;
         slot[k] = t < a.num_tokens ? a.slot_mapping[t] : -1;
     }
-    uint4 c[kTok];
-    uint32_t b[kTok];
+    uint2 ck[kTok], cv[kTok];
+    uint32_t bk[kTok], bv[kTok];
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
-        c[k] = make_uint4(0, 0, 0, 0);  // padding, and a slot outside the pool
-        b[k] = 127;
+        ck[k] = cv[k] = make_uint2(0, 0);  // padding, and a slot outside the pool
+        bk[k] = bv[k] = 127;
         if (slot[k] < 0) continue;
         const int64_t page = q8_page_of(slot[k], a.block_size);
         if (page < a.num_pages) {
             const int o = (int)(slot[k] - page * a.block_size);
-            c[k] = __ldg(reinterpret_cast<const uint4 *>(
-                             cache + page * a.page_stride + ((int64_t)o * a.num_kv_heads + h) * kHeadDim) +
-                         (lane & 15));
-            b[k] = __ldg(scales + page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h);
+            const int64_t at = page * a.page_stride + ((int64_t)o * a.num_kv_heads + h) * kHeadDim;
+            const int64_t sat = page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
+            ck[k] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at) + lane);
+            cv[k] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at) + lane);
+            bk[k] = __ldg(a.k_scales + sat);
+            bv[k] = __ldg(a.v_scales + sat);
         } else if (lane == 0) {
             atomicOr(a.err, kErrSlot);
         }
@@ -236,8 +256,10 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q8_kernel(const Q8GatherAr
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
         const int64_t t = t0 + k * kWarps;
-        if (t < a.num_tokens)
-            widen16(c[k], q8_scale(b[k]), out + (t * a.num_kv_heads + h) * kHeadDim + 16 * (lane & 15));
+        if (t >= a.num_tokens) return;
+        const int64_t row = (t * a.num_kv_heads + h) * kHeadDim;
+        reinterpret_cast<uint4 *>(a.k_out + row)[lane] = widen8(ck[k], q8_scale(bk[k]));
+        reinterpret_cast<uint4 *>(a.v_out + row)[lane] = widen8(cv[k], q8_scale(bv[k]));
     }
 }
 
@@ -297,54 +319,52 @@ __global__ void __launch_bounds__(kWarps * 32) range_q8_kernel(const __grid_cons
 // An FP16 pair of 2^e, e <= 6: exact down to 2^-24.
 __device__ __forceinline__ __half2 half2_pow2(int e) { return __float2half2_rn(__uint_as_float((uint32_t)(e + 127) << 23)); }
 
-// Sixteen codes times 2^d as FP16, to 32 bytes.
-__device__ __forceinline__ void expand16(const uint4 &c, int d, bool nan, uint16_t *out) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// Eight codes times 2^d as FP16.
+__device__ __forceinline__ uint4 expand8(const uint2 &c, int d, bool nan) {
     const __half2 f = nan ? __float2half2_rn(__uint_as_float(0x7fc00000u)) : half2_pow2(max(d, -15));
-    uint32_t r[8];
+    uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t x = i & 1 ? f16x2_of_e4m3_hi(w[i / 2]) : f16x2_of_e4m3(w[i / 2]);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? c.x : c.y, x = i & 1 ? f16x2_of_e4m3_hi(w) : f16x2_of_e4m3(w);
         __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x), f);  // exact
         if (d < -15) y = __hmul2(y, half2_pow2(max(d + 15, -24)));
         r[i] = *reinterpret_cast<uint32_t *>(&y);
     }
-    reinterpret_cast<uint4 *>(out)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4 *>(out)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Warp per (key, head), lanes 0 .. 15 K and the others V, 16 dims a lane; the warps of a CTA on
-// consecutive keys of one head, a warp's kExpandKeys / kWarps keys in flight together.
+// Warp per (key, head), K and V of it, 8 dims a lane; the warps of a CTA on consecutive keys of one
+// head, a warp's kExpandKeys / kWarps keys in flight together.
 __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int kRows = kExpandKeys / kWarps;  // keys of a warp
     __shared__ uint32_t part[2][kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-    const bool is_v = lane >= 16;
     const int64_t key0 = (int64_t)blockIdx.x * kExpandKeys;  // of the stacked, page-padded keys
     int b = 0;
     while (b + 1 < a.num_seqs && key0 >= (int64_t)a.seq[b + 1].page0 * kExpandPage) ++b;
     const ExpandSeq sq = a.seq[b];
     const int k0 = (int)(key0 - (int64_t)sq.page0 * kExpandPage);  // key of the sequence
-    const uint8_t *cache = is_v ? a.v_cache : a.k_cache, *scales = is_v ? a.v_scales : a.k_scales;
     pdl_wait();
     pdl_trigger();
     if (h == 0 && k0 % kExpandPage == 0 && threadIdx.x == 0)
         a.table_out[(int64_t)b * a.table_stride + k0 / kExpandPage] = sq.page0 + k0 / kExpandPage;
     const int32_t *bt = a.block_table + (int64_t)sq.bt_row * a.bt_stride;
-    uint4 c[kRows];
-    uint32_t sc[kRows];
+    uint2 ck[kRows], cv[kRows];
+    uint32_t bk[kRows], bv[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int k = k0 + i * kWarps + warp;
-        c[i] = make_uint4(0, 0, 0, 0);  // a page outside the pool reads as zeros
-        sc[i] = 0;
+        ck[i] = cv[i] = make_uint2(0, 0);  // a page outside the pool reads as zeros
+        bk[i] = bv[i] = 0;
         if (k >= sq.num_keys) continue;
         const int lp = k / a.block_size, o = k - lp * a.block_size, page = bt[lp];
         if (page >= 0 && page < a.num_pages) {
-            c[i] = __ldg(reinterpret_cast<const uint4 *>(
-                             cache + page * a.page_stride + ((int64_t)o * a.num_kv_heads + h) * kHeadDim) +
-                         (lane & 15));
-            sc[i] = __ldg(scales + page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h);
+            const int64_t at = page * a.page_stride + ((int64_t)o * a.num_kv_heads + h) * kHeadDim;
+            const int64_t sat = page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
+            ck[i] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at) + lane);
+            cv[i] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at) + lane);
+            bk[i] = __ldg(a.k_scales + sat);
+            bv[i] = __ldg(a.v_scales + sat);
         } else if (lane == 0) {
             atomicOr(a.err, kErrPage);
         }
@@ -375,8 +395,9 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
     for (int i = 0; i < kRows; ++i) {
         const int k = i * kWarps + warp;
         if (k0 + k >= sq.num_keys) return;
-        const int64_t dst = ((key0 + k) * a.num_kv_heads + h) * kHeadDim + 16 * (lane & 15);
-        expand16(c[i], 6 + (int)sc[i] - (int)top[is_v], sc[i] == 255, (is_v ? a.v_out : a.k_out) + dst);
+        const int64_t dst = ((key0 + k) * a.num_kv_heads + h) * kHeadDim;
+        reinterpret_cast<uint4 *>(a.k_out + dst)[lane] = expand8(ck[i], 6 + (int)bk[i] - (int)top[0], bk[i] == 255);
+        reinterpret_cast<uint4 *>(a.v_out + dst)[lane] = expand8(cv[i], 6 + (int)bv[i] - (int)top[1], bv[i] == 255);
     }
 }
 
@@ -387,8 +408,8 @@ cudaError_t launch_write_q8(const Q8WriteArgs &args, cudaStream_t stream) {
     a.range = a.num_tokens <= 1024 ? 1 : a.num_tokens <= 2048 ? 8 : kMaxRange;
     return launch_pdl(write_q8_kernel,
                       dim3((unsigned)((a.num_tokens - 1) / a.range + 1),
-                           (a.num_kv_heads + kWarps / 2 - 1) / (kWarps / 2)),
-                      dim3(kWarps * 32), 0, stream, a);
+                           (a.num_kv_heads + kWriteWarps / 4 - 1) / (kWriteWarps / 4)),
+                      dim3(kWriteWarps * 32), 0, stream, a);
 }
 
 cudaError_t launch_gather_q8(const Q8GatherArgs &a, cudaStream_t stream) {
