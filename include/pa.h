@@ -636,12 +636,15 @@ int pa_decode_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache, con
 
 /*
  * pa_prefill_chunk_q8, pa_prefill_varlen_q8 -- pa_prefill_chunk and pa_prefill_varlen over the
- * 8-bit cache (the chunk's own tokens included, which must be in it).  As in the 4-bit calls the
- * sequences' keys and values and the queries are first expanded into FP16 in the required
- * workspace, each query row and K and V of each KV head of a sequence scaled by a power of two.
- * Precision: K and V are exact while a block's scale is at least 2^-15 of the head's largest in that
- * sequence (smaller values lose bits below 2^-39 of the largest); queries and weights as in the
- * 4-bit calls, as are the other arguments, errors and what a NaN in V reaches.
+ * 8-bit cache (the chunk's own tokens included, which must be in it).  The sequences' keys and
+ * values are first expanded into the required workspace (1 KB per key and KV head, and room for
+ * split items), K into BF16, which holds its values exactly, V into FP16, each KV head of a
+ * sequence scaled by a power of two.
+ * Precision: queries and K are exact, and V while a block's scale is at least 2^-15 of the largest
+ * of its KV head in that sequence (smaller values are off by up to 2^-39 of the head's largest);
+ * weights are rounded to FP16, off by up to 2^-11 of themselves, and by up to 2^-32 of the row's
+ * largest below 2^-21 of it.  Arguments, errors and what a NaN in V reaches are those of the 4-bit
+ * calls.
  */
 size_t pa_prefill_q8_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
                                     int num_kv_heads, int head_dim, int block_size);

@@ -1042,8 +1042,8 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
                                                                                      : PA_ERR_CUDA;
 }
 
-// Workspace of the 4-bit and the 8-bit prefill: the batch's K, then its V, as FP16 pages, the queries as
-// FP16, the factors that undo their scaling, the heads' ranges, the pages' block tables, and
+// Workspace of the 4-bit and the 8-bit prefill: the batch's K, then its V, as pages of 16-bit
+// values, the queries as FP16 (4-bit: with_q), the factors that undo their scaling, the heads' ranges, the pages' block tables, and
 // the room for split items; each part 256-byte aligned.  Batches are of kPfMaxSeqs chunks,
 // one after another in the same workspace (the queries of all of them are converted with the
 // first).
@@ -1056,8 +1056,8 @@ struct ExpandLayout {
 };
 static size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-static ExpandLayout expand_layout(const pa::PrefillSeq *seqs, int cnt, int total_q,
-                                         int num_q_heads, int num_kv_heads) {
+static ExpandLayout expand_layout(const pa::PrefillSeq *seqs, int cnt, int total_q, int num_q_heads,
+                                  int num_kv_heads, bool with_q) {
     ExpandLayout l;
     for (int b = 0; b < cnt; ++b) {
         const int keys = seqs[b].q_start + seqs[b].q_len;
@@ -1066,8 +1066,10 @@ static ExpandLayout expand_layout(const pa::PrefillSeq *seqs, int cnt, int total
         l.table_stride = std::max(l.table_stride, pages);
         l.ranges += (keys - 1) / pa::kExpandRange + 1;
     }
-    l.q = (size_t)total_q * num_q_heads * pa::kHeadDim * 2;
-    l.q_factor = up256((size_t)total_q * num_q_heads * 4);
+    if (with_q) {
+        l.q = (size_t)total_q * num_q_heads * pa::kHeadDim * 2;
+        l.q_factor = up256((size_t)total_q * num_q_heads * 4);
+    }
     l.kv = (size_t)l.pages * pa::kExpandPage * num_kv_heads * pa::kHeadDim * 2;
     l.kv_factor = up256((size_t)cnt * num_kv_heads * sizeof(float2));
     l.range = up256((size_t)l.ranges * num_kv_heads * sizeof(float2));
@@ -1077,7 +1079,7 @@ static ExpandLayout expand_layout(const pa::PrefillSeq *seqs, int cnt, int total
 
 static size_t expanded_workspace_size(const int32_t *cu_seqlens_q, const int32_t *seq_lens_k,
                                       int num_seqs, int causal, int num_q_heads, int num_kv_heads,
-                                      int head_dim, int block_size) try {
+                                      int head_dim, int block_size, bool with_q) try {
     std::vector<pa::PrefillSeq> seqs;
     if (!varlen_chunks(cu_seqlens_q, seq_lens_k, num_seqs, &seqs) || num_q_heads < 1 ||
         num_kv_heads < 1 || num_q_heads % num_kv_heads || head_dim != pa::kHeadDim ||
@@ -1090,7 +1092,7 @@ static size_t expanded_workspace_size(const int32_t *cu_seqlens_q, const int32_t
     for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
         const int cnt = (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0);
         size_t bytes = expand_layout(&seqs[s0], cnt, cu_seqlens_q[num_seqs], num_q_heads,
-                                         num_kv_heads).fixed();
+                                     num_kv_heads, with_q).fixed();
         if (prefill_schedule(&seqs[s0], cnt, causal ? 1 : 0, num_q_heads, num_q_heads / num_kv_heads,
                              pa::kExpandPage, dev.num_sms,
                              (size_t)pa::kPfMaxPieces * pa::kPfSlotBytes, &sched))
@@ -1104,7 +1106,7 @@ static size_t expanded_workspace_size(const int32_t *cu_seqlens_q, const int32_t
 
 // The prefill over a cache whose format `launch_expand` expands; `cache` holds its checked
 // pointers and sizes (cache_status: what the check found).
-static int prefill_expanded(const pa::ExpandArgs &cache, int cache_status,
+static int prefill_expanded(const pa::ExpandArgs &cache, int cache_status, bool with_q,
                             cudaError_t (*launch_expand)(const pa::ExpandArgs &, int64_t, cudaStream_t),
                             const pa_bf16 *q, const int32_t *block_table, int64_t bt_stride,
                             const int32_t *cu_seqlens_q, const int32_t *seq_lens_k, int num_seqs,
@@ -1130,7 +1132,7 @@ static int prefill_expanded(const pa::ExpandArgs &cache, int cache_status,
     for (size_t s0 = 0; s0 < seqs.size(); s0 += pa::kPfMaxSeqs) {
         layouts.push_back(expand_layout(&seqs[s0],
                                         (int)std::min<size_t>(pa::kPfMaxSeqs, seqs.size() - s0),
-                                        cu_seqlens_q[num_seqs], num_q_heads, num_kv_heads));
+                                        cu_seqlens_q[num_seqs], num_q_heads, num_kv_heads, with_q));
         // Split items are an option (as in pa_prefill_varlen); the pages are not.
         if (workspace_bytes < layouts.back().fixed()) return PA_ERR_INVALID_ARG;
     }
@@ -1144,7 +1146,7 @@ static int prefill_expanded(const pa::ExpandArgs &cache, int cache_status,
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         pa::ExpandArgs x = cache;
         x.q = q;
-        x.q_rows = s0 == 0 ? (int64_t)total_q * num_q_heads : 0;
+        x.q_rows = with_q && s0 == 0 ? (int64_t)total_q * num_q_heads : 0;
         x.block_table = block_table;
         x.bt_stride = bt_stride;
         x.num_seqs = cnt;
@@ -1171,11 +1173,12 @@ static int prefill_expanded(const pa::ExpandArgs &cache, int cache_status,
         }
         if (launch_expand(x, l.pages, st) != cudaSuccess) return PA_ERR_CUDA;
         if (int rc = prefill_launch(
-                x.q_out, total_q, x.k_out, x.v_out, (int64_t)pa::kExpandPage * num_kv_heads * head_dim,
+                with_q ? x.q_out : q, total_q, x.k_out, x.v_out, (int64_t)pa::kExpandPage * num_kv_heads * head_dim,
                 l.pages, x.table_out, l.table_stride, chunk, cnt, causal, num_q_heads, num_kv_heads,
                 head_dim, pa::kExpandPage, scale, out,
                 workspace_bytes > l.fixed() ? ws : nullptr, workspace_bytes - l.fixed(), dev,
-                s0 == 0 ? e0 : nullptr, s0 + cnt == seqs.size() ? e1 : nullptr, st, x.q_factor,
+                s0 == 0 ? e0 : nullptr, s0 + cnt == seqs.size() ? e1 : nullptr, st,
+                with_q ? x.q_factor : nullptr,
                 x.kv_factor))
             return rc;
     }
@@ -1188,7 +1191,7 @@ size_t pa_prefill_varlen_q4_workspace_size(const int32_t *cu_seqlens_q, const in
                                            int num_seqs, int causal, int num_q_heads,
                                            int num_kv_heads, int head_dim, int block_size) {
     return expanded_workspace_size(cu_seqlens_q, seq_lens_k, num_seqs, causal, num_q_heads,
-                                   num_kv_heads, head_dim, block_size);
+                                   num_kv_heads, head_dim, block_size, true);
 }
 
 int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache,
@@ -1206,7 +1209,7 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
     x.num_pages = num_pages;
     x.num_kv_heads = num_kv_heads;
     x.block_size = block_size;
-    return prefill_expanded(x, rc, pa::launch_expand_q4, q, block_table, bt_stride, cu_seqlens_q, seq_lens_k,
+    return prefill_expanded(x, rc, true, pa::launch_expand_q4, q, block_table, bt_stride, cu_seqlens_q, seq_lens_k,
                             num_seqs, causal, num_q_heads, head_dim, scale, out, workspace,
                             workspace_bytes, stream);
 }
@@ -1370,7 +1373,7 @@ size_t pa_prefill_varlen_q8_workspace_size(const int32_t *cu_seqlens_q, const in
                                            int num_seqs, int causal, int num_q_heads,
                                            int num_kv_heads, int head_dim, int block_size) {
     return expanded_workspace_size(cu_seqlens_q, seq_lens_k, num_seqs, causal, num_q_heads,
-                                   num_kv_heads, head_dim, block_size);
+                                   num_kv_heads, head_dim, block_size, false);
 }
 
 int pa_prefill_varlen_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache,
@@ -1392,15 +1395,17 @@ int pa_prefill_varlen_q8(const pa_bf16 *q, const void *k_cache, const void *v_ca
     x.num_pages = num_pages;
     x.num_kv_heads = num_kv_heads;
     x.block_size = block_size;
-    return prefill_expanded(x, rc, pa::launch_expand_q8, q, block_table, bt_stride, cu_seqlens_q, seq_lens_k,
+    return prefill_expanded(x, rc, false, pa::launch_expand_q8, q, block_table, bt_stride, cu_seqlens_q, seq_lens_k,
                             num_seqs, causal, num_q_heads, head_dim, scale, out, workspace,
                             workspace_bytes, stream);
 }
 
 size_t pa_prefill_q8_workspace_size(int q_len, int q_start, int causal, int num_q_heads,
                                     int num_kv_heads, int head_dim, int block_size) {
-    return pa_prefill_q4_workspace_size(q_len, q_start, causal, num_q_heads, num_kv_heads, head_dim,
-                                        block_size);
+    if (q_len < 1 || q_start < 0 || (int64_t)q_start + q_len > 0x7fffffffLL) return 0;
+    const int32_t cu[2] = {0, q_len}, len = q_start + q_len;
+    return pa_prefill_varlen_q8_workspace_size(cu, &len, 1, causal, num_q_heads, num_kv_heads,
+                                               head_dim, block_size);
 }
 
 int pa_prefill_chunk_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache,

@@ -11,7 +11,7 @@
 // these blocks; of a block's tokens the first one's CTA writes it.  So the result does not depend
 // on the order of tokens, no two CTAs touch one block, and of tokens that share a slot the last
 // one counts.  The look through the slots costs 8 bytes of L2 a slot and CTA.
-#include "pa_expand.cuh"
+#include "pa_internal.h"
 #include "pa_q8.cuh"
 
 namespace pa {
@@ -263,23 +263,19 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q8_kernel(const Q8GatherAr
     }
 }
 
-// ---- prefill: FP16 operands from the 8-bit cache and BF16 queries (pa_expand.cuh)
+// ---- prefill: operands from the 8-bit cache
 //
-// A head's codes times 2^(6 + b - its largest b), 2^15 at most: exact while a block's scale is down
-// to 2^-15 of the head's largest (and then for all codes but those near 2^-9).
+// K becomes BF16, which holds a code times a power of two exactly, so that the scores are those of
+// the BF16 queries as they are.  V becomes FP16, which its products with FP16 weights need (a weight
+// takes one FP16 part, but two BF16 ones): a head's codes times 2^(6 + b - its largest b), 2^15
+// at most, exact while a block's scale is down to 2^-15 of the head's largest (and then for all codes
+// but those near 2^-9).
 
-// Blocks [0, num_ranges * num_kv_heads): the largest scale bytes of K and V (but 255) over
-// kExpandRange keys of one head.  The other blocks: kWarps rows of Q each.
+// The largest scale byte of V (but 255) over kExpandRange keys of one head.
 __global__ void __launch_bounds__(kWarps * 32) range_q8_kernel(const __grid_constant__ ExpandArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
-    const int nr = a.num_ranges * a.num_kv_heads;
-    if ((int)blockIdx.x >= nr) {
-        const int64_t row = (int64_t)(blockIdx.x - nr) * kWarps + warp;
-        if (row < a.q_rows) expand_query(a, row, lane);
-        return;
-    }
     const int h = blockIdx.x / a.num_ranges, range = blockIdx.x - h * a.num_ranges;
     int b = 0;
     while (b + 1 < a.num_seqs && range >= a.seq[b + 1].range0) ++b;
@@ -287,32 +283,23 @@ __global__ void __launch_bounds__(kWarps * 32) range_q8_kernel(const __grid_cons
     const int32_t *bt = a.block_table + (int64_t)s.bt_row * a.bt_stride;
     const int k0 = (range - s.range0) * kExpandRange;
     const int k1 = min(s.num_keys, k0 + kExpandRange);
-    uint32_t top[2] = {0, 0};
+    uint32_t top = 0;
     // (a block counts with its first key in the range, which need not be its first row)
     for (int k = k0 + threadIdx.x; k < k1; k += kWarps * 32) {
         const int lp = k / a.block_size, o = k - lp * a.block_size;
         if (o % kQ8Tokens && k > k0) continue;
         const int page = bt[lp];
         if (page < 0 || page >= a.num_pages) continue;  // reported by the expansion
-        const int64_t at = page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
-        const uint32_t kb = __ldg(a.k_scales + at), vb = __ldg(a.v_scales + at);
-        if (kb != 255) top[0] = max(top[0], kb);
-        if (vb != 255) top[1] = max(top[1], vb);
+        const uint32_t vb = __ldg(a.v_scales + page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h);
+        if (vb != 255) top = max(top, vb);
     }
-    __shared__ uint32_t part[2][kWarps];
-    top[0] = __reduce_max_sync(0xffffffffu, top[0]);
-    top[1] = __reduce_max_sync(0xffffffffu, top[1]);
-    if (lane == 0) {
-        part[0][warp] = top[0];
-        part[1][warp] = top[1];
-    }
+    __shared__ uint32_t part[kWarps];
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) part[warp] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 0; w < kWarps; ++w) {
-            top[0] = max(top[0], part[0][w]);
-            top[1] = max(top[1], part[1][w]);
-        }
-        a.ranges[(int64_t)h * a.num_ranges + range] = make_float2((float)top[0], (float)top[1]);
+        for (int w = 0; w < kWarps; ++w) top = max(top, part[w]);
+        a.ranges[(int64_t)h * a.num_ranges + range] = make_float2(0.f, (float)top);
     }
 }
 
@@ -337,7 +324,7 @@ __device__ __forceinline__ uint4 expand8(const uint2 &c, int d, bool nan) {
 // head, a warp's kExpandKeys / kWarps keys in flight together.
 __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_constant__ ExpandArgs a) {
     constexpr int kRows = kExpandKeys / kWarps;  // keys of a warp
-    __shared__ uint32_t part[2][kWarps];
+    __shared__ uint32_t part[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
     const int64_t key0 = (int64_t)blockIdx.x * kExpandKeys;  // of the stacked, page-padded keys
     int b = 0;
@@ -369,35 +356,25 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
             atomicOr(a.err, kErrPage);
         }
     }
-    // The head's largest scales, from all of its sequence's ranges.
-    uint32_t top[2] = {0, 0};
+    // The head's largest scale of V, from all of its sequence's ranges.
+    uint32_t top = 0;
     const int nr = (sq.num_keys - 1) / kExpandRange + 1;
-    for (int i = threadIdx.x; i < nr; i += kWarps * 32) {
-        const float2 t = a.ranges[(int64_t)h * a.num_ranges + sq.range0 + i];
-        top[0] = max(top[0], (uint32_t)t.x);
-        top[1] = max(top[1], (uint32_t)t.y);
-    }
-    top[0] = __reduce_max_sync(0xffffffffu, top[0]);
-    top[1] = __reduce_max_sync(0xffffffffu, top[1]);
-    if (lane == 0) {
-        part[0][warp] = top[0];
-        part[1][warp] = top[1];
-    }
+    for (int i = threadIdx.x; i < nr; i += kWarps * 32)
+        top = max(top, (uint32_t)a.ranges[(int64_t)h * a.num_ranges + sq.range0 + i].y);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) part[warp] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        top[0] = max(top[0], part[0][w]);
-        top[1] = max(top[1], part[1][w]);
-    }
+    for (int w = 0; w < kWarps; ++w) top = max(top, part[w]);
     if (k0 == 0 && threadIdx.x == 0)  // 2^(b - 133)
-        a.kv_factor[b * a.num_kv_heads + h] = make_float2(q8_scale(top[0]) * 0x1p-6f, q8_scale(top[1]) * 0x1p-6f);
+        a.kv_factor[b * a.num_kv_heads + h] = make_float2(1.f, q8_scale(top) * 0x1p-6f);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int k = i * kWarps + warp;
         if (k0 + k >= sq.num_keys) return;
         const int64_t dst = ((key0 + k) * a.num_kv_heads + h) * kHeadDim;
-        reinterpret_cast<uint4 *>(a.k_out + dst)[lane] = expand8(ck[i], 6 + (int)bk[i] - (int)top[0], bk[i] == 255);
-        reinterpret_cast<uint4 *>(a.v_out + dst)[lane] = expand8(cv[i], 6 + (int)bv[i] - (int)top[1], bv[i] == 255);
+        reinterpret_cast<uint4 *>(a.k_out + dst)[lane] = widen8(ck[i], q8_scale(bk[i]));
+        reinterpret_cast<uint4 *>(a.v_out + dst)[lane] = expand8(cv[i], 6 + (int)bv[i] - (int)top, bv[i] == 255);
     }
 }
 
@@ -420,8 +397,8 @@ cudaError_t launch_gather_q8(const Q8GatherArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_expand_q8(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream) {
-    const int64_t blocks = (int64_t)a.num_ranges * a.num_kv_heads + (a.q_rows + kWarps - 1) / kWarps;
-    cudaError_t e = launch_pdl(range_q8_kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, a);
+    cudaError_t e = launch_pdl(range_q8_kernel, dim3((unsigned)a.num_ranges * a.num_kv_heads), dim3(kWarps * 32),
+                               0, stream, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(expand_q8_kernel,
                       dim3((unsigned)(num_pages_out * (kExpandPage / kExpandKeys)), a.num_kv_heads),

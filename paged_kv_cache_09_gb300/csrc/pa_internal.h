@@ -236,8 +236,9 @@ size_t decode_q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads
 cudaError_t launch_decode_q8(const CUtensorMap *tmaps, const DecodeQ8Args &a, cudaStream_t stream);
 
 // ----------------------------------------------------------------- expansion for the prefill
-// Sequences of the 4-bit or the 8-bit cache as FP16 pages of kExpandPage tokens (a multiple of the
-// prefill kernel's 64-key blocks) beside FP16 queries, for the prefill kernel.
+// Sequences of the 4-bit or the 8-bit cache as pages of kExpandPage tokens (a multiple of the
+// prefill kernel's 64-key blocks), for the prefill kernel: K and V in FP16 beside FP16 queries
+// (4-bit), or K in BF16 and V in FP16 (8-bit).
 constexpr int kExpandPage = 256;
 constexpr int kExpandKeys = 64;    // keys of one head per CTA of the expansion
 constexpr int kExpandRange = 1024; // keys of one head per CTA of the range pass
@@ -258,7 +259,7 @@ struct ExpandArgs {
     int num_kv_heads, block_size, num_seqs, num_ranges;
     ExpandSeq seq[32];
     uint16_t *q_out;         // FP16 rows, each scaled by a power of two, and what undoes it
-    float *q_factor;
+    float *q_factor;         // (4-bit cache; the 8-bit cache's prefill reads q itself)
     float2 *ranges;          // [num_kv_heads, num_ranges]: bounds of |K| and |V|
     float2 *kv_factor;       // [num_seqs, num_kv_heads]
     uint16_t *k_out, *v_out;
@@ -266,7 +267,7 @@ struct ExpandArgs {
     int64_t table_stride;
     unsigned *err;
 };
-// Two launches each: ranges and queries, then keys and values.
+// Two launches each: ranges (and queries), then keys and values.
 cudaError_t launch_expand_q4(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
 cudaError_t launch_expand_q8(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
 
@@ -450,8 +451,8 @@ struct PrefillArgs {
     uint16_t *out;
     unsigned *err;
     // FP16 operands (the tensor maps' Q, K and V hold FP16): the powers of two that undo the
-    // scaling of each query row and head, and of each sequence's K and V by KV head.  NULL:
-    // BF16 operands.
+    // scaling of each query row and head, and of each sequence's K and V by KV head.  Without
+    // q_factor Q and K are BF16 and V is FP16; without kv_factor all are BF16.
     const float *q_factor;   // [rows, num_q_heads]
     const float2 *kv_factor; // [num_seqs, num_kv_heads]
     cudaEvent_t ev_start, ev_stop;  // optional: recorded around the prefill kernel

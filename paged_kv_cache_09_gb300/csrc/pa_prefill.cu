@@ -134,7 +134,7 @@ template <bool kHalf>
 struct DevFactors {};
 template <>
 struct DevFactors<true> {
-    const float *q;    // [rows, Hq]: powers of two that undo the rows' scaling
+    const float *q;    // [rows, Hq]: powers of two that undo the rows' scaling (NULL: Q and K BF16)
     const float2 *kv;  // [sequence of the launch, Hkv]: those of K and of V
     int num_kv_heads;
 };
@@ -262,7 +262,8 @@ __device__ int g_test_skip_unit = -1;
 #endif
 
 // kHalf: Q, K and V are FP16, each row of Q and each KV head of a sequence scaled by a power
-// of two (the 4-bit cache's prefill makes them so).  With 11 significant bits P needs one
+// of two (the 4-bit cache's prefill makes them so), or V alone is, and Q and K are BF16 (the 8-bit
+// cache's, whose K is exact in BF16).  With 11 significant bits P needs one
 // part instead of two, and K and V lose an eighth of what they would in BF16.  P is kept 2^7
 // times as large (at most 2^15): full precision down to 2^-21 of a row's largest weight.
 //
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kHalf) {
                 // QK of half G + 1 goes ahead of PV of half G (across items too), so that the
                 // tensor core has the one while the softmax of G makes the other's P.
-                constexpr uint32_t kIdHalf = umma_idesc(true, kBM, kBN / 2, 0, 0);
+                const uint32_t id_qk = umma_idesc(p.f.q != nullptr, kBM, kBN / 2, 0, 0);
                 // Descriptors of the buffers' starts: the address is their low field, in units
                 // of 16 bytes, so an offset within shared memory is added to it.
                 const uint64_t q_desc = umma_sdesc_sw128(q_addr);
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             umma_ss(sb, dq + ((i / 4) * kQChunk + (i & 3) * 32) / 16,
-                                    dk + ((i / 4) * (kUnit / 2) + (i & 3) * 32) / 16, kIdHalf,
+                                    dk + ((i / 4) * (kUnit / 2) + (i & 3) * 32) / 16, id_qk,
                                     (y | i) != 0);
                         umma_commit(&bars[kRingEmpty + s]);
                     }
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kHalf) {
                 const int rh = it.h + (it.hp > 1 ? row - rpos * it.hp : 0);
                 const float fq =
-                    rpos < it.rows
+                    p.f.q && rpos < it.rows
                         ? p.f.q[(int64_t)(it.q_off + it.r0 + rpos) * p.num_q_heads + rh]
                         : 1.f;
                 // (never 0, as p.sc: a masked score is -inf and stays that)
@@ -1378,8 +1379,8 @@ static cudaError_t launch_prefill_as(const CUtensorMap *tmaps, const PrefillArgs
 
 cudaError_t launch_prefill(const CUtensorMap *tmaps, const PrefillArgs &a, cudaStream_t stream) {
     if (a.num_seqs < 1 || a.num_seqs > kPfMaxSeqs) return cudaErrorInvalidValue;
-    return a.q_factor ? launch_prefill_as<true>(tmaps, a, 7, stream)
-                      : launch_prefill_as<false>(tmaps, a, 1, stream);
+    return a.kv_factor ? launch_prefill_as<true>(tmaps, a, 7, stream)
+                       : launch_prefill_as<false>(tmaps, a, 1, stream);
 }
 
 }  // namespace pa
