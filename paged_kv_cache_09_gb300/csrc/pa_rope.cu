@@ -85,9 +85,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     const bool turns = 8 * l < R, second = 8 * l >= half;  // (second: of a pair of halves)
     const int partner = turns && !kNeighbours ? (second ? l - R / 16 : l + R / 16) : l;
     // A CTA takes every gridDim.x-th token, and loads ahead: a token's first rows of each kind into
-    // registers and its angles (this lane's, into shared memory) while the token before is worked
-    // on, its position a token earlier still.  (A padding token's rows are read for nothing.)
-    __shared__ float4 angles[kWarps][2][kNeighbours ? 2 : 4][32];
+    // registers and its angles (this lane's or, with axes, this warp's, into shared memory) while the
+    // token before is worked on, its position a token earlier still.  (A padding token's rows are read
+    // for nothing.)
+    constexpr int kN = kNeighbours ? 1 : 2;  // fours of frequencies of a lane
+    __shared__ float4 angles[kWarps][2][kAxes ? kD / 4 : 2 * kN * 32];
     uint4 raw[kBatch], raw_k, raw_v;  // each is loaded again as soon as its row is done
     int64_t slot_next;
     const uint16_t *q_at, *k_at, *v_at;  // of the token that is loaded
@@ -96,69 +98,75 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         k_at = a.k + t * a.k_stride;
         if (kCache) v_at = a.v + t * a.v_stride;
     };
-    // A token's positions on all axes.
-    struct Pos {
-        int at[kAxes ? 4 : 1];
-        __device__ __forceinline__ int lowest() const {
-            if constexpr (kAxes) return min(min(at[0], at[1]), min(at[2], at[3]));
-            return at[0];
-        }
-        __device__ __forceinline__ int highest() const {
-            if constexpr (kAxes) return max(max(at[0], at[1]), max(at[2], at[3]));
-            return at[0];
-        }
-        __device__ __forceinline__ int on(uint32_t axis) const {
-            if constexpr (kAxes) return axis & 2 ? (axis & 1 ? at[3] : at[2]) : axis & 1 ? at[1] : at[0];
-            return at[0];
-        }
-    };
-    constexpr int kN = kNeighbours ? 1 : 2;  // fours of frequencies of a lane
-    const int freq = kNeighbours ? 4 * l : second ? 8 * l - half : 8 * l;  // its first
-    uint32_t axes[kN] = {};  // of each four, two bits each
+    // With one position, each lane brings its own angles: 2 kN fours of frequencies, cosines before
+    // sines.  With axes, a warp brings the R / 4 fours of the token, lane i fours i and i + 32: a four
+    // of several axes takes four copies, and lanes that share angles need not make them again.  Pairs
+    // of halves take two fours a lane, 2i and 2i + 1: the even fours lie before the odd ones, so
+    // that lanes read neighbouring ones.  (4096 tokens: with axes 31.6 us when each lane brought its own,
+    // 30.3 so; 1000 tokens of 32 + 8 + 8 heads of 128 with axes in turn 9.8 and 6.9; with one position
+    // 28.3 and 29.4.)
+    constexpr int kFours = (kD / 4 + 31) / 32;
+    auto place = [&](int four) { return kNeighbours ? four : (four & 1) * (R / 8) + (four >> 1); };
+    // Position on axis lane % 4 (on axis 0 where there are fewer): each axis' on lane 0 .. 3.
+    const int own_axis = kAxes && (lane & 3) < a.num_axes ? lane & 3 : 0;
+    const int32_t *positions = a.positions + (kAxes ? own_axis * a.position_stride : 0);
+    uint32_t axes[kFours] = {};  // of each four, two bits each
+    bool mixed = false;          // some lane's four has several axes
     if constexpr (kAxes) {
-        if (turns)
 #pragma unroll
-            for (int e = 0; e < kN; ++e) axes[e] = a.axes[(freq + 4 * e) / 16] >> (2 * ((freq + 4 * e) % 16)) & 0xffu;
+        for (int i = 0; i < kFours; ++i) {
+            const int four = lane + 32 * i;
+            if (four < R / 4) {
+                const int freq = 4 * four < half ? 4 * four : 4 * four - half;
+                axes[i] = a.axes[freq / 16] >> (2 * (freq % 16)) & 0xffu;
+                mixed |= axes[i] != (axes[i] & 3) * 0x55u;
+            }
+        }
+        mixed = __any_sync(0xffffffffu, mixed);
     }
-    auto copy = [&](float *dst, const float *src, auto bytes) {
-        if constexpr (decltype(bytes)::value == 16)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    // Whether a token is padding, and whether it lies in the table.
+    auto placed = [&](int pos) { return kAxes ? !__any_sync(0xffffffffu, pos < 0) : pos >= 0; };
+    auto inside = [&](int pos) {
+        return kAxes ? __all_sync(0xffffffffu, pos < a.max_position) : pos < a.max_position;
     };
-    using Four = std::integral_constant<int, 16>;
-    using One = std::integral_constant<int, 4>;
-    auto angles_of = [&](int64_t t, const Pos &pos, int buf) {
+    auto copy16 = [&](float4 *dst, const float *src) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    };
+    auto angles_of = [&](int64_t t, int pos, int buf) {
         slot_next = kCache ? a.slot_mapping[t] : -1;
-        if (turns && pos.lowest() >= 0 && pos.highest() < a.max_position) {
+        float4 *to = angles[threadIdx.x >> 5][buf];
+        if constexpr (!kAxes) {
+            if (turns && placed(pos) && inside(pos)) {
+                const float *row = a.cos_sin + (int64_t)pos * R +
+                                   (kNeighbours ? 4 * l : second ? 8 * l - half : 8 * l);
 #pragma unroll
-            for (int e = 0; e < 2 * kN; ++e) {  // cosines, then sines
-                float *dst = &angles[threadIdx.x >> 5][buf][e][lane].x;
-                const float *column = a.cos_sin + freq + (e / kN) * half + (e % kN) * 4;
-                const uint32_t ax = axes[e % kN];
-                if (!kAxes || ax == (ax & 3) * 0x55u) {
-                    copy(dst, column + (int64_t)pos.on(ax & 3) * R, Four());
+                for (int e = 0; e < 2 * kN; ++e) copy16(to + e * 32 + lane, row + (e / kN) * half + (e % kN) * 4);
+            }
+        } else if (placed(pos) && inside(pos)) {
+#pragma unroll
+            for (int i = 0; i < kFours; ++i) {
+                const int four = lane + 32 * i;
+                const float *column = a.cos_sin + 4 * four;
+                if (!mixed) {
+                    const int row = __shfl_sync(0xffffffffu, pos, axes[i] & 3);
+                    if (four < R / 4) copy16(to + place(four), column + (int64_t)row * R);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        copy(dst + j, column + (int64_t)pos.on(ax >> (2 * j) & 3) * R + j, One());
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = __shfl_sync(0xffffffffu, pos, axes[i] >> (2 * j) & 3);
+                        if (four < R / 4)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + place(four)) + 4 * j),
+                                         "l"(column + (int64_t)row * R + j)
+                                         : "memory");
+                    }
                 }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto position = [&](int64_t t) {
-        Pos p;
-        p.at[0] = t < a.num_tokens ? a.positions[t] : -1;
-        if constexpr (kAxes)
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-                p.at[i] = t < a.num_tokens && i < a.num_axes ? a.positions[i * a.position_stride + t] : p.at[0];
-        return p;
-    };
+    auto position = [&](int64_t t) { return t < a.num_tokens ? positions[t] : -1; };
     const int64_t stride = gridDim.x;
-    Pos pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride);
-    int buf = 0;
+    int pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride), buf = 0;
     at(blockIdx.x);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) raw[b] = row_of(q_at, unit + b * step, hq);
@@ -166,10 +174,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     if (kCache) raw_v = row_of(v_at, unit_v, hkv);
     angles_of(blockIdx.x, pos, 0);
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += stride, buf ^= 1) {
-    const Pos pos_now = pos;
+    const int pos_now = pos;
     const int64_t slot = slot_next;
     const bool more = t + stride < a.num_tokens;
     pos = pos_next;
+    if constexpr (kAxes) __syncwarp();  // the angles of the token before are read
     if (more) {
         at(t + stride);
         angles_of(t + stride, pos, buf ^ 1);
@@ -178,9 +187,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     } else {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
+    if constexpr (kAxes) __syncwarp();  // every lane's angles are there
     // (a token that is not live: its rows stay as they are)
-    const bool placed = pos_now.lowest() >= 0, live = placed && pos_now.highest() < a.max_position;
-    if (placed && !live && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPosition);
+    const bool some = placed(pos_now), in = inside(pos_now), live = some && in;
+    if (some && !in && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrPosition);
     int64_t run = -1;  // the slot's place in the caches (of head 0)
     int o = 0;
     if (kCache && live && slot >= 0) {
@@ -211,17 +221,19 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
             s[j] = 0.f;
         }
         if (turns) {
-            const float4 (*mine)[32] = angles[threadIdx.x >> 5][buf];
+            const float4 *mine = angles[threadIdx.x >> 5][buf];
             if (kNeighbours) {
-                const float4 cv = mine[0][lane], sv = mine[1][lane];
+                const float4 cv = kAxes ? mine[l] : mine[lane], sv = kAxes ? mine[R / 8 + l] : mine[32 + lane];
                 c[0] = c[1] = cv.x; c[2] = c[3] = cv.y; c[4] = c[5] = cv.z; c[6] = c[7] = cv.w;
                 s[1] = sv.x; s[3] = sv.y; s[5] = sv.z; s[7] = sv.w;
                 s[0] = -sv.x; s[2] = -sv.y; s[4] = -sv.z; s[6] = -sv.w;
             } else {
                 const float sign = second ? 1.f : -1.f;
+                const float4 *first = kAxes ? mine + (second ? l - R / 16 : l) : mine + lane;
+                const int next = kAxes ? R / 8 : 32, sines = kAxes ? R / 16 : 64;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float4 cv = mine[e][lane], sv = mine[2 + e][lane];
+                    const float4 cv = first[e * next], sv = first[sines + e * next];
                     c[4 * e] = cv.x; c[4 * e + 1] = cv.y; c[4 * e + 2] = cv.z; c[4 * e + 3] = cv.w;
                     s[4 * e] = sign * sv.x; s[4 * e + 1] = sign * sv.y;
                     s[4 * e + 2] = sign * sv.z; s[4 * e + 3] = sign * sv.w;
