@@ -733,7 +733,7 @@ cudaError_t launch_decode_q4(const DecodeQ4Args &a, cudaStream_t stream) {
     e = launch_pdl(decode_q4_stream_kernel, dim3(grid), dim3(kThreads), kSmem, stream, p);
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
-    return launch_merge(p, a.num_sms, stream);
+    return launch_merge<4>(p, a.num_sms, stream);
 }
 
 }  // namespace pa

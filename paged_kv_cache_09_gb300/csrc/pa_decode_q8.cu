@@ -87,53 +87,83 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share of all tiles, and the segment that it begins with
+    // ---- this CTA's share of all tiles, and the segment that it begins with: tiles [t0, t1) of KV
+    // head g of sequence seq
     const int tpp = p.tiles_per_page;
     Start st;
-    uint32_t &at = st.at, &end = st.end;
-    int &lead = st.lead, &v0 = st.v0, &seq = st.seq, &g = st.g, &seq_len = st.seq_len, &tiles = st.tiles;
+    int t0, t1, n;    // n: this warp's tiles of the segment
+    uint32_t it = 0;  // the warp's tiles so far: slots and phases go on from segment to segment
+    auto begin_segment = [&]() {
+        t0 = max(0, st.v0 - st.lead);
+        t1 = (int)min((uint32_t)st.tiles, st.v0 + (st.end - st.at) - st.lead);
+        n = !*abort && t0 + warp < t1 ? (t1 - t0 - warp + kW - 1) / kW : 0;
+    };
+    // The next segment of the share, KV head after KV head, sequence after sequence.
+    auto next_pair = [&](int &seq, int &g, int &seq_len, int &tiles) {
+        if (++g == p.num_kv_heads) {
+            g = 0;
+            do tiles = seq_tiles(p, ++seq, &seq_len, false);
+            while (tiles == 0 && seq < p.num_seqs);
+        }
+    };
+
+    // ---- the warp's loads, which run ahead of its work into the segments that follow
     const int r = lane >> 2, c = lane & 3;
     const uint32_t q_frag = smem_u32(smem + kOffQ) + lane * 16;
-    const int32_t *bt;
-    int t0, t1, n;                          // the segment's tiles [t0, t1), this warp's count of them
-    int j_in, lp_in, tip_in, page_in;       // the warp's next tile to load
-    uint32_t it = 0;  // the warp's steps: slots and phases go on from segment to segment
-
-    auto begin_segment = [&]() {
-        t0 = max(0, v0 - lead);
-        t1 = (int)min((uint32_t)tiles, v0 + (end - at) - lead);
-        n = !*abort && t0 + warp < t1 ? (t1 - t0 - warp + kW - 1) / kW : 0;
-        bt = p.block_table + (int64_t)seq * p.bt_stride;
-        j_in = t0 + warp;
-        lp_in = (int)p.by_tpp(j_in);
-        tip_in = j_in - lp_in * tpp;
-        page_in = j_in < t1 ? bt[lp_in] : 0;
+    struct {
+        int seq, g, seq_len, tiles, t1;  // the segment
+        uint32_t at;                     // the place of the row that it ends at
+        int j, lp, tip, page;            // the warp's next tile
+        uint32_t count;                  // loads issued
+    } in;
+    in.count = 0;
+    auto load_pair = [&](int first) {
+        in.j = first + warp;
+        in.lp = (int)p.by_tpp(in.j);
+        in.tip = in.j - in.lp * tpp;
+        in.page = in.j < in.t1 ? p.block_table[(int64_t)in.seq * p.bt_stride + in.lp] : 0;
     };
-    // Loads the warp's tile i, its next, into slot i % kDepth; its scale bytes, and its valid rows.
+    auto load_start = [&]() {
+        in.seq = st.seq;
+        in.g = st.g;
+        in.seq_len = st.seq_len;
+        in.tiles = st.tiles;
+        in.t1 = t1;
+        in.at = st.at + st.lead + t1 - st.v0;
+        load_pair(t0);
+    };
+    // A tile's scale bytes, and its valid rows.
     struct Tile {
         uint32_t k_scale, v_scale;
         int rows;
     };
-    auto load = [&](uint32_t i) {
-        const uint32_t s = i % kDepth;
-        const int page = page_in, off = tip_in * kTile;
-        Tile t;
-        t.rows = min(kTile, min(p.block_size - off, seq_len - lp_in * p.block_size - off));
+    // Loads the warp's next tile, if there is one, into slot in.count % kDepth.
+    auto load = [&](Tile &t) {
+        while (in.j >= in.t1) {
+            if (st.end <= in.at + st.lead) return;
+            next_pair(in.seq, in.g, in.seq_len, in.tiles);
+            in.t1 = (int)min((uint32_t)in.tiles, st.end - in.at - st.lead);
+            in.at += st.lead + in.t1;
+            load_pair(0);
+        }
+        const uint32_t i = in.count++, s = i % kDepth;
+        const int page = in.page, off = in.tip * kTile, g = in.g;
+        t.rows = min(kTile, min(p.block_size - off, in.seq_len - in.lp * p.block_size - off));
         t.k_scale = t.v_scale = 127;
         // A page outside the pool is reported, and its box, which lies outside the map, reads as zeros.
         if (page >= 0 && page < p.num_pages) {
-            const int64_t o = page * p.scale_stride + (int64_t)tip_in * p.num_kv_heads + g;
+            const int64_t o = page * p.scale_stride + (int64_t)in.tip * p.num_kv_heads + g;
             t.k_scale = __ldg(p.k_scales + o);
             t.v_scale = __ldg(p.v_scales + o);
         } else if (lane == 0) {
             atomicOr(p.err, kErrPage);
         }
         // The next tile's table entry, read ahead of its use.
-        j_in += kW;
-        for (tip_in += kW; tip_in >= tpp; tip_in -= tpp) ++lp_in;
-        if (j_in < t1) page_in = bt[lp_in];
+        in.j += kW;
+        for (in.tip += kW; in.tip >= tpp; in.tip -= tpp) ++in.lp;
+        if (in.j < in.t1) in.page = p.block_table[(int64_t)in.seq * p.bt_stride + in.lp];
 #ifdef PA_TEST_HOOKS
-        if ((int)i == *reinterpret_cast<volatile int *>(&g_test_skip_tile)) return t;
+        if ((int)i == *reinterpret_cast<volatile int *>(&g_test_skip_tile)) return;
 #endif
         if (lane == 0) {
             uint8_t *dst = ring + s * kSlotBytes;
@@ -142,15 +172,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             tma_load_5d_hint(dst, &k_map, &full[s], 0, off, 0, g, page, policy);
             tma_load_5d_hint(dst + kTileCodes, &v_map, &full[s], 0, off, 0, g, page, policy);
         }
-        return t;
     };
-    int loaded = 0;
     Tile next0{}, next1{};  // of the next tiles
-    auto first_loads = [&]() {
-        loaded = min(n, kDepth - 1);
-        if (n > 0) next0 = load(it);
-        if (n > 1) next1 = load(it + 1);
-    };
     static_assert(kDepth == 3, "two tiles ahead");
     // q as FP16 B fragments in shared memory: lane (head r, column c) holds dims 128a + 32c + 16b +
     // {0..15} (a, b = 0, 1) as two 16-byte words, word w of which are dims 4w and 4w + 1 (or + 2, + 3).
@@ -158,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint4 raw[8];
     auto load_q = [&]() {
         const uint4 *qrow = reinterpret_cast<const uint4 *>(
-            p.q + ((int64_t)seq * p.num_q_heads + g * p.group + (r < p.group ? r : 0)) * kHeadDim);
+            p.q + ((int64_t)st.seq * p.num_q_heads + st.g * p.group + (r < p.group ? r : 0)) * kHeadDim);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             raw[k] = r < p.group ? qrow[(k >> 2) * 16 + 4 * c + (k & 3)] : make_uint4(0, 0, 0, 0);
@@ -201,11 +224,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool guess = p.num_seqs == 1;
     Found found;
     for (;;) {
-        found = guess ? find_start<kMinShare, kPairCost>(p, lane, false, lane == 0 ? tiles_of(p, p.max_seq_len) : 0,
-                                                         p.max_seq_len, st)
-                      : find_start<kMinShare, kPairCost>(p, lane, blockIdx.x == 0 && warp == 0, actual, len, st);
+        found = guess ? find_start<kMinShare, kPairCost, true>(p, lane, false, lane == 0 ? tiles_of(p, p.max_seq_len) : 0,
+                                                               p.max_seq_len, st)
+                      : find_start<kMinShare, kPairCost, true>(p, lane, blockIdx.x == 0 && warp == 0, actual, len, st);
         if (found == Found::kShare) {
             begin_segment();
+            load_start();
             load_q();
         }
         if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
@@ -220,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         return;
     }
-    first_loads();
+    load(next0);
+    load(next1);
     make_q();
     __syncthreads();  // q is ready
     for (;;) {
@@ -238,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < n; ++i) {
             const Tile now = next0;
             next0 = next1;
-            if (loaded < n) next1 = load(it + loaded++);  // into the slot that the previous tile has left
+            load(next1);  // into the slot that the previous tile has left
             const uint32_t s = (it + i) % kDepth;
             if (!__all_sync(0xffffffffu, mbar_wait_abort(&full[s], ((it + i) / kDepth) & 1, p.err, abort))) break;
             const uint32_t base = smem_u32(ring) + s * kSlotBytes;
@@ -345,9 +370,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();  // the slot is free
         }
-        // Every load lands before its slot is loaded again or left (when a wait gave up).
-        for (uint32_t i = it + max(0, loaded - kDepth); i < it + loaded; ++i)
-            mbar_wait(&full[i % kDepth], (i / kDepth) & 1, p.err);
         it += n;
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
@@ -355,26 +377,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
         }
 
-        // ---- the next segment's first loads and its q, before this one's merge
-        const int64_t pair = (int64_t)seq * p.num_kv_heads + g, part = blockIdx.x + pair;
-        const bool whole = t0 == 0 && t1 == tiles;
-        if (threadIdx.x == 0 && t0 == 0)
-            p.info[pair] =
-                make_int2((int)part, whole ? 0 : (int)(st.shares.owner(at - v0 + lead + tiles - 1) - blockIdx.x) + 1);
-        uint16_t *out_rows = p.out + ((int64_t)seq * p.num_q_heads + g * p.group) * kHeadDim;
-        at += lead + t1 - v0;
-        const bool more = end > at + lead;  // (a share that ends before the next pair's first tile is done)
-        const uint32_t spare = (it + kDepth - 1) % kDepth;  // the slot that the next segment loads last
+        // ---- the next segment's q, before this one's merge
+        const int64_t pair = (int64_t)st.seq * p.num_kv_heads + st.g, part = blockIdx.x + pair;
+        const bool whole = t0 == 0 && t1 == st.tiles;
+        if (threadIdx.x == 0 && t0 == 0) {
+            int parts = st.ctas_a_pair;
+            if (parts == 0) parts = (int)(st.shares.owner(st.at - st.v0 + st.lead + st.tiles - 1) - blockIdx.x) + 1;
+            p.info[pair] = make_int2((int)part, whole ? 0 : parts);
+        }
+        uint16_t *out_rows = p.out + ((int64_t)st.seq * p.num_q_heads + st.g * p.group) * kHeadDim;
+        st.at += st.lead + t1 - st.v0;
+        const bool more = st.end > st.at + st.lead;  // (a share that ends before the next pair's first tile is done)
+        const uint32_t spare = (it + kDepth - 1) % kDepth;  // the slot of the last tile: the others hold the next ones
         if (more) {
-            v0 = 0;
-            if (++g == p.num_kv_heads) {
-                g = 0;
-                do tiles = seq_tiles(p, ++seq, &seq_len, false);
-                while (tiles == 0 && seq < p.num_seqs);
-            }
+            st.v0 = 0;
+            next_pair(st.seq, st.g, st.seq_len, st.tiles);
             begin_segment();
             load_q();
-            first_loads();
         }
 
         // ------------------------------------------------------------ merge of the warps
@@ -441,9 +460,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
 
-        if (!more) return;
+        if (!more) break;
         __syncthreads();  // q is ready, and the merge's rows are free
     }
+    // Every load lands before the CTA's memory is left (when a wait gave up).
+    for (uint32_t i = in.count - min(in.count, (uint32_t)kDepth); i < in.count; ++i)
+        mbar_wait(&full[i % kDepth], (i / kDepth) & 1, p.err);
 }
 
 }  // namespace
@@ -468,11 +490,11 @@ cudaError_t launch_decode_q8(const CUtensorMap *tmaps, const DecodeQ8Args &a, cu
     p.v_scales = a.v_scales;
     p.scale_stride = a.scale_stride;
     if (a.ev_start && (e = record_event(a.ev_start, stream)) != cudaSuccess) return e;
-    e = launch_pdl(decode_q8_stream_kernel, dim3(split_grid<kMinShare>(p, a)), dim3(kThreads), kSmem, stream,
+    e = launch_pdl(decode_q8_stream_kernel, dim3(split_grid<kMinShare, true>(p, a)), dim3(kThreads), kSmem, stream,
                    tmaps[0], tmaps[1], p);
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
-    return launch_merge(p, a.num_sms, stream);
+    return launch_merge<10>(p, a.num_sms, stream);
 }
 
 }  // namespace pa

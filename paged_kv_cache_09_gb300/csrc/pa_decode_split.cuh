@@ -97,13 +97,15 @@ struct Start {
     Shares shares;
     uint32_t at, end;
     int lead, v0, seq, g, seq_len, tiles;
+    int ctas_a_pair;  // kAlone: CTAs of each pair, cut by itself (0: the pairs are cut in a row)
 };
 // What was found; refused: more tiles than a share can be found of.
 enum class Found { kNone, kShare, kRefused };
 
 // Finds this CTA's share, with the tiles and lengths of the first 32 sequences given (every warp
-// finds the same).
-template <int kMinShare, int kPairCost>
+// finds the same).  kAlone: with one sequence, each of its pairs is cut by itself, so that no CTA
+// works on two (their beginnings would follow one another).
+template <int kMinShare, int kPairCost, bool kAlone = false>
 __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool report, int first_tiles,
                                             int first_len, Start &st) {
     uint64_t all = 0, used = 0;
@@ -119,6 +121,27 @@ __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool
     if (all == 0) return Found::kNone;  // padding entries only
     if (all > kMaxTiles) {
         return Found::kRefused;
+    }
+    if constexpr (kAlone) {
+        st.ctas_a_pair = 0;
+        if (p.num_seqs == 1 && gridDim.x >= (unsigned)p.num_kv_heads) {
+            const uint32_t tiles = __shfl_sync(0xffffffffu, first_tiles, 0);
+            const uint32_t n = min(gridDim.x / p.num_kv_heads, (tiles + kMinShare - 1) / kMinShare);
+            const uint32_t pair = blockIdx.x / n, i = blockIdx.x - pair * n;
+            if (pair >= (uint32_t)p.num_kv_heads) return Found::kNone;
+            st.ctas_a_pair = (int)n;
+            st.shares.q = tiles / n;
+            st.shares.r = tiles - st.shares.q * n;
+            st.lead = 0;
+            st.seq = 0;
+            st.g = (int)pair;
+            st.tiles = (int)tiles;
+            st.seq_len = __shfl_sync(0xffffffffu, first_len, 0);
+            st.v0 = (int)st.shares.begin(i);
+            st.at = pair * tiles + st.v0;
+            st.end = pair * tiles + st.shares.begin(i + 1);
+            return Found::kShare;
+        }
     }
     const uint32_t ctas = min(gridDim.x, ((uint32_t)all + kMinShare - 1) / kMinShare);
     st.lead = pair_lead<kMinShare, kPairCost>((uint32_t)all, used * p.num_kv_heads, ctas);
@@ -181,7 +204,7 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 }
 
 // Merges a row's parts: sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j, M = max m_j; an empty
-// part has m = -inf.  All loads of a round are in flight together.
+// part has m = -inf.  All loads of a round (kRound parts a warp) are in flight together.
 //   kSplit > 1: that many warps for each 64 dims of a row take its parts in turn, for the
 //               latency of many parts
 //   kSplit = 1: two warps a row (128 dims each), 4 rows a CTA
@@ -193,10 +216,10 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 //     1200 24.2 22.9 25.0   1536 27.1 23.6 26.0
 // so between 2 and 8 rows an SM 4 loses up to 9% to 1 where lengths are alike, and gains as much
 // where one is long.
-template <int kSplit>
+template <int kSplit, int kRound>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const __grid_constant__ SplitParams p) {
     constexpr bool kFew = kSplit > 1;
-    constexpr int kWarps = kSplit, kRound = 4;
+    constexpr int kWarps = kSplit;
     constexpr int kBlocks = 8 / kSplit;  // of 64 dims, in a CTA
     constexpr int kVec = kFew ? 1 : 2;  // float2 a lane
     const int lane = threadIdx.x & 31, all = threadIdx.x >> 5;
@@ -330,22 +353,24 @@ void fill_split(SplitParams &p, const Args &a) {
 }
 
 // CTAs of the streaming kernel: no more than the longest allowed lengths would use.
-template <int kMinShare, typename Args>
+template <int kMinShare, bool kAlone = false, typename Args>
 int split_grid(const SplitParams &p, const Args &a) {
-    const int64_t tiles = (int64_t)a.num_seqs * a.num_kv_heads *
-                          ((int64_t)(a.max_seq_len / a.block_size) * p.tiles_per_page +
-                           (a.max_seq_len % a.block_size + kTile - 1) / kTile);
-    const int64_t most = 2 * a.num_sms, grid = (tiles + kMinShare - 1) / kMinShare;
+    const int64_t tiles = (int64_t)(a.max_seq_len / a.block_size) * p.tiles_per_page +
+                          (a.max_seq_len % a.block_size + kTile - 1) / kTile;
+    const int64_t pairs = (int64_t)a.num_seqs * a.num_kv_heads, most = 2 * a.num_sms;
+    const int64_t grid = kAlone && a.num_seqs == 1 ? pairs * ((tiles + kMinShare - 1) / kMinShare)
+                                                   : (pairs * tiles + kMinShare - 1) / kMinShare;
     return (int)(grid < most ? grid : most);
 }
 
-inline cudaError_t launch_merge(const SplitParams &p, int num_sms, cudaStream_t stream) {
+template <int kFewRound>
+cudaError_t launch_merge(const SplitParams &p, int num_sms, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.num_seqs * p.num_q_heads;
     if (rows <= num_sms)
-        return launch_pdl(decode_merge_kernel<8>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
+        return launch_pdl(decode_merge_kernel<8, kFewRound>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
     if (rows <= 8 * num_sms)
-        return launch_pdl(decode_merge_kernel<4>, dim3((unsigned)(rows * 2)), dim3(256), 0, stream, p);
-    return launch_pdl(decode_merge_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+        return launch_pdl(decode_merge_kernel<4, 4>, dim3((unsigned)(rows * 2)), dim3(256), 0, stream, p);
+    return launch_pdl(decode_merge_kernel<1, 4>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
 }
 
 }  // namespace
