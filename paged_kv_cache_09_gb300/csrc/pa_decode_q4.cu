@@ -302,19 +302,23 @@ __global__ void __launch_bounds__(kThreads, 2) decode_q4_stream_kernel(const __g
 
     // With one sequence, its length is nearly always the longest allowed: the table entry and q are
     // then read beside the length instead of after it.
-    int len;
-    const int actual = seq_tiles(p, lane, &len, blockIdx.x == 0 && warp == 0);
+    Lengths<1> lens, most;
+    lens.tiles[0] = seq_tiles(p, lane, &lens.len[0], blockIdx.x == 0 && warp == 0);
     bool guess = p.num_seqs == 1;
     Found found;
     for (;;) {
-        found = guess ? find_start<kMinShare, kPairCost>(p, lane, false, lane == 0 ? tiles_of(p, p.max_seq_len) : 0,
-                                                         p.max_seq_len, st)
-                      : find_start<kMinShare, kPairCost>(p, lane, blockIdx.x == 0 && warp == 0, actual, len, st);
+        if (guess) {
+            most.tiles[0] = lane == 0 ? tiles_of(p, p.max_seq_len) : 0;
+            most.len[0] = p.max_seq_len;
+            found = find_start<kMinShare, kPairCost>(p, lane, false, most, st);
+        } else {
+            found = find_start<kMinShare, kPairCost>(p, lane, blockIdx.x == 0 && warp == 0, lens, st);
+        }
         if (found == Found::kShare) {
             begin_segment();
             load_q();
         }
-        if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
+        if (!guess || __shfl_sync(0xffffffffu, lens.len[0], 0) == p.max_seq_len) break;
         guess = false;
     }
     if (found != Found::kShare) {

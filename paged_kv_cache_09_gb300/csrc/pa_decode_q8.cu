@@ -37,7 +37,9 @@ static_assert(kDecMaxGroup * kHeadDim * 4 == kSlotBytes, "a slot holds a warp's 
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(kTile == kQ8Tokens, "a tile has one scale");
 constexpr int kMinShare = kW;                         // tiles of the smallest share
-constexpr int kPairCost = 8;                          // of beginning a pair, in tiles
+constexpr int kPairCost = 12;                         // of beginning a pair, in tiles
+constexpr int kBatches = 4;                           // of 32 sequences, whose lengths a warp keeps
+constexpr int kEarlyTiles = 1;                        // of a warp, brought into L2 before the wait
 constexpr float kLag = 8.f;  // log2 units: a score may pass the reference by it
 constexpr float kTop = 6.f;  // log2 of the weight at the reference M'
 
@@ -84,8 +86,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_mbar_init();
     }
     __syncthreads();
-    pdl_wait();
-    pdl_trigger();
 
     // ---- this CTA's share of all tiles, and the segment that it begins with: tiles [t0, t1) of KV
     // head g of sequence seq
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto next_pair = [&](int &seq, int &g, int &seq_len, int &tiles) {
         if (++g == p.num_kv_heads) {
             g = 0;
-            do tiles = seq_tiles(p, ++seq, &seq_len, false);
+            do tiles = seq_tiles<true>(p, ++seq, &seq_len, false);
             while (tiles == 0 && seq < p.num_seqs);
         }
     };
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         in.j = first + warp;
         in.lp = (int)p.by_tpp(in.j);
         in.tip = in.j - in.lp * tpp;
-        in.page = in.j < in.t1 ? p.block_table[(int64_t)in.seq * p.bt_stride + in.lp] : 0;
+        in.page = in.j < in.t1 ? __ldcg(p.block_table + (int64_t)in.seq * p.bt_stride + in.lp) : 0;
     };
     auto load_start = [&]() {
         in.seq = st.seq;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // The next tile's table entry, read ahead of its use.
         in.j += kW;
         for (in.tip += kW; in.tip >= tpp; in.tip -= tpp) ++in.lp;
-        if (in.j < in.t1) in.page = p.block_table[(int64_t)in.seq * p.bt_stride + in.lp];
+        if (in.j < in.t1) in.page = __ldcg(p.block_table + (int64_t)in.seq * p.bt_stride + in.lp);
 #ifdef PA_TEST_HOOKS
         if ((int)i == *reinterpret_cast<volatile int *>(&g_test_skip_tile)) return;
 #endif
@@ -217,26 +217,63 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (warp == 0) own[8 * 32] = make_uint4(__float_as_uint(sc0), __float_as_uint(sc1), 0, 0);
     };
 
-    // With one sequence, its length is nearly always the longest allowed: the table entry and q are
-    // then read beside the length instead of after it.
-    int len;
-    const int actual = seq_tiles(p, lane, &len, blockIdx.x == 0 && warp == 0);
-    bool guess = p.num_seqs == 1;
-    Found found;
-    for (;;) {
-        found = guess ? find_start<kMinShare, kPairCost, true>(p, lane, false, lane == 0 ? tiles_of(p, p.max_seq_len) : 0,
-                                                               p.max_seq_len, st)
-                      : find_start<kMinShare, kPairCost, true>(p, lane, blockIdx.x == 0 && warp == 0, actual, len, st);
+    // The share is found before the wait for earlier work on the stream, from lengths that this work may
+    // still write, and holds if they are the same after it; if not, and with more sequences than a warp
+    // keeps, it is found again.  Meanwhile the first tiles come into L2 (their table entries only
+    // steer that).  What is read before the wait bypasses L1.
+    auto find = [&](const Lengths<kBatches> &lens, bool report) {
+        return find_start<kMinShare, kPairCost, true, true, kBatches>(p, lane, report, lens, st);
+    };
+    auto lengths = [&](bool report) {
+        Lengths<kBatches> l;
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b) l.tiles[b] = seq_tiles<true>(p, 32 * b + lane, &l.len[b], report);
+        return l;
+    };
+    const bool early = p.num_seqs <= 32 * kBatches;
+    Lengths<kBatches> lens;
+    Found found = Found::kNone;
+    if (early) {
+        lens = lengths(false);
+        found = find(lens, false);
+    }
+    if (found == Found::kShare) {
+        begin_segment();
+        load_start();
+        if (lane == 0) {
+            const uint64_t policy = l2_evict_first_policy();
+            int lp = in.lp, tip = in.tip, page = in.page;
+            for (int j = in.j; j < min(in.t1, in.j + kEarlyTiles * kW); j += kW) {
+                if (page >= 0 && page < p.num_pages) {
+                    tma_prefetch_l2_5d_hint(&k_map, 0, tip * kTile, 0, in.g, page, policy);
+                    tma_prefetch_l2_5d_hint(&v_map, 0, tip * kTile, 0, in.g, page, policy);
+                }
+                const int was = lp;
+                for (tip += kW; tip >= tpp; tip -= tpp) ++lp;
+                if (lp != was && j + kW < in.t1) page = __ldcg(p.block_table + (int64_t)in.seq * p.bt_stride + lp);
+            }
+        }
+    }
+    pdl_wait();
+    pdl_trigger();
+    const Lengths<kBatches> now = lengths(blockIdx.x == 0 && warp == 0);
+    if (found == Found::kShare) {
+        load_q();
+        load_pair(t0);  // (the table entry)
+    }
+    bool changed = !early;
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) changed |= early && now.len[b] != lens.len[b];
+    if (__any_sync(0xffffffffu, changed)) {
+        found = find(now, blockIdx.x == 0 && warp == 0);
         if (found == Found::kShare) {
             begin_segment();
             load_start();
             load_q();
         }
-        if (!guess || __shfl_sync(0xffffffffu, len, 0) == p.max_seq_len) break;
-        guess = false;
     }
     if (found != Found::kShare) {
-        if (found == Found::kRefused) {  // (not by a guess) tells the merge so: the pairs have no parts
+        if (found == Found::kRefused) {  // tells the merge so: the pairs have no parts
             if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrSeqLen);
             const int64_t pairs = (int64_t)p.num_seqs * p.num_kv_heads;
             for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < pairs; x += gridDim.x * kThreads)

@@ -58,9 +58,11 @@ __device__ __forceinline__ int tiles_of(const SplitParams &p, int len) {
     return full * p.tiles_per_page + ((len - full * p.block_size + kTile - 1) >> 4);
 }
 
-// Tiles of sequence s (none past the last); lengths out of range are cut to it.
+// Tiles of sequence s (none past the last); lengths out of range are cut to it.  kEarly: read from L2
+// alone, so that a read before earlier work has written the lengths leaves no stale copy in L1.
+template <bool kEarly = false>
 __device__ __forceinline__ int seq_tiles(const SplitParams &p, int s, int *len, bool report) {
-    int L = s < p.num_seqs ? p.seq_lens[s] : 0;
+    int L = s >= p.num_seqs ? 0 : kEarly ? __ldcg(p.seq_lens + s) : p.seq_lens[s];
     if (L < 0 || L > p.max_seq_len) {
         if (report) atomicOr(p.err, kErrSeqLen);
         L = L < 0 ? 0 : p.max_seq_len;
@@ -102,20 +104,30 @@ struct Start {
 // What was found; refused: more tiles than a share can be found of.
 enum class Found { kNone, kShare, kRefused };
 
-// Finds this CTA's share, with the tiles and lengths of the first 32 sequences given (every warp
-// finds the same).  kAlone: with one sequence, each of its pairs is cut by itself, so that no CTA
-// works on two (their beginnings would follow one another).
-template <int kMinShare, int kPairCost, bool kAlone = false>
-__device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool report, int first_tiles,
-                                            int first_len, Start &st) {
+// Tiles and lengths of kBatches times 32 sequences, a lane's being 32 b + lane.
+template <int kBatches>
+struct Lengths {
+    int tiles[kBatches], len[kBatches];
+};
+
+// Finds this CTA's share, with the first sequences' lengths given (every warp finds the same).  kAlone: with one sequence, each of its pairs is cut by itself, so that no CTA
+// works on two (their beginnings would follow one another).  kEarly: as for seq_tiles.
+template <int kMinShare, int kPairCost, bool kAlone = false, bool kEarly = false, int kBatches = 1>
+__device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool report,
+                                            const Lengths<kBatches> &first, Start &st) {
     uint64_t all = 0, used = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        int len;
-        uint64_t t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, report);
+    auto count = [&](uint64_t t) {
         used += __popc(__ballot_sync(0xffffffffu, t > 0));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
         all += t;
+    };
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b)
+        if (b == 0 || 32 * b < p.num_seqs) count(first.tiles[b]);
+    for (int s0 = 32 * kBatches; s0 < p.num_seqs; s0 += 32) {
+        int len;
+        count(seq_tiles<kEarly>(p, s0 + lane, &len, report));
     }
     all *= p.num_kv_heads;
     if (all == 0) return Found::kNone;  // padding entries only
@@ -125,7 +137,7 @@ __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool
     if constexpr (kAlone) {
         st.ctas_a_pair = 0;
         if (p.num_seqs == 1 && gridDim.x >= (unsigned)p.num_kv_heads) {
-            const uint32_t tiles = __shfl_sync(0xffffffffu, first_tiles, 0);
+            const uint32_t tiles = __shfl_sync(0xffffffffu, first.tiles[0], 0);
             const uint32_t n = min(gridDim.x / p.num_kv_heads, (tiles + kMinShare - 1) / kMinShare);
             const uint32_t pair = blockIdx.x / n, i = blockIdx.x - pair * n;
             if (pair >= (uint32_t)p.num_kv_heads) return Found::kNone;
@@ -136,7 +148,7 @@ __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool
             st.seq = 0;
             st.g = (int)pair;
             st.tiles = (int)tiles;
-            st.seq_len = __shfl_sync(0xffffffffu, first_len, 0);
+            st.seq_len = __shfl_sync(0xffffffffu, first.len[0], 0);
             st.v0 = (int)st.shares.begin(i);
             st.at = pair * tiles + st.v0;
             st.end = pair * tiles + st.shares.begin(i + 1);
@@ -152,9 +164,7 @@ __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool
     st.at = st.shares.begin(blockIdx.x);
     st.end = st.shares.begin(blockIdx.x + 1);
     uint32_t before = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        int len = first_len;
-        const int t = s0 == 0 ? first_tiles : seq_tiles(p, s0 + lane, &len, false);
+    auto here = [&](int s0, int t, int len) {
         const uint32_t span = t > 0 ? t + st.lead : 0;  // a pair's places
         uint32_t sum = span;
 #pragma unroll
@@ -171,9 +181,19 @@ __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool
             const uint32_t rem = st.at - (before + __shfl_sync(0xffffffffu, sum - span, l)) * p.num_kv_heads;
             st.g = (int)(rem / (uint32_t)(st.tiles + st.lead));
             st.v0 = (int)(rem - (uint32_t)st.g * (st.tiles + st.lead));
-            return Found::kShare;
+            return true;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
+        return false;
+    };
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b)
+        if (b == 0 || 32 * b < p.num_seqs)
+            if (here(32 * b, first.tiles[b], first.len[b])) return Found::kShare;
+    for (int s0 = 32 * kBatches; s0 < p.num_seqs; s0 += 32) {
+        int len;
+        const int t = seq_tiles<kEarly>(p, s0 + lane, &len, false);
+        if (here(s0, t, len)) return Found::kShare;
     }
     return Found::kNone;  // (not reached: at < total)
 }
