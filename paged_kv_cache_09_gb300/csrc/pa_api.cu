@@ -1275,7 +1275,7 @@ int pa_reshape_and_cache_q8(const pa_bf16 *key, int64_t key_stride, const pa_bf1
     const pa::Q8WriteArgs a{key, value, key_stride, value_stride, static_cast<uint8_t *>(k_cache),
                             static_cast<uint8_t *>(v_cache), k_scales, v_scales, page_stride,
                             scale_stride, num_pages, slot_mapping, num_tokens, num_kv_heads,
-                            block_size, dev.err, 0};
+                            block_size, dev.err, dev.num_sms, 0};
     return pa::launch_write_q8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                     : PA_ERR_CUDA;
 }

@@ -7,10 +7,13 @@
 //     rows of W: rne(x 2^(127 - b')); the others: rne(c 2^(b - b')) where b' > b
 // The tokens of a block share its scale, so one warp has to see them all, wherever in the call
 // they stand.  A CTA takes a range of tokens, notes which blocks they fall into (a bitmap by
-// slot / 16 and a list), and looks through the slots of the whole call for further tokens of
+// slot / 16 and a hash table), and looks through the slots of the whole call for further tokens of
 // these blocks; of a block's tokens the first one's CTA writes it.  So the result does not depend
 // on the order of tokens, no two CTAs touch one block, and of tokens that share a slot the last
-// one counts.  The look through the slots costs 8 bytes of L2 a slot and CTA.
+// one counts.  The look through the slots costs 8 bytes of L2 a slot and CTA: with two CTAs an SM,
+// about a tenth of the call's own bytes.
+#include <algorithm>
+
 #include "pa_internal.h"
 #include "pa_q8.cuh"
 
@@ -19,10 +22,10 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kWriteWarps = 16;
-constexpr int kMaxRange = 16;      // tokens of a CTA of the write
-constexpr int kScan = 8;           // slots of a thread in flight
-constexpr int kMapBits = 4096;
+constexpr int kMaxRange = 256;     // tokens of a CTA of the write (its threads at most)
+constexpr int kTableBits = 9, kTable = 1 << kTableBits;  // places for their blocks
+constexpr int kScan = 16;          // slots of a thread in flight
+constexpr int kMapBits = 16384;
 
 __device__ __forceinline__ uint32_t map_bit(long long slot) { return (uint32_t)(slot >> 4) % kMapBits; }
 
@@ -55,117 +58,163 @@ __device__ __forceinline__ uint32_t codes_down(uint32_t c, float f) {
     return e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-// Two warps for each head of K and of V: the first and the last 8 rows of a block, 8 dims a lane.
-__global__ void __launch_bounds__(kWriteWarps * 32, 2) write_q8_kernel(const Q8WriteArgs a) {
-    constexpr int kThreads = kWriteWarps * 32, kHalf = kQ8Tokens / 2;
-    __shared__ long long first[kMaxRange];  // a block's first slot
-    __shared__ int rows[kMaxRange];         // its rows in the page (0: no block)
-    __shared__ int lowest[kMaxRange];       // its first token
-    __shared__ __align__(16) int token[kMaxRange][kQ8Tokens];
-    __shared__ uint32_t map[kMapBits / 32];
-    __shared__ uint32_t tops[2][kWriteWarps];
+__device__ __forceinline__ uint32_t hash_of(long long first) {
+    return ((uint32_t)(first >> 4) * 0x9E3779B1u) >> (32 - kTableBits);
+}
+
+// Where a slot's block starts, its row in it and the block's rows; false: outside the pool.
+struct Place {
+    long long first;
+    int row, rows;
+};
+__device__ __forceinline__ bool block_of(const Q8WriteArgs &a, long long slot, Place *p) {
+    const int64_t page = q8_page_of(slot, a.block_size);
+    const int o = (int)(slot - page * a.block_size);
+    p->row = o % kQ8Tokens;
+    p->first = slot - p->row;
+    p->rows = min(kQ8Tokens, a.block_size - o + p->row);
+    return page < a.num_pages;
+}
+
+// A warp for each block and head of K and of V, 8 dims of its 16 rows a lane.
+// kOne: the CTA's range is one token, so there is one block, which needs no table.
+template <bool kOne>
+__global__ void __launch_bounds__(kWarps * 32, 2) write_q8_kernel(const __grid_constant__ Q8WriteArgs a) {
+    constexpr int kThreads = kWarps * 32, kPlaces = kOne ? 1 : kTable, kSlots = kOne ? 2 : kScan;
+    __shared__ long long keys[kPlaces];                       // first slots of blocks (-1: none)
+    __shared__ int lowest[kPlaces];                           // a block's first token
+    __shared__ __align__(16) int token[kPlaces][kQ8Tokens];   // the token of each row (-1: none)
+    __shared__ int list[kOne ? 1 : kMaxRange], count;         // the blocks' places
+    __shared__ uint32_t map[kOne ? 1 : kMapBits / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * a.range, n = min(a.range, a.num_tokens - t0);
-    const int h = blockIdx.y * (kWriteWarps / 4) + (warp >> 2);  // this warp's head
-    const bool is_v = warp & 2;                                  // of K or of V
-    const int r0 = (warp & 1) * kHalf;                           // its first row
-    const uint16_t *x = (is_v ? a.value : a.key) + (int64_t)h * kHeadDim + 8 * lane;
-    const int64_t x_stride = is_v ? a.value_stride : a.key_stride;
+    const int64_t t0 = (int64_t)blockIdx.x * a.range;
+    const int n = (int)min((int64_t)a.range, a.num_tokens - t0);
+    const int kinds = 2 * a.num_kv_heads;  // (head, K or V)
     pdl_wait();
     pdl_trigger();
     // The first slots of all, and the rows of this CTA's tokens, are on their way while the
     // blocks are found.
-    long long s[kScan];
+    long long s[kSlots];
 #pragma unroll
-    for (int k = 0; k < kScan; ++k) {
+    for (int k = 0; k < kSlots; ++k) {
         const int j = threadIdx.x + k * kThreads;
         s[k] = j < a.num_tokens ? a.slot_mapping[j] : -1;
     }
-    const long long slot = warp == 0 && lane < n ? a.slot_mapping[t0 + lane] : -1;
-    if (h < a.num_kv_heads)
-        for (int i = (lane >> 2) + r0; i < n; i += kQ8Tokens)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (int64_t)(t0 + i) * x_stride - 8 * lane + 64 * (lane & 3)));
-    for (int i = threadIdx.x; i < kMapBits / 32; i += kThreads) map[i] = 0;
-    for (int i = threadIdx.x; i < kMaxRange * kQ8Tokens; i += kThreads) (&token[0][0])[i] = -1;
-    if (threadIdx.x < kMaxRange) {
-        rows[threadIdx.x] = 0;
-        lowest[threadIdx.x] = 0x7fffffff;
+    const long long slot = kOne ? a.slot_mapping[t0] : (int)threadIdx.x < n ? a.slot_mapping[t0 + threadIdx.x] : -1;
+    for (int i = blockIdx.y * kThreads + threadIdx.x; i < n * kinds * 4; i += gridDim.y * kThreads) {
+        const int t = i / (kinds * 4), line = i - t * (kinds * 4), half = a.num_kv_heads * 4;
+        const uint16_t *row = line < half ? a.key + (t0 + t) * a.key_stride + line * 64
+                                          : a.value + (t0 + t) * a.value_stride + (line - half) * 64;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
     }
-    __syncthreads();
-    if (warp == 0) {
-        long long f = -1;
-        int count = 0;
-        if (slot >= 0) {
-            const int64_t page = q8_page_of(slot, a.block_size);
-            const int o = (int)(slot - page * a.block_size) & ~(kQ8Tokens - 1);
-            if (page < a.num_pages) {
-                f = page * a.block_size + o;
-                count = min(kQ8Tokens, a.block_size - o);
-            } else if (blockIdx.y == 0) {
-                atomicOr(a.err, kErrSlot);
+    Place own = {-1, 0, 0};
+    const bool live = slot >= 0 && block_of(a, slot, &own);
+    if (slot >= 0 && !live && blockIdx.y == 0 && (!kOne || threadIdx.x == 0)) atomicOr(a.err, kErrSlot);
+    if constexpr (kOne) {
+        if (!live) return;
+        if (threadIdx.x < kQ8Tokens) token[0][threadIdx.x] = -1;
+        if (threadIdx.x == 0) {
+            keys[0] = own.first;
+            lowest[0] = 0x7fffffff;
+            list[0] = 0;
+            count = 1;
+        }
+    } else {
+        for (int i = threadIdx.x; i < kMapBits / 32; i += kThreads) map[i] = 0;
+        for (int i = threadIdx.x; i < kTable; i += kThreads) keys[i] = -1;
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        if (live) {
+            uint32_t at = hash_of(own.first);
+            long long was;
+            while ((was = (long long)atomicCAS(reinterpret_cast<unsigned long long *>(&keys[at]), ~0ull,
+                                               (unsigned long long)own.first)) != -1 && was != own.first)
+                at = (at + 1) % kTable;
+            if (was == -1) {  // a new block
+                lowest[at] = 0x7fffffff;
+#pragma unroll
+                for (int i = 0; i < kQ8Tokens / 4; ++i)
+                    reinterpret_cast<int4 *>(token[at])[i] = make_int4(-1, -1, -1, -1);
+                list[atomicAdd(&count, 1)] = (int)at;
+                // (its slots may lie in two of the map's sixteens)
+                for (const uint32_t bit : {map_bit(own.first), map_bit(own.first + own.rows - 1)})
+                    atomicOr(&map[bit / 32], 1u << (bit % 32));
             }
         }
-        const unsigned same = __match_any_sync(0xffffffffu, f);
-        if (f >= 0 && __ffs(same) - 1 == lane) {
-            first[lane] = f;
-            rows[lane] = count;
-            // (a block's slots may lie in two of the map's sixteens)
-            for (const uint32_t bit : {map_bit(f), map_bit(f + count - 1)})
-                atomicOr(&map[bit / 32], 1u << (bit % 32));
-        }
     }
     __syncthreads();
-    for (int j0 = 0; j0 < a.num_tokens; j0 += kScan * kThreads) {
+    for (int64_t j0 = 0; j0 < a.num_tokens; j0 += kSlots * kThreads) {
+        if (j0 > 0)
 #pragma unroll
-        for (int k = 0; k < kScan; ++k) {
-            const int j = j0 + threadIdx.x + k * kThreads;
-            if (j0 > 0) s[k] = j < a.num_tokens ? a.slot_mapping[j] : -1;
-        }
+            for (int k = 0; k < kSlots; ++k) {
+                const int64_t j = j0 + threadIdx.x + k * kThreads;
+                s[k] = j < a.num_tokens ? a.slot_mapping[j] : -1;
+            }
 #pragma unroll
-        for (int k = 0; k < kScan; ++k) {
-            const uint32_t bit = map_bit(s[k]);
-            if (map[bit / 32] >> (bit % 32) & 1)
-                for (int e = 0; e < n; ++e) {
-                    const unsigned long long at = (unsigned long long)(s[k] - first[e]);
-                    if (rows[e] && at < (unsigned)rows[e]) {
-                        const int j = j0 + threadIdx.x + k * kThreads;
-                        atomicMax(&token[e][at], j);
-                        atomicMin(&lowest[e], j);
-                    }
+        for (int k = 0; k < kSlots; ++k) {
+            const int j = (int)(j0 + threadIdx.x + k * kThreads);
+            int at = -1, row = 0;
+            if constexpr (kOne) {
+                const unsigned long long r = (unsigned long long)(s[k] - own.first);
+                if (r < (unsigned)own.rows) {
+                    at = 0;
+                    row = (int)r;
                 }
+            } else {
+                const uint32_t bit = map_bit(s[k]);
+                if ((map[bit / 32] >> (bit % 32) & 1) && s[k] >= 0) {
+                    Place p;
+                    block_of(a, s[k], &p);
+                    at = (int)hash_of(p.first);
+                    while (keys[at] != p.first && keys[at] != -1) at = (at + 1) % kTable;
+                    if (keys[at] == -1) at = -1;
+                    row = p.row;
+                }
+            }
+            if (at >= 0) {
+                atomicMax(&token[at][row], j);
+                atomicMin(&lowest[at], j);
+            }
         }
     }
     __syncthreads();
-    if (h >= a.num_kv_heads) return;
+    const int jobs = count * kinds;
     const int64_t row_stride = (int64_t)a.num_kv_heads * kHeadDim;
-    int turn = 0;
-    for (int e = 0; e < n; ++e) {
-        const int in_page = rows[e];
-        if (in_page == 0 || lowest[e] < t0) continue;  // none, or another CTA's
-        const long long f = first[e];
+    for (int job = blockIdx.y * kWarps + warp; job < jobs; job += gridDim.y * kWarps) {
+        const int e = job / kinds, kind = job - e * kinds, at = list[e];
+        if (lowest[at] < t0) continue;  // another CTA's
+        const int h = kind >> 1;
+        const bool is_v = kind & 1;
+        const long long f = keys[at];
         const int64_t page = q8_page_of(f, a.block_size);
         const int o = (int)(f - page * a.block_size);
         uint8_t *scale = (is_v ? a.v_scales : a.k_scales) + page * a.scale_stride +
                          (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
         const uint32_t old = *scale;
-        const int4 at[2] = {*reinterpret_cast<const int4 *>(&token[e][r0]),
-                            *reinterpret_cast<const int4 *>(&token[e][r0 + 4])};
-        auto token_of = [&](int i) { return (&at[i / 4].x)[i % 4]; };
-        uint4 v[kHalf];
+        const uint16_t *x = (is_v ? a.value : a.key) + h * kHeadDim + 8 * lane;
+        const int64_t x_stride = is_v ? a.value_stride : a.key_stride;
+        uint4 v[kQ8Tokens];
+#pragma unroll
+        for (int q = 0; q < kQ8Tokens / 4; ++q) {
+            const int4 t4 = reinterpret_cast<const int4 *>(token[at])[q];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = i == 0 ? t4.x : i == 1 ? t4.y : i == 2 ? t4.z : t4.w;
+                v[4 * q + i] = make_uint4(0, 0, 0, 0);
+                if (t >= 0) v[4 * q + i] = __ldg(reinterpret_cast<const uint4 *>(x + t * x_stride));
+            }
+        }
+        // Rows that are written.
+        const uint32_t rows = __ballot_sync(0xffffffffu, lane < kQ8Tokens && token[at][lane & 15] >= 0);
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (token_of(i) >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(x + token_of(i) * x_stride));
-        }
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i)
+        for (int i = 0; i < kQ8Tokens; ++i)
             top = abs_max2(abs_max2(abs_max2(abs_max2(top, v[i].x), v[i].y), v[i].z), v[i].w);
         uint32_t m = warp_top(top);
         if (m >= 0x7f80u) {  // infinities and NaN: codes of NaN, and no part in the scale
             top = 0;
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) {
+            for (int i = 0; i < kQ8Tokens; ++i) {
                 top = abs_max2(abs_max2(top, without_inf<true>(v[i].x)), without_inf<true>(v[i].y));
                 top = abs_max2(abs_max2(top, without_inf<true>(v[i].z)), without_inf<true>(v[i].w));
                 v[i].x = without_inf<false>(v[i].x);
@@ -175,32 +224,28 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 2) write_q8_kernel(const Q8W
             }
             m = warp_top(top);
         }
-        // The two warps meet; both have read the old byte by then.
-        if (lane == 0) tops[turn][warp] = m;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-        m = max(m, tops[turn][warp ^ 1]);
-        turn ^= 1;
         // m = 1.f 2^(E - 127) <= 448 2^(b - 127) = 1.75 2^8 2^(b - 127): b = E - 8, or one more
         // where f > .75
         const uint32_t need = (uint32_t)max(1, (int)(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0));
-        const bool anew = token[e][0] >= 0 || old == 255;
+        const bool anew = (rows & 1) || old == 255;
         const uint32_t b = anew ? need : max(old, need);
         const float up = b == 254 ? 0x1p-127f : __uint_as_float((254 - b) << 23);
         uint8_t *row = (is_v ? a.v_cache : a.k_cache) + page * a.page_stride +
-                       ((int64_t)(o + r0) * a.num_kv_heads + h) * kHeadDim + 8 * lane;
-        if (lane == 0 && r0 == 0 && b != old) *scale = (uint8_t)b;
+                       ((int64_t)o * a.num_kv_heads + h) * kHeadDim + 8 * lane;
+        if (lane == 0 && b != old) *scale = (uint8_t)b;
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i)
-            if (token_of(i) >= 0) *reinterpret_cast<uint2 *>(row + i * row_stride) = codes_of(v[i], up);
-        if (!anew && b > old) {
+        for (int i = 0; i < kQ8Tokens; ++i)
+            if (rows >> i & 1) *reinterpret_cast<uint2 *>(row + i * row_stride) = codes_of(v[i], up);
+        const uint32_t others = ~rows & ((1u << min(kQ8Tokens, a.block_size - o)) - 1);
+        if (!anew && b > old && others) {
             const float down = b - old > 126 ? 0.f : __uint_as_float((127 - (b - old)) << 23);
-            uint2 c[kHalf];
+            uint2 c[kQ8Tokens];
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i)
-                if (r0 + i < in_page && token_of(i) < 0) c[i] = *reinterpret_cast<const uint2 *>(row + i * row_stride);
+            for (int i = 0; i < kQ8Tokens; ++i)
+                if (others >> i & 1) c[i] = *reinterpret_cast<const uint2 *>(row + i * row_stride);
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i)
-                if (r0 + i < in_page && token_of(i) < 0)
+            for (int i = 0; i < kQ8Tokens; ++i)
+                if (others >> i & 1)
                     *reinterpret_cast<uint2 *>(row + i * row_stride) =
                         make_uint2(codes_down(c[i].x, down), codes_down(c[i].y, down));
         }
@@ -382,11 +427,13 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
 
 cudaError_t launch_write_q8(const Q8WriteArgs &args, cudaStream_t stream) {
     Q8WriteArgs a = args;
-    a.range = a.num_tokens <= 1024 ? 1 : a.num_tokens <= 2048 ? 8 : kMaxRange;
-    return launch_pdl(write_q8_kernel,
-                      dim3((unsigned)((a.num_tokens - 1) / a.range + 1),
-                           (a.num_kv_heads + kWriteWarps / 4 - 1) / (kWriteWarps / 4)),
-                      dim3(kWriteWarps * 32), 0, stream, a);
+    // Two CTAs an SM while that gives each a range of at most kMaxRange tokens.
+    const int ctas = 2 * a.num_sms;
+    a.range = std::min(kMaxRange, (a.num_tokens - 1) / ctas + 1);
+    const int x = (a.num_tokens - 1) / a.range + 1;
+    const int y = std::min((2 * a.num_kv_heads - 1) / kWarps + 1, std::max(1, ctas / x));
+    return launch_pdl(a.range == 1 ? write_q8_kernel<true> : write_q8_kernel<false>, dim3(x, y), dim3(kWarps * 32), 0,
+                      stream, a);
 }
 
 cudaError_t launch_gather_q8(const Q8GatherArgs &a, cudaStream_t stream) {

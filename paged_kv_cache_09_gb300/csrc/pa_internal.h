@@ -202,6 +202,7 @@ struct Q8WriteArgs {
     const int64_t *slot_mapping;
     int num_tokens, num_kv_heads, block_size;
     unsigned *err;
+    int num_sms;
     int range;  // set by the launch: tokens of a CTA
 };
 cudaError_t launch_write_q8(const Q8WriteArgs &a, cudaStream_t stream);
