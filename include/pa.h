@@ -438,8 +438,8 @@ int pa_qk_norm_rope_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, 
  * position on each of several axes (time, height and width of an image's or a video's tokens; text
  * tokens have the same on all).  Frequency i turns by the position on axis axes[i]: the pair it
  * turns takes cos_sin[positions[axes[i]][t]][i] and [rotary_dim / 2 + i].
- *   positions   int32 [num_axes, num_tokens], axes position_stride elements apart (at least
- *               num_tokens).  A token with a negative one on any axis is padding; otherwise one >=
+ *   positions   int32 [num_axes, num_tokens], axes position_stride elements apart (0 where all axes
+ *               have the same).  A token with a negative one on any axis is padding; otherwise one >=
  *               max_position leaves the token's outputs as they were and sets PA_DEVERR_POSITION.
  *   num_axes    1 .. PA_MAX_AXES
  *   axes        HOST array of rotary_dim / 2 entries below num_axes, read during the call only
@@ -595,7 +595,8 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
  * written in order, as a serving layer does; a page needs no clearing before its next use.)
  * Tokens may stand in the call in any order; of several with one slot the last one counts and the
  * others are ignored.  A negative slot is skipped; one outside the pool is skipped and sets
- * PA_DEVERR_SLOT.  The caches, the scales and the new rows must not overlap one another.
+ * PA_DEVERR_SLOT.  The caches, the scales and the new rows must not overlap one another (one array as
+ * both K's and V's is refused: PA_ERR_INVALID_ARG).
  */
 int pa_reshape_and_cache_q8(const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value,
                             int64_t value_stride, void *k_cache, void *v_cache, uint8_t *k_scales,
@@ -622,7 +623,8 @@ int pa_gather_cache_q8(const void *k_cache, const void *v_cache, const uint8_t *
  * pa_decode_q8_workspace_size.  Weights times scales of V are rounded to FP16 relative to each
  * head's largest (2^-11 of them at most down to 2^-20 of that largest); a head's q is FP16 relative
  * to its largest value (values down to 2^-24 of it exact, smaller ones off by up to 2^-34 of it).
- * Values of V of 2^100 and more may overflow, and outputs below 2^-110 may come out as 0.
+ * Values of V of 2^100 and more may overflow, and outputs below 2^-110 may come out as 0.  Calls that
+ * run at the same time need separate workspaces.
  */
 size_t pa_decode_q8_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                    int block_size, int max_seq_len);
@@ -641,7 +643,8 @@ int pa_decode_q8(const pa_bf16 *q, const void *k_cache, const void *v_cache, con
  * split items), K into BF16, which holds its values exactly, V into FP16, each KV head of a
  * sequence scaled by a power of two.
  * Precision: queries and K are exact, and V while a block's scale is at least 2^-15 of the largest
- * of its KV head in that sequence (smaller values are off by up to 2^-39 of the head's largest);
+ * of its KV head in that sequence (smaller values are off by up to 2^-39 of the head's largest); a
+ * key of 2^128, which rounding up can make of the largest BF16 values, is an infinity here;
  * weights are rounded to FP16, off by up to 2^-11 of themselves, and by up to 2^-32 of the row's
  * largest below 2^-21 of it.  Arguments, errors and what a NaN in V reaches are those of the 4-bit
  * calls.

@@ -937,6 +937,21 @@ def q8_cache_shapes(num_pages, block_size, num_kv_heads):
 def _q8_cache(k_cache, v_cache, k_scales, v_scales, dev):
     """(the four addresses, page stride and scale stride in bytes, pages), block size, KV heads of
     an 8-bit cache."""
+    try:  # what a call usually gets, in one expression: a small call's time is its checks
+        shape, stride, sshape, sstride = k_cache.shape, k_cache.stride(), k_scales.shape, k_scales.stride()
+        pages, bs, heads, dim = shape
+        if k_cache.dtype is _E4M3 and v_cache.dtype is _E4M3 and k_scales.dtype is _U8 and \
+                v_scales.dtype is _U8 and dim == 256 and stride[1:] == (heads * 256, 256, 1) and \
+                sshape == (pages, (bs + 15) // 16, heads) and sstride[1:] == (heads, 1) and \
+                v_cache.shape == shape and v_cache.stride() == stride and \
+                v_scales.shape == sshape and v_scales.stride() == sstride and \
+                k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == \
+                v_scales.get_device() == dev:
+            return (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                    stride[0], sstride[0], pages), bs, heads
+    except (AttributeError, ValueError, TypeError):
+        pass
+    # Anything else: a single page's strides, sizes of 1, or an error to name.
     shape = _need(k_cache, "k_cache", _E4M3, 4, dev)
     pages, bs, heads, dim = shape
     stride = k_cache.stride()
@@ -1013,8 +1028,10 @@ def decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, sc
     if width * bs < max_seq_len:
         raise ValueError("block_table rows are too short for max_seq_len")
     out = _q4_out(out, q, dev)
-    _keep, ws, ws_bytes = _q4_workspace(
-        workspace, lambda: decode_q8_workspace_size(S, hq, hkv, d, bs, max_seq_len), dev, q.device)
+    if workspace is None:
+        workspace = torch.empty(max(256, decode_q8_workspace_size(S, hq, hkv, d, bs, max_seq_len)),
+                                dtype=_U8, device=q.device)
+    _keep, ws, ws_bytes = _q4_workspace(workspace, None, dev, None)
     _raise(lib.pa_decode_q8(q.data_ptr(), *cache, block_table.data_ptr(), row, lens, S, max_seq_len,
                             hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes, _stream()),
            "pa_decode_q8")

@@ -789,8 +789,7 @@ static int rope_impl(pa::RopeArgs &a, void *stream) {
         !(a.eps >= 0.f) || !isfinite(a.eps) || !isfinite(a.weight_bias))
         return PA_ERR_INVALID_ARG;
     if (a.rotary_dim % 16 || a.rotary_dim > a.head_dim) return PA_ERR_INVALID_ARG;
-    if (a.num_axes && (a.num_axes < 1 || a.num_axes > PA_MAX_AXES || a.position_stride < a.num_tokens))
-        return PA_ERR_INVALID_ARG;
+    if (a.num_axes < 0 || a.num_axes > PA_MAX_AXES || a.position_stride < 0) return PA_ERR_INVALID_ARG;
     if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return PA_ERR_UNSUPPORTED;
     if (a.cache == 2 && a.head_dim != pa::kHeadDim) return PA_ERR_UNSUPPORTED;
     if (a.num_tokens == 0) return PA_OK;
@@ -1268,7 +1267,7 @@ int pa_reshape_and_cache_q8(const pa_bf16 *key, int64_t key_stride, const pa_bf1
         return rc;
     const int64_t row = (int64_t)num_kv_heads * head_dim;
     if (!rows_ok(key, key_stride, row) || !rows_ok(value, value_stride, row) || !slot_mapping ||
-        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || k_cache == v_cache || k_scales == v_scales)
         return PA_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (int rc = device_info(&dev)) return rc;

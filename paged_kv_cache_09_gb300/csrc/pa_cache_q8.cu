@@ -10,7 +10,9 @@
 // slot / 16 and a hash table), and looks through the slots of the whole call for further tokens of
 // these blocks; of a block's tokens the first one's CTA writes it.  So the result does not depend
 // on the order of tokens, no two CTAs touch one block, and of tokens that share a slot the last
-// one counts.  The look through the slots costs 8 bytes of L2 a slot and CTA: with two CTAs an SM,
+// one counts.  (Rows, codes and scales may come from the kernel before, whose end this one's start
+// overlaps: they are read with ordinary loads or past L1, not through the read-only path.)  The look
+// through the slots costs 8 bytes of L2 a slot and CTA: with two CTAs an SM,
 // about a tenth of the call's own bytes.
 #include <algorithm>
 
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) write_q8_kernel(const __grid_c
             for (int i = 0; i < 4; ++i) {
                 const int t = i == 0 ? t4.x : i == 1 ? t4.y : i == 2 ? t4.z : t4.w;
                 v[4 * q + i] = make_uint4(0, 0, 0, 0);
-                if (t >= 0) v[4 * q + i] = __ldg(reinterpret_cast<const uint4 *>(x + t * x_stride));
+                if (t >= 0) v[4 * q + i] = __ldcg(reinterpret_cast<const uint4 *>(x + t * x_stride));
             }
         }
         // Rows that are written.
@@ -290,10 +292,10 @@ __global__ void __launch_bounds__(kWarps * 32) gather_q8_kernel(const Q8GatherAr
             const int o = (int)(slot[k] - page * a.block_size);
             const int64_t at = page * a.page_stride + ((int64_t)o * a.num_kv_heads + h) * kHeadDim;
             const int64_t sat = page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
-            ck[k] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at) + lane);
-            cv[k] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at) + lane);
-            bk[k] = __ldg(a.k_scales + sat);
-            bv[k] = __ldg(a.v_scales + sat);
+            ck[k] = __ldcg(reinterpret_cast<const uint2 *>(a.k_cache + at) + lane);
+            cv[k] = __ldcg(reinterpret_cast<const uint2 *>(a.v_cache + at) + lane);
+            bk[k] = a.k_scales[sat];
+            bv[k] = a.v_scales[sat];
         } else if (lane == 0) {
             atomicOr(a.err, kErrSlot);
         }
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kWarps * 32) range_q8_kernel(const __grid_cons
         if (o % kQ8Tokens && k > k0) continue;
         const int page = bt[lp];
         if (page < 0 || page >= a.num_pages) continue;  // reported by the expansion
-        const uint32_t vb = __ldg(a.v_scales + page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h);
+        const uint32_t vb = a.v_scales[page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h];
         if (vb != 255) top = max(top, vb);
     }
     __shared__ uint32_t part[kWarps];
@@ -393,10 +395,10 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
         if (page >= 0 && page < a.num_pages) {
             const int64_t at = page * a.page_stride + ((int64_t)o * a.num_kv_heads + h) * kHeadDim;
             const int64_t sat = page * a.scale_stride + (int64_t)(o / kQ8Tokens) * a.num_kv_heads + h;
-            ck[i] = __ldg(reinterpret_cast<const uint2 *>(a.k_cache + at) + lane);
-            cv[i] = __ldg(reinterpret_cast<const uint2 *>(a.v_cache + at) + lane);
-            bk[i] = __ldg(a.k_scales + sat);
-            bv[i] = __ldg(a.v_scales + sat);
+            ck[i] = __ldcg(reinterpret_cast<const uint2 *>(a.k_cache + at) + lane);
+            cv[i] = __ldcg(reinterpret_cast<const uint2 *>(a.v_cache + at) + lane);
+            bk[i] = a.k_scales[sat];
+            bv[i] = a.v_scales[sat];
         } else if (lane == 0) {
             atomicOr(a.err, kErrPage);
         }

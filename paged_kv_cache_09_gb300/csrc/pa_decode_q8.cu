@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         // A page outside the pool is reported, and its box, which lies outside the map, reads as zeros.
         if (page >= 0 && page < p.num_pages) {
             const int64_t o = page * p.scale_stride + (int64_t)in.tip * p.num_kv_heads + g;
-            t.k_scale = __ldg(p.k_scales + o);
-            t.v_scale = __ldg(p.v_scales + o);
+            t.k_scale = __ldcg(p.k_scales + o);
+            t.v_scale = __ldcg(p.v_scales + o);
         } else if (lane == 0) {
             atomicOr(p.err, kErrPage);
         }

@@ -60,9 +60,10 @@ def test_mrope_of_equal_positions_is_rope(cuda_lib, T, dim, interleaved):
     q, k, v, w, table, pos = _case(T, 24, 4, dim, 64, 1, seed=T)
     want = pa.qk_norm_rope(q, k, w[0], w[1], table, pos[0], 1e-6, interleaved=interleaved)
     for turn in (False, True):
-        got = pa.qk_norm_mrope(q, k, w[0], w[1], table, pos.expand(3, -1).contiguous(),
-                               pa.mrope_axes([16, 8, 8], turn), 1e-6, interleaved=interleaved)
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for p in (pos.expand(3, -1).contiguous(), pos.expand(3, -1)):
+            got = pa.qk_norm_mrope(q, k, w[0], w[1], table, p, pa.mrope_axes([16, 8, 8], turn), 1e-6,
+                                   interleaved=interleaved)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_mrope_padding_range_strides_and_in_place(cuda_lib):
@@ -132,7 +133,7 @@ def test_mrope_refuses(cuda_lib):
     pa = cuda_lib
     q, k, v, w, table, pos = _case(4, 4, 2, 256, 64)
     good = pa.mrope_axes([16, 8, 8])
-    for p, axes in ((pos[0], good), (pos[:, :3], good), (pos, good[:-1]), (pos.expand(5, 3, 4)[:, 0], good),
+    for p, axes in ((pos[0], good), (pos[:, :3], good), (pos, good[:-1]),
                     (torch.zeros(5, 4, dtype=torch.int32, device="cuda"), good),
                     (torch.zeros(4, 3, dtype=torch.int32, device="cuda").T, good)):
         with pytest.raises(ValueError):

@@ -281,6 +281,93 @@ def test_decode_long_shares(cuda_lib, bs, hq, hkv, lens):
     assert cuda_lib.device_errors() == 0
 
 
+# One sequence, whose pairs are cut by themselves: from a tile to one part a CTA of the GPU, and more
+# KV heads than fit; and more sequences than a warp keeps the lengths of.
+@pytest.mark.parametrize("bs,hq,hkv,lens", [
+    (16, 5, 1, [20001]), (832, 8, 1, [40000]), (64, 16, 16, [130]), (16, 320, 320, [37]), (7, 64, 32, [100]),
+    (16, 4, 1, [(i * 61) % 97 for i in range(131)]), (64, 8, 2, [(i * 61) % 301 for i in range(200)]),
+    (16, 2, 2, [(i * 7) % 40 for i in range(128)]),
+])
+def test_decode_one_sequence_and_many(cuda_lib, bs, hq, hkv, lens):
+    c = _case(cuda_lib, lens, bs, hq, hkv, seed=bs)
+    _check_decode(_decode(cuda_lib, c), c)
+    assert cuda_lib.device_errors() == 0
+
+
+def test_decode_longest_length_of_a_short_sequence(cuda_lib):
+    # One sequence of 100 keys whose table has room for 2^31 - 1: no error.
+    pa = cuda_lib
+    bs, hkv = 1 << 16, 16
+    codes, scales = pa.q8_cache_shapes(1, bs, hkv)
+    cache = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in (codes, codes, scales, scales)]
+    cache[:2] = [c.view(torch.float8_e4m3fn) for c in cache[:2]]
+    table = torch.zeros(1, 1 << 15, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 16, 256, device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn(100, hkv, 256, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pa.reshape_and_cache_q8(k, v, *cache, torch.arange(100, device="cuda"))
+    lens = torch.tensor([100], dtype=torch.int32, device="cuda")
+    out = pa.decode_q8(q, *cache, table, lens, 0.0625, 2**31 - 1)
+    assert pa.device_errors() == 0
+    # (as many CTAs as the length allows, so other parts, whose sums may round a result to the next
+    # BF16 value: 2^-7 of it at most)
+    want = pa.decode_q8(q, *cache, table, lens, 0.0625, 100)
+    assert (out.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()
+
+
+@pytest.mark.parametrize("S", [1, 4, 40])
+def test_decode_of_lengths_that_the_kernel_before_writes(cuda_lib, S):
+    # The decode looks at lengths and tables before the preparation that writes them has ended.
+    pa = cuda_lib
+    c = _case(pa, [900] * S, 64, 24, 4, seed=5)
+    free = torch.zeros(S * 20, dtype=torch.int32, device="cuda")
+    new = torch.ones(S, dtype=torch.int32, device="cuda")
+    steps, prep = [], None
+    for i in range(12):
+        # (odd: no sequence begins a page, which the preparation would take from the free list)
+        computed = torch.tensor([(j * 131 + i * 377) % 899 | 1 for j in range(S)], dtype=torch.int32, device="cuda")
+        tables = c["bt"][torch.randperm(S, generator=torch.Generator().manual_seed(i))].contiguous()
+        steps.append((computed, tables))
+    bt = c["bt"].clone()
+    ws = torch.empty(pa.decode_q8_workspace_size(S, 24, 4, 256, 64, 900), dtype=torch.uint8, device="cuda")
+    outs = []
+    for computed, tables in steps:
+        pa.copy(bt, tables) if bt.numel() * 4 % 16 == 0 else bt.copy_(tables)
+        prep = pa.batch_input_prep(computed, new, [bt], [64], [free], S, out=prep)
+        outs.append(pa.decode_q8(c["q"], *c["cache"], bt, prep["seq_lens"], 0.0625, 900, workspace=ws))
+    torch.cuda.synchronize()
+    for (computed, tables), out in zip(steps, outs):
+        assert torch.equal(out, pa.decode_q8(c["q"], *c["cache"], tables, computed + 1, 0.0625, 900))
+        torch.cuda.synchronize()
+    assert pa.device_errors() == 0
+
+
+def test_steps_of_write_and_decode_back_to_back(cuda_lib):
+    # Each step's write grows scales that the step before has read: no stale ones are used.
+    pa = cuda_lib
+    S, bs, hkv, start, steps = 6, 64, 4, 700, 40
+    c = _case(pa, [start + steps] * S, bs, 24, hkv, seed=6)
+    plain = [x.clone() for x in c["cache"]]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rows = torch.arange(S, device="cuda") * (start + steps) + start
+    lens = [torch.full((S,), start + i + 1, dtype=torch.int32, device="cuda") for i in range(steps)]
+    slots = [c["slots"][rows + i].contiguous() for i in range(steps)]
+    kv = [[(torch.randn(S, hkv, 256, generator=g, device="cuda") * 2.0 ** (i % 16)).to(torch.bfloat16)
+           for _ in range(2)] for i in range(steps)]
+    ws = torch.empty(pa.decode_q8_workspace_size(S, 24, hkv, 256, bs, start + steps), dtype=torch.uint8, device="cuda")
+    outs = []
+    for i in range(steps):
+        pa.reshape_and_cache_q8(*kv[i], *c["cache"], slots[i])
+        outs.append(pa.decode_q8(c["q"], *c["cache"], c["bt"], lens[i], 0.0625, start + steps, workspace=ws))
+    torch.cuda.synchronize()
+    for i in range(steps):
+        pa.reshape_and_cache_q8(*kv[i], *plain, slots[i])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], pa.decode_q8(c["q"], *plain, c["bt"], lens[i], 0.0625, start + steps)), i
+        torch.cuda.synchronize()
+    for a, b in zip(c["cache"], plain):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
 def test_decode_scales(cuda_lib, scale):
     c = _case(cuda_lib, [300, 17], 64, 6, 1, seed=9)

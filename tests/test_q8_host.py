@@ -37,7 +37,7 @@ _CACHE = [(dict(k=None), INVALID), (dict(vs=None), INVALID), (dict(k=FAKE + 8), 
           (dict(bs=(1 << 20) + 1, page_stride=1 << 39, scale_stride=1 << 30), INVALID),
           (dict(hkv=0), INVALID), (dict(d=128), UNSUPPORTED)]
 
-_WRITE = dict(key=FAKE, kst=1024, value=FAKE, vst=1024, k=FAKE, v=FAKE, ks=FAKE, vs=FAKE + 3,
+_WRITE = dict(key=FAKE, kst=1024, value=FAKE, vst=1024, k=FAKE, v=2 * FAKE, ks=FAKE, vs=FAKE + 3,
               page_stride=PAGE, scale_stride=SCALES, num_pages=8, slots=FAKE, T=5, hkv=4, d=256, bs=832,
               stream=None)
 
@@ -45,7 +45,7 @@ _WRITE = dict(key=FAKE, kst=1024, value=FAKE, vst=1024, k=FAKE, v=FAKE, ks=FAKE,
 @pytest.mark.parametrize("kw,want", _CACHE + [
     (dict(T=-1), INVALID), (dict(T=0, key=None, k=None), 0), (dict(key=None), INVALID),
     (dict(slots=None), INVALID), (dict(slots=FAKE + 4), INVALID), (dict(kst=1016), INVALID),
-    (dict(vst=1028), INVALID), (dict(key=FAKE + 8), INVALID)])
+    (dict(vst=1028), INVALID), (dict(key=FAKE + 8), INVALID), (dict(v=FAKE), INVALID), (dict(vs=FAKE), INVALID)])
 def test_write_q8_refuses(lib, kw, want):
     assert _call(lib.pa_reshape_and_cache_q8, _WRITE, kw) == want
 
@@ -101,7 +101,7 @@ _ROPE = dict(q=FAKE, qs=24 * 256, k=FAKE, ks=1024, v=FAKE, vs=1024, qw=FAKE, kw=
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(n=0), INVALID), (dict(n=5), INVALID), (dict(axes=None), INVALID), (dict(pos_stride=2), INVALID),
+    (dict(n=0), INVALID), (dict(n=5), INVALID), (dict(axes=None), INVALID), (dict(pos_stride=-1), INVALID),
     (dict(axes=bytes(31) + b"\x03"), INVALID), (dict(axes=b"\xff" + bytes(31)), INVALID),
     (dict(q=None), INVALID), (dict(v=None), INVALID), (dict(table=None), INVALID), (dict(pos=None), INVALID),
     (dict(fmt=2), INVALID), (dict(rot=24), INVALID), (dict(rot=272, axes=bytes(136)), INVALID),
