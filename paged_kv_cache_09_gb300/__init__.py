@@ -2,7 +2,9 @@
 
 This module only marshals arguments: it takes torch CUDA tensors, checks their dtype,
 device and layout, and passes raw pointers, sizes and the current CUDA stream to the
-C ABI declared in include/pa.h.  Every step of the computation runs in the library's
+C ABI declared in include/pa.h (the calls of the 8-bit cache and of rotation by axes through a
+compiled module, csrc/pa_bind.cpp, where their arguments are as usual: a small call's time is its
+checks).  Every step of the computation runs in the library's
 CUDA kernels.  There is no CPU or PyTorch fallback: if libpa.so is missing or cannot be
 loaded, every call raises.
 
@@ -37,6 +39,8 @@ Functions (names follow the C ABI):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -67,6 +71,7 @@ Q8_TOKENS = 16  # PA_Q8_TOKENS: tokens of a page under one scale of the 8-bit ca
 ERR_TIMEOUT = 4  # PA_ERR_TIMEOUT
 
 _lib = None
+_bind = None  # the module of the short calls
 _lock = threading.Lock()
 
 
@@ -84,7 +89,7 @@ def build(force: bool = False) -> str:
 
 def load():
     """Load libpa.so and declare the C signatures.  Raises if it is not built."""
-    global _lib
+    global _lib, _bind
     if _lib is not None:
         return _lib
     with _lock:
@@ -161,7 +166,13 @@ def load():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
-        _lib = lib
+        if not os.path.exists(_build.BIND):
+            raise RuntimeError(f"{_build.BIND} is not built; run __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("pa_bind", _build.BIND)
+        bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_bind", loader))
+        loader.exec_module(bind)
+        bind.load(LIB_PATH)
+        _bind, _lib = bind, lib
         return lib
 
 
@@ -496,6 +507,14 @@ def prefill_plan_pieces(q_len, q_start, causal, num_q_heads, num_kv_heads, block
     return list(items)[:ni.value], pieces, mc.value
 
 
+def _short():
+    """The module of the short calls, whose functions give None where the arguments are not as usual,
+    and a status where the library refuses them."""
+    if _bind is None:
+        load()
+    return _bind
+
+
 _BF16, _I32, _I64, _U8, _F32 = (torch.bfloat16, torch.int32, torch.int64, torch.uint8,
                                 torch.float32)
 _E4M3 = torch.float8_e4m3fn
@@ -726,6 +745,11 @@ def qk_norm_mrope(q, k, q_weight, k_weight, cos_sin, positions, axes, eps, inter
     """qk_norm_rope with positions on several axes (see pa_qk_norm_mrope): positions int32 [axes,
     T], axes the axis of each of the rotary_dim / 2 frequencies (bytes or ints, see mrope_axes).
     Returns (q_out, k_out)."""
+    if q_out is None and k_out is None:
+        r = (_bind or _short()).mrope(q, k, q_weight, k_weight, cos_sin, positions, axes, eps,
+                                      interleaved, weight_bias)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r, "pa_qk_norm_mrope")
     lib, dev = _lib or load(), _device()
     T, hq, hkv, d, qs, ks, qw, kw, rows, rot = _rope_args(q, k, q_weight, k_weight, cos_sin, dev)
     pos, stride, n, axes = _axis_rows(positions, axes, T, rot, dev)
@@ -743,6 +767,11 @@ def qk_norm_mrope(q, k, q_weight, k_weight, cos_sin, positions, axes, eps, inter
 def qk_norm_mrope_cache(q, k, v, q_weight, k_weight, cos_sin, positions, axes, eps, k_cache,
                         v_cache, slot_mapping, interleaved=False, weight_bias=0.0, q_out=None):
     """qk_norm_rope_cache with positions on several axes (see qk_norm_mrope).  Returns q_out."""
+    if q_out is None:
+        r = (_bind or _short()).mrope_cache(q, k, q_weight, k_weight, cos_sin, positions, axes, eps,
+                                            interleaved, weight_bias, v, k_cache, v_cache, slot_mapping)
+        if r is not None:
+            return r if type(r) is not int else _raise(r, "pa_qk_norm_mrope_cache")
     lib, dev = _lib or load(), _device()
     T, hq, hkv, d, qs, ks, qw, kw, rows, rot = _rope_args(q, k, q_weight, k_weight, cos_sin, dev)
     pos, stride, n, axes = _axis_rows(positions, axes, T, rot, dev)
@@ -937,21 +966,6 @@ def q8_cache_shapes(num_pages, block_size, num_kv_heads):
 def _q8_cache(k_cache, v_cache, k_scales, v_scales, dev):
     """(the four addresses, page stride and scale stride in bytes, pages), block size, KV heads of
     an 8-bit cache."""
-    try:  # what a call usually gets, in one expression: a small call's time is its checks
-        shape, stride, sshape, sstride = k_cache.shape, k_cache.stride(), k_scales.shape, k_scales.stride()
-        pages, bs, heads, dim = shape
-        if k_cache.dtype is _E4M3 and v_cache.dtype is _E4M3 and k_scales.dtype is _U8 and \
-                v_scales.dtype is _U8 and dim == 256 and stride[1:] == (heads * 256, 256, 1) and \
-                sshape == (pages, (bs + 15) // 16, heads) and sstride[1:] == (heads, 1) and \
-                v_cache.shape == shape and v_cache.stride() == stride and \
-                v_scales.shape == sshape and v_scales.stride() == sstride and \
-                k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == \
-                v_scales.get_device() == dev:
-            return (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                    stride[0], sstride[0], pages), bs, heads
-    except (AttributeError, ValueError, TypeError):
-        pass
-    # Anything else: a single page's strides, sizes of 1, or an error to name.
     shape = _need(k_cache, "k_cache", _E4M3, 4, dev)
     pages, bs, heads, dim = shape
     stride = k_cache.stride()
@@ -980,6 +994,9 @@ def _q8_cache(k_cache, v_cache, k_scales, v_scales, dev):
 def reshape_and_cache_q8(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping):
     """Quantise key/value [T, Hkv, 256] into the 8-bit caches at slot_mapping (in place; see
     pa_reshape_and_cache_q8 for how a block's scale follows its tokens)."""
+    r = (_bind or _short()).write_q8(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
+    if r is not None:
+        return None if r is True else _raise(r, "pa_reshape_and_cache_q8")
     lib, dev = _lib or load(), _device()
     cache, bs, hkv = _q8_cache(k_cache, v_cache, k_scales, v_scales, dev)
     T, heads, dim = _need(key, "key", _BF16, 3, dev)
@@ -996,6 +1013,10 @@ def reshape_and_cache_q8(key, value, k_cache, v_cache, k_scales, v_scales, slot_
 def gather_cache_q8(k_cache, v_cache, k_scales, v_scales, slot_mapping, k_out=None, v_out=None):
     """The tokens at slot_mapping [T] as BF16 (k, v), each [T, Hkv, 256]; zeros for negative
     slots."""
+    if k_out is None and v_out is None:
+        r = (_bind or _short()).gather_q8(k_cache, v_cache, k_scales, v_scales, slot_mapping)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r, "pa_gather_cache_q8")
     lib, dev = _lib or load(), _device()
     cache, bs, hkv = _q8_cache(k_cache, v_cache, k_scales, v_scales, dev)
     slots = _vector(slot_mapping, "slot_mapping", _I64, None, dev)
@@ -1018,6 +1039,10 @@ def decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, sc
     """q=1 decode over the 8-bit cache (see pa_decode_q8): row s of q [S, Hq, 256] attends to
     sequence s of seq_lens [S] and of block_table (S rows or more).  Returns out [S, Hq, 256]
     BF16; rows of sequences of length 0 are zeros."""
+    r = (_bind or _short()).decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
+                                      scale, max_seq_len, out, workspace)
+    if r is not None:
+        return r if type(r) is not int else _raise(r, "pa_decode_q8")
     lib, dev = _lib or load(), _device()
     S, hq, d = _need(q, "q", _BF16, 3, dev)
     q = q.contiguous()
@@ -1028,10 +1053,8 @@ def decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, sc
     if width * bs < max_seq_len:
         raise ValueError("block_table rows are too short for max_seq_len")
     out = _q4_out(out, q, dev)
-    if workspace is None:
-        workspace = torch.empty(max(256, decode_q8_workspace_size(S, hq, hkv, d, bs, max_seq_len)),
-                                dtype=_U8, device=q.device)
-    _keep, ws, ws_bytes = _q4_workspace(workspace, None, dev, None)
+    _keep, ws, ws_bytes = _q4_workspace(
+        workspace, lambda: decode_q8_workspace_size(S, hq, hkv, d, bs, max_seq_len), dev, q.device)
     _raise(lib.pa_decode_q8(q.data_ptr(), *cache, block_table.data_ptr(), row, lens, S, max_seq_len,
                             hq, hkv, d, bs, float(scale), out.data_ptr(), ws, ws_bytes, _stream()),
            "pa_decode_q8")

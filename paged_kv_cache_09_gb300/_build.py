@@ -3,6 +3,9 @@
 Each .cu file is compiled to an object in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  Output: paged_kv_cache_09_gb300/_build/.
 
+build() also makes the Python module of the short calls (csrc/pa_bind.cpp, against the installed
+torch) with g++: _build/pa_bind-<torch version>.so.
+
 build_test() makes the failure-path test library _build/test/libpa_test.so from the same
 sources with PA_TEST_HOOKS defined (a hook that leaves one ring stage's loads out, and
 a 20 ms limit on bounded waits instead of 2 s).  Only the tests load it.
@@ -11,9 +14,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa.so")
+BIND = os.path.join(BUILD, f"pa_bind-{importlib.metadata.version('torch')}.so")
 TEST_BUILD = os.path.join(BUILD, "test")
 TEST_LIB = os.path.join(TEST_BUILD, "libpa_test.so")
 TEST_DEFS = ["-DPA_TEST_HOOKS", "-DPA_WAIT_LIMIT_NS=20000000ull"]
@@ -54,8 +61,35 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libpa.so if any source is newer than it.  Returns its path."""
-    return _build_lib(LIB, BUILD, [], force, verbose)
+    """Compile and link libpa.so and the module of the short calls, each if a source is newer than
+    it.  Returns the library's path."""
+    with cf.ThreadPoolExecutor(1) as ex:
+        bind = ex.submit(_build_bind, force)
+        _build_lib(LIB, BUILD, [], force, verbose)
+        bind.result()
+    return LIB
+
+
+def _build_bind(force: bool = False) -> str:
+    src, header = os.path.join(CSRC, "pa_bind.cpp"), os.path.join(INCLUDE, "pa.h")
+    if not force and os.path.exists(BIND) and \
+            max(os.path.getmtime(src), os.path.getmtime(header)) <= os.path.getmtime(BIND):
+        return BIND
+    os.makedirs(BUILD, exist_ok=True)
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    includes = [INCLUDE, os.path.join(torch, "include"), os.path.join(cuda, "include"),
+                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = BIND + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] +
+                       [f"-I{i}" for i in includes] + ["-o", tmp, src, "-L" + os.path.join(torch, "lib"),
+                        "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on pa_bind.cpp:\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
 
 
 def build_test(force: bool = False, verbose: bool = False) -> str:

@@ -752,6 +752,57 @@ def test_prefill_nan_key_bad_page_and_graph(cuda_lib):
     assert pa.device_errors() == pa.DEVERR_PAGE
 
 
+class _Nothing:
+    """In the place of the short calls: takes none."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def test_short_calls_are_the_others(cuda_lib, monkeypatch):
+    # What the compiled module takes gives what the Python checks and ctypes give, and what it leaves
+    # to them is taken: other number types, one page, one token, a row of the table, given outputs.
+    pa = cuda_lib
+    c = _case(pa, [300, 77], 64, 24, 4, seed=40)
+    k, v = (torch.randn(77, 4, 256, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cs = torch.randn(100, 64, device="cuda")
+    w = torch.randn(256, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(0, 100, (3, 77), device="cuda", dtype=torch.int32)
+    q = torch.randn(77, 24, 256, device="cuda").to(torch.bfloat16)
+    axes = pa.mrope_axes([16, 8, 8])
+    slots = c["slots"][300:].contiguous()
+
+    def calls():
+        cache = [x.clone() for x in c["cache"]]
+        got = [pa.reshape_and_cache_q8(k, v, *cache, slots)] + cache
+        got += pa.gather_cache_q8(*cache, slots)
+        got.append(pa.decode_q8(c["q"], *cache, c["bt"], c["lens"], 0.0625, 300))
+        out, ws = torch.empty_like(c["q"]), torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+        assert pa.decode_q8(c["q"], *cache, c["bt"], c["lens"], 0.0625, 300, out, ws) is out
+        got += [out, pa.decode_q8(c["q"][:1], *cache, c["bt"][:1], c["lens"][:1], 1, np.int64(300))]
+        got += pa.qk_norm_mrope(q, k, w, w, cs, pos, axes, 1e-6)
+        got += pa.qk_norm_mrope(q, k, w, w, cs, pos, list(axes), np.float32(1e-6), 1, 0)
+        bf = torch.zeros(2, 2, 64, 4, 256, dtype=torch.bfloat16, device="cuda")
+        at = torch.arange(77, device="cuda")
+        got.append(pa.qk_norm_mrope_cache(q, k, v, w, w, cs, pos, axes, 1e-6, bf[:, 0], bf[:, 1], at))
+        one = [x[:1] for x in cache]
+        got += [bf] + list(pa.gather_cache_q8(*one, at[:1])) + list(pa.gather_cache_q8(*one, at[:0]))
+        return [x if x is None else x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x for x in got]
+
+    short = calls()
+    monkeypatch.setattr(pa, "_bind", _Nothing())
+    for a, b in zip(short, calls(), strict=True):
+        assert a is b is None or torch.equal(a, b)
+    monkeypatch.undo()
+    for bind in (pa._bind, _Nothing()):
+        monkeypatch.setattr(pa, "_bind", bind)
+        with pytest.raises(pa.PAError):  # refused by the library either way
+            pa.reshape_and_cache_q8(k, v, c["cache"][0], c["cache"][0], *c["cache"][2:], slots)
+        with pytest.raises(pa.PAError):
+            pa.decode_q8(c["q"], *c["cache"], c["bt"], c["lens"], float("inf"), 300)
+    assert pa.device_errors() == 0
+
+
 def test_layout_refusals(cuda_lib):
     pa = cuda_lib
     c = _case(pa, [100], 16, 6, 2, seed=36)

@@ -138,6 +138,18 @@ def test_calls_refuse_what_is_no_cuda_tensor(lib):
         pa.gather_cache_q8(kc, kc, ks, ks, bt[0])
 
 
+def test_short_calls_leave_the_unusual_to_python(lib):
+    import paged_kv_cache_09_gb300 as pa
+    assert pa._bind is not None
+    t = torch.zeros(3, 6, 256, dtype=torch.bfloat16)
+    for name, n in (("write_q8", 7), ("gather_q8", 5), ("decode_q8", 11), ("mrope", 10), ("mrope_cache", 14)):
+        f = getattr(pa._bind, name)
+        for args in ([], [None] * n, [t] * n, [t] * (n + 1), [3] * n, ["x"] * n):
+            assert f(*args) is None
+    with pytest.raises(RuntimeError):
+        pa._bind.load("/nowhere/libpa.so")
+
+
 def test_axes_of_sections(lib):
     import paged_kv_cache_09_gb300 as pa
     assert list(pa.mrope_axes([3, 2, 1])) == [0, 0, 0, 1, 1, 2]
