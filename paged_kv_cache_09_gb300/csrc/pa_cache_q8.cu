@@ -26,6 +26,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMaxRange = 256;     // tokens of a CTA of the write (its threads at most)
 constexpr int kTableBits = 9, kTable = 1 << kTableBits;  // places for their blocks
+constexpr int kMaxCut = 4;          // CTAs that share a range's heads
 constexpr int kScan = 16;          // slots of a thread in flight
 constexpr int kMapBits = 16384;
 
@@ -429,11 +430,13 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
 
 cudaError_t launch_write_q8(const Q8WriteArgs &args, cudaStream_t stream) {
     Q8WriteArgs a = args;
-    // Two CTAs an SM while that gives each a range of at most kMaxRange tokens.
-    const int ctas = 2 * a.num_sms;
-    a.range = std::min(kMaxRange, (a.num_tokens - 1) / ctas + 1);
+    // Two CTAs an SM.  A call of few tokens gives each a token; others first cut the heads, so that a
+    // CTA's warps work on one block at a time, then the tokens.
+    const int ctas = 2 * a.num_sms, heads = (2 * a.num_kv_heads - 1) / kWarps + 1;
+    const bool few = a.num_tokens <= ctas;
+    const int y = few ? std::min(heads, ctas / a.num_tokens) : std::min(heads, kMaxCut);
+    a.range = few ? 1 : std::min(kMaxRange, (a.num_tokens - 1) / (ctas / y) + 1);
     const int x = (a.num_tokens - 1) / a.range + 1;
-    const int y = std::min((2 * a.num_kv_heads - 1) / kWarps + 1, std::max(1, ctas / x));
     return launch_pdl(a.range == 1 ? write_q8_kernel<true> : write_q8_kernel<false>, dim3(x, y), dim3(kWarps * 32), 0,
                       stream, a);
 }
