@@ -1095,6 +1095,10 @@ def prefill_varlen_q8(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_s
     """Chunks of several sequences stacked row-wise in q, over the 8-bit cache (see
     pa_prefill_varlen_q8).  cu_seqlens_q and seq_lens_k are host sequences of ints.  Without a
     workspace, one of prefill_varlen_q8_workspace_size bytes is allocated for the call."""
+    r = (_bind or _short()).prefill_q8(q, k_cache, v_cache, k_scales, v_scales, block_table,
+                                       cu_seqlens_q, seq_lens_k, causal, scale, out, workspace)
+    if r is not None:
+        return r if type(r) is not int else _raise(r, "pa_prefill_varlen_q8")
     lib, dev = _lib or load(), _device()
     rows, hq, d = _need(q, "q", _BF16, 3, dev)
     q = q.contiguous()

@@ -13,6 +13,9 @@
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <vector>
+
 #include "pa.h"
 
 namespace {
@@ -22,6 +25,8 @@ struct Library {
     decltype(&pa_gather_cache_q8) gather_q8 = nullptr;
     decltype(&pa_decode_q8_workspace_size) decode_q8_size = nullptr;
     decltype(&pa_decode_q8) decode_q8 = nullptr;
+    decltype(&pa_prefill_varlen_q8_workspace_size) prefill_q8_size = nullptr;
+    decltype(&pa_prefill_varlen_q8) prefill_q8 = nullptr;
     decltype(&pa_qk_norm_mrope) mrope = nullptr;
     decltype(&pa_qk_norm_mrope_cache) mrope_cache = nullptr;
 } lib;
@@ -64,6 +69,16 @@ struct Call {
         int over = 0;
         const long long v = PyLong_AsLongLongAndOverflow(o, &over);
         if (over || v < low || v > high) usual = false;
+        return v;
+    }
+    // A list or tuple of ints that fit 32 bits.
+    std::vector<int32_t> integers(PyObject *o) {
+        std::vector<int32_t> v;
+        if (!PyList_CheckExact(o) && !PyTuple_CheckExact(o)) return fail(), v;
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+        PyObject **items = PySequence_Fast_ITEMS(o);
+        v.reserve(n + 1);
+        for (Py_ssize_t i = 0; i < n; ++i) v.push_back((int32_t)integer(items[i], INT32_MIN, INT32_MAX));
         return v;
     }
     float number(PyObject *o) {
@@ -172,6 +187,36 @@ PyObject *gather_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// A caller's output like q, or a new one.
+bool output(Call &c, PyObject *o, const at::Tensor *q, at::Tensor *out) {
+    if (o == Py_None) {
+        *out = new_rows(q, q->sizes());
+        return true;
+    }
+    const at::Tensor *t = c.tensor(o, Type::BFloat16, 3);
+    if (!t || t->sizes() != q->sizes() || !t->is_contiguous()) return false;
+    *out = *t;
+    return true;
+}
+
+// A caller's workspace, or a new one of need() bytes.
+template <typename F>
+bool workspace(Call &c, PyObject *o, const at::Tensor *q, at::Tensor *ws, F need) {
+    if (o == Py_None) {
+        *ws = at::empty({(int64_t)std::max<size_t>(need(), 256)}, q->options().dtype(Type::Byte));
+        return true;
+    }
+    if (!THPVariable_Check(o)) return false;
+    *ws = THPVariable_Unpack(o);
+    return ws->defined() && ws->is_cuda() && ws->get_device() == c.dev && ws->is_contiguous();
+}
+
+PyObject *given_or(PyObject *o, at::Tensor &&t) {
+    if (o == Py_None) return THPVariable_Wrap(std::move(t));
+    Py_INCREF(o);
+    return o;
+}
+
 // q, the four caches, block_table, seq_lens, scale, max_seq_len, out, workspace -> out
 PyObject *decode_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 11, [&]() -> PyObject * {
@@ -188,31 +233,45 @@ PyObject *decode_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
             return none();
         const int64_t table_stride = table->size(0) > 1 ? table->stride(0) : table->size(1);
         at::Tensor out, ws;
-        if (a[9] != Py_None) {
-            const at::Tensor *o = c.tensor(a[9], Type::BFloat16, 3);
-            if (!o || o->sizes() != q->sizes() || !o->is_contiguous()) return none();
-            out = *o;
-        } else {
-            out = new_rows(q, q->sizes());
-        }
-        if (a[10] != Py_None) {
-            if (!THPVariable_Check(a[10])) return none();
-            ws = THPVariable_Unpack(a[10]);
-            if (!ws.defined() || !ws.is_cuda() || ws.get_device() != c.dev || !ws.is_contiguous()) return none();
-        } else {
-            const size_t need = lib.decode_q8_size((int)S, (int)hq, cache.heads, 256, cache.block_size, (int)most);
-            ws = at::empty({(int64_t)std::max<size_t>(need, 256)}, q->options().dtype(Type::Byte));
-        }
+        if (!output(c, a[9], q, &out) || !workspace(c, a[10], q, &ws, [&] {
+                return lib.decode_q8_size((int)S, (int)hq, cache.heads, 256, cache.block_size, (int)most);
+            }))
+            return none();
         const int rc = lib.decode_q8(ptr<pa_bf16>(q), cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
                                      cache.scale_stride, cache.pages, ptr<int32_t>(table), table_stride,
                                      ptr<int32_t>(lens), (int)S, (int)most, (int)hq, cache.heads, 256,
                                      cache.block_size, scale, ptr<pa_bf16>(&out), ptr(&ws), ws.nbytes(), c.stream());
-        if (rc) return status(rc);
-        if (a[9] != Py_None) {
-            Py_INCREF(a[9]);
-            return a[9];
-        }
-        return THPVariable_Wrap(std::move(out));
+        return rc ? status(rc) : given_or(a[9], std::move(out));
+    });
+}
+
+// q, the four caches, block_table, cu_seqlens_q, seq_lens_k, causal, scale, out, workspace -> out
+PyObject *prefill_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject * {
+        Call c;
+        CacheQ8 cache;
+        const at::Tensor *q = c.tensor(a[0], Type::BFloat16, 3);
+        if (!q || !q->is_contiguous() || !cache.read(c, a + 1)) return none();
+        const at::Tensor *table = c.tensor(a[5], Type::Int, 2);
+        const std::vector<int32_t> cu = c.integers(a[6]), lens = c.integers(a[7]);
+        const float scale = c.number(a[9]);
+        if (!c.usual || !PyBool_Check(a[8]) || lens.empty() || cu.size() != lens.size() + 1 ||
+            lens.size() > 0x7fffffff || cu.back() != q->size(0) || q->size(2) != 256 || q->size(1) < 1 ||
+            q->size(1) > 65535 || table->size(0) < (int64_t)lens.size() || table->stride(1) != 1 ||
+            table->size(1) * cache.block_size < *std::max_element(lens.begin(), lens.end()))
+            return none();
+        const int64_t table_stride = table->size(0) > 1 ? table->stride(0) : table->size(1);
+        const int B = (int)lens.size(), hq = (int)q->size(1), causal = a[8] == Py_True;
+        at::Tensor out, ws;
+        if (!output(c, a[10], q, &out) || !workspace(c, a[11], q, &ws, [&] {
+                return lib.prefill_q8_size(cu.data(), lens.data(), B, causal, hq, cache.heads, 256, cache.block_size);
+            }))
+            return none();
+        const int rc = lib.prefill_q8(ptr<pa_bf16>(q), cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
+                                      cache.scale_stride, cache.pages, ptr<int32_t>(table), table_stride, cu.data(),
+                                      lens.data(), B, causal, hq, cache.heads, 256, cache.block_size, scale,
+                                      ptr<pa_bf16>(&out), ptr(&ws), ws.nbytes(), c.stream());
+        return rc ? status(rc) : given_or(a[10], std::move(out));
     });
 }
 
@@ -316,6 +375,8 @@ PyObject *load(PyObject *, PyObject *path) {
     find(lib.gather_q8, "pa_gather_cache_q8");
     find(lib.decode_q8_size, "pa_decode_q8_workspace_size");
     find(lib.decode_q8, "pa_decode_q8");
+    find(lib.prefill_q8_size, "pa_prefill_varlen_q8_workspace_size");
+    find(lib.prefill_q8, "pa_prefill_varlen_q8");
     find(lib.mrope, "pa_qk_norm_mrope");
     find(lib.mrope_cache, "pa_qk_norm_mrope_cache");
     if (!all) {
@@ -330,6 +391,7 @@ PyMethodDef methods[] = {{"load", load, METH_O, nullptr},
                          {"write_q8", FAST(write_q8)},
                          {"gather_q8", FAST(gather_q8)},
                          {"decode_q8", FAST(decode_q8)},
+                         {"prefill_q8", FAST(prefill_q8)},
                          {"mrope", FAST(mrope)},
                          {"mrope_cache", FAST(mrope_cache)},
                          {nullptr, nullptr, 0, nullptr}};

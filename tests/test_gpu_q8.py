@@ -780,6 +780,10 @@ def test_short_calls_are_the_others(cuda_lib, monkeypatch):
         out, ws = torch.empty_like(c["q"]), torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
         assert pa.decode_q8(c["q"], *cache, c["bt"], c["lens"], 0.0625, 300, out, ws) is out
         got += [out, pa.decode_q8(c["q"][:1], *cache, c["bt"][:1], c["lens"][:1], 1, np.int64(300))]
+        for how in (dict(), dict(out=torch.empty_like(c["q"]), workspace=ws)):
+            got.append(pa.prefill_varlen_q8(c["q"], *cache, c["bt"], [0, 1, 2], [300, 77], True, 0.0625, **how))
+        got.append(pa.prefill_chunk_q8(c["q"], *cache, c["bt"][0], 200, False, 0.0625))
+        got.append(pa.prefill_varlen_q8(c["q"], *cache, c["bt"], np.array([0, 1, 2]), (300, 77), 1, 0.0625))
         got += pa.qk_norm_mrope(q, k, w, w, cs, pos, axes, 1e-6)
         got += pa.qk_norm_mrope(q, k, w, w, cs, pos, list(axes), np.float32(1e-6), 1, 0)
         bf = torch.zeros(2, 2, 64, 4, 256, dtype=torch.bfloat16, device="cuda")
@@ -800,6 +804,8 @@ def test_short_calls_are_the_others(cuda_lib, monkeypatch):
             pa.reshape_and_cache_q8(k, v, c["cache"][0], c["cache"][0], *c["cache"][2:], slots)
         with pytest.raises(pa.PAError):
             pa.decode_q8(c["q"], *c["cache"], c["bt"], c["lens"], float("inf"), 300)
+        with pytest.raises(pa.PAError):
+            pa.prefill_varlen_q8(c["q"], *c["cache"], c["bt"], [0, 2, 2], [1, 77], True, 0.0625)
     assert pa.device_errors() == 0
 
 

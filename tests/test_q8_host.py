@@ -142,7 +142,7 @@ def test_short_calls_leave_the_unusual_to_python(lib):
     import paged_kv_cache_09_gb300 as pa
     assert pa._bind is not None
     t = torch.zeros(3, 6, 256, dtype=torch.bfloat16)
-    for name, n in (("write_q8", 7), ("gather_q8", 5), ("decode_q8", 11), ("mrope", 10), ("mrope_cache", 14)):
+    for name, n in (("write_q8", 7), ("gather_q8", 5), ("decode_q8", 11), ("prefill_q8", 12), ("mrope", 10), ("mrope_cache", 14)):
         f = getattr(pa._bind, name)
         for args in ([], [None] * n, [t] * n, [t] * (n + 1), [3] * n, ["x"] * n):
             assert f(*args) is None
