@@ -27,6 +27,7 @@ constexpr int kWarps = 8;
 constexpr int kMaxRange = 256;     // tokens of a CTA of the write (its threads at most)
 constexpr int kTableBits = 9, kTable = 1 << kTableBits;  // places for their blocks
 constexpr int kMaxCut = 4;          // CTAs that share a range's heads
+constexpr int kExpandLook = 16384;  // keys whose scales every CTA of the expansion looks at
 constexpr int kScan = 16;          // slots of a thread in flight
 constexpr int kMapBits = 16384;
 
@@ -404,11 +405,23 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
             atomicOr(a.err, kErrPage);
         }
     }
-    // The head's largest scale of V, from all of its sequence's ranges.
+    // The head's largest scale of V: over all of its sequence's blocks, or from their ranges.
     uint32_t top = 0;
-    const int nr = (sq.num_keys - 1) / kExpandRange + 1;
-    for (int i = threadIdx.x; i < nr; i += kWarps * 32)
-        top = max(top, (uint32_t)a.ranges[(int64_t)h * a.num_ranges + sq.range0 + i].y);
+    if (a.num_ranges == 0) {
+        const int in_page = (a.block_size - 1) / kQ8Tokens + 1, full = sq.num_keys / a.block_size;
+        const int blocks = full * in_page + (sq.num_keys - full * a.block_size + kQ8Tokens - 1) / kQ8Tokens;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < blocks; i += kWarps * 32) {
+            const int lp = i / in_page, page = bt[lp];
+            if (page < 0 || page >= a.num_pages) continue;
+            const uint32_t vb = a.v_scales[page * a.scale_stride + (int64_t)(i - lp * in_page) * a.num_kv_heads + h];
+            if (vb != 255) top = max(top, vb);
+        }
+    } else {
+        const int nr = (sq.num_keys - 1) / kExpandRange + 1;
+        for (int i = threadIdx.x; i < nr; i += kWarps * 32)
+            top = max(top, (uint32_t)a.ranges[(int64_t)h * a.num_ranges + sq.range0 + i].y);
+    }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) part[warp] = top;
     __syncthreads();
@@ -448,10 +461,19 @@ cudaError_t launch_gather_q8(const Q8GatherArgs &a, cudaStream_t stream) {
                     : launch_pdl(gather_q8_kernel<1>, grid, dim3(kWarps * 32), 0, stream, a);
 }
 
-cudaError_t launch_expand_q8(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream) {
-    cudaError_t e = launch_pdl(range_q8_kernel, dim3((unsigned)a.num_ranges * a.num_kv_heads), dim3(kWarps * 32),
-                               0, stream, a);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_expand_q8(const ExpandArgs &args, int64_t num_pages_out, cudaStream_t stream) {
+    ExpandArgs a = args;
+    // Every CTA looks at all scales of V of its sequence and head while that takes it a few reads a
+    // thread; longer sequences' are gone through beforehand.
+    int longest = 0;
+    for (int b = 0; b < a.num_seqs; ++b) longest = std::max(longest, a.seq[b].num_keys);
+    if (longest <= kExpandLook) {
+        a.num_ranges = 0;
+    } else {
+        const cudaError_t e = launch_pdl(range_q8_kernel, dim3((unsigned)a.num_ranges * a.num_kv_heads),
+                                         dim3(kWarps * 32), 0, stream, a);
+        if (e != cudaSuccess) return e;
+    }
     return launch_pdl(expand_q8_kernel,
                       dim3((unsigned)(num_pages_out * (kExpandPage / kExpandKeys)), a.num_kv_heads),
                       dim3(kWarps * 32), 0, stream, a);

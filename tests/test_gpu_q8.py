@@ -647,6 +647,7 @@ def _check_prefill(got, c, cu, lens, causal=True, scale=0.0625):
     (1, 0, 16, 4, 1, True), (1, 4000, 832, 24, 4, True), (130, 900, 832, 24, 4, True),
     (128, 0, 64, 6, 1, False), (300, 77, 7, 8, 2, True), (257, 1000, 784, 10, 2, False),
     (40, 3000, 48, 5, 5, True), (2, 255, 1, 3, 1, True), (513, 0, 100, 2, 2, True),
+    (3, 16384, 64, 4, 2, True), (3, 16381, 7, 4, 2, True), (2, 40001, 20, 2, 1, False),
 ])
 def test_prefill_chunk_matches_plain(cuda_lib, q_len, q_start, bs, hq, hkv, causal):
     pa = cuda_lib
