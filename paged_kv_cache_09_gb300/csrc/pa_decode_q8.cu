@@ -33,12 +33,18 @@ constexpr int kSlotBytes = 2 * kTileCodes;            // K, V
 constexpr int kOffQ = kW * kDepth * kSlotBytes, kOffMl = kOffQ + 9 * 512;
 constexpr int kOffBars = kOffMl + kW * kDecMaxGroup * 8, kOffMisc = kOffBars + kW * kDepth * 8;
 constexpr int kSmem = kOffMisc + 32 + 1024;           // (the rings start at a multiple of 1024)
+constexpr int kOffPart = kOffMisc + 32;               // in a cluster, the CTA's part: sums, references
+constexpr int kSmemCluster = kSmem + kSlotBytes + kDecMaxGroup * 8;
+static_assert(kOffPart % 16 == 0, "loads of 16 bytes");
 static_assert(kDecMaxGroup * kHeadDim * 4 == kSlotBytes, "a slot holds a warp's sums");
-static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+static_assert(2 * (kSmemCluster + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(kTile == kQ8Tokens, "a tile has one scale");
 constexpr int kMinShare = kW;                         // tiles of the smallest share
 constexpr int kPairCost = 12;                         // of beginning a pair, in tiles
 constexpr int kBatches = 4;                           // of 32 sequences, whose lengths a warp keeps
+constexpr int kMaxCluster = 8;                        // CTAs of a cluster
+constexpr int kClusterSteps = 3;                      // tiles a warp at most, in a cluster: of one sequence
+constexpr int kClusterStepsMany = 8;                  // and of several
 constexpr int kEarlyTiles = 1;                        // of a warp, brought into L2 before the wait
 constexpr float kLag = 8.f;  // log2 units: a score may pass the reference by it
 constexpr float kTop = 6.f;  // log2 of the weight at the reference M'
@@ -46,6 +52,7 @@ constexpr float kTop = 6.f;  // log2 of the weight at the reference M'
 struct Params : SplitParams {
     const uint8_t *k_scales, *v_scales;
     int64_t scale_stride;
+    int cluster;  // CTAs of a pair (kCluster)
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -59,12 +66,34 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// All threads of the cluster's CTAs meet; what they wrote to shared memory is seen by the others.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// From the shared memory of CTA `rank` of the cluster, at this CTA's address `addr`.
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr, int rank) {
+    float2 v;
+    asm volatile("{.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];}"
+                 : "=f"(v.x), "=f"(v.y) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, int rank) {
+    float4 v;
+    asm volatile("{.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
 #ifdef PA_TEST_HOOKS
 // Test build only: the tile (counted over each warp's run) whose loads are left out (-1: none),
 // so that the warp's wait runs out.
 __device__ int g_test_skip_tile = -1;
 #endif
 
+// kCluster: short sequences.  A cluster of p.cluster CTAs takes a pair and cuts its tiles evenly; its
+// parts are merged through the CTAs' shared memory, and no second kernel follows.
+template <bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_q8_stream_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                             const __grid_constant__ Params p) {
@@ -221,17 +250,37 @@ __global__ void __launch_bounds__(kThreads, 2)
     // still write, and holds if they are the same after it; if not, and with more sequences than a warp
     // keeps, it is found again.  Meanwhile the first tiles come into L2 (their table entries only
     // steer that).  What is read before the wait bypasses L1.
-    auto find = [&](const Lengths<kBatches> &lens, bool report) {
-        return find_start<kMinShare, kPairCost, true, true, kBatches>(p, lane, report, lens, st);
+    constexpr int kB = kCluster ? 1 : kBatches;
+    const int pair_of_cluster = blockIdx.x / p.cluster, rank = blockIdx.x - pair_of_cluster * p.cluster;
+    auto find = [&](const Lengths<kB> &lens, bool report) {
+        if constexpr (!kCluster) {
+            return find_start<kMinShare, kPairCost, true, true, kB>(p, lane, report, lens, st);
+        } else {  // (every CTA takes part in its cluster's merge)
+            st.ctas_a_pair = p.cluster;
+            st.lead = 0;
+            st.seq = pair_of_cluster / p.num_kv_heads;
+            st.g = pair_of_cluster - st.seq * p.num_kv_heads;
+            st.tiles = lens.tiles[0];
+            st.seq_len = lens.len[0];
+            st.shares.q = st.tiles / p.cluster;
+            st.shares.r = st.tiles - st.shares.q * p.cluster;
+            st.at = st.v0 = (int)st.shares.begin(rank);
+            st.end = st.shares.begin(rank + 1);
+            return Found::kShare;
+        }
     };
     auto lengths = [&](bool report) {
-        Lengths<kBatches> l;
+        Lengths<kB> l;
 #pragma unroll
-        for (int b = 0; b < kBatches; ++b) l.tiles[b] = seq_tiles<true>(p, 32 * b + lane, &l.len[b], report);
+        for (int b = 0; b < kB; ++b) {
+            const int s = kCluster ? pair_of_cluster / p.num_kv_heads : 32 * b + lane;
+            l.tiles[b] = seq_tiles<true>(p, s, &l.len[b], report);
+        }
         return l;
     };
-    const bool early = p.num_seqs <= 32 * kBatches;
-    Lengths<kBatches> lens;
+    const bool reports = (kCluster ? rank == 0 && pair_of_cluster % p.num_kv_heads == 0 : blockIdx.x == 0) && warp == 0;
+    const bool early = kCluster || p.num_seqs <= 32 * kB;
+    Lengths<kB> lens;
     Found found = Found::kNone;
     if (early) {
         lens = lengths(false);
@@ -256,16 +305,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     pdl_wait();
     pdl_trigger();
-    const Lengths<kBatches> now = lengths(blockIdx.x == 0 && warp == 0);
+    const Lengths<kB> now = lengths(reports);
     if (found == Found::kShare) {
         load_q();
         load_pair(t0);  // (the table entry)
     }
     bool changed = !early;
 #pragma unroll
-    for (int b = 0; b < kBatches; ++b) changed |= early && now.len[b] != lens.len[b];
+    for (int b = 0; b < kB; ++b) changed |= early && now.len[b] != lens.len[b];
     if (__any_sync(0xffffffffu, changed)) {
-        found = find(now, blockIdx.x == 0 && warp == 0);
+        found = find(now, reports);
         if (found == Found::kShare) {
             begin_segment();
             load_start();
@@ -417,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---- the next segment's q, before this one's merge
         const int64_t pair = (int64_t)st.seq * p.num_kv_heads + st.g, part = blockIdx.x + pair;
         const bool whole = t0 == 0 && t1 == st.tiles;
-        if (threadIdx.x == 0 && t0 == 0) {
+        if (!kCluster && threadIdx.x == 0 && t0 == 0) {
             int parts = st.ctas_a_pair;
             if (parts == 0) parts = (int)(st.shares.owner(st.at - st.v0 + st.lead + st.tiles - 1) - blockIdx.x) + 1;
             p.info[pair] = make_int2((int)part, whole ? 0 : parts);
         }
         uint16_t *out_rows = p.out + ((int64_t)st.seq * p.num_q_heads + st.g * p.group) * kHeadDim;
         st.at += st.lead + t1 - st.v0;
-        const bool more = st.end > st.at + st.lead;  // (a share that ends before the next pair's first tile is done)
+        const bool more = !kCluster && st.end > st.at + st.lead;  // (a share that ends before the next pair's first tile is done)
         const uint32_t spare = (it + kDepth - 1) % kDepth;  // the slot of the last tile: the others hold the next ones
         if (more) {
             st.v0 = 0;
@@ -487,7 +536,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 M = -CUDART_INF_F;
                 L = 0.f;
             }
-            if (whole) {
+            if constexpr (kCluster) {
+                reinterpret_cast<float4 *>(smem + kOffPart)[qd] = O;
+                if (d == 0) reinterpret_cast<float2 *>(smem + kOffPart + kSlotBytes)[h] = make_float2(M, L);
+            } else if (whole) {
                 const float inv = L > 0.f ? 1.f / L : 0.f;
                 *reinterpret_cast<uint2 *>(out_rows + h * kHeadDim + d) =
                     make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
@@ -497,6 +549,43 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
 
+        if constexpr (kCluster) {
+            cluster_sync();  // every CTA's part is there
+            const int units = p.group * (kHeadDim / 4);
+            for (int u = threadIdx.x * p.cluster + rank; u < units; u += kThreads * p.cluster) {
+                const int h = u / (kHeadDim / 4);
+                const uint32_t at_o = smem_u32(smem + kOffPart) + u * 16, at_ml = smem_u32(smem + kOffPart + kSlotBytes) + h * 8;
+                float4 f[kMaxCluster];
+                float2 ml[kMaxCluster];
+#pragma unroll
+                for (int v = 0; v < kMaxCluster; ++v) {
+                    ml[v] = make_float2(-CUDART_INF_F, 0.f);
+                    f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (v < p.cluster) {
+                        ml[v] = ld_cluster_f2(at_ml, v);
+                        f[v] = ld_cluster_f4(at_o, v);
+                    }
+                }
+                float M = -CUDART_INF_F, L = 0.f;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int v = 0; v < kMaxCluster; ++v) M = fmaxf(M, ml[v].x);
+#pragma unroll
+                for (int v = 0; v < kMaxCluster; ++v) {
+                    const float e = ml[v].x == -CUDART_INF_F ? 0.f : ex2_approx(ml[v].x - M);
+                    L = fmaf(e, ml[v].y, L);
+                    O.x = fmaf(e, f[v].x, O.x);
+                    O.y = fmaf(e, f[v].y, O.y);
+                    O.z = fmaf(e, f[v].z, O.z);
+                    O.w = fmaf(e, f[v].w, O.w);
+                }
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                *reinterpret_cast<uint2 *>(out_rows + u * 4) =
+                    make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+            }
+            cluster_sync();  // every part has been read
+            break;
+        }
         if (!more) break;
         __syncthreads();  // q is ready, and the merge's rows are free
     }
@@ -518,20 +607,54 @@ cudaError_t set_decode_q8_test_hook(int skip_tile) {
 }
 #endif
 
+// CTAs of a pair's cluster, if the longest allowed sequence is short enough for that; else 0.
+static int cluster_of(const SplitParams &p, const DecodeQ8Args &a) {
+    const int64_t tiles = (int64_t)(a.max_seq_len / a.block_size) * p.tiles_per_page +
+                          (a.max_seq_len % a.block_size + kTile - 1) / kTile;
+    const int64_t pairs = (int64_t)a.num_seqs * a.num_kv_heads;
+    const int steps = a.num_seqs == 1 ? kClusterSteps : kClusterStepsMany;
+    int n = 1;
+    while (n < kMaxCluster && tiles > n * kW && pairs * (2 * n) <= 2 * a.num_sms) n *= 2;
+    return pairs * n <= 2 * a.num_sms && tiles <= (int64_t)n * kW * steps ? n : 0;
+}
+
 cudaError_t launch_decode_q8(const CUtensorMap *tmaps, const DecodeQ8Args &a, cudaStream_t stream) {
-    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_q8_stream_kernel), kSmem, 9);
-    if (e != cudaSuccess) return e;
     Params p;
     fill_split(p, a);
     p.k_scales = a.k_scales;
     p.v_scales = a.v_scales;
     p.scale_stride = a.scale_stride;
+    p.cluster = cluster_of(p, a);
+    const void *kernel = reinterpret_cast<const void *>(
+        p.cluster ? decode_q8_stream_kernel<true> : decode_q8_stream_kernel<false>);
+    cudaError_t e = set_smem_once(kernel, p.cluster ? kSmemCluster : kSmem, p.cluster ? 12 : 9);
+    if (e != cudaSuccess) return e;
     if (a.ev_start && (e = record_event(a.ev_start, stream)) != cudaSuccess) return e;
-    e = launch_pdl(decode_q8_stream_kernel, dim3(split_grid<kMinShare, true>(p, a)), dim3(kThreads), kSmem, stream,
-                   tmaps[0], tmaps[1], p);
+    if (p.cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(a.num_seqs * a.num_kv_heads * p.cluster));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemCluster;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = p.cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, decode_q8_stream_kernel<true>, tmaps[0], tmaps[1], p);
+    } else {
+        p.cluster = 1;
+        e = launch_pdl(decode_q8_stream_kernel<false>, dim3(split_grid<kMinShare, true>(p, a)), dim3(kThreads), kSmem,
+                       stream, tmaps[0], tmaps[1], p);
+    }
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
-    return launch_merge<10>(p, a.num_sms, stream);
+    return kernel == reinterpret_cast<const void *>(decode_q8_stream_kernel<true>)
+               ? cudaSuccess
+               : launch_merge<10>(p, a.num_sms, stream);
 }
 
 }  // namespace pa

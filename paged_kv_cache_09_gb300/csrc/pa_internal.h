@@ -17,8 +17,8 @@ uintptr_t current_context();
 // Raises a kernel's dynamic shared-memory limit once per (kernel slot, device context),
 // so that later launches (possibly under stream capture) make no attribute call.  Slots:
 // 0 and 3 the two decode kernel shapes, 1, 2, 4, 5 the four prefill kernel variants with
-// BF16 operands, 7, 8, 10, 11 those with FP16 operands, 6 the 4-bit decode, 9 the 8-bit one.
-constexpr int kSmemSlots = 12;
+// BF16 operands, 7, 8, 10, 11 those with FP16 operands, 6 the 4-bit decode, 9 and 12 the 8-bit one.
+constexpr int kSmemSlots = 13;
 cudaError_t set_smem_once(const void *kernel, int bytes, int slot);
 
 // Launches a kernel with programmatic dependent launch allowed: it may start while the

@@ -281,6 +281,26 @@ def test_decode_long_shares(cuda_lib, bs, hq, hkv, lens):
     assert cuda_lib.device_errors() == 0
 
 
+# Clusters of 1 to 16 CTAs, parts without a tile, empty sequences beside others, lengths at the ends of
+# tiles and pages and of what a cluster takes.
+@pytest.mark.parametrize("bs,hq,hkv,lens", [
+    (16, 8, 1, [1]), (16, 8, 1, [64]), (16, 6, 1, [65]), (64, 8, 2, [128, 0, 1]), (832, 24, 4, [1024]),
+    (832, 24, 4, [1025, 3]), (64, 24, 4, [3072]), (64, 24, 4, [3073]), (7, 7, 1, [130, 7, 0, 8, 64]),
+    (100, 3, 3, [257, 256, 255]), (16, 64, 8, [500, 499]), (48, 12, 4, [0, 700]),
+    (64, 16, 4, [(i * 37) % 130 for i in range(19)]), (16, 300, 300, [5]), (1, 2, 2, [33, 17]),
+])
+def test_decode_short_sequences(cuda_lib, bs, hq, hkv, lens):
+    pa = cuda_lib
+    c = _case(pa, lens, bs, hq, hkv, seed=bs + len(lens))
+    out = _decode(pa, c)
+    _check_decode(out, c)
+    assert torch.equal(out, _decode(pa, c))
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert not out[s].any()
+    assert pa.device_errors() == 0
+
+
 # One sequence, whose pairs are cut by themselves: from a tile to one part a CTA of the GPU, and more
 # KV heads than fit; and more sequences than a warp keeps the lengths of.
 @pytest.mark.parametrize("bs,hq,hkv,lens", [
