@@ -15,8 +15,23 @@
 // weight is 2^(kTop + kLag) at most, and those down to 2^(-14 - kTop) = 2^-20 of the largest keep
 // all of FP16's bits, whatever the scales of tokens without weight are.
 //
-// Bytes: 512 and 2 of scales for a 16-token tile's token and KV head; at the copy bandwidth an SM
-// has to take a tile (8 KB) about every 185 ns (370 cycles).
+// Bytes: 8192 of codes and 2 of scales for a tile of K and V; at the copy bandwidth an SM has to take a
+// tile about every 185 ns (370 cycles).  A warp's tile takes some 550 instructions (128 of them widen
+// codes, two each; q's and the tile's fragments, 32 MMAs), so issue slots are 36% used and memory
+// bounds long batches; short ones are bound by the chain of latencies.
+//
+// Long sequences: the tiles are cut evenly over two CTAs an SM (pa_decode_split.cuh).  Within a CTA each
+// warp streams every kW-th tile through a ring of its own, a box of K and one of V a tile: two
+// tiles ahead of the one it works on, so that 128 KB an SM are on their way.  A warp's loads do not stop
+// at the end of a pair but go on into the next ones of the share.  Nothing is exchanged between
+// warps before the CTA's merge, whose rows stand in the ring's slots that are free then.
+// One sequence: each pair is cut by itself, so that no CTA begins two (1701 keys 9.7 -> 7.7 us).
+// Short sequences: a cluster a pair, whose CTAs' parts are merged through their shared memory; no
+// second kernel.  (A CTA waits at the cluster's barriers for the others, whose own waits are bounded.)
+//
+// Measured, calls one after another in a graph, 4 KV heads of 6 query heads unless said: 16 sequences of
+// 4096..32768 keys 102 us, 6.7 TB/s; 64 of 1..2048, 8 KV heads of 4, pages of 16: 47.3 us (5.1 TB/s: begin, end and
+// the slowest CTAs); one of 32768 keys 17.3 us, of 1701 7.3; 16 of 1..700 8.7 us, of 1..300 7.3.
 #include "pa_decode_split.cuh"
 #include "pa_q8.cuh"
 
@@ -39,13 +54,20 @@ static_assert(kOffPart % 16 == 0, "loads of 16 bytes");
 static_assert(kDecMaxGroup * kHeadDim * 4 == kSlotBytes, "a slot holds a warp's sums");
 static_assert(2 * (kSmemCluster + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(kTile == kQ8Tokens, "a tile has one scale");
-constexpr int kMinShare = kW;                         // tiles of the smallest share
-constexpr int kPairCost = 12;                         // of beginning a pair, in tiles
-constexpr int kBatches = 4;                           // of 32 sequences, whose lengths a warp keeps
-constexpr int kMaxCluster = 8;                        // CTAs of a cluster
-constexpr int kClusterSteps = 3;                      // tiles a warp at most, in a cluster: of one sequence
-constexpr int kClusterStepsMany = 8;                  // and of several
-constexpr int kEarlyTiles = 1;                        // of a warp, brought into L2 before the wait
+// Tiles of the smallest share.  One sequence of 1701 keys with 4, 8 and 16: 7.1, 7.7 and 9.4 us.
+constexpr int kMinShare = kW;
+// Of beginning a pair, in tiles.  64 sequences of 1..2048 keys (8 KV heads) with 2, 4, 8, 12 and 20: 65,
+// 59, 51, 49 and 50 us; 200 of 1..1024: 109, 99, 89, 83 and 85; 32 of 1..4096 (4): 37, 35, 31, 31 and 31.
+constexpr int kPairCost = 12;
+// Of 32 sequences, whose lengths a warp keeps.  64 sequences with 1 and 4: 49.2 and 47.0 us; one
+// sequence 0.1 us more.
+constexpr int kBatches = 4;
+// CTAs of a cluster, and the tiles that it may take a warp, of one sequence and of several.  Without and with
+// a cluster: one sequence of 200 keys 6.4 and 5.5 us, of 900 6.9 and 6.8, of 1701 7.3 and 8.8; 16 of
+// 1..700 16.5 and 8.7, 16 of 1500 16.0 and 13.1; 64 of 300 15.9 and 12.0; beyond 8 tiles even lengths still
+// gain (16 of 3000 23.0 and 20.1) and uneven ones lose (16 of 1..3000 15.9 and 17.5).  Clusters of 16 start
+// later: 4 sequences of 1000 keys 14.4 us, in clusters of 8 7.9, without 11.3.
+constexpr int kMaxCluster = 8, kClusterSteps = 3, kClusterStepsMany = 8;
 constexpr float kLag = 8.f;  // log2 units: a score may pass the reference by it
 constexpr float kTop = 6.f;  // log2 of the weight at the reference M'
 
@@ -248,8 +270,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // The share is found before the wait for earlier work on the stream, from lengths that this work may
     // still write, and holds if they are the same after it; if not, and with more sequences than a warp
-    // keeps, it is found again.  Meanwhile the first tiles come into L2 (their table entries only
-    // steer that).  What is read before the wait bypasses L1.
+    // keeps, it is found again.  Meanwhile each warp's first tile comes into L2 (its table entry only
+    // steers that).  What is read before the wait bypasses L1.  No tile, one, two and four: one
+    // sequence of 32768 keys 18.6, 17.5, 17.5 and 18.5 us, 16 of 4096..32768 104.1, 101.3, 102.0 and 102.7.
     constexpr int kB = kCluster ? 1 : kBatches;
     const int pair_of_cluster = blockIdx.x / p.cluster, rank = blockIdx.x - pair_of_cluster * p.cluster;
     auto find = [&](const Lengths<kB> &lens, bool report) {
@@ -289,18 +312,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (found == Found::kShare) {
         begin_segment();
         load_start();
-        if (lane == 0) {
-            const uint64_t policy = l2_evict_first_policy();
-            int lp = in.lp, tip = in.tip, page = in.page;
-            for (int j = in.j; j < min(in.t1, in.j + kEarlyTiles * kW); j += kW) {
-                if (page >= 0 && page < p.num_pages) {
-                    tma_prefetch_l2_5d_hint(&k_map, 0, tip * kTile, 0, in.g, page, policy);
-                    tma_prefetch_l2_5d_hint(&v_map, 0, tip * kTile, 0, in.g, page, policy);
-                }
-                const int was = lp;
-                for (tip += kW; tip >= tpp; tip -= tpp) ++lp;
-                if (lp != was && j + kW < in.t1) page = __ldcg(p.block_table + (int64_t)in.seq * p.bt_stride + lp);
-            }
+        if (lane == 0 && in.j < in.t1 && in.page >= 0 && in.page < p.num_pages) {
+            tma_prefetch_l2_5d_hint(&k_map, 0, in.tip * kTile, 0, in.g, in.page, l2_evict_first_policy());
+            tma_prefetch_l2_5d_hint(&v_map, 0, in.tip * kTile, 0, in.g, in.page, l2_evict_first_policy());
         }
     }
     pdl_wait();

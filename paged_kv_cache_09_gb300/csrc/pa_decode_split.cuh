@@ -71,7 +71,7 @@ __device__ __forceinline__ int seq_tiles(const SplitParams &p, int s, int *len, 
     return tiles_of(p, L);
 }
 
-constexpr uint32_t kMaxTiles = 0x7fffffffu;  // of all pairs, with their leads (9.9 TB, shared pages counted again)
+constexpr uint32_t kMaxTiles = 0x7fffffffu;  // of all pairs, with their leads
 
 // Places ahead of each of `pairs` pairs' tiles, when `tiles` (at most kMaxTiles) are cut over `ctas`
 // shares: half a share at most, and none where they would not be numbered in 31 bits.
@@ -110,8 +110,9 @@ struct Lengths {
     int tiles[kBatches], len[kBatches];
 };
 
-// Finds this CTA's share, with the first sequences' lengths given (every warp finds the same).  kAlone: with one sequence, each of its pairs is cut by itself, so that no CTA
-// works on two (their beginnings would follow one another).  kEarly: as for seq_tiles.
+// Finds this CTA's share, with the first sequences' lengths given (every warp finds the same).
+// kAlone: with one sequence, each of its pairs is cut by itself, so that no CTA works on two (their
+// beginnings would follow one another).  kEarly: as for seq_tiles.
 template <int kMinShare, int kPairCost, bool kAlone = false, bool kEarly = false, int kBatches = 1>
 __device__ __forceinline__ Found find_start(const SplitParams &p, int lane, bool report,
                                             const Lengths<kBatches> &first, Start &st) {
