@@ -285,7 +285,7 @@ def test_decode_long_shares(cuda_lib, bs, hq, hkv, lens):
 # tiles and pages and of what a cluster takes.
 @pytest.mark.parametrize("bs,hq,hkv,lens", [
     (16, 8, 1, [1]), (16, 8, 1, [64]), (16, 6, 1, [65]), (64, 8, 2, [128, 0, 1]), (832, 24, 4, [1024]),
-    (832, 24, 4, [1025, 3]), (64, 24, 4, [3072]), (64, 24, 4, [3073]), (7, 7, 1, [130, 7, 0, 8, 64]),
+    (832, 24, 4, [1025, 3]), (64, 24, 4, [1536]), (64, 24, 4, [1537]), (7, 7, 1, [130, 7, 0, 8, 64]),
     (100, 3, 3, [257, 256, 255]), (16, 64, 8, [500, 499]), (48, 12, 4, [0, 700]),
     (64, 16, 4, [(i * 37) % 130 for i in range(19)]), (16, 300, 300, [5]), (1, 2, 2, [33, 17]),
 ])
