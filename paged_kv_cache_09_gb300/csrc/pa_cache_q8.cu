@@ -189,10 +189,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) write_q8_kernel(const __grid_c
         }
     }
     __syncthreads();
-    const int jobs = count * kinds;
+    // (The CTAs of a range each have kinds of their own: their lists are in orders of their own.)
+    const int per = (kinds - 1) / (int)gridDim.y + 1, kind0 = blockIdx.y * per;
+    const int mine = min(per, kinds - kind0), jobs = mine > 0 ? count * mine : 0;
     const int64_t row_stride = (int64_t)a.num_kv_heads * kHeadDim;
-    for (int job = blockIdx.y * kWarps + warp; job < jobs; job += gridDim.y * kWarps) {
-        const int e = job / kinds, kind = job - e * kinds, at = list[e];
+    for (int job = warp; job < jobs; job += kWarps) {
+        const int e = job / mine, kind = kind0 + job - e * mine, at = list[e];
         if (lowest[at] < t0) continue;  // another CTA's
         const int h = kind >> 1;
         const bool is_v = kind & 1;

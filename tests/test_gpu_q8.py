@@ -86,7 +86,9 @@ def test_write_matches_plain_bits(cuda_lib, kind, bs, hkv, T):
     assert pa.device_errors() == 0
 
 
-@pytest.mark.parametrize("T,hkv,bs", [(1500, 2, 16), (2500, 1, 64), (5000, 2, 7), (700, 9, 48)])
+# (Heads that do not divide among the CTAs of a range; ranges of more than a warp's tokens.)
+@pytest.mark.parametrize("T,hkv,bs", [(1500, 2, 16), (2500, 1, 64), (5000, 2, 7), (700, 9, 48), (20000, 5, 16),
+                                      (12000, 7, 20)])
 @pytest.mark.parametrize("order", ["straight", "shuffled"])
 def test_write_many_tokens_in_any_order(cuda_lib, T, hkv, bs, order):
     pa = cuda_lib
