@@ -419,7 +419,8 @@ int pa_qk_norm_rope(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k, int64_
  * the caches, as pa_reshape_and_cache (cache_format PA_CACHE_BF16) or
  * pa_reshape_and_cache_q4 (PA_CACHE_Q4; head_dim 256) would write them.  page_stride is in
  * elements for a BF16 cache, in bytes for a 4-bit one.  Slots as in those calls; a token
- * whose position is padding or out of range writes nothing.
+ * whose position is padding or out of range writes nothing.  (The 8-bit cache's write is a call of its
+ * own: the tokens of a block share a scale.)
  */
 enum pa_cache_format { PA_CACHE_BF16 = 0, PA_CACHE_Q4 = 1 };
 
@@ -700,10 +701,10 @@ int pa_get_device_errors(unsigned int *bits, int clear, void *stream);
 
 /*
  * pa_set_kernel_events -- measurement hook.  The next pa_decode, pa_decode_append,
- * pa_prefill_chunk or pa_prefill_varlen call, or 4-bit decode or prefill call, made by this
+ * pa_prefill_chunk or pa_prefill_varlen call, or 4-bit or 8-bit decode or prefill call, made by this
  * host thread records `start` on its stream immediately before it launches its main kernel
  * (the split-context or streaming decode kernel, or the prefill kernel) and `stop` immediately
- * after that launch, then forgets both.  A 4-bit prefill's expansion, two kernels before the
+ * after that launch, then forgets both.  A 4-bit or 8-bit prefill's expansion, the kernels before the
  * main one, is not between them (that of later batches is, when a call has more than 32
  * chunks).  Inside a stream capture the records carry cudaEventRecordExternal, so they
  * become event record nodes that every replay of the graph records.  The arguments are
