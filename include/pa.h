@@ -597,7 +597,9 @@ int pa_prefill_varlen_q4(const pa_bf16 *q, const void *k_cache, const void *v_ca
  * Tokens may stand in the call in any order; of several with one slot the last one counts and the
  * others are ignored.  A negative slot is skipped; one outside the pool is skipped and sets
  * PA_DEVERR_SLOT.  The caches, the scales and the new rows must not overlap one another (one array as
- * both K's and V's is refused: PA_ERR_INVALID_ARG).
+ * both K's and V's is refused: PA_ERR_INVALID_ARG).  A call may rewrite a block's scale and older codes,
+ * so calls that write to or read from the same block are ordered, e.g. on one stream, even where
+ * their slots differ.
  */
 int pa_reshape_and_cache_q8(const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value,
                             int64_t value_stride, void *k_cache, void *v_cache, uint8_t *k_scales,

@@ -1042,10 +1042,10 @@ int pa_decode_q4(const pa_bf16 *q, const void *k_cache, const void *v_cache, int
 }
 
 // Workspace of the 4-bit and the 8-bit prefill: the batch's K, then its V, as pages of 16-bit
-// values, the queries as FP16 (4-bit: with_q), the factors that undo their scaling, the heads' ranges, the pages' block tables, and
-// the room for split items; each part 256-byte aligned.  Batches are of kPfMaxSeqs chunks,
-// one after another in the same workspace (the queries of all of them are converted with the
-// first).
+// values, the queries as FP16 (4-bit: with_q), the factors that undo their scaling, the heads'
+// ranges, the pages' block tables, and the room for split items; each part 256-byte aligned.
+// Batches are of kPfMaxSeqs chunks, one after another in the same workspace (the queries of all
+// of them are converted with the first).
 struct ExpandLayout {
     int64_t pages = 0;      // output pages of the batch
     int table_stride = 0;   // pages of its longest sequence

@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto begin_segment = [&]() {
         t0 = max(0, st.v0 - st.lead);
         t1 = (int)min((uint32_t)st.tiles, st.v0 + (st.end - st.at) - st.lead);
-        n = !*abort && t0 + warp < t1 ? (t1 - t0 - warp + kW - 1) / kW : 0;
+        const bool stop = __any_sync(0xffffffffu, *abort != 0);  // (n is the warp's: its lanes wait together)
+        n = !stop && t0 + warp < t1 ? (t1 - t0 - warp + kW - 1) / kW : 0;
     };
     // The next segment of the share, KV head after KV head, sequence after sequence.
     auto next_pair = [&](int &seq, int &g, int &seq_len, int &tiles) {
