@@ -662,14 +662,15 @@ cudaError_t launch_decode_q8(const CUtensorMap *tmaps, const DecodeQ8Args &a, cu
         e = cudaLaunchKernelEx(&cfg, decode_q8_stream_kernel<true>, tmaps[0], tmaps[1], p);
     } else {
         p.cluster = 1;
-        e = launch_pdl(decode_q8_stream_kernel<false>, dim3(split_grid<kMinShare, true>(p, a)), dim3(kThreads), kSmem,
-                       stream, tmaps[0], tmaps[1], p);
+        p.ctas = split_grid<kMinShare, true>(p, a);
+        e = launch_pdl(decode_q8_stream_kernel<false>, dim3(p.ctas), dim3(kThreads), kSmem, stream, tmaps[0],
+                       tmaps[1], p);
     }
     if (e != cudaSuccess) return e;
     if (a.ev_stop && (e = record_event(a.ev_stop, stream)) != cudaSuccess) return e;
     return kernel == reinterpret_cast<const void *>(decode_q8_stream_kernel<true>)
                ? cudaSuccess
-               : launch_merge<10>(p, a.num_sms, stream);
+               : launch_merge<10, kMinShare>(p, a.num_sms, stream);
 }
 
 }  // namespace pa

@@ -41,6 +41,7 @@ struct SplitParams {
     int64_t bt_stride;
     const int32_t *seq_lens;
     int num_seqs, max_seq_len, num_q_heads, num_kv_heads, group, block_size, tiles_per_page;
+    int ctas;  // of the streaming kernel (for a merge with kShare)
     FastDiv by_block, by_tpp;
     float scale_log2;
     // Part i: fp32 sums [group, 256] and (reference, sum of weights) [group].  CTA b's part of
@@ -237,7 +238,9 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 //     1200 24.2 22.9 25.0   1536 27.1 23.6 26.0
 // so between 2 and 8 rows an SM 4 loses up to 9% to 1 where lengths are alike, and gains as much
 // where one is long.
-template <int kSplit, int kRound>
+// kShare: one sequence whose pairs were cut alone (find_start, kMinShare); the parts follow from its
+// length, which stands before the streaming kernel ends: no look at p.info after the wait.
+template <int kSplit, int kRound, int kShare = 0>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const __grid_constant__ SplitParams p) {
     constexpr bool kFew = kSplit > 1;
     constexpr int kWarps = kSplit;
@@ -247,12 +250,22 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const __grid_constant
     const int warp = kFew ? all % kWarps : all, block = kFew ? all / kWarps : 0;
     const int64_t row = kFew ? blockIdx.x / (4 / kBlocks) : (int64_t)blockIdx.x * 4 + (warp >> 1);
     const int d0 = kFew ? (blockIdx.x % (4 / kBlocks) * kBlocks + block) * 64 : (warp & 1) * 128;
+    int2 info;
+    int len;
+    if constexpr (kShare > 0) {
+        const int pair = (int)row / p.group, tiles = seq_tiles<true>(p, 0, &len, false);
+        const int n = min(p.ctas / p.num_kv_heads, (tiles + kShare - 1) / kShare);
+        const bool cut = n > 1 && (uint64_t)tiles * p.num_kv_heads <= kMaxTiles;
+        info = make_int2(pair * (n + 1), cut ? n : 0);
+    }
     pdl_wait();
     pdl_trigger();
     if (row >= (int64_t)p.num_seqs * p.num_q_heads) return;  // (warp-uniform; kFew: never)
     const int seq = (int)(row / p.num_q_heads), h = (int)(row - (int64_t)seq * p.num_q_heads);
-    const int len = p.seq_lens[seq];
-    const int2 info = p.info[(int64_t)seq * p.num_kv_heads + h / p.group];
+    if constexpr (kShare == 0) {
+        len = p.seq_lens[seq];
+        info = p.info[(int64_t)seq * p.num_kv_heads + h / p.group];
+    }
     uint16_t *out = p.out + row * kHeadDim + d0;
     if (len <= 0) {
         if (kFew ? warp == 0 : true)
@@ -371,6 +384,7 @@ void fill_split(SplitParams &p, const Args &a) {
     p.parts = l.parts;
     p.out = a.out;
     p.err = a.err;
+    p.ctas = 0;
 }
 
 // CTAs of the streaming kernel: no more than the longest allowed lengths would use.
@@ -384,9 +398,13 @@ int split_grid(const SplitParams &p, const Args &a) {
     return (int)(grid < most ? grid : most);
 }
 
-template <int kFewRound>
+template <int kFewRound, int kShare = 0>
 cudaError_t launch_merge(const SplitParams &p, int num_sms, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.num_seqs * p.num_q_heads;
+    if constexpr (kShare > 0)
+        if (p.num_seqs == 1 && rows <= num_sms && p.ctas >= p.num_kv_heads)
+            return launch_pdl(decode_merge_kernel<8, kFewRound, kShare>, dim3((unsigned)(rows * 4)), dim3(256), 0,
+                              stream, p);
     if (rows <= num_sms)
         return launch_pdl(decode_merge_kernel<8, kFewRound>, dim3((unsigned)(rows * 4)), dim3(256), 0, stream, p);
     if (rows <= 8 * num_sms)
