@@ -15,12 +15,11 @@
 // per token and kind of row,
 //     out_j = inv (x_j A_j + x_p B_j),   A_j = w_j cos, B_j = +- w_p sin   (p: j's partner),
 // the partners are exchanged as packed BF16, before any arithmetic, and the arithmetic is on pairs.
-// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 28.7 us, 4.8 TB/s (43 with the
-// weights applied to every row, 29.6 with the rows summed one by one); into a 4-bit cache 33.6 us,
-// without a cache 26.3.  32 + 8 + 8 heads 45.9 us, 16 + 4 + 4 24.8, 12 + 2 + 2 20.5 (4.5, 4.2 and
-// 3.5 TB/s: warps with fewer rows of a token on their way).  16 warps an SM with 8 rows each on
-// their way move more than 20 or 24 with fewer (33 and 40 us): a row on its way is registers.
-// 16 tokens: 2.3 us.
+// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 25.5 us, 5.3 TB/s (43 with the
+// weights applied to every row, 0.9 more with the rows summed one by one, 28.1 with a warp's next rows
+// in registers instead of shared memory, which are on their way for a shorter time); into a 4-bit
+// cache 32.0 us, without a cache 23.5.  32 + 8 + 8 heads 39.2 us, 12 + 2 + 2 17.4 (5.1 and 3.9 TB/s); 64
+// + 8 + 8 of 128 36.2 (4.6 TB/s).  16 tokens: 2.2 us.
 //
 // Positions on several axes (time, height, width of a token): frequency i takes its angle from the
 // position on the axis that the caller gives it.  Only the fetch of the angles differs: four
@@ -36,7 +35,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBatch = 6;  // query rows of a warp that are loaded a token ahead (24 heads over 4 warps)
+constexpr int kBatch = 6;  // query rows of a warp that are copied a token ahead (24 heads over 4 warps)
 
 // Pairs of fp32 in one register pair.
 typedef unsigned long long f32x2;
@@ -84,13 +83,15 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     const int R = a.rotary_dim, half = R / 2;
     const bool turns = 8 * l < R, second = 8 * l >= half;  // (second: of a pair of halves)
     const int partner = turns && !kNeighbours ? (second ? l - R / 16 : l + R / 16) : l;
-    // A CTA takes every gridDim.x-th token, and loads ahead: a token's first rows of each kind into
-    // registers and its angles (this lane's or, with axes, this warp's, into shared memory) while the
-    // token before is worked on, its position a token earlier still.  (A padding token's rows are read
-    // for nothing.)
+    // A CTA takes every gridDim.x-th token, and copies ahead into shared memory: a token's first rows of
+    // each kind (a lane its own 16 bytes, which no other reads) and its angles (this lane's or, with
+    // axes, this warp's) while the token before is worked on, its position a token earlier still.  (A
+    // padding token's rows are read for nothing.)
     constexpr int kN = kNeighbours ? 1 : 2;  // fours of frequencies of a lane
     __shared__ float4 angles[kWarps][2][kAxes ? kD / 4 : 2 * kN * 32];
-    uint4 raw[kBatch], raw_k, raw_v;  // each is loaded again as soon as its row is done
+    constexpr int kK = kBatch, kV = kBatch + (kCache ? 1 : 0);  // places of the first key and value row
+    __shared__ uint4 staged[kWarps][2][kV + 1][32];
+    uint4 (*rows)[kV + 1][32] = staged[threadIdx.x >> 5];
     int64_t slot_next;
     const uint16_t *q_at, *k_at, *v_at;  // of the token that is loaded
     auto at = [&](int64_t t) {
@@ -98,13 +99,26 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         k_at = a.k + t * a.k_stride;
         if (kCache) v_at = a.v + t * a.v_stride;
     };
+    // (A row that there is not is zeros, or not looked at.)
+    auto stage = [&](uint4 *to, const uint16_t *p, int r, int n) {
+        if (r - sub >= n) return;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to + lane)),
+                     "l"(r < n ? p + r * kD + 8 * l : p), "r"(r < n ? 16 : 0)
+                     : "memory");
+    };
+    auto stage_rows = [&](uint4 (*to)[32]) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) stage(to[b], q_at, unit + b * step, hq);
+        stage(to[kK], k_at, unit_k, hkv);
+        if (kCache) stage(to[kV], v_at, unit_v, hkv);
+    };
     // With one position, each lane brings its own angles: 2 kN fours of frequencies, cosines before
     // sines.  With axes, a warp brings the R / 4 fours of the token, lane i fours i and i + 32: a four
     // of several axes takes four copies, and lanes that share angles need not make them again.  Pairs
     // of halves take two fours a lane, 2i and 2i + 1: the even fours lie before the odd ones, so
-    // that lanes read neighbouring ones.  (4096 tokens: with axes 31.6 us when each lane brought its own,
-    // 30.3 so; 1000 tokens of 32 + 8 + 8 heads of 128 with axes in turn 9.8 and 6.9; with one position
-    // 28.3 and 29.4.)
+    // that lanes read neighbouring ones.  (Before the rows were copied ahead, 4096 tokens: with axes 31.6 us when
+    // each lane brought its own, 30.3 so; 1000 tokens of 32 + 8 + 8 heads of 128 with axes in turn 9.8 and 6.9;
+    // with one position 28.3 and 29.4.)
     constexpr int kFours = (kD / 4 + 31) / 32;
     auto place = [&](int four) { return kNeighbours ? four : (four & 1) * (R / 8) + (four >> 1); };
     // Position on axis lane % 4 (on axis 0 where there are fewer): each axis' on lane 0 .. 3.
@@ -168,10 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     const int64_t stride = gridDim.x;
     int pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride), buf = 0;
     at(blockIdx.x);
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) raw[b] = row_of(q_at, unit + b * step, hq);
-    raw_k = row_of(k_at, unit_k, hkv);
-    if (kCache) raw_v = row_of(v_at, unit_v, hkv);
+    stage_rows(rows[0]);
     angles_of(blockIdx.x, pos, 0);
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += stride, buf ^= 1) {
     const int pos_now = pos;
@@ -181,6 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     if constexpr (kAxes) __syncwarp();  // the angles of the token before are read
     if (more) {
         at(t + stride);
+        stage_rows(rows[buf ^ 1]);
         angles_of(t + stride, pos, buf ^ 1);
         pos_next = position(t + 2 * stride);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         float v[8];
 #pragma unroll
         for (int b = 0; b < 8; ++b)
-            v[b] = b < kBatch ? squares(raw[b]) : b == kBatch ? squares(raw_k) : 0.f;
+            v[b] = b <= kK ? squares(rows[buf][b][lane]) : 0.f;
 #pragma unroll
         for (int n = 4, d = 16; n > 0; n >>= 1, d >>= 1)
 #pragma unroll
@@ -321,9 +333,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     for (int b = 0; b < kBatch; ++b) {
         const int r = unit + b * step;
         if (r - sub >= hq) break;  // warp-uniform
-        const uint4 out = turned(raw[b], joint ? inv[b] : inverse_of(raw[b]));
+        const uint4 row = rows[buf][b][lane], out = turned(row, joint ? inv[b] : inverse_of(row));
         if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
-        if (more) raw[b] = row_of(q_at, r, hq);
     }
     for (int r = unit + kBatch * step; r - sub < hq; r += step) {  // many heads
         const uint4 row = row_of(a.q + t * a.q_stride, r, hq), out = turned(row, inverse_of(row));
@@ -331,8 +342,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     }
     if (unit_k - sub < hkv) factors(a.k_weight);
     for (int r = unit_k; r - sub < hkv; r += step) {
-        const uint4 row = r == unit_k ? raw_k : row_of(a.k + t * a.k_stride, r, hkv);
-        const uint4 out = turned(row, joint && r == unit_k ? inv[kBatch] : inverse_of(row));
+        const uint4 row = r == unit_k ? rows[buf][kK][lane] : row_of(a.k + t * a.k_stride, r, hkv);
+        const uint4 out = turned(row, joint && r == unit_k ? inv[kK] : inverse_of(row));
         if (live && r < hkv) {
             if (kCache == 0)
                 *reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + r * kD + 8 * l) = out;
@@ -342,11 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     }
     if (kCache)
         for (int r = unit_v; r < hkv; r += step)
-            to_cache(a.v_cache, r, r == unit_v ? raw_v : row_of(a.v + t * a.v_stride, r, hkv));
-    if (more) {
-        raw_k = row_of(k_at, unit_k, hkv);
-        if (kCache) raw_v = row_of(v_at, unit_v, hkv);
-    }
+            to_cache(a.v_cache, r, r == unit_v ? rows[buf][kV][lane] : row_of(a.v + t * a.v_stride, r, hkv));
     }
 }
 
