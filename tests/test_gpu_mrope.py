@@ -34,6 +34,7 @@ def _ref(x, w, table, pos, axes, interleaved, bias=0.0, eps=1e-6):
     (128, 128, 32, 8, 40, False, "runs"), (128, 32, 6, 2, 7, True, "runs"), (64, 64, 9, 3, 20, False, "turns"),
     (64, 16, 3, 1, 5, True, "random"), (256, 0, 8, 2, 4, False, "runs"), (256, 256, 7, 7, 600, True, "random"),
     (128, 16, 1, 1, 513, False, "random"), (64, 48, 4, 4, 900, False, "turns"),
+    (256, 256, 24, 4, 1300, False, "runs"), (64, 64, 15, 5, 2000, True, "runs"), (256, 192, 40, 2, 700, False, "runs"),
 ])
 @pytest.mark.parametrize("n", [1, 2, 3, 4])
 def test_mrope_matches_plain(cuda_lib, dim, rot, hq, hkv, T, interleaved, axes, n):
