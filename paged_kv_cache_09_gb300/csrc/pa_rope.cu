@@ -11,20 +11,22 @@
 //
 // Every value is read once and written once; bound by memory for a prompt chunk, by launch
 // and one round trip for a decode batch.  D / 8 lanes hold a row, 8 dims (16 bytes) a lane.
-// Instructions come close to bounding it too, so the weights are multiplied into the angles once
-// per token and kind of row,
+// Instructions come close to bounding it too (issue slots 60% used), so the weights are multiplied into the
+// angles once per token and kind of row,
 //     out_j = inv (x_j A_j + x_p B_j),   A_j = w_j cos, B_j = +- w_p sin   (p: j's partner),
-// the partners are exchanged as packed BF16, before any arithmetic, and the arithmetic is on pairs.
-// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 25.5 us, 5.3 TB/s (43 with the
-// weights applied to every row, 0.9 more with the rows summed one by one, 28.1 with a warp's next rows
-// in registers instead of shared memory, which are on their way for a shorter time); into a 4-bit
-// cache 32.0 us, without a cache 23.5.  32 + 8 + 8 heads 39.2 us, 12 + 2 + 2 17.4 (5.1 and 3.9 TB/s); 64
-// + 8 + 8 of 128 36.2 (4.6 TB/s).  16 tokens: 2.2 us.
+// from weights that a CTA keeps in shared memory as it needs them; the partners are exchanged as packed
+// BF16, before any arithmetic, and the arithmetic is on pairs.
+// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 22.8 us, 5.9 TB/s.  With the weights made
+// ready at each token 25.5; besides, with a warp's next rows in registers instead of shared memory, which
+// are on their way for a shorter time, 28.1, with the rows summed one by one 29, and with the weights
+// applied to every row 43.  Into a 4-bit cache 30.2 us, without a cache 20.4.  32 + 8 + 8 heads 36.5 us, 12 + 2
+// + 2 16.7 (5.5 and 4.0 TB/s), 64 + 8 + 8 of 128 34.1 (4.9 TB/s).  16 tokens 2.2 us.  20 warps an SM instead of
+// 16: 23.1 us, and 64 + 8 + 8 heads of 128 33.3, but 512 tokens 5.0 instead of 4.5.
 //
 // Positions on several axes (time, height, width of a token): frequency i takes its angle from the
 // position on the axis that the caller gives it.  Only the fetch of the angles differs: fours of
 // frequencies, each on one axis, come as 16-byte copies, as with one position, others one by one: 4096
-// tokens 26.5 and 27.4 us (27.5 and 28.6 by one kernel that chose for each token).
+// tokens 23.4 and 25.2 us (by one kernel that chose for each token a microsecond more).
 #include <algorithm>
 #include <type_traits>
 
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     // axes, this warp's) while the token before is worked on, its position a token earlier still.  (A
     // padding token's rows are read for nothing.)
     constexpr int kN = kNeighbours ? 1 : 2;  // fours of frequencies of a lane
-    __shared__ float4 angles[kWarps][2][kAxes ? kD / 4 : 2 * kN * 32];
+    __shared__ float4 angles[kWarps][2][kD / 4];
     constexpr int kK = kBatch, kV = kBatch + (kCache ? 1 : 0);  // places of the first key and value row
     __shared__ uint4 staged[kWarps][2][kV + 1][32];
     uint4 (*rows)[kV + 1][32] = staged[threadIdx.x >> 5];
@@ -128,14 +130,35 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         stage(to[kK], k_at, unit_k, hkv);
         if (kCache) stage(to[kV], v_at, unit_v, hkv);
     };
+    // The weights with their bias, those of a lane's dims and of their partners (these with the sign of
+    // the sine that they meet), of query and key rows.
+    __shared__ float4 weights[2][4][32];
+    auto keep_weights = [&](const uint4 &own, const uint4 &other, float4 (*to)[32]) {
+        const uint32_t x[4] = {own.x, own.y, own.z, own.w}, y[4] = {other.x, other.y, other.z, other.w};
+        float wo[8], wp[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wo[2 * i] = bf16_lo(x[i]) + a.weight_bias;
+            wo[2 * i + 1] = bf16_hi(x[i]) + a.weight_bias;
+            const float lo = bf16_lo(y[i]) + a.weight_bias, hi = bf16_hi(y[i]) + a.weight_bias;
+            wp[2 * i] = kNeighbours ? (turns ? -hi : hi) : second ? lo : -lo;
+            wp[2 * i + 1] = kNeighbours ? lo : second ? hi : -hi;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            to[i][lane] = make_float4(wo[4 * i], wo[4 * i + 1], wo[4 * i + 2], wo[4 * i + 3]);
+            to[2 + i][lane] = make_float4(wp[4 * i], wp[4 * i + 1], wp[4 * i + 2], wp[4 * i + 3]);
+        }
+    };
     // With one position, each lane brings its own angles: 2 kN fours of frequencies, cosines before
-    // sines.  With axes, a warp brings the R / 4 fours of the token, lane i fours i and i + 32: a four
+    // sines (lanes of the same angles bring them to one place, each for itself).  With axes, a warp brings the R / 4 fours of the token, lane i fours i and i + 32: a four
     // of several axes takes four copies, and lanes that share angles need not make them again.  Pairs
     // of halves take two fours a lane, 2i and 2i + 1: the even fours lie before the odd ones, so
     // that lanes read neighbouring ones.  (Before the rows were copied ahead, 4096 tokens: with axes 31.6 us when
     // each lane brought its own, 30.3 so; 1000 tokens of 32 + 8 + 8 heads of 128 with axes in turn 9.8 and 6.9;
     // with one position 28.3 and 29.4.)
-    constexpr int kFours = (kD / 4 + 31) / 32;
+    constexpr int kFours = (kD / 4 + 31) / 32, kOwn = kNeighbours ? kLanes : kLanes / 2;
+    const int own = !kNeighbours && second ? l - R / 16 : l;  // the lane's place (where it turns)
     auto place = [&](int four) { return kNeighbours ? four : (four & 1) * (R / 8) + (four >> 1); };
     uint32_t axes[kFours] = {};  // of each four, two bits each
     if constexpr (kAxes > 0) {
@@ -163,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
                 const float *row = a.cos_sin + (int64_t)pos * R +
                                    (kNeighbours ? 4 * l : second ? 8 * l - half : 8 * l);
 #pragma unroll
-                for (int e = 0; e < 2 * kN; ++e) copy16(to + e * 32 + lane, row + (e / kN) * half + (e % kN) * 4);
+                for (int e = 0; e < 2 * kN; ++e) copy16(to + e * kOwn + own, row + (e / kN) * half + (e % kN) * 4);
             }
         } else if (placed(pos) && inside(pos)) {
 #pragma unroll
@@ -191,13 +214,21 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     int pos = position(blockIdx.x), pos_next = position(blockIdx.x + stride), buf = 0;
     at(blockIdx.x);
     stage_rows(rows[0]);
+    uint4 w_own, w_other;  // (the first two warps': on their way before the position is waited for)
+    if (threadIdx.x < 64) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(threadIdx.x < 32 ? a.q_weight : a.k_weight);
+        w_own = w[l];
+        w_other = w[partner];
+    }
     angles_of(blockIdx.x, pos, 0);
+    if (threadIdx.x < 64) keep_weights(w_own, w_other, weights[threadIdx.x >> 5]);
+    __syncthreads();
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += stride, buf ^= 1) {
     const int pos_now = pos;
     const int64_t slot = slot_next;
     const bool more = t + stride < a.num_tokens;
     pos = pos_next;
-    if constexpr (kAxes) __syncwarp();  // the angles of the token before are read
+    __syncwarp();  // the angles of the token before are read
     if (more) {
         at(t + stride);
         stage_rows(rows[buf ^ 1]);
@@ -223,47 +254,37 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     }
     // A and B of this lane's dims for rows with these weights.
     f32x2 A[4], B[4];
-    auto factors = [&](const uint16_t *w) {
-        float wo[8], wp[8], c[8], s[8];
-        const uint4 own = __ldg(reinterpret_cast<const uint4 *>(w) + l);
-        const uint4 other = __ldg(reinterpret_cast<const uint4 *>(w) + partner);
-        const uint32_t x[4] = {own.x, own.y, own.z, own.w}, y[4] = {other.x, other.y, other.z, other.w};
+    auto factors = [&](const float4 (*w)[32]) {
+        float4 c[2], sn[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            wo[2 * i] = bf16_lo(x[i]) + a.weight_bias;
-            wo[2 * i + 1] = bf16_hi(x[i]) + a.weight_bias;
-            wp[2 * i + (kNeighbours ? 1 : 0)] = bf16_lo(y[i]) + a.weight_bias;
-            wp[2 * i + (kNeighbours ? 0 : 1)] = bf16_hi(y[i]) + a.weight_bias;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            c[j] = 1.f;
-            s[j] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+            c[e] = make_float4(1.f, 1.f, 1.f, 1.f);
+            sn[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (turns) {
-            const float4 *mine = angles[threadIdx.x >> 5][buf];
+            const float4 *mine = angles[threadIdx.x >> 5][buf] + own;
             if (kNeighbours) {
-                const float4 cv = kAxes ? mine[l] : mine[lane], sv = kAxes ? mine[R / 8 + l] : mine[32 + lane];
-                c[0] = c[1] = cv.x; c[2] = c[3] = cv.y; c[4] = c[5] = cv.z; c[6] = c[7] = cv.w;
-                s[1] = sv.x; s[3] = sv.y; s[5] = sv.z; s[7] = sv.w;
-                s[0] = -sv.x; s[2] = -sv.y; s[4] = -sv.z; s[6] = -sv.w;
+                const float4 cv = mine[0], sv = mine[kAxes ? R / 8 : kOwn];
+                c[0] = make_float4(cv.x, cv.x, cv.y, cv.y);
+                c[1] = make_float4(cv.z, cv.z, cv.w, cv.w);
+                sn[0] = make_float4(sv.x, sv.x, sv.y, sv.y);
+                sn[1] = make_float4(sv.z, sv.z, sv.w, sv.w);
             } else {
-                const float sign = second ? 1.f : -1.f;
-                const float4 *first = kAxes ? mine + (second ? l - R / 16 : l) : mine + lane;
-                const int next = kAxes ? R / 8 : 32, sines = kAxes ? R / 16 : 64;
+                const int next = kAxes ? R / 8 : kOwn, sines = kAxes ? R / 16 : 2 * kOwn;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float4 cv = first[e * next], sv = first[sines + e * next];
-                    c[4 * e] = cv.x; c[4 * e + 1] = cv.y; c[4 * e + 2] = cv.z; c[4 * e + 3] = cv.w;
-                    s[4 * e] = sign * sv.x; s[4 * e + 1] = sign * sv.y;
-                    s[4 * e + 2] = sign * sv.z; s[4 * e + 3] = sign * sv.w;
+                    c[e] = mine[e * next];
+                    sn[e] = mine[sines + e * next];
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            A[i] = pair(wo[2 * i] * c[2 * i], wo[2 * i + 1] * c[2 * i + 1]);
-            B[i] = pair(wp[2 * i] * s[2 * i], wp[2 * i + 1] * s[2 * i + 1]);
+        for (int e = 0; e < 2; ++e) {
+            const float4 wo = w[e][lane], wp = w[2 + e][lane];
+            A[2 * e] = mul(pair(wo.x, wo.y), pair(c[e].x, c[e].y));
+            A[2 * e + 1] = mul(pair(wo.z, wo.w), pair(c[e].z, c[e].w));
+            B[2 * e] = mul(pair(wp.x, wp.y), pair(sn[e].x, sn[e].y));
+            B[2 * e + 1] = mul(pair(wp.z, wp.w), pair(sn[e].z, sn[e].w));
         }
     };
 
@@ -310,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     };
 
     // The shuffles need whole warps, so a warp goes on while any of its rows is left.
-    factors(a.q_weight);
+    factors(weights[0]);
     // A warp with several whole rows sums them together: each step of the reduction halves the
     // rows that a lane has (9 exchanges and 7 for the results, instead of 5 a row), and every
     // lane takes one row's root.
@@ -348,7 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         const uint4 row = row_of(a.q + t * a.q_stride, r, hq), out = turned(row, inverse_of(row));
         if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
     }
-    if (unit_k - sub < hkv) factors(a.k_weight);
+    if (unit_k - sub < hkv) factors(weights[1]);
     for (int r = unit_k; r - sub < hkv; r += step) {
         const uint4 row = r == unit_k ? rows[buf][kK][lane] : row_of(a.k + t * a.k_stride, r, hkv);
         const uint4 out = turned(row, joint && r == unit_k ? inv[kK] : inverse_of(row));
