@@ -151,12 +151,13 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         }
     };
     // With one position, each lane brings its own angles: 2 kN fours of frequencies, cosines before
-    // sines (lanes of the same angles bring them to one place, each for itself).  With axes, a warp brings the R / 4 fours of the token, lane i fours i and i + 32: a four
-    // of several axes takes four copies, and lanes that share angles need not make them again.  Pairs
-    // of halves take two fours a lane, 2i and 2i + 1: the even fours lie before the odd ones, so
-    // that lanes read neighbouring ones.  (Before the rows were copied ahead, 4096 tokens: with axes 31.6 us when
-    // each lane brought its own, 30.3 so; 1000 tokens of 32 + 8 + 8 heads of 128 with axes in turn 9.8 and 6.9;
-    // with one position 28.3 and 29.4.)
+    // sines (lanes of the same angles bring them to one place, each for itself).  With axes, a warp
+    // brings the R / 4 fours of the token, lane i fours i and i + 32: a four of several axes takes four
+    // copies, and lanes that share angles need not make them again.  Pairs of halves take two fours a
+    // lane, 2i and 2i + 1: the even fours lie before the odd ones, so that lanes read neighbouring ones.
+    // (Before the rows were copied ahead, 4096 tokens: with axes 31.6 us when each lane brought its own,
+    // 30.3 so; 1000 tokens of 32 + 8 + 8 heads of 128 with axes in turn 9.8 and 6.9; with one position
+    // 28.3 and 29.4.)
     constexpr int kFours = (kD / 4 + 31) / 32, kOwn = kNeighbours ? kLanes : kLanes / 2;
     const int own = !kNeighbours && second ? l - R / 16 : l;  // the lane's place (where it turns)
     auto place = [&](int four) { return kNeighbours ? four : (four & 1) * (R / 8) + (four >> 1); };
@@ -392,10 +393,9 @@ cudaError_t launch_dim(RopeArgs a, cudaStream_t stream) {
     // A small call: a row a warp, as many CTAs a token as that takes.  A large one: a token over as
     // few CTAs as give each warp kBatch query rows, and four CTAs an SM that go from token to token.
     // Small is what is resident at once, with the rows of a call that writes the cache (so that the
-    // calls with and without a cache sum a row in the same order).  24 + 4 + 4 heads of 256, 8 CTAs
-    // a token, small and large: 16 tokens 2.3 and 2.9 us, 64 2.7 and 3.0, 128 4.5 and 2.9, 256 7.3
-    // and 3.4, 512 14.3 and 5.5; 32 + 8 + 8 heads, 12 CTAs: 16 tokens 2.3 and 2.8, 64 4.2 and 2.8;
-    // 16 + 4 + 4 of 64, 2 CTAs: 128 tokens 2.3 and 2.3, 384 4.0 and 2.8.
+    // calls with and without a cache sum a row in the same order).  24 + 4 + 4 heads of 256, 8 CTAs a
+    // token and one: 16 tokens 2.2 and 2.8 us, 64 2.8 and 2.9, 100 4.0 and 2.9, 200 5.6 and 3.4; 32 + 8 + 8 of
+    // 128, 6 CTAs and one: 16 tokens 2.1 and 2.8, 64 2.8 and 2.9, 150 4.1 and 2.9.
     const int y_small = (a.num_q_heads + 2 * a.num_kv_heads + per - 1) / per;
     const bool small = (int64_t)a.num_tokens * y_small <= 4 * a.num_sms;
     const int y = small ? y_small : (a.num_q_heads + per * kBatch - 1) / (per * kBatch);
