@@ -363,6 +363,42 @@ def test_decode_of_lengths_that_the_kernel_before_writes(cuda_lib, S):
     assert pa.device_errors() == 0
 
 
+@pytest.mark.parametrize("S,n", [(1, 5000), (1, 200), (3, 260), (24, 2000)])
+def test_decode_of_a_table_that_the_kernel_before_writes(cuda_lib, S, n):
+    # What the decode looks at before that kernel ends: valid pages, but of other sequences, entries
+    # outside the pool, other lengths.
+    pa = cuda_lib
+    c = _case(pa, [n] * (S + 2), 16, 12, 2, seed=S)
+    width = c["bt"].shape[1] // 4 * 4  # (copies of whole 16 bytes)
+    most = width * 16
+    bt = torch.zeros(S, width, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(S + 3 & ~3, dtype=torch.int32, device="cuda")
+    steps = []
+    for i in range(16):
+        pick = torch.randperm(S + 2, generator=torch.Generator().manual_seed(i))[:S]
+        table = c["bt"][pick, :width].contiguous()
+        count = torch.full_like(lens, most if i % 4 < 3 else most - 70 - i)
+        if i % 5 == 4:
+            count[0], table[0] = 0, -7  # no keys: its entries are not looked at
+        steps.append((table, count))
+    ws = torch.empty(pa.decode_q8_workspace_size(S, 12, 2, 256, 16, most), dtype=torch.uint8, device="cuda")
+    outs = []
+    for table, count in steps:
+        pa.copy(lens, count)
+        pa.copy(bt, table)
+        outs.append(pa.decode_q8(c["q"][:S], *c["cache"], bt, lens[:S], 0.0625, most, workspace=ws))
+    for table, count in steps:
+        pa.copy(bt, table)
+        pa.copy(lens, count)
+        outs.append(pa.decode_q8(c["q"][:S], *c["cache"], bt, lens[:S], 0.0625, most, workspace=ws))
+    torch.cuda.synchronize()
+    for (table, count), *got in zip(steps, outs[:16], outs[16:]):
+        want = pa.decode_q8(c["q"][:S], *c["cache"], table, count[:S], 0.0625, most)
+        assert torch.equal(got[0], want) and torch.equal(got[1], want)
+        torch.cuda.synchronize()
+    assert pa.device_errors() == 0
+
+
 def test_steps_of_write_and_decode_back_to_back(cuda_lib):
     # Each step's write grows scales that the step before has read: no stale ones are used.
     pa = cuda_lib
