@@ -15,12 +15,14 @@
 // through the slots costs 8 bytes of L2 a slot and CTA: with two CTAs an SM, about a tenth of the
 // call's own bytes.
 //
-// Measured, 4 KV heads unless said: 16 tokens written in 2.7 us and 256 read in 1.7 (launch and three
-// round trips: slots, rows, stores); 4096 written in 7.1 us and read in 4.6 (3.5 and 5.4 TB/s); 8192 in 12.0
-// and 8.4; 12 x 333 tokens of 8 heads in 12.1 and 8.4.  The write's warps hold a block's 16 rows at
+// Measured, 4 KV heads unless said: 16 tokens written in 2.6 us and 256 read in 1.7 (launch and three
+// round trips: slots, rows, stores); 4096 written in 6.3 us and read in 4.6 (4.0 and 5.4 TB/s); 8192 in 11.6
+// and 8.4; 12 x 333 tokens of 8 heads in 12.0 and 8.4.  The write's warps hold a block's 16 rows at
 // once (64 registers): 16 warps an SM, and a call's first instructions are a fifth of its time.  With two
 // warps a block and the blocks found by every 16 tokens, 4096 tokens took 9.1 us and 32768, whose every
-// CTA looks through all slots, 121 (now 43).
+// CTA looks through all slots, 121 (now 40).  Its code runs once a warp, so that it is fetched as it runs: a
+// loop over the slots that may be of the CTA's blocks, instead of what follows such a slot written out for
+// each of a thread's 16, took 4096 tokens from 7.2 to 6.4 us.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -57,8 +59,13 @@ __device__ __forceinline__ uint32_t without_inf(uint32_t w) {
 
 // Eight BF16 values times f, as codes.
 __device__ __forceinline__ uint2 codes_of(const uint4 &v, float f) {
-    return make_uint2(e4m3x4(bf16_lo(v.x) * f, bf16_hi(v.x) * f, bf16_lo(v.y) * f, bf16_hi(v.y) * f),
-                      e4m3x4(bf16_lo(v.z) * f, bf16_hi(v.z) * f, bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // (a pair is one instruction)
+        asm("{.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;}"
+            : "=f"(x[2 * i]), "=f"(x[2 * i + 1]) : "f"(bf16_lo(w[i])), "f"(bf16_hi(w[i])), "f"(f));
+    return make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
 }
 
 // Four codes times f (a power of two below 1), as codes.
@@ -161,29 +168,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2) write_q8_kernel(const __grid_c
                 const int64_t j = j0 + threadIdx.x + k * kThreads;
                 s[k] = j < a.num_tokens ? a.slot_mapping[j] : -1;
             }
+        uint32_t hits = 0;  // the slots that may be of these blocks
+        if constexpr (!kOne) {
 #pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-            const int j = (int)(j0 + threadIdx.x + k * kThreads);
-            int at = -1, row = 0;
-            if constexpr (kOne) {
+            for (int k = 0; k < kSlots; ++k) {
+                const uint32_t bit = map_bit(s[k]);
+                hits |= (s[k] >= 0 ? map[bit / 32] >> (bit % 32) & 1u : 0u) << k;
+            }
+        }
+        if constexpr (kOne) {
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k) {
+                const int j = (int)(j0 + threadIdx.x + k * kThreads);
                 const unsigned long long r = (unsigned long long)(s[k] - own.first);
                 if (r < (unsigned)own.rows) {
-                    at = 0;
-                    row = (int)r;
-                }
-            } else {
-                const uint32_t bit = map_bit(s[k]);
-                if ((map[bit / 32] >> (bit % 32) & 1) && s[k] >= 0) {
-                    Place p;
-                    block_of(a, s[k], &p);
-                    at = (int)hash_of(p.first);
-                    while (keys[at] != p.first && keys[at] != -1) at = (at + 1) % kTable;
-                    if (keys[at] == -1) at = -1;
-                    row = p.row;
+                    atomicMax(&token[0][(int)r], j);
+                    atomicMin(&lowest[0], j);
                 }
             }
-            if (at >= 0) {
-                atomicMax(&token[at][row], j);
+        } else {
+            for (; hits; hits &= hits - 1) {
+                const int j = (int)(j0 + threadIdx.x + (__ffs(hits) - 1) * kThreads);
+                Place p;
+                block_of(a, a.slot_mapping[j], &p);
+                int at = (int)hash_of(p.first);
+                while (keys[at] != p.first && keys[at] != -1) at = (at + 1) % kTable;
+                if (keys[at] == -1) continue;
+                atomicMax(&token[at][p.row], j);
                 atomicMin(&lowest[at], j);
             }
         }
@@ -455,10 +466,15 @@ __global__ void __launch_bounds__(kWarps * 32) expand_q8_kernel(const __grid_con
 cudaError_t launch_write_q8(const Q8WriteArgs &args, cudaStream_t stream) {
     Q8WriteArgs a = args;
     // Two CTAs an SM.  A call of few tokens gives each a token; others first cut the heads, so that a
-    // CTA's warps work on one block at a time, then the tokens.
-    const int ctas = 2 * a.num_sms, heads = (2 * a.num_kv_heads - 1) / kWarps + 1;
-    const bool few = a.num_tokens <= ctas;
-    const int y = few ? std::min(heads, ctas / a.num_tokens) : std::min(heads, kMaxCut);
+    // CTA's warps work on one block at a time, then the tokens.  Calls of up to about one job a warp cut
+    // the heads once more, so that blocks are spread over more SMs.  With 4 heads, 8 and 4 kinds a CTA: 16
+    // tokens 2.8 and 2.6 us, 1000 5.4 and 4.3, 4096 7.1 and 6.4, 6000 10.6 and 9.4; 8192 11.7 and 12.6, 32768 40 and
+    // 41; with 8 heads 2000 6.3 and 6.2, 4096 11.0 and 12.2.
+    const int ctas = 2 * a.num_sms, kinds = 2 * a.num_kv_heads;
+    const int heads = (kinds - 1) / kWarps + 1, twice = (kinds - 1) / (kWarps / 2) + 1;
+    const bool few = a.num_tokens <= ctas, small = (int64_t)a.num_tokens * kinds <= (int64_t)10 * kQ8Tokens * ctas;
+    int y = std::min(small ? twice : heads, kMaxCut);
+    if (few) y = (int64_t)a.num_tokens * twice <= ctas ? twice : std::min(heads, ctas / a.num_tokens);
     a.range = few ? 1 : std::min(kMaxRange, (a.num_tokens - 1) / (ctas / y) + 1);
     const int x = (a.num_tokens - 1) / a.range + 1;
     return launch_pdl(a.range == 1 ? write_q8_kernel<true> : write_q8_kernel<false>, dim3(x, y), dim3(kWarps * 32), 0,
