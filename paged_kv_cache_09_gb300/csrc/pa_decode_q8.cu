@@ -31,7 +31,7 @@
 //
 // Measured, calls one after another in a graph, 4 KV heads of 6 query heads unless said: 16 sequences of
 // 4096..32768 keys 102 us, 6.7 TB/s; 64 of 1..2048, 8 KV heads of 4, pages of 16: 47.3 us (5.1 TB/s: begin, end and
-// the slowest CTAs); one of 32768 keys 17.2 us, of 1701 7.1; 16 of 1..700 8.7 us, of 1..300 7.3.
+// the slowest CTAs); one of 32768 keys 17.0 us, of 1701 7.0; 16 of 1..700 8.7 us, of 1..300 7.3.
 #include "pa_decode_split.cuh"
 #include "pa_q8.cuh"
 
