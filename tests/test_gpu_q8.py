@@ -634,13 +634,13 @@ def test_write_and_decode_in_two_graphs_with_their_own_workspaces(cuda_lib):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             step()
-        plans.append((graph, out, want))
+        plans.append((graph, out, want, step))  # (step holds the tensors that the graph reads)
     for _ in range(3):
-        for graph, out, want in plans:
+        for graph, out, want, _step in plans:
             out.fill_(9.0)
             graph.replay()
         torch.cuda.synchronize()
-        for graph, out, want in plans:
+        for graph, out, want, _step in plans:
             assert torch.equal(out, want)
     assert pa.device_errors() == 0
 
