@@ -97,7 +97,23 @@ T *ptr(const at::Tensor *t) {
     return static_cast<T *>(t->data_ptr());
 }
 
+// What may wait is done without the interpreter's lock, as ctypes and torch do it: a launch waits where the
+// stream's queue is full, an allocation perhaps for the GPU, and meanwhile other threads go on, and host
+// functions of the stream that take the lock.  Python objects are read before.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// A call of the library.
+template <typename R, typename... P, typename... A>
+R call(R (*f)(P...), A... args) {
+    Unlocked u;
+    return f(args...);
+}
+
 at::Tensor new_rows(const at::Tensor *like, at::IntArrayRef shape) {
+    Unlocked u;
     return at::empty(shape, like->options().dtype(Type::BFloat16).requires_grad(false));
 }
 
@@ -157,9 +173,9 @@ PyObject *write_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t T = key->size(0);
         const at::Tensor *value = c.rows(a[1], T, cache.heads, 256, &vs), *slots = c.vector(a[6], Type::Long, T);
         if (!c.usual || T > 0x7fffffff) return none();
-        const int rc = lib.write_q8(ptr<pa_bf16>(key), ks, ptr<pa_bf16>(value), vs, cache.k, cache.v, cache.ks,
-                                    cache.vs, cache.page_stride, cache.scale_stride, cache.pages, ptr<int64_t>(slots),
-                                    (int)T, cache.heads, 256, cache.block_size, c.stream());
+        const int rc = call(lib.write_q8, ptr<pa_bf16>(key), ks, ptr<pa_bf16>(value), vs, cache.k, cache.v, cache.ks,
+                            cache.vs, cache.page_stride, cache.scale_stride, cache.pages, ptr<int64_t>(slots), (int)T,
+                            cache.heads, 256, cache.block_size, c.stream());
         if (rc) return status(rc);
         Py_RETURN_TRUE;
     });
@@ -175,9 +191,9 @@ PyObject *gather_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!slots || slots->size(0) > 0x7fffffff) return none();
         const int64_t T = slots->size(0);
         at::Tensor k = new_rows(slots, {T, cache.heads, 256}), v = new_rows(slots, {T, cache.heads, 256});
-        const int rc = lib.gather_q8(cache.k, cache.v, cache.ks, cache.vs, cache.page_stride, cache.scale_stride,
-                                     cache.pages, ptr<int64_t>(slots), (int)T, cache.heads, 256, cache.block_size,
-                                     ptr<pa_bf16>(&k), ptr<pa_bf16>(&v), c.stream());
+        const int rc = call(lib.gather_q8, cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
+                            cache.scale_stride, cache.pages, ptr<int64_t>(slots), (int)T, cache.heads, 256,
+                            cache.block_size, ptr<pa_bf16>(&k), ptr<pa_bf16>(&v), c.stream());
         if (rc) return status(rc);
         PyObject *kp = THPVariable_Wrap(std::move(k)), *vp = THPVariable_Wrap(std::move(v));
         PyObject *pair = kp && vp ? PyTuple_Pack(2, kp, vp) : nullptr;
@@ -203,7 +219,9 @@ bool output(Call &c, PyObject *o, const at::Tensor *q, at::Tensor *out) {
 template <typename F>
 bool workspace(Call &c, PyObject *o, const at::Tensor *q, at::Tensor *ws, F need) {
     if (o == Py_None) {
-        *ws = at::empty({(int64_t)std::max<size_t>(need(), 256)}, q->options().dtype(Type::Byte));
+        const int64_t bytes = (int64_t)std::max<size_t>(need(), 256);
+        Unlocked u;
+        *ws = at::empty({bytes}, q->options().dtype(Type::Byte));
         return true;
     }
     if (!THPVariable_Check(o)) return false;
@@ -234,13 +252,13 @@ PyObject *decode_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t table_stride = table->size(0) > 1 ? table->stride(0) : table->size(1);
         at::Tensor out, ws;
         if (!output(c, a[9], q, &out) || !workspace(c, a[10], q, &ws, [&] {
-                return lib.decode_q8_size((int)S, (int)hq, cache.heads, 256, cache.block_size, (int)most);
+                return call(lib.decode_q8_size, (int)S, (int)hq, cache.heads, 256, cache.block_size, (int)most);
             }))
             return none();
-        const int rc = lib.decode_q8(ptr<pa_bf16>(q), cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
-                                     cache.scale_stride, cache.pages, ptr<int32_t>(table), table_stride,
-                                     ptr<int32_t>(lens), (int)S, (int)most, (int)hq, cache.heads, 256,
-                                     cache.block_size, scale, ptr<pa_bf16>(&out), ptr(&ws), ws.nbytes(), c.stream());
+        const int rc = call(lib.decode_q8, ptr<pa_bf16>(q), cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
+                            cache.scale_stride, cache.pages, ptr<int32_t>(table), table_stride, ptr<int32_t>(lens),
+                            (int)S, (int)most, (int)hq, cache.heads, 256, cache.block_size, scale,
+                            ptr<pa_bf16>(&out), ptr(&ws), ws.nbytes(), c.stream());
         return rc ? status(rc) : given_or(a[9], std::move(out));
     });
 }
@@ -264,13 +282,14 @@ PyObject *prefill_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int B = (int)lens.size(), hq = (int)q->size(1), causal = a[8] == Py_True;
         at::Tensor out, ws;
         if (!output(c, a[10], q, &out) || !workspace(c, a[11], q, &ws, [&] {
-                return lib.prefill_q8_size(cu.data(), lens.data(), B, causal, hq, cache.heads, 256, cache.block_size);
+                return call(lib.prefill_q8_size, cu.data(), lens.data(), B, causal, hq, cache.heads, 256,
+                            cache.block_size);
             }))
             return none();
-        const int rc = lib.prefill_q8(ptr<pa_bf16>(q), cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
-                                      cache.scale_stride, cache.pages, ptr<int32_t>(table), table_stride, cu.data(),
-                                      lens.data(), B, causal, hq, cache.heads, 256, cache.block_size, scale,
-                                      ptr<pa_bf16>(&out), ptr(&ws), ws.nbytes(), c.stream());
+        const int rc = call(lib.prefill_q8, ptr<pa_bf16>(q), cache.k, cache.v, cache.ks, cache.vs, cache.page_stride,
+                            cache.scale_stride, cache.pages, ptr<int32_t>(table), table_stride, cu.data(),
+                            lens.data(), B, causal, hq, cache.heads, 256, cache.block_size, scale,
+                            ptr<pa_bf16>(&out), ptr(&ws), ws.nbytes(), c.stream());
         return rc ? status(rc) : given_or(a[10], std::move(out));
     });
 }
@@ -319,10 +338,10 @@ PyObject *mrope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!r.read(c, a)) return none();
         at::Tensor q = new_rows(r.q, {r.T, r.hq, r.dim}), k = new_rows(r.q, {r.T, r.hkv, r.dim});
         const int rc =
-            lib.mrope(ptr<pa_bf16>(r.q), r.qs, ptr<pa_bf16>(r.k), r.ks, ptr<pa_bf16>(r.qw), ptr<pa_bf16>(r.kw), r.bias,
-                      r.eps, ptr<float>(r.table), (int)r.table->size(0), (int)r.rot, r.interleaved,
-                      ptr<int32_t>(r.positions), r.axes_stride, r.num_axes, r.axes, (int)r.T, (int)r.hq, (int)r.hkv,
-                      (int)r.dim, ptr<pa_bf16>(&q), r.hq * r.dim, ptr<pa_bf16>(&k), r.hkv * r.dim, c.stream());
+            call(lib.mrope, ptr<pa_bf16>(r.q), r.qs, ptr<pa_bf16>(r.k), r.ks, ptr<pa_bf16>(r.qw), ptr<pa_bf16>(r.kw),
+                 r.bias, r.eps, ptr<float>(r.table), (int)r.table->size(0), (int)r.rot, r.interleaved,
+                 ptr<int32_t>(r.positions), r.axes_stride, r.num_axes, r.axes, (int)r.T, (int)r.hq, (int)r.hkv,
+                 (int)r.dim, ptr<pa_bf16>(&q), r.hq * r.dim, ptr<pa_bf16>(&k), r.hkv * r.dim, c.stream());
         if (rc) return status(rc);
         PyObject *qp = THPVariable_Wrap(std::move(q)), *kp = THPVariable_Wrap(std::move(k));
         PyObject *pair = qp && kp ? PyTuple_Pack(2, qp, kp) : nullptr;
@@ -346,12 +365,12 @@ PyObject *mrope_cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
             vc->sizes() != kc->sizes() || vc->strides() != kc->strides())
             return none();
         at::Tensor q = new_rows(r.q, {r.T, r.hq, r.dim});
-        const int rc = lib.mrope_cache(
-            ptr<pa_bf16>(r.q), r.qs, ptr<pa_bf16>(r.k), r.ks, ptr<pa_bf16>(v), vs, ptr<pa_bf16>(r.qw),
-            ptr<pa_bf16>(r.kw), r.bias, r.eps, ptr<float>(r.table), (int)r.table->size(0), (int)r.rot, r.interleaved,
-            ptr<int32_t>(r.positions), r.axes_stride, r.num_axes, r.axes, (int)r.T, (int)r.hq, (int)r.hkv, (int)r.dim,
-            ptr<pa_bf16>(&q), r.hq * r.dim, PA_CACHE_BF16, ptr(kc), ptr(vc), kc->stride(0), kc->size(0),
-            ptr<int64_t>(slots), (int)kc->size(1), c.stream());
+        const int rc =
+            call(lib.mrope_cache, ptr<pa_bf16>(r.q), r.qs, ptr<pa_bf16>(r.k), r.ks, ptr<pa_bf16>(v), vs,
+                 ptr<pa_bf16>(r.qw), ptr<pa_bf16>(r.kw), r.bias, r.eps, ptr<float>(r.table), (int)r.table->size(0),
+                 (int)r.rot, r.interleaved, ptr<int32_t>(r.positions), r.axes_stride, r.num_axes, r.axes, (int)r.T,
+                 (int)r.hq, (int)r.hkv, (int)r.dim, ptr<pa_bf16>(&q), r.hq * r.dim, (int)PA_CACHE_BF16, ptr(kc),
+                 ptr(vc), kc->stride(0), kc->size(0), ptr<int64_t>(slots), (int)kc->size(1), c.stream());
         if (rc) return status(rc);
         return THPVariable_Wrap(std::move(q));
     });
