@@ -6,7 +6,8 @@ C ABI declared in include/pa.h (the calls of the 8-bit cache and of rotation by 
 compiled module, csrc/pa_bind.cpp, where their arguments are as usual: a small call's time is its
 checks).  Every step of the computation runs in the library's
 CUDA kernels.  There is no CPU or PyTorch fallback: if libpa.so is missing or cannot be
-loaded, every call raises.
+loaded, every call raises.  The module is an option: without it those calls are checked in Python,
+with one warning.
 
 Functions (names follow the C ABI):
     slot_mapping(positions, block_table, block_size, seq_idx=None)    -> int64 slots
@@ -43,6 +44,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -166,14 +168,34 @@ def load():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
-        if not os.path.exists(_build.BIND):
-            raise RuntimeError(f"{_build.BIND} is not built; run __graft_entry__.build()")
+        _bind, _lib = _load_bind(), lib
+        return lib
+
+
+class _NoShortCalls:
+    """In the place of the module of the short calls where it is missing: takes no call, so that each
+    is checked and made in Python (some 10 us slower), and says so once."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        why, self._why = self._why, None
+        if why is not None:
+            warnings.warn(f"no pa_bind module ({why}): the short calls take the way through ctypes; "
+                          "__graft_entry__.build() makes it", RuntimeWarning, stacklevel=3)
+        return lambda *args: None
+
+
+def _load_bind():
+    try:
         loader = importlib.machinery.ExtensionFileLoader("pa_bind", _build.BIND)
         bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_bind", loader))
         loader.exec_module(bind)
         bind.load(LIB_PATH)
-        _bind, _lib = bind, lib
-        return lib
+        return bind
+    except (ImportError, RuntimeError) as e:  # not there, of another Python or torch, of another libpa.so
+        return _NoShortCalls(str(e))
 
 
 def _stream():

@@ -1,0 +1,45 @@
+"""The compiled module of the short calls is an option: what it is not there for runs without it.
+CPU only."""
+import shutil
+import warnings
+
+import pytest
+import torch
+
+from paged_kv_cache_09_gb300 import _build
+
+
+@pytest.fixture
+def pa():
+    if shutil.which("nvcc") is None:
+        pytest.skip("nvcc not available")
+    import paged_kv_cache_09_gb300
+    paged_kv_cache_09_gb300.build()
+    return paged_kv_cache_09_gb300
+
+
+@pytest.mark.parametrize("there", [False, True])
+def test_calls_without_the_module(pa, monkeypatch, tmp_path, there):
+    # Not there, or no module of this interpreter: the library's other calls do not look at it, and those
+    # that would take the short way check their arguments in Python, as they do for unusual ones.
+    path = tmp_path / "pa_bind.so"
+    if there:
+        path.write_bytes(b"no module")
+    monkeypatch.setattr(_build, "BIND", str(path))
+    monkeypatch.setattr(pa, "_lib", None)
+    monkeypatch.setattr(pa, "_bind", None)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")  # (no word before a call that wants it)
+        assert isinstance(pa.prefill_workspace_size(10, 0, True, 24, 4, 256, 832), int)
+        assert pa.q8_cache_shapes(1, 16, 1)[1] == (1, 1, 1)
+    x = torch.zeros(3, 1, 256, dtype=torch.bfloat16)
+    codes = torch.zeros(1, 16, 1, 256, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    args = (x, x, codes, codes, x[:1, :, :1].to(torch.uint8), x[:1, :, :1].to(torch.uint8), torch.arange(3))
+    with pytest.warns(RuntimeWarning, match="pa_bind"), pytest.raises(TypeError, match="must be a CUDA tensor"):
+        pa.reshape_and_cache_q8(*args)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")  # (said once)
+        with pytest.raises(TypeError, match="must be a CUDA tensor"):
+            pa.decode_q8(x, *args[2:6], torch.zeros(3, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 1.0, 16)
+        with pytest.raises(TypeError, match="must be a CUDA tensor"):
+            pa.gather_cache_q8(*args[2:])
