@@ -20,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -62,11 +63,17 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libpa.so and the module of the short calls, each if a source is newer than
-    it.  Returns the library's path."""
+    it.  Returns the library's path.  Where the module cannot be made (no g++, no headers of torch) a
+    warning says so, and the library is used without it."""
     with cf.ThreadPoolExecutor(1) as ex:
         bind = ex.submit(_build_bind, force)
         _build_lib(LIB, BUILD, [], force, verbose)
-        bind.result()
+        try:
+            bind.result()
+        except (OSError, RuntimeError) as e:
+            if os.path.exists(BIND):  # of older sources: it may call the library otherwise than this one takes it
+                os.remove(BIND)
+            warnings.warn(f"pa_bind is not built: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 

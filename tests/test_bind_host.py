@@ -1,5 +1,6 @@
 """The compiled module of the short calls is an option: what it is not there for runs without it.
 CPU only."""
+import os
 import shutil
 import warnings
 
@@ -43,3 +44,20 @@ def test_calls_without_the_module(pa, monkeypatch, tmp_path, there):
             pa.decode_q8(x, *args[2:6], torch.zeros(3, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 1.0, 16)
         with pytest.raises(TypeError, match="must be a CUDA tensor"):
             pa.gather_cache_q8(*args[2:])
+
+
+@pytest.mark.parametrize("compiler", ["none", "fails"])
+def test_build_without_a_compiler_for_the_module(pa, monkeypatch, tmp_path, compiler):
+    # The library is built all the same, and no module of other sources than its own stays beside it.
+    stale, tools = tmp_path / "pa_bind.so", tmp_path / "bin"
+    stale.write_bytes(b"")
+    os.utime(stale, (0, 0))
+    tools.mkdir()
+    if compiler == "fails":
+        (tools / "g++").write_text("#!/bin/sh\necho no headers >&2\nexit 1\n")
+        (tools / "g++").chmod(0o755)
+    monkeypatch.setattr(_build, "BIND", str(stale))
+    monkeypatch.setenv("PATH", str(tools))
+    with pytest.warns(RuntimeWarning, match="pa_bind" if compiler == "none" else "no headers"):
+        assert _build.build() == _build.LIB
+    assert not stale.exists()
