@@ -14,13 +14,13 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
-import importlib.metadata
-import importlib.util
 import os
 import shutil
 import subprocess
 import sysconfig
 import warnings
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,7 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa.so")
-BIND = os.path.join(BUILD, f"pa_bind-{importlib.metadata.version('torch')}.so")
+BIND = os.path.join(BUILD, f"pa_bind-{torch.__version__}.so")
 TEST_BUILD = os.path.join(BUILD, "test")
 TEST_LIB = os.path.join(TEST_BUILD, "libpa_test.so")
 TEST_DEFS = ["-DPA_TEST_HOOKS", "-DPA_WAIT_LIMIT_NS=20000000ull"]
@@ -83,14 +83,14 @@ def _build_bind(force: bool = False) -> str:
             max(os.path.getmtime(src), os.path.getmtime(header)) <= os.path.getmtime(BIND):
         return BIND
     os.makedirs(BUILD, exist_ok=True)
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    includes = [INCLUDE, os.path.join(torch, "include"), os.path.join(cuda, "include"),
-                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+    includes = [INCLUDE, os.path.join(at, "include"), os.path.join(cuda, "include"),
+                os.path.join(at, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"]]
     tmp = BIND + f".tmp{os.getpid()}"
     r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] +
-                       [f"-I{i}" for i in includes] + ["-o", tmp, src, "-L" + os.path.join(torch, "lib"),
+                       [f"-I{i}" for i in includes] + ["-o", tmp, src, "-L" + os.path.join(at, "lib"),
                         "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"],
                        capture_output=True, text=True)
     if r.returncode != 0:

@@ -2,6 +2,8 @@
 CPU only."""
 import os
 import shutil
+import subprocess
+import sys
 import warnings
 
 import pytest
@@ -61,3 +63,21 @@ def test_build_without_a_compiler_for_the_module(pa, monkeypatch, tmp_path, comp
     with pytest.warns(RuntimeWarning, match="pa_bind" if compiler == "none" else "no headers"):
         assert _build.build() == _build.LIB
     assert not stale.exists()
+
+
+def _imported(code):
+    """The package imported by a fresh interpreter after `code`: what it says the module's file is."""
+    run = subprocess.run([sys.executable, "-c", code + "\nfrom paged_kv_cache_09_gb300 import _build\n"
+                          "print(_build.BIND)"], cwd=_build.ROOT, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
+    return run.stdout.strip()
+
+
+def test_import_needs_no_metadata_of_torch():
+    # (A torch that is used from where it was built has none.)
+    path = _imported("""
+import importlib.metadata as m, torch
+def version(name):
+    raise m.PackageNotFoundError(name)
+m.version = version""")
+    assert path == _build.BIND and torch.__version__ in path
