@@ -4,7 +4,7 @@ Each .cu file is compiled to an object in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  Output: paged_kv_cache_09_gb300/_build/.
 
 build() also makes the Python module of the short calls (csrc/pa_bind.cpp, against the installed
-torch) with g++: _build/pa_bind-<torch version>.so.
+torch) with g++: _build/pa_bind-<torch version>.<interpreter and machine>.so.
 
 build_test() makes the failure-path test library _build/test/libpa_test.so from the same
 sources with PA_TEST_HOOKS defined (a hook that leaves one ring stage's loads out, and
@@ -28,7 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa.so")
-BIND = os.path.join(BUILD, f"pa_bind-{torch.__version__}.so")
+BIND = os.path.join(BUILD, f"pa_bind-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 TEST_BUILD = os.path.join(BUILD, "test")
 TEST_LIB = os.path.join(TEST_BUILD, "libpa_test.so")
 TEST_DEFS = ["-DPA_TEST_HOOKS", "-DPA_WAIT_LIMIT_NS=20000000ull"]

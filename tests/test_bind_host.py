@@ -81,3 +81,11 @@ def version(name):
     raise m.PackageNotFoundError(name)
 m.version = version""")
     assert path == _build.BIND and torch.__version__ in path
+
+
+def test_another_python_looks_for_a_module_of_its_own():
+    path = _imported("""
+import torch, sysconfig
+was = sysconfig.get_config_var
+sysconfig.get_config_var = lambda name: '.cpython-399-another.so' if name == 'EXT_SUFFIX' else was(name)""")
+    assert path.endswith(".cpython-399-another.so") and path != _build.BIND
