@@ -38,7 +38,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBatch = 6;  // query rows of a warp that are copied a token ahead (24 heads over 4 warps)
+constexpr int kBatch = 6;  // query rows of a warp at most, copied a token ahead (24 heads over 4 warps)
 
 // Pairs of fp32 in one register pair.
 typedef unsigned long long f32x2;
@@ -363,22 +363,26 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     for (int b = 0; b < kBatch; ++b) {
         const int r = unit + b * step;
         if (r - sub >= hq) break;  // warp-uniform
+        asm volatile("" ::: "memory");  // (else the compiler brings all rounds' rows ahead of the first test)
         const uint4 row = rows[buf][b][lane], out = turned(row, joint ? inv[b] : inverse_of(row));
         if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
     }
-    for (int r = unit + kBatch * step; r - sub < hq; r += step) {  // many heads
-        const uint4 row = row_of(a.q + t * a.q_stride, r, hq), out = turned(row, inverse_of(row));
-        if (live && r < hq) *reinterpret_cast<uint4 *>(q_out + r * kD) = out;
-    }
-    if (unit_k - sub < hkv) factors(weights[1]);
-    for (int r = unit_k; r - sub < hkv; r += step) {
-        const uint4 row = r == unit_k ? rows[buf][kK][lane] : row_of(a.k + t * a.k_stride, r, hkv);
-        const uint4 out = turned(row, joint && r == unit_k ? inv[kK] : inverse_of(row));
+    auto key_row = [&](int r, const uint4 &row, float root) {
+        const uint4 out = turned(row, root);
         if (live && r < hkv) {
             if (kCache == 0)
                 *reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride + r * kD + 8 * l) = out;
             else
                 to_cache(a.k_cache, r, out);
+        }
+    };
+    if (unit_k - sub < hkv) {
+        factors(weights[1]);
+        const uint4 first = rows[buf][kK][lane];
+        key_row(unit_k, first, joint ? inv[kK] : inverse_of(first));
+        for (int r = unit_k + step; r - sub < hkv; r += step) {  // many heads
+            const uint4 row = row_of(a.k + t * a.k_stride, r, hkv);
+            key_row(r, row, inverse_of(row));
         }
     }
     if (kCache)
@@ -400,7 +404,7 @@ cudaError_t launch_dim(RopeArgs a, cudaStream_t stream) {
     const bool small = (int64_t)a.num_tokens * y_small <= 4 * a.num_sms;
     const int y = small ? y_small : (a.num_q_heads + per * kBatch - 1) / (per * kBatch);
     constexpr int one = 256 / kD;  // rows of a warp
-    const int step = y * per;
+    const int step = y * per;  // (kBatch rounds of it take all query heads, either way)
     a.shift_k = (a.num_q_heads + one - 1) / one * one % step;
     a.shift_v = (a.shift_k + (a.num_kv_heads + one - 1) / one * one) % step;
     const int x = small ? a.num_tokens : std::min(a.num_tokens, std::max(1, 4 * a.num_sms / y));

@@ -1,5 +1,5 @@
-"""Rotation by axes of calls whose KV heads take a token's warps more than one round: rows that are not
-copied ahead."""
+"""Rotation of calls with many heads: KV heads that take a token's warps more than one round, whose rows
+are not copied ahead, and query heads at the ends of what a token's CTAs take."""
 import numpy as np
 import pytest
 import torch
@@ -47,4 +47,21 @@ def test_many_kv_heads(cuda_lib, T, hq, hkv, dim, interleaved, turn, one):
         pa.reshape_and_cache_q4(ko, v, wk, wv, live)
         got = how[1](q, k, v, *w, *args, kc, vc, slots, interleaved=interleaved)
         assert torch.equal(got[rows], qo[rows]) and torch.equal(kc, wk) and torch.equal(vc, wv)
+    assert pa.device_errors() == 0
+
+
+# 24 * 256 / dim query heads a CTA in a large call, one a warp in a small one.
+@pytest.mark.parametrize("hq,hkv,dim", [(24, 1, 256), (25, 1, 256), (49, 7, 256), (48, 2, 128), (97, 1, 128), (96, 3, 64),
+                                        (193, 1, 64)])
+@pytest.mark.parametrize("T", [2, 620])
+def test_many_query_heads(cuda_lib, T, hq, hkv, dim):
+    pa = cuda_lib
+    q, k, v, w, table, pos = _case(T, hq, hkv, dim, 64, seed=hq)
+    axes = pa.mrope_axes([16, 8, 8])
+    for il in (False, True):
+        got = pa.qk_norm_mrope(q, k, *w, table, pos, axes, 1e-6, interleaved=il)
+        got += pa.qk_norm_rope(q, k, *w, table, pos[0], 1e-6, interleaved=il)
+        for out, x, ww, p in zip(got, (q, k, q, k), w + w, (pos, pos, pos[:1], pos[:1])):
+            ref, tol = _ref(x, ww, table, p, axes if p is pos else bytes(32), il)
+            assert (np.abs(f64(out) - ref) <= tol).all()
     assert pa.device_errors() == 0
