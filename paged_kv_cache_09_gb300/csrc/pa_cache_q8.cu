@@ -12,8 +12,10 @@
 // on the order of tokens, no two CTAs touch one block, and of tokens that share a slot the last
 // one counts.  (Rows, codes and scales may come from the kernel before, whose end this one's start
 // overlaps: they are read with ordinary loads or past L1, not through the read-only path.)  The look
-// through the slots costs 8 bytes of L2 a slot and CTA: with two CTAs an SM, about a tenth of the
-// call's own bytes.
+// through the slots costs 8 bytes of L2 a slot and CTA: with two CTAs an SM 2.4 KB a token, beside the 1.5
+// KB that a token's row of each KV head takes.  A CTA takes 256 tokens at most, so from 78000 tokens on (4
+// heads; 39000 with 8) there are more CTAs, and the look grows as the square of the tokens: 32768 of 4 heads
+// 43 us (4.7 TB/s), 131072 201 (4.0), 262144 519 (3.1).
 //
 // Measured, 4 KV heads unless said: 16 tokens written in 2.6 us and 256 read in 1.7 (launch and three
 // round trips: slots, rows, stores); 4096 written in 6.3 us and read in 4.6 (4.0 and 5.4 TB/s); 8192 in 11.6

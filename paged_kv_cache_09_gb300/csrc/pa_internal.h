@@ -268,7 +268,8 @@ struct ExpandArgs {
     int64_t table_stride;
     unsigned *err;
 };
-// Two launches each: ranges (and queries), then keys and values.
+// Two launches: ranges (and queries), then keys and values; of the 8-bit cache, one without ranges up to
+// 16384 keys.
 cudaError_t launch_expand_q4(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
 cudaError_t launch_expand_q8(const ExpandArgs &a, int64_t num_pages_out, cudaStream_t stream);
 

@@ -16,17 +16,20 @@
 //     out_j = inv (x_j A_j + x_p B_j),   A_j = w_j cos, B_j = +- w_p sin   (p: j's partner),
 // from weights that a CTA keeps in shared memory as it needs them; the partners are exchanged as packed
 // BF16, before any arithmetic, and the arithmetic is on pairs.
-// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 22.8 us, 5.9 TB/s.  With the weights made
+// 4096 tokens of 24 + 4 + 4 heads of 256, into a BF16 cache: 22.2 us, 6.0 TB/s.  With the weights made
 // ready at each token 25.5; besides, with a warp's next rows in registers instead of shared memory, which
 // are on their way for a shorter time, 28.1, with the rows summed one by one 29, and with the weights
-// applied to every row 43.  Into a 4-bit cache 30.2 us, without a cache 20.4.  32 + 8 + 8 heads 36.5 us, 12 + 2
-// + 2 16.7 (5.5 and 4.0 TB/s), 64 + 8 + 8 of 128 34.1 (4.9 TB/s).  16 tokens 2.2 us.  20 warps an SM instead of
-// 16: 23.1 us, and 64 + 8 + 8 heads of 128 33.3, but 512 tokens 5.0 instead of 4.5.
+// applied to every row 43.  Into a 4-bit cache 29.5 us, without a cache 20.0.  32 + 8 + 8 heads 35.4 us, 12 + 2
+// + 2 16.2 (5.7 and 4.1 TB/s), 64 + 8 + 8 of 128 35.0 (4.8 TB/s).  16 tokens 2.2 us.  20 warps an SM instead of
+// 16 (when that took 22.8 and 34.1): 23.1 us, and 64 + 8 + 8 heads of 128 33.3, but 512 tokens 5.0 instead of
+// 4.5.  Copying rows ahead pays where a CTA has several tokens of several rows: calls of 200 to 1500 tokens
+// with one or two rows a warp and token lose 0.1 to 0.3 us to it (400 tokens of 32 + 8 + 8 heads of 128 3.9 and
+// 4.2 us).
 //
 // Positions on several axes (time, height, width of a token): frequency i takes its angle from the
 // position on the axis that the caller gives it.  Only the fetch of the angles differs: fours of
 // frequencies, each on one axis, come as 16-byte copies, as with one position, others one by one: 4096
-// tokens 23.4 and 25.2 us (by one kernel that chose for each token a microsecond more).
+// tokens 22.9 and 24.6 us (by one kernel that chose for each token a microsecond more).
 #include <algorithm>
 #include <type_traits>
 
