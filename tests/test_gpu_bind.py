@@ -80,3 +80,40 @@ def test_other_threads_run_while_a_call_waits(cuda_lib, waiting, name):
     entered.value = 1  # (the thread ends whatever the call did)
     thread.join()
     assert got is not None and type(got) is not int  # (a status: it was not let go)
+
+
+def test_two_threads_on_streams_of_their_own(cuda_lib):
+    # Steps of writes, decodes and prefills from two threads at once: the bits of one thread after another.
+    pa = cuda_lib
+    S, hq, hkv, bs, steps = 4, 8, 2, 16, 60
+
+    def run(seed, stream, out):
+        with torch.cuda.stream(stream):
+            g = torch.Generator(device="cuda").manual_seed(seed)
+            codes, scales = pa.q8_cache_shapes(S * 8, bs, hkv)
+            cache = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in (codes, codes, scales, scales)]
+            cache[:2] = [c.view(torch.float8_e4m3fn) for c in cache[:2]]
+            table = torch.arange(S * 8, dtype=torch.int32, device="cuda").view(S, 8)
+            x = torch.randn(steps, 3, S, hq, 256, generator=g, device="cuda").to(torch.bfloat16)
+            for i in range(steps):
+                q, k, v = x[i, 0], x[i, 1, :, :hkv], x[i, 2, :, :hkv]
+                pa.reshape_and_cache_q8(k, v, *cache, torch.arange(S, device="cuda") * 8 * bs + i)
+                lens = torch.full((S,), i + 1, dtype=torch.int32, device="cuda")
+                out.append(pa.decode_q8(q, *cache, table, lens, 0.0625, steps))
+                out.append(pa.prefill_varlen_q8(q, *cache, table, list(range(S + 1)), [i + 1] * S, True, 0.0625))
+            out += pa.gather_cache_q8(*cache, torch.arange(steps, device="cuda"))
+            stream.synchronize()
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    want, got = [[], []], [[], []]
+    for i in range(2):
+        run(i, streams[i], want[i])
+    threads = [threading.Thread(target=run, args=(i, streams[i], got[i])) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert len(a) == len(b) == 2 * steps + 2
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert pa.device_errors() == 0
